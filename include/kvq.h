@@ -52,7 +52,7 @@ typedef enum {
   KVQ_EUNSUPPORTED = 4,  /* layout/dtype combination not provided */
   KVQ_EALIGN = 5,        /* a pointer is not 16-byte aligned (workspace: 256) */
   KVQ_ECUDA = 6,         /* a CUDA launch failed */
-  KVQ_EWORKSPACE = 7     /* workspace_bytes smaller than kvq_attend_workspace_bytes() */
+  KVQ_EWORKSPACE = 7     /* workspace_bytes smaller than the call's *_workspace_bytes() */
 } kvq_status;
 
 typedef enum {
@@ -323,6 +323,155 @@ kvq_status kvq_paged_append_decode_attend(const kvq_paged_cache *cache, const vo
                                           int32_t max_kv_len, int32_t causal, float attn_scale, int32_t chunk,
                                           float *out, void *workspace, size_t workspace_bytes,
                                           kvq_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Rotary positions (no counterpart on the pages, which start at rotated keys): the table of cosines
+ * and sines, and the append that rotates the new keys and queries.
+ */
+typedef enum {
+  KVQ_ROPE_NONE = 0,     /* f_i = base^(-2i / rot_dim), i = 0 .. rot_dim/2 - 1 */
+  KVQ_ROPE_LINEAR = 1,   /* f_i / factor */
+  KVQ_ROPE_NTK = 2,      /* base * factor^(rot_dim / (rot_dim - 2)) in place of base */
+  KVQ_ROPE_BANDED = 3,   /* by the turns u = original_len * f_i / (2 pi) within the trained length:
+                            f_i for u >= high, f_i / factor for u <= low, in between the mix with
+                            weight (u - low) / (high - low) on f_i */
+  KVQ_ROPE_YARN = 4      /* f_i / factor and f_i mixed by a ramp over i: it rises from 0 (f_i) at
+                            floor(d(high)) to 1 (f_i / factor) at ceil(d(low)), d(u) = rot_dim
+                            ln(original_len / (2 pi u)) / (2 ln base), both clamped into
+                            [0, rot_dim - 1]; magnitude 0.1 ln(factor) + 1 (1 for factor <= 1) */
+} kvq_rope_scaling;
+
+typedef struct kvq_rope_config {
+  int32_t rot_dim;       /* rotated dims: a multiple of 16 in [16, 256] */
+  int32_t scaling;       /* kvq_rope_scaling */
+  double base;           /* > 1 */
+  double factor;         /* > 0; unused by KVQ_ROPE_NONE */
+  double original_len;   /* > 0; BANDED and YARN: the trained context length */
+  double low, high;      /* BANDED and YARN: turns within the trained length, 0 < low < high */
+} kvq_rope_config;
+
+/* The frequencies of a configuration, in radians per position: inv_freq host [rot_dim / 2]; and the
+ * magnitude its table is multiplied by. Host arithmetic only. */
+kvq_status kvq_rope_frequencies(const kvq_rope_config *config, double *inv_freq, float *magnitude);
+
+/*
+ * Rows [pos0, pos0 + n_pos) of a rotary table: row p holds cos(p inv_freq[i]) * magnitude for
+ * i = 0 .. rot_dim/2 - 1, then sin(p inv_freq[i]) * magnitude.
+ *   inv_freq  host [rot_dim / 2], in [0, 65536], read before the call returns
+ *   table     device f32 [n_pos][rot_dim]
+ * The angle is reduced exactly (64-bit fractions of a turn), so far positions are as exact as near
+ * ones. n_pos == 0 is a no-op; pos0 + n_pos may not exceed INT32_MAX.
+ */
+kvq_status kvq_rope_table(const double *inv_freq, int32_t rot_dim, int32_t pos0, int32_t n_pos, float magnitude,
+                          float *table, kvq_stream_t stream);
+
+typedef struct kvq_rope {
+  const float *table;          /* device f32 [n_pos][rot_dim], as kvq_rope_table writes it */
+  int32_t n_pos;
+  int32_t rot_dim;             /* a multiple of 16 in [16, head_dim]; later dims stay as they are */
+  int32_t interleaved;         /* 0: dims (i, i + rot_dim/2) are a pair; else dims (2i, 2i + 1) */
+  const int32_t *positions;    /* device i32 [batch][n_new]: the position of every new row, which need
+                                  not be its slot (an evicted cache); NULL: the slot. One outside
+                                  [0, n_pos) is clamped into the table. */
+} kvq_rope;
+
+/* Rows [batch][heads][n_new][head_dim] at element strides (>= 0; the head_dim axis is contiguous):
+ * views of a fused projection's output need no copy. The data and every stride are 16-byte aligned. */
+typedef struct kvq_rows {
+  const void *data;
+  int64_t batch_stride, head_stride, token_stride;
+} kvq_rows;
+
+/*
+ * kvq_store with rotary positions: k_new is rotated, then stored as the layout's store does it; v_new
+ * is stored; q (optional) is rotated and written to q_out, rounded once to `dtype`:
+ *   y_a = x_a c - x_b s,  y_b = x_b c + x_a s   per pair (a, b), each product and sum rounded to f32
+ * (so the packed bytes are those of kvq_store on the f32 rotated keys, bit for bit).
+ *   k_new, v_new, q  in `dtype`; q NULL: no queries (n_q_heads 0, q_out NULL)
+ *   q_out            device [batch][n_q_heads][n_new][head_dim] in `dtype`; overlaps no input
+ * One kernel launch (mixed K/V layouts: one per plane). n_new == 0 is a no-op.
+ */
+kvq_status kvq_rope_store(const kvq_cache *cache, const kvq_rope *rope, const kvq_rows *k_new, const kvq_rows *v_new,
+                          const kvq_rows *q, int32_t dtype, int32_t n_q_heads, int32_t n_new, int32_t pos0,
+                          void *q_out, kvq_stream_t stream);
+/* The same into a paged pool: sequence b's rows at slots [slots[b], slots[b] + n_new) (device i32
+ * [batch]); as in kvq_paged_store a row whose slot lies outside the sequence is not written (its q row
+ * is). */
+kvq_status kvq_paged_rope_store(const kvq_paged_cache *cache, const kvq_rope *rope, const kvq_rows *k_new,
+                                const kvq_rows *v_new, const kvq_rows *q, int32_t dtype, int32_t n_q_heads,
+                                int32_t n_new, const int32_t *slots, void *q_out, kvq_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * A cache inside a budget (no counterpart on the pages): running attention weight per token, the
+ * selection of the tokens to keep, and the compaction of their rows.
+ *
+ * kvq_decode_attend (arguments as there; for chunk 0 its own choice, never longer than that of
+ * kvq_decode_attend) that also updates every token's score:
+ *   scores_out[b][kv head][t] = decay * scores_in[b][kv head][t] + the softmax weights of token t
+ *                               summed over the query rows of its kv head,  0 <= t < kv_len
+ *   scores_in, scores_out  device f32 [batch][n_kv_heads][scores_stride], scores_stride >= kv_len;
+ *                          they may be the same buffer, else they do not overlap. scores_in NULL or
+ *                          decay 0: no earlier scores are read. Entries t >= kv_len are left as they
+ *                          were. A row that sees no token adds nothing.
+ *   workspace              at least kvq_attend_weights_workspace_bytes (shared with no call in flight)
+ * Deterministic: no atomics.
+ */
+size_t kvq_attend_weights_workspace_bytes(const kvq_cache *cache, int32_t n_q_heads, int32_t n_q, int32_t kv_len,
+                                          int32_t chunk);
+kvq_status kvq_decode_attend_weights(const kvq_cache *cache, const void *q, int32_t q_dtype, int32_t n_q_heads,
+                                     int32_t n_q, int32_t kv_len, int32_t causal, int32_t q_pos0, float attn_scale,
+                                     int32_t chunk, float *out, const float *scores_in, float *scores_out,
+                                     int64_t scores_stride, float decay, void *workspace, size_t workspace_bytes,
+                                     kvq_stream_t stream);
+/* The same as kvq_paged_decode_attend: scores of sequence b's tokens t < seq_lens[b] (scores_stride >=
+ * max_kv_len). */
+size_t kvq_paged_attend_weights_workspace_bytes(const kvq_paged_cache *cache, int32_t n_q_heads, int32_t n_q,
+                                                int32_t max_kv_len, int32_t chunk);
+kvq_status kvq_paged_decode_attend_weights(const kvq_paged_cache *cache, const void *q, int32_t q_dtype,
+                                           int32_t n_q_heads, int32_t n_q, const int32_t *seq_lens,
+                                           int32_t max_kv_len, int32_t causal, float attn_scale, int32_t chunk,
+                                           float *out, const float *scores_in, float *scores_out,
+                                           int64_t scores_stride, float decay, void *workspace,
+                                           size_t workspace_bytes, kvq_stream_t stream);
+
+/*
+ * The tokens that (batch, kv head) keeps: the first n_sink, the last n_recent, and among the others the
+ * highest scores, ties going to the lowest index (NaN counts as -infinity, -0 as +0), n_keep in all.
+ *   scores    device f32 [batch][n_kv_heads][scores_stride]
+ *   seq_lens  device i32 [batch], each clamped into [0, kv_len], or NULL: every length is kv_len
+ *   keep      device i32 [batch][n_kv_heads][n_keep]: ascending; a sequence of at most n_keep tokens
+ *             keeps all of them, and -1 fills the rest
+ *   new_lens  device i32 [batch]: min(length, n_keep), or NULL; not seq_lens itself (every head reads
+ *             the old lengths, and so does kvq_paged_evict_compact)
+ * n_sink + n_recent <= n_keep; 1 <= kv_len <= 2^27. One launch.
+ */
+kvq_status kvq_evict_select(const float *scores, int32_t batch, int32_t n_kv_heads, int64_t scores_stride,
+                            int32_t kv_len, const int32_t *seq_lens, int32_t n_keep, int32_t n_sink,
+                            int32_t n_recent, int32_t *keep, int32_t *new_lens, kvq_stream_t stream);
+
+/*
+ * Move the kept tokens together: row keep[b][h][i] of every plane becomes row i, i < min(kv_len, n_keep),
+ * bit for bit; afterwards the cache holds min(kv_len, n_keep) tokens and the next append goes there.
+ *   keep    as kvq_evict_select writes it (ascending per (batch, kv head)). An entry outside [0, kv_len)
+ *           moves nothing; a list in any other order gives unspecified rows. No access leaves the cache.
+ *   dst     NULL (or the cache itself): in place. Else another cache of the same layout, batch,
+ *           n_kv_heads, head_dim and n_recent with room for min(kv_len, n_keep) tokens, no plane shared.
+ *   scores  device f32 [batch][n_kv_heads][scores_stride] or NULL: moved likewise, in place, or (with
+ *           another dst) to scores_out [batch][n_kv_heads][out_stride]; entries behind the kept ones up
+ *           to min(stride, kv_len) become 0, ready for new tokens.
+ * HAD_INT4 / HAD_INT2 with n_recent > 0: the list has to keep the last n_recent tokens (n_keep >=
+ * n_recent), and the window ring is turned so that they stay at (new index mod n_recent).
+ * 1 <= kv_len <= 2^27. Two launches at most.
+ */
+kvq_status kvq_evict_compact(const kvq_cache *cache, const kvq_cache *dst, const int32_t *keep, int32_t n_keep,
+                             int32_t kv_len, float *scores, int64_t scores_stride, float *scores_out,
+                             int64_t out_stride, kvq_stream_t stream);
+/* In place in a paged pool, every sequence by its own length (seq_lens: the lengths before, device i32
+ * [batch], clamped into [0, max_kv_len]); a sequence of at most n_keep tokens stays as it is. The pages
+ * of a sequence that is cut may be shared with no other sequence. */
+kvq_status kvq_paged_evict_compact(const kvq_paged_cache *cache, const int32_t *keep, int32_t n_keep,
+                                   const int32_t *seq_lens, int32_t max_kv_len, float *scores,
+                                   int64_t scores_stride, kvq_stream_t stream);
 
 /* ------------------------------------------------------------------------------------------
  * Host-buffer forms of the two append + attend calls, for callers whose new rows and queries are

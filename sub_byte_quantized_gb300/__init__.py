@@ -9,5 +9,8 @@ from .api import (  # noqa: F401
     PagedKVCache, paged_store, paged_decode_attend, paged_append_decode_attend, paged_attend_workspace_bytes,
     paged_attend_chunk, paged_attend_plan_chunk, append_decode_attend_host, append_decode_attend_host_workspace_bytes,
     paged_append_decode_attend_host, paged_append_decode_attend_host_workspace_bytes,
+    rope_frequencies, rope_table, rope_store, paged_rope_store,
+    decode_attend_weights, paged_decode_attend_weights, attend_weights_workspace_bytes,
+    paged_attend_weights_workspace_bytes, evict_select, evict_compact, paged_evict_compact,
 )
 from ._lib import KvqError, LAYOUT_IDS, EXPORTS  # noqa: F401

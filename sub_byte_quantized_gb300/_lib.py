@@ -39,7 +39,12 @@ EXPORTS = ("kvq_row_bytes", "kvq_cache_bytes", "kvq_store_q4_0", "kvq_store_q6_0
            "kvq_paged_decode_attend", "kvq_paged_append_decode_attend", "kvq_store_q8_0", "kvq_store_hadamard_int2",
            "kvq_store", "kvq_paged_attend_plan_chunk", "kvq_append_decode_attend_host_workspace_bytes",
            "kvq_append_decode_attend_host", "kvq_paged_append_decode_attend_host_workspace_bytes",
-           "kvq_paged_append_decode_attend_host", "kvq_debug_attend_scores_i32")
+           "kvq_paged_append_decode_attend_host", "kvq_debug_attend_scores_i32",
+           "kvq_rope_frequencies", "kvq_rope_table", "kvq_rope_store", "kvq_paged_rope_store",
+           "kvq_attend_weights_workspace_bytes", "kvq_decode_attend_weights",
+           "kvq_paged_attend_weights_workspace_bytes", "kvq_paged_decode_attend_weights",
+           "kvq_evict_select", "kvq_evict_compact", "kvq_paged_evict_compact")
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "banded": 3, "yarn": 4}   # kvq_rope_scaling
 STATIC_SCRATCH_BYTES = 16 * 1024 * 1024   # KVQ_STATIC_SCRATCH_BYTES in include/kvq.h
 
 
@@ -61,6 +66,21 @@ class KvqPagedCache(C.Structure):
                 ("k_zero", C.c_void_p), ("v_zero", C.c_void_p),
                 ("k_recent", C.c_void_p), ("v_recent", C.c_void_p),
                 ("block_table", C.c_void_p)]
+
+
+class KvqRopeConfig(C.Structure):
+    _fields_ = [("rot_dim", C.c_int32), ("scaling", C.c_int32), ("base", C.c_double), ("factor", C.c_double),
+                ("original_len", C.c_double), ("low", C.c_double), ("high", C.c_double)]
+
+
+class KvqRope(C.Structure):
+    _fields_ = [("table", C.c_void_p), ("n_pos", C.c_int32), ("rot_dim", C.c_int32), ("interleaved", C.c_int32),
+                ("positions", C.c_void_p)]
+
+
+class KvqRows(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("batch_stride", C.c_int64), ("head_stride", C.c_int64),
+                ("token_stride", C.c_int64)]
 
 
 class KvqError(RuntimeError):
@@ -126,6 +146,24 @@ def lib() -> C.CDLL:
     L.kvq_paged_append_decode_attend_host_workspace_bytes.restype = SZ
     L.kvq_paged_append_decode_attend_host.argtypes = L.kvq_paged_append_decode_attend.argtypes
     L.kvq_paged_append_decode_attend_host.restype = I32
+    rope_p, rows_p, I64, F = C.POINTER(KvqRope), C.POINTER(KvqRows), C.c_int64, C.c_float
+    for name, args in (
+            ("kvq_rope_frequencies", [C.POINTER(KvqRopeConfig), P, C.POINTER(F)]),
+            ("kvq_rope_table", [P, I32, I32, I32, F, P, P]),
+            ("kvq_rope_store", [cache_p, rope_p, rows_p, rows_p, rows_p, I32, I32, I32, I32, P, P]),
+            ("kvq_paged_rope_store", [paged_p, rope_p, rows_p, rows_p, rows_p, I32, I32, I32, P, P, P]),
+            ("kvq_decode_attend_weights", [cache_p, P, I32, I32, I32, I32, I32, I32, F, I32, P, P, P, I64, F, P, SZ, P]),
+            ("kvq_paged_decode_attend_weights", [paged_p, P, I32, I32, I32, P, I32, I32, F, I32, P, P, P, I64, F, P, SZ,
+                                                 P]),
+            ("kvq_evict_select", [P, I32, I32, I64, I32, P, I32, I32, I32, P, P, P]),
+            ("kvq_evict_compact", [cache_p, cache_p, P, I32, I32, P, I64, P, I64, P]),
+            ("kvq_paged_evict_compact", [paged_p, P, I32, P, I32, P, I64, P])):
+        f = getattr(L, name)
+        f.argtypes, f.restype = args, I32
+    L.kvq_attend_weights_workspace_bytes.argtypes = [cache_p, I32, I32, I32, I32]
+    L.kvq_attend_weights_workspace_bytes.restype = SZ
+    L.kvq_paged_attend_weights_workspace_bytes.argtypes = [paged_p, I32, I32, I32, I32]
+    L.kvq_paged_attend_weights_workspace_bytes.restype = SZ
     L.kvq_status_string.argtypes, L.kvq_status_string.restype = [I32], C.c_char_p
     L.kvq_last_error.argtypes, L.kvq_last_error.restype = [], C.c_char_p
     L.kvq_profile_phase1_events.argtypes, L.kvq_profile_phase1_events.restype = [P, P], I32

@@ -1,8 +1,8 @@
 """Build libkvq.so in-tree for sm_103a with nvcc (no cmake, no torch extension machinery).
 
 Each .cu translation unit is compiled in parallel to an object file under `_build/`, then
-linked into `sub_byte_quantized_gb300/libkvq.so` against the shared CUDA runtime. The store
-translation unit is compiled with -fmad=false so quantisation arithmetic is never contracted.
+linked into `sub_byte_quantized_gb300/libkvq.so` against the shared CUDA runtime. The append
+translation units are compiled with -fmad=false so quantisation arithmetic is never contracted.
 """
 from __future__ import annotations
 
@@ -22,7 +22,7 @@ LIB = os.path.join(PKG, "libkvq.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
                  "-I", INCLUDE, "-I", CSRC, "--expt-relaxed-constexpr"]
-PER_FILE = {"store.cu": ["-fmad=false"]}
+PER_FILE = {"store.cu": ["-fmad=false"], "rope.cu": ["-fmad=false"]}
 
 
 def nvcc() -> str:

@@ -2,6 +2,7 @@
 // Nothing here allocates, synchronises or prints; failures return a kvq_status and record a
 // one-line reason readable through kvq_last_error().
 #include <climits>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -263,6 +264,7 @@ kvq_status resolve_core(int n_q_heads, int n_q, int kv_len, int causal, int q_po
   a.fresh_tail = 0;
   a.cap_scores = nullptr;
   a.cap_sq = nullptr;
+  a.lse = nullptr;
   const size_t rows = (size_t)c.B * n_q_heads * n_q;
   size_t off = 0;
   const size_t o_m = off; off = round_up(off + rows * a.C * sizeof(float), 256);
@@ -789,6 +791,392 @@ kvq_status kvq_paged_append_decode_attend(const kvq_paged_cache *cache, const vo
                                                    reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(KVQ_ECUDA, "append/attend launch: %s", cudaGetErrorString(e));
   return KVQ_OK;
+}
+
+// ------------------------------------------------------------------ rotary positions
+namespace {
+
+constexpr double kTwoPi = 6.283185307179586476925286766559;
+
+kvq_status check_rot_dim(int rot_dim, int max_dim) {
+  if (rot_dim < 16 || rot_dim > max_dim || rot_dim % 16)
+    return fail(KVQ_ESHAPE, "rot_dim %d not a multiple of 16 in [16, %d]", rot_dim, max_dim);
+  return KVQ_OK;
+}
+
+// Rows read by their strides: pointer and strides 16-byte aligned (the kernels load 16 bytes at a time).
+kvq_status check_rows(const char *name, const kvq_rows *r, int dtype, kvq::RowsIn &in) {
+  if (!r || !r->data) return fail(KVQ_EINVAL, "%s is NULL", name);
+  const int64_t st[] = {r->batch_stride, r->head_stride, r->token_stride};
+  for (int64_t x : st) {
+    if (x < 0) return fail(KVQ_EINVAL, "%s has a negative stride", name);
+    if ((x * (int64_t)dtype_bytes(dtype)) % 16) return fail(KVQ_EALIGN, "%s: a stride is not a multiple of 16 bytes", name);
+  }
+  if (!aligned(r->data, 16)) return fail(KVQ_EALIGN, "%s not 16-byte aligned", name);
+  in = {r->data, r->batch_stride, r->head_stride, r->token_stride};
+  return KVQ_OK;
+}
+
+// The arguments both rotary appends share, for a checked cache view.
+kvq_status check_rope_store(const kvq::CacheView &v, const kvq_rope *rope, const kvq_rows *k_new, const kvq_rows *v_new,
+                            const kvq_rows *q, int dtype, int n_q_heads, int n_new, void *q_out, kvq::RopeStore &g) {
+  if (!rope || !rope->table) return fail(KVQ_EINVAL, "rope or its table is NULL");
+  if (dtype < KVQ_F32 || dtype > KVQ_F16) return fail(KVQ_EINVAL, "unknown dtype %d", dtype);
+  if (n_new < 0) return fail(KVQ_EINVAL, "n_new must be >= 0");
+  if (n_q_heads < 0) return fail(KVQ_EINVAL, "n_q_heads must be >= 0");
+  kvq_status st = check_rot_dim(rope->rot_dim, v.D);
+  if (st != KVQ_OK) return st;
+  if (rope->n_pos < 1) return fail(KVQ_EINVAL, "the rotary table has no positions");
+  if (!aligned(rope->table, 16) || !aligned(rope->positions, 16))
+    return fail(KVQ_EALIGN, "rotary table/positions not 16-byte aligned");
+  if ((q != nullptr) != (n_q_heads > 0)) return fail(KVQ_EINVAL, "q and n_q_heads go together");
+  if (n_q_heads % v.H) return fail(KVQ_ESHAPE, "n_q_heads %d not a multiple of n_kv_heads %d", n_q_heads, v.H);
+  if (q && !q_out) return fail(KVQ_EINVAL, "q_out is NULL");
+  if (q && !aligned(q_out, 16)) return fail(KVQ_EALIGN, "q_out not 16-byte aligned");
+  if ((long double)v.B * (2.0L * v.H + n_q_heads) * n_new * 32 > 256.0L * INT_MAX)
+    return fail(KVQ_ESHAPE, "too many rows for one launch");
+  if (n_new == 0) return KVQ_OK;
+  st = check_rows("k_new", k_new, dtype, g.in[0]);
+  if (st == KVQ_OK) st = check_rows("v_new", v_new, dtype, g.in[1]);
+  g.in[2] = {nullptr, 0, 0, 0};
+  if (st == KVQ_OK && q) st = check_rows("q", q, dtype, g.in[2]);
+  if (st != KVQ_OK) return st;
+  g.dtype = dtype; g.Hq = n_q_heads; g.n_new = n_new; g.pos0 = 0; g.slots = nullptr;
+  g.table = rope->table; g.n_pos = rope->n_pos; g.rot = rope->rot_dim; g.interleaved = rope->interleaved ? 1 : 0;
+  g.positions = rope->positions;
+  g.q_out = q_out;
+  g.k_rows = g.v_rows = g.q_rows = 0;
+  g.row_bytes = 0;
+  return KVQ_OK;
+}
+
+}  // namespace
+
+kvq_status kvq_rope_frequencies(const kvq_rope_config *config, double *inv_freq, float *magnitude) {
+  g_last_error[0] = 0;
+  if (!config || !inv_freq || !magnitude) return fail(KVQ_EINVAL, "config/inv_freq/magnitude is NULL");
+  const kvq_rope_config &c = *config;
+  const kvq_status st = check_rot_dim(c.rot_dim, 2 * kvq::kMaxRotHalf);
+  if (st != KVQ_OK) return st;
+  if (c.scaling < KVQ_ROPE_NONE || c.scaling > KVQ_ROPE_YARN) return fail(KVQ_EINVAL, "unknown scaling %d", c.scaling);
+  if (!(c.base > 1.0) || std::isinf(c.base)) return fail(KVQ_EINVAL, "base must be finite and > 1");
+  if (c.scaling != KVQ_ROPE_NONE && (!(c.factor > 0.0) || std::isinf(c.factor)))
+    return fail(KVQ_EINVAL, "factor must be finite and > 0");
+  const bool bands = c.scaling == KVQ_ROPE_BANDED || c.scaling == KVQ_ROPE_YARN;
+  if (bands && (!(c.original_len > 0.0) || std::isinf(c.original_len) || !(c.low > 0.0) || !(c.high > c.low) || std::isinf(c.high)))
+    return fail(KVQ_EINVAL, "original_len > 0 and 0 < low < high are needed");
+  const int n = c.rot_dim / 2;
+  const double base = c.scaling == KVQ_ROPE_NTK ? c.base * std::pow(c.factor, (double)c.rot_dim / (c.rot_dim - 2)) : c.base;
+  if (!(base > 0.0) || std::isinf(base)) return fail(KVQ_EINVAL, "the scaled base is out of range");
+  double lo = 0.0, hi = 0.0;
+  if (c.scaling == KVQ_ROPE_YARN) {
+    const double k = c.rot_dim / (2.0 * std::log(c.base));
+    lo = std::fmin(std::fmax(std::floor(k * std::log(c.original_len / (c.high * kTwoPi))), 0.0), c.rot_dim - 1.0);
+    hi = std::fmin(std::fmax(std::ceil(k * std::log(c.original_len / (c.low * kTwoPi))), 0.0), c.rot_dim - 1.0);
+    if (hi <= lo) hi = lo + 0.001;                       // a step instead of a ramp
+  }
+  for (int i = 0; i < n; ++i) {
+    const double f = std::pow(base, -2.0 * i / c.rot_dim);
+    double own = 1.0;                                    // the share of the unscaled frequency
+    if (c.scaling == KVQ_ROPE_LINEAR) own = 0.0;
+    if (c.scaling == KVQ_ROPE_BANDED)
+      own = std::fmin(std::fmax((c.original_len * f / kTwoPi - c.low) / (c.high - c.low), 0.0), 1.0);
+    if (c.scaling == KVQ_ROPE_YARN) own = 1.0 - std::fmin(std::fmax((i - lo) / (hi - lo), 0.0), 1.0);
+    inv_freq[i] = own == 1.0 ? f : f / c.factor * (1.0 - own) + f * own;
+  }
+  *magnitude = c.scaling == KVQ_ROPE_YARN && c.factor > 1.0 ? (float)(0.1 * std::log(c.factor) + 1.0) : 1.0f;
+  return KVQ_OK;
+}
+
+kvq_status kvq_rope_table(const double *inv_freq, int32_t rot_dim, int32_t pos0, int32_t n_pos, float magnitude,
+                          float *table, kvq_stream_t stream) {
+  g_last_error[0] = 0;
+  const kvq_status st = check_rot_dim(rot_dim, 2 * kvq::kMaxRotHalf);
+  if (st != KVQ_OK) return st;
+  if (pos0 < 0 || n_pos < 0 || (long long)pos0 + n_pos > INT_MAX)
+    return fail(KVQ_EINVAL, "positions [%d, %lld) out of range", pos0, (long long)pos0 + n_pos);
+  if (!std::isfinite(magnitude)) return fail(KVQ_EINVAL, "magnitude must be finite");
+  if (n_pos == 0) return KVQ_OK;
+  if (!inv_freq || !table) return fail(KVQ_EINVAL, "inv_freq/table is NULL");
+  if (!aligned(table, 16)) return fail(KVQ_EALIGN, "table not 16-byte aligned");
+  kvq::RopeTurns f = {};
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    if (!(inv_freq[i] >= 0.0 && inv_freq[i] <= 65536.0)) return fail(KVQ_EINVAL, "inv_freq[%d] not in [0, 65536]", i);
+    // inv_freq / 2 pi to 2^-64 of a turn: 1 / 2 pi as two doubles, the first product's rounding by an fma;
+    // whole turns change nothing
+    constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57;
+    const double turns = inv_freq[i] * kHi, rest = std::fma(inv_freq[i], kHi, -turns) + inv_freq[i] * kLo;
+    f.turn[i] = (unsigned long long)std::ldexp(turns - std::floor(turns), 64) +
+                (unsigned long long)std::llrint(std::ldexp(rest, 64));
+  }
+  const cudaError_t e = kvq::launch_rope_table(f, rot_dim, pos0, n_pos, magnitude, table, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(KVQ_ECUDA, "rope table launch: %s", cudaGetErrorString(e));
+  return KVQ_OK;
+}
+
+kvq_status kvq_rope_store(const kvq_cache *cache, const kvq_rope *rope, const kvq_rows *k_new, const kvq_rows *v_new,
+                          const kvq_rows *q, int32_t dtype, int32_t n_q_heads, int32_t n_new, int32_t pos0, void *q_out,
+                          kvq_stream_t stream) {
+  g_last_error[0] = 0;
+  kvq::CacheView v;
+  kvq::RopeStore g;
+  kvq_status st = check_cache(cache, v);
+  if (st == KVQ_OK) st = check_rope_store(v, rope, k_new, v_new, q, dtype, n_q_heads, n_new, q_out, g);
+  if (st != KVQ_OK) return st;
+  if (pos0 < 0) return fail(KVQ_EINVAL, "pos0 must be >= 0");
+  if ((long long)pos0 + n_new > v.cap) return fail(KVQ_ECAPACITY, "pos0 + n_new = %lld > capacity %d", (long long)pos0 + n_new, v.cap);
+  if (n_new == 0) return KVQ_OK;
+  g.pos0 = pos0;
+  const cudaError_t e = kvq::launch_rope_store(v, g, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(KVQ_ECUDA, "rope store launch: %s", cudaGetErrorString(e));
+  return KVQ_OK;
+}
+
+kvq_status kvq_paged_rope_store(const kvq_paged_cache *cache, const kvq_rope *rope, const kvq_rows *k_new,
+                                const kvq_rows *v_new, const kvq_rows *q, int32_t dtype, int32_t n_q_heads, int32_t n_new,
+                                const int32_t *slots, void *q_out, kvq_stream_t stream) {
+  g_last_error[0] = 0;
+  kvq::CacheView v;
+  kvq::RopeStore g;
+  kvq_status st = check_paged_cache(cache, v);
+  if (st == KVQ_OK) st = check_rope_store(v, rope, k_new, v_new, q, dtype, n_q_heads, n_new, q_out, g);
+  if (st != KVQ_OK) return st;
+  if (n_new > v.cap) return fail(KVQ_ECAPACITY, "n_new %d > sequence capacity %d", n_new, v.cap);
+  if (n_new == 0) return KVQ_OK;
+  if (!slots) return fail(KVQ_EINVAL, "slots is NULL");
+  if (!aligned(slots, 16)) return fail(KVQ_EALIGN, "slots not 16-byte aligned");
+  g.slots = slots;
+  const cudaError_t e = kvq::launch_rope_store(v, g, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(KVQ_ECUDA, "rope store launch: %s", cudaGetErrorString(e));
+  return KVQ_OK;
+}
+
+// ------------------------------------------------------------------ a cache inside a budget
+namespace {
+
+constexpr int kMaxEvictTokens = 1 << 27;
+
+// Chunk of an attention call that also scores the tokens, for chunk 0: the attention's own choice, with
+// two bounds. 2560 tokens: its float32 result carries the truncation of the tensor cores' accumulation,
+// which grows with the tokens a warp adds up (16 sequences of up to 16379 tokens in Q8_0: 9.1e-6 of the
+// output's norm at the automatic 4608 tokens). And on the tcgen05 kernel as many chunks as fill the SMs
+// (it takes at most eight by itself: 64 CTAs for 128 rows and 8 kv heads).
+int weights_chunk(const kvq::CacheView &c, int n_q_heads, int n_q, int kv_len, int auto_chunk) {
+  int chunk = auto_chunk < 2560 ? auto_chunk : 2560;
+  const int rows = n_q_heads / c.H * n_q;
+  if (kvq::tc_prefill_shape(c.layout, c.v_layout, c.D, rows)) {
+    int dev = 0, sms = 148;
+    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const long long units = (long long)((rows + kvq::kTcRows - 1) / kvq::kTcRows) * c.B * c.H;
+    const long long n = sms / units, body = kv_len > c.n_recent ? kv_len - c.n_recent : 1;
+    if (n > 1) {
+      const long long fill = ((body + n - 1) / n + 63) / 64 * 64;
+      if (fill < chunk) chunk = (int)fill;
+    }
+  }
+  return chunk;
+}
+int contiguous_chunk(const kvq_cache *cache, int n_q_heads, int n_q, int kv_len, int chunk) {
+  kvq::AttendArgs a;
+  size_t need = 0;
+  if (chunk || resolve_attend(cache, n_q_heads, n_q, kv_len, 0, 0, 0, a, need, nullptr) != KVQ_OK) return chunk;
+  return weights_chunk(a.cache, n_q_heads, n_q, kv_len, a.chunk);
+}
+int paged_chunk(const kvq_paged_cache *cache, int n_q_heads, int n_q, int max_kv_len, int chunk) {
+  kvq::AttendArgs a;
+  size_t need = 0;
+  if (chunk || resolve_paged(cache, n_q_heads, n_q, max_kv_len, 0, 0, a, need, nullptr) != KVQ_OK) return chunk;
+  return weights_chunk(a.cache, n_q_heads, n_q, max_kv_len, a.chunk);
+}
+
+// The rows' log-sum-exp follow the attention's workspace.
+size_t weights_need(size_t attend_need, size_t rows) { return round_up(attend_need, 256) + round_up(rows * sizeof(float), 256); }
+
+kvq_status check_scores(const float *scores_in, const float *scores_out, int64_t stride, int kv_len, float decay) {
+  if (!scores_out) return fail(KVQ_EINVAL, "scores_out is NULL");
+  if (!aligned(scores_in, 16) || !aligned(scores_out, 16)) return fail(KVQ_EALIGN, "scores not 16-byte aligned");
+  if (stride < kv_len) return fail(KVQ_ESHAPE, "scores_stride %lld < kv_len %d", (long long)stride, kv_len);
+  if (!std::isfinite(decay)) return fail(KVQ_EINVAL, "decay must be finite");
+  return KVQ_OK;
+}
+
+kvq_status run_weights(kvq::AttendArgs &a, size_t attend_need, void *workspace, size_t workspace_bytes, const float *scores_in,
+                       float *scores_out, int64_t stride, float decay, cudaStream_t s) {
+  const size_t need = weights_need(attend_need, (size_t)a.cache.B * a.Hq * a.n_q);
+  if (workspace_bytes < need) return fail(KVQ_EWORKSPACE, "workspace %zu < required %zu", workspace_bytes, need);
+  a.lse = reinterpret_cast<float *>(static_cast<char *>(workspace) + round_up(attend_need, 256));
+  cudaError_t e = launch_attend_sequence(a, s, true);
+  if (e == cudaSuccess) e = kvq::launch_attend_weights(a, scores_in, scores_out, stride, decay, s);
+  if (e != cudaSuccess) return fail(KVQ_ECUDA, "attend weights launch: %s", cudaGetErrorString(e));
+  return KVQ_OK;
+}
+
+kvq_status check_evict(const int32_t *keep, int n_keep, int kv_len, const int32_t *seq_lens) {
+  if (!keep) return fail(KVQ_EINVAL, "keep is NULL");
+  if (!aligned(keep, 16) || !aligned(seq_lens, 16)) return fail(KVQ_EALIGN, "keep/seq_lens not 16-byte aligned");
+  if (n_keep < 1) return fail(KVQ_EINVAL, "n_keep must be >= 1");
+  if (kv_len < 1) return fail(KVQ_EINVAL, "kv_len must be >= 1");
+  if (kv_len > kMaxEvictTokens) return fail(KVQ_ECAPACITY, "kv_len %d > %d", kv_len, kMaxEvictTokens);
+  return KVQ_OK;
+}
+
+// The planes of a compaction, and its launch. Both views are checked; scores may be NULL.
+kvq_status run_compact(const kvq::CacheView &src, const kvq::CacheView &dst, bool in_place, const int32_t *keep, int n_keep,
+                       int kv_len, const int32_t *seq_lens, float *scores, int64_t scores_stride, float *scores_out,
+                       int64_t out_stride, cudaStream_t s) {
+  if (n_keep < src.n_recent) return fail(KVQ_EINVAL, "n_keep %d < n_recent %d: the window's tokens stay", n_keep, src.n_recent);
+  const int most = n_keep < kv_len ? n_keep : kv_len;
+  if (scores) {
+    if (!aligned(scores, 16) || !aligned(scores_out, 16)) return fail(KVQ_EALIGN, "scores not 16-byte aligned");
+    if (scores_stride < kv_len) return fail(KVQ_ESHAPE, "scores_stride %lld < kv_len %d", (long long)scores_stride, kv_len);
+    if (out_stride < most) return fail(KVQ_ESHAPE, "out_stride %lld < %d kept tokens", (long long)out_stride, most);
+  }
+  kvq::CompactArgs a;
+  a.src = src;
+  a.dst = dst;
+  a.keep = keep;
+  a.seq_lens = seq_lens;
+  a.n_keep = n_keep;
+  a.kv_len = kv_len;
+  a.n_parts = 0;
+  a.ranks = 1;
+  a.scores_stride = scores_stride;
+  a.out_stride = out_stride;
+  auto part = [&](const void *from, void *to, int row_bytes, int is_scores) {
+    const int unit = row_bytes % 16 == 0 ? 16 : (row_bytes % 8 == 0 ? 8 : 4);
+    a.part[a.n_parts++] = {static_cast<const uint8_t *>(from), static_cast<uint8_t *>(to), row_bytes, unit, is_scores};
+  };
+  const int layouts[2] = {src.layout, src.v_layout}, bytes[2] = {src.row_bytes, src.v_row_bytes};
+  for (int t = 0; t < 2; ++t) part(src.payload[t], dst.payload[t], bytes[t], 0);
+  for (int t = 0; t < 2; ++t) {
+    part(src.scale[t], dst.scale[t], kvq::is_hadamard(layouts[t]) ? 4 : src.D / kvq::kBlock * 2, 0);
+    if (layouts[t] == KVQ_ASYM4_G32) part(src.zero[t], dst.zero[t], src.D / kvq::kBlock * 2, 0);
+  }
+  if (scores) part(scores, scores_out, 4, 1);
+  const cudaError_t e = kvq::launch_evict_compact(a, in_place, s);
+  if (e != cudaSuccess) return fail(KVQ_ECUDA, "compact launch: %s", cudaGetErrorString(e));
+  return KVQ_OK;
+}
+
+}  // namespace
+
+size_t kvq_attend_weights_workspace_bytes(const kvq_cache *cache, int32_t n_q_heads, int32_t n_q, int32_t kv_len,
+                                          int32_t chunk) {
+  chunk = contiguous_chunk(cache, n_q_heads, n_q, kv_len, chunk);
+  const size_t need = kvq_attend_workspace_bytes(cache, n_q_heads, n_q, kv_len, chunk);
+  return need ? weights_need(need, (size_t)cache->batch * n_q_heads * n_q) : 0;
+}
+
+size_t kvq_paged_attend_weights_workspace_bytes(const kvq_paged_cache *cache, int32_t n_q_heads, int32_t n_q,
+                                                int32_t max_kv_len, int32_t chunk) {
+  chunk = paged_chunk(cache, n_q_heads, n_q, max_kv_len, chunk);
+  const size_t need = kvq_paged_attend_workspace_bytes(cache, n_q_heads, n_q, max_kv_len, chunk);
+  return need ? weights_need(need, (size_t)cache->batch * n_q_heads * n_q) : 0;
+}
+
+kvq_status kvq_decode_attend_weights(const kvq_cache *cache, const void *q, int32_t q_dtype, int32_t n_q_heads,
+                                     int32_t n_q, int32_t kv_len, int32_t causal, int32_t q_pos0, float attn_scale,
+                                     int32_t chunk, float *out, const float *scores_in, float *scores_out,
+                                     int64_t scores_stride, float decay, void *workspace, size_t workspace_bytes,
+                                     kvq_stream_t stream) {
+  g_last_error[0] = 0;
+  kvq::AttendArgs a;
+  chunk = contiguous_chunk(cache, n_q_heads, n_q, kv_len, chunk);
+  kvq_status st = prepare_attend(cache, q, q_dtype, n_q_heads, n_q, kv_len, causal, q_pos0, attn_scale, chunk, out,
+                                 workspace, workspace_bytes, a);
+  if (st == KVQ_OK) st = check_scores(scores_in, scores_out, scores_stride, kv_len, decay);
+  if (st != KVQ_OK) return st;
+  const size_t need = kvq_attend_workspace_bytes(cache, n_q_heads, n_q, kv_len, chunk);
+  return run_weights(a, need, workspace, workspace_bytes, scores_in, scores_out, scores_stride, decay,
+                     reinterpret_cast<cudaStream_t>(stream));
+}
+
+kvq_status kvq_paged_decode_attend_weights(const kvq_paged_cache *cache, const void *q, int32_t q_dtype,
+                                           int32_t n_q_heads, int32_t n_q, const int32_t *seq_lens, int32_t max_kv_len,
+                                           int32_t causal, float attn_scale, int32_t chunk, float *out,
+                                           const float *scores_in, float *scores_out, int64_t scores_stride, float decay,
+                                           void *workspace, size_t workspace_bytes, kvq_stream_t stream) {
+  g_last_error[0] = 0;
+  kvq::AttendArgs a;
+  chunk = paged_chunk(cache, n_q_heads, n_q, max_kv_len, chunk);
+  kvq_status st = prepare_paged(cache, q, q_dtype, n_q_heads, n_q, seq_lens, max_kv_len, causal, attn_scale, chunk, out,
+                                workspace, workspace_bytes, a);
+  if (st == KVQ_OK) st = check_scores(scores_in, scores_out, scores_stride, max_kv_len, decay);
+  if (st != KVQ_OK) return st;
+  const size_t need = kvq_paged_attend_workspace_bytes(cache, n_q_heads, n_q, max_kv_len, chunk);
+  return run_weights(a, need, workspace, workspace_bytes, scores_in, scores_out, scores_stride, decay,
+                     reinterpret_cast<cudaStream_t>(stream));
+}
+
+kvq_status kvq_evict_select(const float *scores, int32_t batch, int32_t n_kv_heads, int64_t scores_stride, int32_t kv_len,
+                            const int32_t *seq_lens, int32_t n_keep, int32_t n_sink, int32_t n_recent, int32_t *keep,
+                            int32_t *new_lens, kvq_stream_t stream) {
+  g_last_error[0] = 0;
+  const kvq_status st = check_evict(keep, n_keep, kv_len, seq_lens);
+  if (st != KVQ_OK) return st;
+  if (!scores) return fail(KVQ_EINVAL, "scores is NULL");
+  if (!aligned(scores, 16) || !aligned(new_lens, 16)) return fail(KVQ_EALIGN, "scores/new_lens not 16-byte aligned");
+  if (new_lens && new_lens == seq_lens) return fail(KVQ_EINVAL, "new_lens must not be seq_lens");
+  if (batch < 1 || n_kv_heads < 1) return fail(KVQ_EINVAL, "batch and n_kv_heads must be >= 1");
+  if ((long long)batch * n_kv_heads > 1 << 24) return fail(KVQ_ESHAPE, "batch * n_kv_heads > 2^24");
+  if (scores_stride < kv_len) return fail(KVQ_ESHAPE, "scores_stride %lld < kv_len %d", (long long)scores_stride, kv_len);
+  if (n_sink < 0 || n_recent < 0 || (long long)n_sink + n_recent > n_keep)
+    return fail(KVQ_EINVAL, "n_sink and n_recent must be >= 0 and together at most n_keep");
+  kvq::SelectArgs a = {batch, n_kv_heads, kv_len, n_keep, n_sink, n_recent, scores_stride, scores, seq_lens, keep, new_lens};
+  const cudaError_t e = kvq::launch_evict_select(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(KVQ_ECUDA, "select launch: %s", cudaGetErrorString(e));
+  return KVQ_OK;
+}
+
+kvq_status kvq_evict_compact(const kvq_cache *cache, const kvq_cache *dst, const int32_t *keep, int32_t n_keep,
+                             int32_t kv_len, float *scores, int64_t scores_stride, float *scores_out, int64_t out_stride,
+                             kvq_stream_t stream) {
+  g_last_error[0] = 0;
+  kvq::CacheView v, d;
+  kvq_status st = check_cache(cache, v);
+  if (st == KVQ_OK) st = check_cache(dst ? dst : cache, d);
+  if (st == KVQ_OK) st = check_evict(keep, n_keep, kv_len, nullptr);
+  if (st != KVQ_OK) return st;
+  if (kv_len > v.cap) return fail(KVQ_ECAPACITY, "kv_len %d > capacity %d", kv_len, v.cap);
+  if (v.layout != d.layout || v.v_layout != d.v_layout || v.B != d.B || v.H != d.H || v.D != d.D || v.n_recent != d.n_recent)
+    return fail(KVQ_ESHAPE, "dst differs from the cache in layout, batch, heads, head_dim or n_recent");
+  // the same cache means every plane; a plane shared between two caches would be overwritten while it is read
+  int same = 0, planes = 0;
+  for (int t = 0; t < 2; ++t) {
+    const int layout = t ? v.v_layout : v.layout;
+    same += v.payload[t] == d.payload[t];
+    same += v.scale[t] == d.scale[t];
+    planes += 2;
+    if (layout == KVQ_ASYM4_G32) same += v.zero[t] == d.zero[t], ++planes;
+    if (v.n_recent > 0) same += v.ring[t] == d.ring[t], ++planes;
+  }
+  const bool in_place = same == planes && v.cap == d.cap;
+  if (!in_place && same) return fail(KVQ_EINVAL, "dst shares planes with the cache");
+  const int most = n_keep < kv_len ? n_keep : kv_len;
+  if (most > d.cap) return fail(KVQ_ECAPACITY, "%d kept tokens > dst capacity %d", most, d.cap);
+  if (in_place) {
+    if (scores_out && scores_out != scores) return fail(KVQ_EINVAL, "in place the scores move in place too");
+    scores_out = scores;
+    out_stride = scores_stride;
+  } else if (scores && (!scores_out || scores_out == scores)) {
+    return fail(KVQ_EINVAL, "with another dst the scores go to a scores_out of their own");
+  }
+  return run_compact(v, d, in_place, keep, n_keep, kv_len, nullptr, scores, scores_stride, scores_out, out_stride,
+                     reinterpret_cast<cudaStream_t>(stream));
+}
+
+kvq_status kvq_paged_evict_compact(const kvq_paged_cache *cache, const int32_t *keep, int32_t n_keep,
+                                   const int32_t *seq_lens, int32_t max_kv_len, float *scores, int64_t scores_stride,
+                                   kvq_stream_t stream) {
+  g_last_error[0] = 0;
+  kvq::CacheView v;
+  kvq_status st = check_paged_cache(cache, v);
+  if (st == KVQ_OK && !seq_lens) st = fail(KVQ_EINVAL, "seq_lens is NULL");
+  if (st == KVQ_OK) st = check_evict(keep, n_keep, max_kv_len, seq_lens);
+  if (st != KVQ_OK) return st;
+  if (max_kv_len > v.cap) return fail(KVQ_ECAPACITY, "max_kv_len %d > capacity %d", max_kv_len, v.cap);
+  return run_compact(v, v, true, keep, n_keep, max_kv_len, seq_lens, scores, scores_stride, scores, scores_stride,
+                     reinterpret_cast<cudaStream_t>(stream));
 }
 
 // ------------------------------------------------------------------ host-buffer calls

@@ -77,6 +77,16 @@ __device__ __forceinline__ void unpack6(uint32_t w, uint32_t h, uint32_t (&o)[4]
   o[3] = lop3<0xEC>(w8, (hx << 2) & 0x03000300u, 0x00F000F0u);
 }
 
+// The same with exact signed codes u - 32 in every pair: the field under the exponent of 1024, then one
+// f16 add (or fma, for the odd positions' 16 u).
+__device__ __forceinline__ void unpack6_signed(uint32_t w, uint32_t h, uint32_t (&o)[4]) {
+  const uint32_t hx = h ^ 0x00AA00AAu, w8 = w >> 8;
+  o[0] = hadd2(lop3<0xEC>(w, ((hx << 4) & 0x00300030u) | 0x64006400u, 0x000F000Fu), 0xE420E420u);
+  o[1] = hfma2(lop3<0xEC>(w, ((hx << 6) & 0x03000300u) | 0x64006400u, 0x00F000F0u), kH16th, 0xD600D600u);
+  o[2] = hadd2(lop3<0xEC>(w8, (hx & 0x00300030u) | 0x64006400u, 0x000F000Fu), 0xE420E420u);
+  o[3] = hfma2(lop3<0xEC>(w8, ((hx << 2) & 0x03000300u) | 0x64006400u, 0x00F000F0u), kH16th, 0xD600D600u);
+}
+
 // Last token query row r (of the gqa * n_q rows of a kv head) may see; negative if none.
 __device__ __forceinline__ int row_limit_of(const AttendArgs &a, const SeqLen &sl, int r) {
   return row_limit(a, sl, r % a.n_q);
@@ -84,7 +94,10 @@ __device__ __forceinline__ int row_limit_of(const AttendArgs &a, const SeqLen &s
 
 __device__ __forceinline__ uint32_t lds32(const uint8_t *p) { return *reinterpret_cast<const uint32_t *>(p); }
 
-template <int D, bool PAGED>
+// SIGNED: V codes enter as exact signed values, no offset mass goes through the long P'V accumulation
+// (calls that also score the tokens, whose output is held to float32: error 4e-5 -> see the table of
+// value-path precision).
+template <int D, bool PAGED, bool SIGNED>
 __global__ void __launch_bounds__(kThreads, kMmaQ6CtasPerSm(D)) attend_mma_q6_kernel(AttendArgs a) {
   using G = Geom<D>;
   constexpr int NB = G::NB;
@@ -415,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, kMmaQ6CtasPerSm(D)) attend_mma_q6_ke
         s2c8[0] = x8.x; s2c8[1] = x8.y; s2c9[0] = x9.x; s2c9[1] = x9.y;
       }
       // W term: rows g < NB of its A operand hold block g's V scales
-      {
+      if constexpr (!SIGNED) {
         const uint32_t wa = *reinterpret_cast<const uint16_t *>(sa + 2 * gb);
         const uint32_t wb = *reinterpret_cast<const uint16_t *>(sa + G::SB + 2 * gb);
         const uint32_t wc = *reinterpret_cast<const uint16_t *>(sa + 8 * G::SB + 2 * gb);
@@ -431,8 +444,13 @@ __global__ void __launch_bounds__(kThreads, kMmaQ6CtasPerSm(D)) attend_mma_q6_ke
         const uint32_t Ha = prmt(lds32(va + hi), lds32(vb + hi), sel_v);
         const uint32_t Hb = prmt(lds32(vc + hi), lds32(vd + hi), sel_v);
         uint32_t ua[4], ub[4];
-        unpack6(wa, Ha, ua);
-        unpack6(wb, Hb, ub);
+        if constexpr (SIGNED) {
+          unpack6_signed(wa, Ha, ua);
+          unpack6_signed(wb, Hb, ub);
+        } else {
+          unpack6(wa, Ha, ua);
+          unpack6(wb, Hb, ub);
+        }
         const uint32_t sel = (b & 1) ? 0x7632u : 0x5410u;
         const uint32_t sp0 = prmt(s2c[b >> 1], s2c1[b >> 1], sel), sp1 = prmt(s2c8[b >> 1], s2c9[b >> 1], sel);
         // hi columns: rn(p_hi s); lo columns: rn(p_lo s + (p_hi s - rn(p_hi s))), the error term
@@ -458,7 +476,9 @@ __global__ void __launch_bounds__(kThreads, kMmaQ6CtasPerSm(D)) attend_mma_q6_ke
     asm volatile("cp.async.wait_group 0;\n" ::: "memory");
     __syncthreads();                                     // every warp is done with the rings
     float *co = reinterpret_cast<float *>(smem) + 32;     // [tile][4][D] after cm/cl
-    // value = u * s_v - 32 s_v: even dims entered as u * 2^-24, odd dims as 16 u * 2^-24
+    // value = u * s_v - 32 s_v: even dims entered as u * 2^-24, odd dims as 16 u * 2^-24 (SIGNED: the
+    // codes themselves, Dw stays 0)
+    constexpr float kEven = SIGNED ? 1.0f : 16777216.0f, kOdd = SIGNED ? 1.0f : 1048576.0f;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       const float w0 = 32.0f * __shfl_sync(0xffffffffu, Dw[0], 4 * b + c);
@@ -468,9 +488,9 @@ __global__ void __launch_bounds__(kThreads, kMmaQ6CtasPerSm(D)) attend_mma_q6_ke
         for (int h = 0; h < 2; ++h) {
           const int d = 32 * b + 4 * g + 2 * h;
           *reinterpret_cast<float2 *>(co + (tw * 4 + r0) * D + d) =
-              make_float2(fmaf(O[b][h][0], 16777216.0f, -w0), fmaf(O[b][h][2], 1048576.0f, -w0));
+              make_float2(fmaf(O[b][h][0], kEven, -w0), fmaf(O[b][h][2], kOdd, -w0));
           *reinterpret_cast<float2 *>(co + (tw * 4 + r1) * D + d) =
-              make_float2(fmaf(O[b][h][1], 16777216.0f, -w1), fmaf(O[b][h][3], 1048576.0f, -w1));
+              make_float2(fmaf(O[b][h][1], kEven, -w1), fmaf(O[b][h][3], kOdd, -w1));
         }
       }
     }
@@ -506,10 +526,10 @@ __global__ void __launch_bounds__(kThreads, kMmaQ6CtasPerSm(D)) attend_mma_q6_ke
   }
 }
 
-template <int D, bool PAGED>
+template <int D, bool PAGED, bool SIGNED>
 cudaError_t launch_t(const AttendArgs &a, cudaStream_t st) {
   static std::atomic<bool> configured[kMaxDevices];
-  cudaError_t e = set_smem_once(configured, attend_mma_q6_kernel<D, PAGED>, Geom<D>::SMEM);
+  cudaError_t e = set_smem_once(configured, attend_mma_q6_kernel<D, PAGED, SIGNED>, Geom<D>::SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.n_chunks, a.cache.B * a.cache.H, (a.gqa * a.n_q + 3) / 4);
@@ -521,7 +541,7 @@ cudaError_t launch_t(const AttendArgs &a, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attend_mma_q6_kernel<D, PAGED>, a);
+  return cudaLaunchKernelEx(&cfg, attend_mma_q6_kernel<D, PAGED, SIGNED>, a);
 }
 
 }  // namespace
@@ -531,9 +551,17 @@ bool mma_q6_supported(const AttendArgs &a) {
          a.chunk % kStage == 0;
 }
 
+namespace {
+template <bool SIGNED>
+cudaError_t launch_pages(const AttendArgs &a, cudaStream_t st) {
+  if (a.cache.page_shift >= 0)
+    return a.cache.D == 256 ? launch_t<256, true, SIGNED>(a, st) : launch_t<128, true, SIGNED>(a, st);
+  return a.cache.D == 256 ? launch_t<256, false, SIGNED>(a, st) : launch_t<128, false, SIGNED>(a, st);
+}
+}  // namespace
+
 cudaError_t launch_attend_mma_q6(const AttendArgs &a, cudaStream_t st) {
-  if (a.cache.page_shift >= 0) return a.cache.D == 256 ? launch_t<256, true>(a, st) : launch_t<128, true>(a, st);
-  return a.cache.D == 256 ? launch_t<256, false>(a, st) : launch_t<128, false>(a, st);
+  return a.lse ? launch_pages<true>(a, st) : launch_pages<false>(a, st);
 }
 
 }  // namespace kvq

@@ -6,6 +6,7 @@
 #include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
+#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include "kvq.h"
@@ -168,6 +169,9 @@ struct AttendArgs {
   // cap_scores [B][Hq][n_q][n_body] and each row's int8 query scale to cap_sq [B][Hq][n_q].
   int32_t *cap_scores;
   float *cap_sq;
+  // natural log of each row's sum of exponentials [B][Hq][n_q] (-infinity: the row sees nothing),
+  // written by phase 2 when not nullptr
+  float *lse;
 };
 // Row index (b, hq, qi) of query row r (of the gqa * n_q rows of kv head kvh).
 __device__ __forceinline__ size_t query_row_index(const AttendArgs &a, int bb, int kvh, int r) {
@@ -184,6 +188,71 @@ __device__ __forceinline__ void capture_score(const AttendArgs &a, int bb, int k
 cudaError_t launch_store(const CacheView &c, const void *k_new, const void *v_new, int dtype,
                          int n_new, int pos0, cudaStream_t st, const int32_t *seq_pos = nullptr,
                          int pos_offset = 0);
+// Rotary table rows of positions [pos0, pos0 + n_pos); the frequencies as 2^-64 fractions of a turn.
+constexpr int kMaxRotHalf = 128;
+struct RopeTurns {
+  unsigned long long turn[kMaxRotHalf];
+};
+cudaError_t launch_rope_table(const RopeTurns &f, int rot, int pos0, int n_pos, float mag, float *table, cudaStream_t st);
+// Rotary append: rows [batch][heads][n_new][D] of k, v (and q, when Hq > 0) by their strides in
+// elements. Slots are pos0 + j, or slots[b] + j (device); rotary positions positions[b][j] (device),
+// or the slots when nullptr; a position outside the table is clamped into it. The launcher fills the
+// row counts and the row bytes.
+struct RowsIn {
+  const void *data;
+  long long batch, head, token;
+};
+struct RopeStore {
+  RowsIn in[3];                // k, v, q
+  int dtype, Hq, n_new, pos0;
+  const int32_t *slots;
+  const float *table;
+  int n_pos, rot, interleaved;
+  const int32_t *positions;
+  void *q_out;
+  long long k_rows, v_rows, q_rows;
+  int row_bytes;
+};
+cudaError_t launch_rope_store(const CacheView &c, RopeStore g, cudaStream_t st);
+// Selection of the tokens a cache keeps (scores [B][H][stride], keep [B][H][n_keep], new_lens [B] or
+// nullptr; seq_lens [B] on the device, each clamped into [0, kv_len], or nullptr).
+struct SelectArgs {
+  int B, H, kv_len, n_keep, n_sink, n_recent;
+  long long stride;
+  const float *scores;
+  const int32_t *seq_lens;
+  int32_t *keep, *new_lens;
+};
+cudaError_t launch_evict_select(const SelectArgs &a, cudaStream_t st);
+// Compaction: the planes (and the scores) whose rows move; rows of row_bytes bytes in units of 16, 8
+// or 4 bytes. Planes are addressed as cache rows, the scores as [B][H][stride].
+struct MovePart {
+  const uint8_t *src;
+  uint8_t *dst;
+  int row_bytes, unit, is_scores;
+};
+struct CompactArgs {
+  CacheView src, dst;
+  const int32_t *keep, *seq_lens;
+  int n_keep, kv_len, n_parts, ranks;   // ranks: CTAs per plane of one (batch, kv head), set by the launcher
+  long long scores_stride, out_stride;
+  MovePart part[7];            // payload, scale and zero-point of K and V, scores
+};
+cudaError_t launch_evict_compact(CompactArgs a, bool in_place, cudaStream_t st);
+// Per-token attention weight after an attention call that wrote a.lse: scores_out[t] = decay *
+// scores_in[t] (nullptr: 0) + the softmax weights of token t summed over the query rows of its kv
+// head; [B][H][stride].
+struct WeightArgs {
+  AttendArgs a;
+  const float *scores_in;
+  float *scores_out;
+  long long stride;
+  float decay;
+  int tiles;                   // 16-token tiles per warp
+  int n_ctas;                  // CTAs over the body's tokens; the window's follow
+};
+cudaError_t launch_attend_weights(const AttendArgs &a, const float *scores_in, float *scores_out, long long stride,
+                                  float decay, cudaStream_t st);
 // Hadamard query preparation into the workspace: int8 codes and scales, and (write_rot) the f32
 // rotated rows.
 cudaError_t launch_had_prep(const AttendArgs &a, cudaStream_t st, bool write_rot = true);

@@ -1,0 +1,242 @@
+// Rotary positions: the table of cosines and sines, and the append that rotates.
+//
+// Table. Row p holds cos(p f_i) m, i = 0 .. h-1, then sin(p f_i) m, h = rot_dim / 2. A far position's
+// angle has lost its fraction of a turn in float32 (p f = 1e5 leaves 2^-7 of a radian), so the angle is
+// counted in turns: f_i / 2 pi as a 64-bit binary fraction, and p times it in wrapping 64-bit integers,
+// which takes whole turns off exactly. The nearest quarter turn goes into signs and a swap; what is
+// left, in [-1/8, 1/8) of a turn, is rounded to float32 once and given to sinpif / cospif.
+//
+// Append with rotary positions. One launch reads q, k and v from wherever their projection left them
+// (any strides between batches, heads and tokens), rotates q and k, and writes q in its own type and k
+// and v packed: nothing is rotated into memory and read again. Half layout: dims (i, i + h) are a pair;
+// interleaved: dims (2 i, 2 i + 1); dims from rot_dim on stay as they are.
+//   y_a = x_a c - x_b s,   y_b = x_b c + x_a s
+// Each product and each sum is rounded to float32 by itself (this file is compiled with -fmad=false),
+// so the packed bytes follow from the table's entries exactly. Block layouts: one thread holds eight
+// dims of a row; its partners' eight (half layout) are a second 16-byte load of the same row, which the
+// L1 answers. Hadamard layouts: one warp per row, as in the plain append.
+//
+// Bound by memory: 8192 tokens, 16 q and 8 kv heads of 256 dims (f16) move 148 MB.
+#include "store_quant.cuh"
+
+namespace kvq {
+namespace {
+
+constexpr int kTableThreads = 256;
+
+__global__ void __launch_bounds__(kTableThreads) rope_table_kernel(RopeTurns f, int half, int pos0, int n_pos, float mag,
+                                                                   float *__restrict__ table) {
+  // four neighbouring frequencies of one position per thread: 16-byte stores
+  const int quads = half >> 2;
+  const long long id = (long long)blockIdx.x * kTableThreads + threadIdx.x;
+  const long long p = id / quads;
+  if (p >= n_pos) return;
+  const int i0 = 4 * (int)(id - p * quads);
+  const unsigned long long pos = (unsigned long long)pos0 + (unsigned long long)p;
+  float c[4], s[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const unsigned long long t = pos * f.turn[i0 + k];            // the angle in 2^-64 turns, whole turns gone
+    const unsigned quarter = (unsigned)((t + (1ull << 61)) >> 62);   // nearest quarter turn (0 .. 3)
+    const long long rest = (long long)(t - ((unsigned long long)quarter << 62));   // [-2^61, 2^61)
+    const float half_turns = __ll2float_rn(rest) * 0x1.0p-63f;     // in units of pi
+    const float sr = sinpif(half_turns), cr = cospif(half_turns);
+    const float sv = (quarter & 1) ? cr : sr, cv = (quarter & 1) ? sr : cr;
+    s[k] = __fmul_rn((quarter & 2) ? -sv : sv, mag);
+    c[k] = __fmul_rn(((quarter + 1) & 2) ? -cv : cv, mag);         // cos is negative in quarters 1 and 2
+  }
+  float *row = table + (size_t)p * (2 * half) + i0;
+  *reinterpret_cast<float4 *>(row) = make_float4(c[0], c[1], c[2], c[3]);
+  *reinterpret_cast<float4 *>(row + half) = make_float4(s[0], s[1], s[2], s[3]);
+}
+
+// Which row a thread or warp works on: K rows first, then V, then q.
+struct RopeRow {
+  int what;                 // 0 = K, 1 = V, 2 = q
+  int b, head, j, pos;      // batch, head (kv or query), row of the append, cache slot
+  long long crow;           // plane row (K and V)
+  bool live;                // q, or a slot inside the cache
+};
+__device__ __forceinline__ RopeRow rope_row(const CacheView &c, const RopeStore &g, long long r) {
+  RopeRow w;
+  w.what = r < g.k_rows ? 0 : (r < g.k_rows + g.v_rows ? 1 : 2);
+  r -= w.what == 0 ? 0 : (w.what == 1 ? g.k_rows : g.k_rows + g.v_rows);
+  const int heads = w.what == 2 ? g.Hq : c.H;
+  if (r <= 0x7FFFFFFFLL) {                                // 32-bit divisions
+    const unsigned bh = (unsigned)r / (unsigned)g.n_new;
+    w.j = (int)((unsigned)r - bh * (unsigned)g.n_new);
+    w.b = (int)(bh / (unsigned)heads);
+    w.head = (int)(bh - (unsigned)w.b * (unsigned)heads);
+  } else {
+    const long long bh = r / g.n_new;
+    w.j = (int)(r - bh * g.n_new);
+    w.b = (int)(bh / heads);
+    w.head = (int)(bh - (long long)w.b * heads);
+  }
+  // a slot is 64-bit until it is known to lie inside the cache
+  const long long slot = (g.slots ? (long long)__ldg(g.slots + w.b) : (long long)g.pos0) + w.j;
+  const bool inside = slot >= 0 && slot < c.cap;
+  w.pos = (int)min(max(slot, (long long)INT_MIN), (long long)INT_MAX);   // also the default rotary position
+  w.live = w.what == 2 || inside;
+  w.crow = w.what != 2 && inside ? (long long)cache_row(c, w.b, w.head, w.pos) : 0;
+  return w;
+}
+
+// N (4 or 8) consecutive dims from d0 of one row, rotated when the row is K or q and d0 < rot_dim.
+template <int N>
+__device__ __forceinline__ void load_n(const void *base, int dtype, size_t e, float (&v)[N]) {
+  if constexpr (N == 8) load8_f32(base, dtype, e, v);
+  else load4_f32(base, dtype, e, v);
+}
+template <int N>
+__device__ __forceinline__ void rope_load(const RopeStore &g, const RopeRow &w, int d0, float (&y)[N]) {
+  const RowsIn &in = g.in[w.what];
+  const size_t e = (size_t)w.b * in.batch + (size_t)w.head * in.head + (size_t)w.j * in.token + d0;
+  float x[N];
+  load_n<N>(in.data, g.dtype, e, x);
+  if (w.what == 1 || d0 >= g.rot) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) y[i] = x[i];
+    return;
+  }
+  const int at = g.positions ? __ldg(g.positions + (size_t)w.b * g.n_new + w.j) : w.pos;
+  const float *row = g.table + (size_t)min(max(at, 0), g.n_pos - 1) * g.rot;
+  const int half = g.rot >> 1;
+  if (g.interleaved) {
+    float c[N / 2], s[N / 2];
+    if constexpr (N == 8) {
+      *reinterpret_cast<float4 *>(c) = __ldg(reinterpret_cast<const float4 *>(row + (d0 >> 1)));
+      *reinterpret_cast<float4 *>(s) = __ldg(reinterpret_cast<const float4 *>(row + half + (d0 >> 1)));
+    } else {
+      *reinterpret_cast<float2 *>(c) = __ldg(reinterpret_cast<const float2 *>(row + (d0 >> 1)));
+      *reinterpret_cast<float2 *>(s) = __ldg(reinterpret_cast<const float2 *>(row + half + (d0 >> 1)));
+    }
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      y[2 * i] = __fsub_rn(__fmul_rn(x[2 * i], c[i]), __fmul_rn(x[2 * i + 1], s[i]));
+      y[2 * i + 1] = __fadd_rn(__fmul_rn(x[2 * i + 1], c[i]), __fmul_rn(x[2 * i], s[i]));
+    }
+    return;
+  }
+  const bool second = d0 >= half;                        // half is a multiple of 8: all N dims are on one side
+  const int i0 = second ? d0 - half : d0;
+  float p[N], c[N], s[N];
+  load_n<N>(in.data, g.dtype, second ? e - half : e + half, p);
+  load_n<N>(row, KVQ_F32, i0, c);
+  load_n<N>(row, KVQ_F32, half + i0, s);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float a = __fmul_rn(x[i], c[i]), b = __fmul_rn(p[i], s[i]);
+    y[i] = second ? __fadd_rn(a, b) : __fsub_rn(a, b);
+  }
+}
+
+__device__ __forceinline__ uint32_t pack2(int dtype, float lo, float hi) {
+  if (dtype == KVQ_BF16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+  }
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+// q rows are written [batch][n_q_heads][n_new][head_dim], rounded once to their type
+template <int N>
+__device__ __forceinline__ void write_q(const RopeStore &g, const RopeRow &w, int D, int d0, const float (&y)[N]) {
+  const size_t e = (((size_t)w.b * g.Hq + w.head) * g.n_new + w.j) * D + d0;
+  if (g.dtype == KVQ_F32) {
+    float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(g.q_out) + e);
+    o[0] = make_float4(y[0], y[1], y[2], y[3]);
+    if constexpr (N == 8) o[1] = make_float4(y[4], y[5], y[6], y[7]);
+    return;
+  }
+  uint16_t *o = static_cast<uint16_t *>(g.q_out) + e;
+  if constexpr (N == 8)
+    *reinterpret_cast<uint4 *>(o) = make_uint4(pack2(g.dtype, y[0], y[1]), pack2(g.dtype, y[2], y[3]),
+                                               pack2(g.dtype, y[4], y[5]), pack2(g.dtype, y[6], y[7]));
+  else
+    *reinterpret_cast<uint2 *>(o) = make_uint2(pack2(g.dtype, y[0], y[1]), pack2(g.dtype, y[2], y[3]));
+}
+
+// Neither kernel lets a dependent launch start early: the attention call that follows reads q_out, and
+// its query preparation does not wait for its predecessor.
+template <int LAYOUT>
+__global__ void __launch_bounds__(256) rope_store_block_kernel(CacheView c, RopeStore g) {
+  const int shift = c.D == 128 ? 4 : 5;                   // D / 8 threads per row
+  const long long gt = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  const long long r = gt >> shift;
+  const int tr = (int)(gt & ((1 << shift) - 1));
+  // threads past the last row take part in the quad shuffles (full-warp masks) but load and store nothing
+  RopeRow w = {};
+  bool valid = r < g.k_rows + g.v_rows + g.q_rows;
+  if (valid) {
+    w = rope_row(c, g, r);
+    valid = w.live;
+  }
+  float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (valid) rope_load<8>(g, w, 8 * tr, y);
+  if (valid && w.what == 2) write_q<8>(g, w, c.D, 8 * tr, y);
+  quant_block<LAYOUT>(c, w.what == 1, w.crow, g.row_bytes, c.D / kBlock, tr >> 2, tr & 3, y, valid && w.what != 2);
+}
+
+template <int V, int BITS>
+__global__ void __launch_bounds__(256) rope_store_had_kernel(CacheView c, RopeStore g) {
+  const int lane = threadIdx.x & 31;
+  const long long r = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  if (r >= g.k_rows + g.v_rows + g.q_rows) return;         // whole warp (one row)
+  const RopeRow w = rope_row(c, g, r);
+  if (!w.live) return;
+  float y[V];
+  rope_load<V>(g, w, V * lane, y);
+  if (w.what == 2) {
+    write_q<V>(g, w, 32 * V, V * lane, y);
+    return;
+  }
+  quant_had<V, BITS>(c, w.what, w.crow, g.row_bytes, lane, y, c.n_recent > 0 && w.j >= g.n_new - c.n_recent,
+                     (long long)w.b * c.H + w.head, w.pos);
+}
+
+cudaError_t launch_plane(const CacheView &c, int layout, const RopeStore &g, cudaStream_t st) {
+  const long long rows = g.k_rows + g.v_rows + g.q_rows;
+  const unsigned blocks = (unsigned)((rows * (is_hadamard(layout) ? 32 : c.D / 8) + 255) / 256);
+  switch (layout) {
+    case KVQ_Q4_0: rope_store_block_kernel<KVQ_Q4_0><<<blocks, 256, 0, st>>>(c, g); break;
+    case KVQ_Q6_0: rope_store_block_kernel<KVQ_Q6_0><<<blocks, 256, 0, st>>>(c, g); break;
+    case KVQ_Q8_0: rope_store_block_kernel<KVQ_Q8_0><<<blocks, 256, 0, st>>>(c, g); break;
+    case KVQ_ASYM4_G32: rope_store_block_kernel<KVQ_ASYM4_G32><<<blocks, 256, 0, st>>>(c, g); break;
+    case KVQ_HAD_INT4:
+      if (c.D == 128) rope_store_had_kernel<4, 4><<<blocks, 256, 0, st>>>(c, g);
+      else rope_store_had_kernel<8, 4><<<blocks, 256, 0, st>>>(c, g);
+      break;
+    default:
+      if (c.D == 128) rope_store_had_kernel<4, 2><<<blocks, 256, 0, st>>>(c, g);
+      else rope_store_had_kernel<8, 2><<<blocks, 256, 0, st>>>(c, g);
+      break;
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_rope_table(const RopeTurns &f, int rot, int pos0, int n_pos, float mag, float *table, cudaStream_t st) {
+  const long long threads = (long long)n_pos * (rot / 8);
+  rope_table_kernel<<<(unsigned)((threads + kTableThreads - 1) / kTableThreads), kTableThreads, 0, st>>>(
+      f, rot / 2, pos0, n_pos, mag, table);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_rope_store(const CacheView &c, RopeStore g, cudaStream_t st) {
+  const long long rows = (long long)c.B * c.H * g.n_new;
+  g.k_rows = rows;
+  g.v_rows = c.layout == c.v_layout ? rows : 0;
+  g.q_rows = (long long)c.B * g.Hq * g.n_new;
+  g.row_bytes = c.row_bytes;
+  cudaError_t e = launch_plane(c, c.layout, g, st);
+  if (e != cudaSuccess || g.v_rows) return e;
+  // mixed K/V precision: the V plane's rows in a launch of their own layout
+  g.k_rows = g.q_rows = 0;
+  g.v_rows = rows;
+  g.row_bytes = c.v_row_bytes;
+  return launch_plane(c, c.v_layout, g, st);
+}
+
+}  // namespace kvq

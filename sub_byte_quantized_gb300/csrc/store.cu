@@ -9,12 +9,10 @@
 // vectors, stores are the thread's 4 payload bytes (+ 2 high-plane bytes for Q6_0; 8 bytes for
 // Q8_0).
 // Hadamard int4 / int2: one warp per token row; the FWHT runs in registers and shuffles.
-#include "kvq_internal.cuh"
+#include "store_quant.cuh"
 
 namespace kvq {
 namespace {
-
-constexpr float kF16Max = 65504.0f;
 
 struct StoreGeom {
   int B, H, D, cap, n_new, pos0, row_bytes, nb;
@@ -54,26 +52,6 @@ __device__ __forceinline__ bool row_coords(const CacheView &c, const StoreGeom &
   return ok;
 }
 
-__device__ __forceinline__ float quad_max(float v) {
-  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-}
-__device__ __forceinline__ float quad_min(float v) {
-  v = fminf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-  return fminf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-}
-
-__device__ __forceinline__ __half f16_sat(float x) {
-  return __float2half_rn(fminf(fmaxf(x, -kF16Max), kF16Max));
-}
-
-// q = clamp(rint(x / s), lo, hi), or 0 when s == 0.
-__device__ __forceinline__ int sym_code(float x, float s, int lo, int hi) {
-  if (!(s > 0.0f)) return 0;
-  const float r = rintf(__fdiv_rn(x, s));
-  return (int)fminf(fmaxf(r, (float)lo), (float)hi);
-}
-
 // LAYOUT: KVQ_Q4_0, KVQ_Q6_0, KVQ_Q8_0 or KVQ_ASYM4_G32.
 template <int LAYOUT>
 __global__ void __launch_bounds__(256) store_block_kernel(CacheView c, const void *__restrict__ k_new,
@@ -96,78 +74,7 @@ __global__ void __launch_bounds__(256) store_block_kernel(CacheView c, const voi
 
   float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   if (valid) load8_f32(kv ? v_new : k_new, dtype, (size_t)in_row * g.D + (size_t)tr * 8, v);
-  uint8_t *prow = (kv ? c.payload[1] : c.payload[0]) + (size_t)crow * g.row_bytes;
-  __half *srow = static_cast<__half *>((kv ? c.scale[1] : c.scale[0])) + (size_t)crow * g.nb;
-
-  if (LAYOUT == KVQ_ASYM4_G32) {
-    float mn = v[0], mx = v[0];
-#pragma unroll
-    for (int i = 1; i < 8; ++i) { mn = fminf(mn, v[i]); mx = fmaxf(mx, v[i]); }
-    mn = quad_min(mn);
-    mx = quad_max(mx);
-    const __half sh = f16_sat(__fdiv_rn(__fsub_rn(mx, mn), 15.0f));
-    const __half zh = f16_sat(mn);
-    const float s = __half2float(sh), z = __half2float(zh);
-    uint32_t w = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      int q = 0;
-      if (s > 0.0f) {
-        const float rr = rintf(__fdiv_rn(__fsub_rn(v[i], z), s));
-        q = (int)fminf(fmaxf(rr, 0.0f), 15.0f);
-      }
-      w |= (uint32_t)q << (4 * i);
-    }
-    if (!valid) return;
-    *reinterpret_cast<uint32_t *>(prow + blk * 16 + lb * 4) = w;
-    if (lb == 0) {
-      srow[blk] = sh;
-      (kv ? c.zero[1] : c.zero[0])[(size_t)crow * g.nb + blk] = zh;
-    }
-    return;
-  }
-
-  float amax = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
-  amax = quad_max(amax);
-  if (LAYOUT == KVQ_Q4_0) {
-    const __half sh = f16_sat(__fdiv_rn(amax, 8.0f));
-    const float s = __half2float(sh);
-    uint32_t w = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w |= ((uint32_t)sym_code(v[i], s, -8, 7) & 0xFu) << (4 * i);
-    if (!valid) return;
-    *reinterpret_cast<uint32_t *>(prow + blk * 16 + lb * 4) = w;
-    if (lb == 0) srow[blk] = sh;
-  } else if (LAYOUT == KVQ_Q8_0) {
-    const __half sh = f16_sat(__fdiv_rn(amax, 128.0f));
-    const float s = __half2float(sh);
-    uint32_t w0 = 0, w1 = 0;                   // byte i = value i (two's complement)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      w0 |= ((uint32_t)sym_code(v[i], s, -128, 127) & 0xFFu) << (8 * i);
-      w1 |= ((uint32_t)sym_code(v[4 + i], s, -128, 127) & 0xFFu) << (8 * i);
-    }
-    if (!valid) return;
-    *reinterpret_cast<uint2 *>(prow + blk * 32 + lb * 8) = make_uint2(w0, w1);
-    if (lb == 0) srow[blk] = sh;
-  } else {  // Q6_0
-    const __half sh = f16_sat(__fdiv_rn(amax, 32.0f));
-    const float s = __half2float(sh);
-    uint32_t lo = 0, hi = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t u = (uint32_t)sym_code(v[i], s, -32, 31) & 0x3Fu;
-      lo |= (u & 0xFu) << (4 * i);
-      hi |= ((u >> 4) & 0x3u) << (2 * i);      // values 4k..4k+3 -> byte k, bits 0,2,4,6
-    }
-    if (!valid) return;
-    uint8_t *bp = prow + blk * 24;
-    *reinterpret_cast<uint32_t *>(bp + lb * 4) = lo;
-    *reinterpret_cast<uint16_t *>(bp + 16 + lb * 2) = (uint16_t)hi;
-    if (lb == 0) srow[blk] = sh;
-  }
+  quant_block<LAYOUT>(c, kv, crow, g.row_bytes, g.nb, blk, lb, v, valid);
 }
 
 // Hadamard int4 (BITS 4: scale amax / 7, codes [-7, 7], two per byte) or int2 (BITS 2: scale
@@ -192,39 +99,9 @@ __global__ void __launch_bounds__(256) store_had_kernel(CacheView c, const void 
   } else {
     load8_f32(src, dtype, (size_t)in_row * g.D + lane * 8, x);
   }
-  warp_fwht<V>(x, lane);
-  const float cD = inv_sqrt_dim(g.D);
-  float amax = 0.0f;
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    x[i] = __fmul_rn(x[i], cD);
-    amax = fmaxf(amax, fabsf(x[i]));
-  }
-#pragma unroll
-  for (int m = 16; m; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
-  constexpr int QMAX = BITS == 4 ? 7 : 1;
-  const float s = __fdiv_rn(amax, (float)QMAX);
-  uint32_t w = 0;                                           // field i of the lane at bits BITS*i
-#pragma unroll
-  for (int i = 0; i < V; ++i)
-    w |= ((uint32_t)sym_code(x[i], s, -QMAX, QMAX) & ((1u << BITS) - 1u)) << (BITS * i);
-  uint8_t *prow = (kv ? c.payload[1] : c.payload[0]) + (size_t)crow * g.row_bytes;
-  if (V * BITS == 8) {
-    prow[lane] = (uint8_t)w;
-  } else if (V * BITS == 16) {
-    *reinterpret_cast<uint16_t *>(prow + lane * 2) = (uint16_t)w;
-  } else {
-    *reinterpret_cast<uint32_t *>(prow + lane * 4) = w;
-  }
-  if (lane == 0) static_cast<float *>((kv ? c.scale[1] : c.scale[0]))[crow] = s;
   // Exact-f32 ring of the newest tokens: only the last min(n_new, n_recent) rows of this call,
   // so no two rows of one call write the same slot.
-  if (c.n_recent > 0 && j >= g.n_new - c.n_recent) {
-    float *dst = (kv ? c.ring[1] : c.ring[0]) + ((size_t)bh * c.n_recent + (size_t)(pos % c.n_recent)) * g.D + lane * V;
-#pragma unroll
-    for (int i = 0; i < V; i += 4)
-      *reinterpret_cast<float4 *>(dst + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-  }
+  quant_had<V, BITS>(c, kv, crow, g.row_bytes, lane, x, c.n_recent > 0 && j >= g.n_new - c.n_recent, bh, pos);
 }
 
 }  // namespace
