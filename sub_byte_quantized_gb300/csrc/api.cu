@@ -265,6 +265,8 @@ kvq_status resolve_core(int n_q_heads, int n_q, int kv_len, int causal, int q_po
   a.cap_scores = nullptr;
   a.cap_sq = nullptr;
   a.lse = nullptr;
+  a.part_s = nullptr;
+  a.s_rows = a.s_tokens = 0;
   const size_t rows = (size_t)c.B * n_q_heads * n_q;
   size_t off = 0;
   const size_t o_m = off; off = round_up(off + rows * a.C * sizeof(float), 256);
@@ -989,8 +991,22 @@ int paged_chunk(const kvq_paged_cache *cache, int n_q_heads, int n_q, int max_kv
   return weights_chunk(a.cache, n_q_heads, n_q, max_kv_len, a.chunk);
 }
 
-// The rows' log-sum-exp follow the attention's workspace.
-size_t weights_need(size_t attend_need, size_t rows) { return round_up(attend_need, 256) + round_up(rows * sizeof(float), 256); }
+// A weights call's workspace behind the attention's: the rows' log-sum-exp, then the scores that phase 1
+// leaves behind on the kernels that can (score_rows).
+struct WeightsSpace {
+  size_t lse, scores, total;
+  int rows, tokens;
+};
+WeightsSpace weights_space(const kvq::AttendArgs &a, size_t attend_need) {
+  const kvq::CacheView &c = a.cache;
+  WeightsSpace w;
+  w.rows = kvq::score_rows(c.layout, c.v_layout, c.D, a.gqa * a.n_q);
+  w.tokens = (a.n_body + 63) / 64 * 64;
+  w.lse = round_up(attend_need, 256);
+  w.scores = w.lse + round_up((size_t)c.B * a.Hq * a.n_q * sizeof(float), 256);
+  w.total = w.scores + (size_t)c.B * c.H * w.tokens * w.rows * sizeof(float);
+  return w;
+}
 
 kvq_status check_scores(const float *scores_in, const float *scores_out, int64_t stride, int kv_len, float decay) {
   if (!scores_out) return fail(KVQ_EINVAL, "scores_out is NULL");
@@ -1002,9 +1018,15 @@ kvq_status check_scores(const float *scores_in, const float *scores_out, int64_t
 
 kvq_status run_weights(kvq::AttendArgs &a, size_t attend_need, void *workspace, size_t workspace_bytes, const float *scores_in,
                        float *scores_out, int64_t stride, float decay, cudaStream_t s) {
-  const size_t need = weights_need(attend_need, (size_t)a.cache.B * a.Hq * a.n_q);
-  if (workspace_bytes < need) return fail(KVQ_EWORKSPACE, "workspace %zu < required %zu", workspace_bytes, need);
-  a.lse = reinterpret_cast<float *>(static_cast<char *>(workspace) + round_up(attend_need, 256));
+  const WeightsSpace w = weights_space(a, attend_need);
+  if (workspace_bytes < w.total) return fail(KVQ_EWORKSPACE, "workspace %zu < required %zu", workspace_bytes, w.total);
+  char *ws = static_cast<char *>(workspace);
+  a.lse = reinterpret_cast<float *>(ws + w.lse);
+  if (w.rows > 0 && w.tokens > 0) {
+    a.part_s = reinterpret_cast<float *>(ws + w.scores);
+    a.s_rows = w.rows;
+    a.s_tokens = w.tokens;
+  }
   cudaError_t e = launch_attend_sequence(a, s, true);
   if (e == cudaSuccess) e = kvq::launch_attend_weights(a, scores_in, scores_out, stride, decay, s);
   if (e != cudaSuccess) return fail(KVQ_ECUDA, "attend weights launch: %s", cudaGetErrorString(e));
@@ -1062,16 +1084,20 @@ kvq_status run_compact(const kvq::CacheView &src, const kvq::CacheView &dst, boo
 
 size_t kvq_attend_weights_workspace_bytes(const kvq_cache *cache, int32_t n_q_heads, int32_t n_q, int32_t kv_len,
                                           int32_t chunk) {
+  kvq::AttendArgs a;
+  size_t need = 0;
   chunk = contiguous_chunk(cache, n_q_heads, n_q, kv_len, chunk);
-  const size_t need = kvq_attend_workspace_bytes(cache, n_q_heads, n_q, kv_len, chunk);
-  return need ? weights_need(need, (size_t)cache->batch * n_q_heads * n_q) : 0;
+  if (resolve_attend(cache, n_q_heads, n_q, kv_len, 0, 0, chunk, a, need, nullptr) != KVQ_OK) return 0;
+  return weights_space(a, need).total;
 }
 
 size_t kvq_paged_attend_weights_workspace_bytes(const kvq_paged_cache *cache, int32_t n_q_heads, int32_t n_q,
                                                 int32_t max_kv_len, int32_t chunk) {
+  kvq::AttendArgs a;
+  size_t need = 0;
   chunk = paged_chunk(cache, n_q_heads, n_q, max_kv_len, chunk);
-  const size_t need = kvq_paged_attend_workspace_bytes(cache, n_q_heads, n_q, max_kv_len, chunk);
-  return need ? weights_need(need, (size_t)cache->batch * n_q_heads * n_q) : 0;
+  if (resolve_paged(cache, n_q_heads, n_q, max_kv_len, 0, chunk, a, need, nullptr) != KVQ_OK) return 0;
+  return weights_space(a, need).total;
 }
 
 kvq_status kvq_decode_attend_weights(const kvq_cache *cache, const void *q, int32_t q_dtype, int32_t n_q_heads,
@@ -1086,7 +1112,7 @@ kvq_status kvq_decode_attend_weights(const kvq_cache *cache, const void *q, int3
                                  workspace, workspace_bytes, a);
   if (st == KVQ_OK) st = check_scores(scores_in, scores_out, scores_stride, kv_len, decay);
   if (st != KVQ_OK) return st;
-  const size_t need = kvq_attend_workspace_bytes(cache, n_q_heads, n_q, kv_len, chunk);
+  const size_t need = kvq_attend_workspace_bytes(cache, n_q_heads, n_q, kv_len, chunk);   // of the same chunk
   return run_weights(a, need, workspace, workspace_bytes, scores_in, scores_out, scores_stride, decay,
                      reinterpret_cast<cudaStream_t>(stream));
 }

@@ -122,7 +122,8 @@ __device__ __forceinline__ void unpack4_s8_t(uint32_t w, uint32_t &d0, uint32_t 
 
 // CAP: score capture (Hadamard layout, contiguous cache): the exact integer score of every
 // (row, body token) this CTA computes and each row's int8 query scale go to a.cap_scores / a.cap_sq.
-template <int LAYOUT, int VLAYOUT, bool QSPLIT, bool PAGED, bool CAP = false>
+// SCORES: the masked scores go to a.part_s, for the kernel that sums the tokens' weights.
+template <int LAYOUT, int VLAYOUT, bool QSPLIT, bool PAGED, bool CAP = false, bool SCORES = false>
 __global__ void __launch_bounds__(kWarps * 32, kMinBlocks) attend_mma_kernel(AttendArgs a) {
   constexpr bool HAD = is_hadamard(LAYOUT), HAD2 = LAYOUT == KVQ_HAD_INT2;
   static_assert(LAYOUT != KVQ_ASYM4_G32 && VLAYOUT != KVQ_ASYM4_G32, "the asymmetric layout has its own kernel");
@@ -572,6 +573,10 @@ __global__ void __launch_bounds__(kWarps * 32, kMinBlocks) attend_mma_kernel(Att
         if (!(tb < t1 && tb <= lim1)) s[tile][3] = -INFINITY;
       }
     }
+    if constexpr (SCORES) {
+#pragma unroll
+      for (int tile = 0; tile < kTiles; ++tile) keep_scores(a, bh, ts + tile * 16 + g, r0, s[tile], t1);
+    }
     // ---------------- online softmax (base 2), rows r0 / r1
     float mx0 = fmaxf(s[0][0], s[0][2]), mx1 = fmaxf(s[0][1], s[0][3]);
 #pragma unroll
@@ -807,10 +812,10 @@ __global__ void __launch_bounds__(kWarps * 32, kMinBlocks) attend_mma_kernel(Att
   }
 }
 
-template <int LAYOUT, int VLAYOUT, bool QSPLIT, bool PAGED, bool CAP = false>
+template <int LAYOUT, int VLAYOUT, bool QSPLIT, bool PAGED, bool CAP = false, bool SCORES = false>
 cudaError_t launch_t(const AttendArgs &a, cudaStream_t st) {
   static std::atomic<bool> configured[kMaxDevices];
-  cudaError_t e = set_smem_once(configured, attend_mma_kernel<LAYOUT, VLAYOUT, QSPLIT, PAGED, CAP>, smem_bytes<LAYOUT, VLAYOUT>());
+  cudaError_t e = set_smem_once(configured, attend_mma_kernel<LAYOUT, VLAYOUT, QSPLIT, PAGED, CAP, SCORES>, smem_bytes<LAYOUT, VLAYOUT>());
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.n_chunks, a.cache.B * a.cache.H);
@@ -822,15 +827,18 @@ cudaError_t launch_t(const AttendArgs &a, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attend_mma_kernel<LAYOUT, VLAYOUT, QSPLIT, PAGED, CAP>, a);
+  return cudaLaunchKernelEx(&cfg, attend_mma_kernel<LAYOUT, VLAYOUT, QSPLIT, PAGED, CAP, SCORES>, a);
 }
 
+template <int LAYOUT, int VLAYOUT, bool QSPLIT>
+cudaError_t launch_kind_t(const AttendArgs &a, cudaStream_t st) {
+  const bool paged = a.cache.page_shift >= 0;
+  if (a.part_s) return paged ? launch_t<LAYOUT, VLAYOUT, QSPLIT, true, false, true>(a, st) : launch_t<LAYOUT, VLAYOUT, QSPLIT, false, false, true>(a, st);
+  return paged ? launch_t<LAYOUT, VLAYOUT, QSPLIT, true>(a, st) : launch_t<LAYOUT, VLAYOUT, QSPLIT, false>(a, st);
+}
 template <int LAYOUT, int VLAYOUT>
 cudaError_t launch_pair_t(const AttendArgs &a, cudaStream_t st) {
-  const bool paged = a.cache.page_shift >= 0;
-  if (a.q_dtype == KVQ_F32)
-    return paged ? launch_t<LAYOUT, VLAYOUT, true, true>(a, st) : launch_t<LAYOUT, VLAYOUT, true, false>(a, st);
-  return paged ? launch_t<LAYOUT, VLAYOUT, false, true>(a, st) : launch_t<LAYOUT, VLAYOUT, false, false>(a, st);
+  return a.q_dtype == KVQ_F32 ? launch_kind_t<LAYOUT, VLAYOUT, true>(a, st) : launch_kind_t<LAYOUT, VLAYOUT, false>(a, st);
 }
 
 }  // namespace
@@ -856,13 +864,11 @@ cudaError_t launch_attend_mma(const AttendArgs &a, cudaStream_t st) {
   if (L == KVQ_Q6_0) return launch_attend_mma_q6(a, st);
   if (L == KVQ_HAD_INT4) {                               // int8 query codes are exact
     if (a.cap_scores) return paged ? cudaErrorNotSupported : launch_t<KVQ_HAD_INT4, KVQ_HAD_INT4, false, false, true>(a, st);
-    return paged ? launch_t<KVQ_HAD_INT4, KVQ_HAD_INT4, false, true>(a, st)
-                 : launch_t<KVQ_HAD_INT4, KVQ_HAD_INT4, false, false>(a, st);
+    return launch_kind_t<KVQ_HAD_INT4, KVQ_HAD_INT4, false>(a, st);
   }
   if (L == KVQ_HAD_INT2) {
     if (a.cap_scores) return paged ? cudaErrorNotSupported : launch_t<KVQ_HAD_INT2, KVQ_HAD_INT2, false, false, true>(a, st);
-    return paged ? launch_t<KVQ_HAD_INT2, KVQ_HAD_INT2, false, true>(a, st)
-                 : launch_t<KVQ_HAD_INT2, KVQ_HAD_INT2, false, false>(a, st);
+    return launch_kind_t<KVQ_HAD_INT2, KVQ_HAD_INT2, false>(a, st);
   }
   if (L == KVQ_Q4_0 && VL == KVQ_Q4_0) return launch_pair_t<KVQ_Q4_0, KVQ_Q4_0>(a, st);
   if (L == KVQ_Q8_0 && VL == KVQ_Q8_0) return launch_pair_t<KVQ_Q8_0, KVQ_Q8_0>(a, st);

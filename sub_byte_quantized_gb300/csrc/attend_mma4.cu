@@ -70,7 +70,8 @@ __device__ __forceinline__ uint32_t swz(int row, int j) {
   return (uint32_t)(row * kRowBytes + ((j ^ ((row >> 1) & 3)) << 4));
 }
 
-template <int LAYOUT, bool QSPLIT, bool PAGED>
+// SCORES: the masked scores go to a.part_s, for the kernel that sums the tokens' weights.
+template <int LAYOUT, bool QSPLIT, bool PAGED, bool SCORES>
 __global__ void __launch_bounds__(kThreads, kMma4CtasPerSm) attend_mma4_kernel(AttendArgs a) {
   using G = Geo4<LAYOUT>;
   constexpr bool ASYM = G::ASYM, HAD = G::HAD;
@@ -381,6 +382,7 @@ __global__ void __launch_bounds__(kThreads, kMma4CtasPerSm) attend_mma4_kernel(A
         if (!(tb < t1 && tb <= lim0)) s[2] = -INFINITY;
         if (!(tb < t1 && tb <= lim1)) s[3] = -INFINITY;
       }
+      if constexpr (SCORES) keep_scores(a, bh, ts + g, r0, s, t1);
       // online softmax (base 2), rows r0 / r1
       float mx0 = fmaxf(s[0], s[2]), mx1 = fmaxf(s[1], s[3]);
 #pragma unroll
@@ -610,10 +612,10 @@ __global__ void __launch_bounds__(kThreads, kMma4CtasPerSm) attend_mma4_kernel(A
   }
 }
 
-template <int LAYOUT, bool QSPLIT, bool PAGED>
+template <int LAYOUT, bool QSPLIT, bool PAGED, bool SCORES>
 cudaError_t launch_t(const AttendArgs &a, cudaStream_t st) {
   static std::atomic<bool> configured[kMaxDevices];
-  cudaError_t e = set_smem_once(configured, attend_mma4_kernel<LAYOUT, QSPLIT, PAGED>, Geo4<LAYOUT>::SMEM);
+  cudaError_t e = set_smem_once(configured, attend_mma4_kernel<LAYOUT, QSPLIT, PAGED, SCORES>, Geo4<LAYOUT>::SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.n_chunks, a.cache.B * a.cache.H);
@@ -625,17 +627,22 @@ cudaError_t launch_t(const AttendArgs &a, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attend_mma4_kernel<LAYOUT, QSPLIT, PAGED>, a);
+  return cudaLaunchKernelEx(&cfg, attend_mma4_kernel<LAYOUT, QSPLIT, PAGED, SCORES>, a);
+}
+
+template <bool SCORES>
+cudaError_t launch_kind(const AttendArgs &a, cudaStream_t st) {
+  const bool split = a.q_dtype == KVQ_F32;
+  const bool paged = a.cache.page_shift >= 0;
+  if (split) return paged ? launch_t<KVQ_ASYM4_G32, true, true, SCORES>(a, st) : launch_t<KVQ_ASYM4_G32, true, false, SCORES>(a, st);
+  return paged ? launch_t<KVQ_ASYM4_G32, false, true, SCORES>(a, st) : launch_t<KVQ_ASYM4_G32, false, false, SCORES>(a, st);
 }
 
 }  // namespace
 
 cudaError_t launch_attend_mma4(const AttendArgs &a, cudaStream_t st) {
-  const bool split = a.q_dtype == KVQ_F32;
-  const bool paged = a.cache.page_shift >= 0;
   if (a.cache.layout != KVQ_ASYM4_G32) return cudaErrorNotSupported;   // built for the layout that uses it
-  if (split) return paged ? launch_t<KVQ_ASYM4_G32, true, true>(a, st) : launch_t<KVQ_ASYM4_G32, true, false>(a, st);
-  return paged ? launch_t<KVQ_ASYM4_G32, false, true>(a, st) : launch_t<KVQ_ASYM4_G32, false, false>(a, st);
+  return a.part_s ? launch_kind<true>(a, st) : launch_kind<false>(a, st);
 }
 
 }  // namespace kvq

@@ -322,6 +322,10 @@ __global__ void __launch_bounds__(kThreads, kMmaQ6CtasPerSm(D)) attend_mma_q6_ke
         if (!(tb < t1 && tb <= lim0)) s[2] = -INFINITY;
         if (!(tb < t1 && tb <= lim1)) s[3] = -INFINITY;
       }
+      // SIGNED calls may keep the masked scores too (lanes c and c ^ 2 hold the same rows)
+      if constexpr (SIGNED) {
+        if (a.part_s && c < 2) keep_scores(a, bh, ts + g, rbase + r0, s, t1);
+      }
       // online softmax (base 2)
       float mx0 = fmaxf(s[0], s[2]), mx1 = fmaxf(s[1], s[3]);
 #pragma unroll

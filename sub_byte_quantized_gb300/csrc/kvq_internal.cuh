@@ -172,7 +172,26 @@ struct AttendArgs {
   // natural log of each row's sum of exponentials [B][Hq][n_q] (-infinity: the row sees nothing),
   // written by phase 2 when not nullptr
   float *lse;
+  // masked scores in base 2, [B][H_kv][s_tokens][s_rows] (query rows of the kv head, tokens of the body),
+  // written by the decode kernels when not nullptr; tokens no row sees are left out
+  float *part_s;
+  int s_rows, s_tokens;
 };
+// Rows per token of the scores a call's phase 1 can leave behind (0: the kernel it runs on has none).
+// Up to eight query rows on the tensor-core decode kernels.
+__host__ __device__ constexpr int score_rows(int kl, int vl, int D, int rows) {
+  return rows <= 8 && ((D == 128 && decode_kernel(kl, vl)) || (D == 256 && kl == KVQ_Q6_0 && vl == kl))
+             ? (rows <= 2 ? 2 : rows <= 4 ? 4 : 8) : 0;
+}
+// Two rows' scores of tokens t and t + 8 (accumulator order: rows r, r + 1 of t, then of t + 8). Tokens
+// from `end` on belong to another chunk or to none.
+__device__ __forceinline__ void keep_scores(const AttendArgs &a, int bh, int t, int r, const float (&s)[4], int end) {
+  if (r < a.s_rows) {
+    float *p = a.part_s + ((size_t)bh * a.s_tokens + t) * a.s_rows + r;
+    if (t < end) *reinterpret_cast<float2 *>(p) = make_float2(s[0], s[1]);
+    if (t + 8 < end) *reinterpret_cast<float2 *>(p + 8 * a.s_rows) = make_float2(s[2], s[3]);
+  }
+}
 // Row index (b, hq, qi) of query row r (of the gqa * n_q rows of kv head kvh).
 __device__ __forceinline__ size_t query_row_index(const AttendArgs &a, int bb, int kvh, int r) {
   return ((size_t)bb * a.Hq + kvh * a.gqa + r / a.n_q) * a.n_q + r % a.n_q;
@@ -248,7 +267,7 @@ struct WeightArgs {
   float *scores_out;
   long long stride;
   float decay;
-  int tiles;                   // 16-token tiles per warp
+  int units;                   // many rows: 32-token units per CTA
   int n_ctas;                  // CTAs over the body's tokens; the window's follow
 };
 cudaError_t launch_attend_weights(const AttendArgs &a, const float *scores_in, float *scores_out, long long stride,

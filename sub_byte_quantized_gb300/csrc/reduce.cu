@@ -28,6 +28,8 @@ __global__ void __launch_bounds__(kWarps * 32) attend_reduce_kernel(AttendArgs a
   __shared__ __align__(16) float sm_qw[HAD ? kWarps : 1][HAD ? D : 4];   // per-warp rotated query (window)
 #if defined(__CUDA_ARCH__) && __CUDA_ARCH__ >= 900
   asm volatile("griddepcontrol.wait;" ::: "memory");     // phase-1 partials are complete
+  // the kernel that scores the tokens may start; it waits for this grid before it reads the lse
+  if (a.lse) asm volatile("griddepcontrol.launch_dependents;");
 #endif
   const size_t row = blockIdx.x;                          // (b * H_q + h) * n_q + i
   const int qi = (int)(row % a.n_q);
@@ -223,6 +225,8 @@ __global__ void __launch_bounds__(kWarps * 32, KB >= 8 ? 1 : (D == 128 ? 8 - KB 
   constexpr int VPL = D / 32;
 #if defined(__CUDA_ARCH__) && __CUDA_ARCH__ >= 900
   asm volatile("griddepcontrol.wait;" ::: "memory");     // phase-1 partials are complete
+  // the kernel that scores the tokens may start; it waits for this grid before it reads the lse
+  if (a.lse) asm volatile("griddepcontrol.launch_dependents;");
 #endif
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const size_t row = (size_t)blockIdx.x * kWarps + warp;
@@ -307,7 +311,9 @@ cudaError_t launch_attend_reduce(const AttendArgs &a, cudaStream_t st, bool pdl)
   int dev = 0, sms = 148;
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   // many rows and no window work here: one warp per row
-  const bool per_warp = !a.win_in_reduce && rows >= 4u * (unsigned)sms * kWarps;
+  // (calls that also score the tokens: one warp per row from one row per SM on, where the Hadamard CTA per
+  // row, whose registers the window code sets, runs seven waves: 1024 rows of 20 partials 16.6 -> REDUCE_US us)
+  const bool per_warp = !a.win_in_reduce && rows >= (a.lse && had ? 1u : 4u * kWarps) * (unsigned)sms;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = per_warp ? dim3((rows + kWarps - 1) / kWarps) : dim3(rows, had ? 1 : a.cache.D / 32);
   cfg.blockDim = dim3(kWarps * 32);
