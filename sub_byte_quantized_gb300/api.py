@@ -504,12 +504,35 @@ def paged_append_decode_attend_host(cache: PagedKVCache, k_new: torch.Tensor, v_
 
 
 # ------------------------------------------------------------------ rotary positions
-def _on_device(*named) -> None:
-    """Every tensor lives on the current device, whose stream the call uses."""
-    dev = torch.cuda.current_device()
+# The calls below check with few torch calls: a decode step makes them once per layer, and their kernels
+# take a few microseconds.
+_DEVICE, _RAW_STREAM = (getattr(torch._C, n, None) for n in ("_cuda_getDevice", "_cuda_getCurrentRawStream"))
+
+
+def _here(*named) -> int:
+    """The current device, which every one of the (name, tensor) pairs has to live on (None passes)."""
+    dev = _DEVICE()
     for name, t in named:
-        if t is not None and t.device.index != dev:
+        if t is not None and t.get_device() != dev:
+            if not t.is_cuda:
+                raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
             raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{dev}")
+    return dev
+
+
+def _stream_of(stream, dev: int) -> int:
+    return _RAW_STREAM(dev) if stream is None else _stream(stream)
+
+
+def _dense(name: str, t: torch.Tensor, dtype, shape=None) -> None:
+    """Checks a contiguous tensor of a type (and shape, where given)."""
+    if t.dtype is not dtype or not t.is_contiguous() or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor" + (f" of shape {tuple(shape)}" if shape is not None else ""))
+
+
+def _ints(name: str, t: torch.Tensor | None, n: int) -> None:
+    if t is not None and (t.dtype is not torch.int32 or t.numel() != n or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous int32 tensor of {n} entries")
 
 
 def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -537,56 +560,55 @@ def rope_table(inv_freq: torch.Tensor, n_pos: int, pos0: int = 0, magnitude: flo
     rot_dim = 2 * inv_freq.numel()
     if out is None:
         out = torch.empty((max(n_pos, 0), rot_dim), dtype=torch.float32, device=device)
-    _need_cuda("out", out)
-    _on_device(("out", out))
-    if out.dtype != torch.float32 or tuple(out.shape) != (n_pos, rot_dim):
-        raise ValueError("out must be float32 [n_pos][rot_dim]")
-    L.check(L.lib().kvq_rope_table(inv_freq.data_ptr(), rot_dim, pos0, n_pos, float(magnitude), out.data_ptr(),
-                                   _stream(stream)), "kvq_rope_table")
+    dev = _here(("out", out))
+    _dense("out", out, torch.float32, (n_pos, rot_dim))
+    L.check(L.lib().kvq_rope_table(inv_freq.data_ptr(), rot_dim, pos0, n_pos, magnitude, out.data_ptr(),
+                                   _stream_of(stream, dev)), "kvq_rope_table")
     return out
 
 
-def _rows(name: str, t: torch.Tensor, shape: tuple, dtype) -> L.KvqRows:
+def _rows(name: str, t: torch.Tensor) -> L.KvqRows:
     """A [batch][heads][n_new][head_dim] tensor by its strides (the last axis contiguous)."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
-    if tuple(t.shape) != shape or t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype} of shape {shape}")
-    st = t.stride()
-    if st[3] != 1:
+    (b, h, n, d), (sb, sh, sn, sd) = t.shape, t.stride()
+    if sd != 1 and d > 1:
         raise ValueError(f"{name}: the head_dim axis must be contiguous")
     # the stride of an axis of one entry is never used
-    return L.KvqRows(t.data_ptr(), *(s if n > 1 else 0 for s, n in zip(st[:3], shape[:3])))
+    return L.KvqRows(t.data_ptr(), sb if b > 1 else 0, sh if h > 1 else 0, sn if n > 1 else 0)
 
 
-def _rope_call(cache, table, k_new, v_new, q, positions, interleaved, q_out):
-    """The arguments both rotary appends share: (rope, k, v, q or None, dtype id, n_q_heads, n_new, q_out)."""
-    _need_cuda("table", table)
-    if table.dtype != torch.float32 or table.dim() != 2:
-        raise ValueError("table must be float32 [n_pos][rot_dim]")
-    B, H, n_new, D = k_new.shape
-    if (B, H, D) != (cache.batch, cache.n_kv_heads, cache.head_dim):
+def _rope_call(cache, table, k_new, v_new, slots, q, positions, interleaved, q_out, stream):
+    """The arguments both rotary appends share."""
+    shape, dtype = k_new.shape, k_new.dtype
+    if len(shape) != 4 or shape[0] != cache.batch or shape[1] != cache.n_kv_heads or shape[3] != cache.head_dim:
         raise ValueError("k_new shape does not match the cache")
-    if k_new.dtype not in _DTYPES:
-        raise ValueError(f"unsupported dtype {k_new.dtype}")
-    k, v = _rows("k_new", k_new, (B, H, n_new, D), k_new.dtype), _rows("v_new", v_new, (B, H, n_new, D), k_new.dtype)
-    if positions is not None:
-        _i32_vec("positions", positions, B * n_new)
+    if dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {dtype}")
+    if v_new.shape != shape or v_new.dtype is not dtype:
+        raise ValueError("k_new and v_new must have the same shape and dtype")
+    _dense("table", table, torch.float32)
+    if table.dim() != 2:
+        raise ValueError("table must be float32 [n_pos][rot_dim]")
+    B, _, n_new, D = shape
+    _ints("positions", positions, B * n_new)
+    _ints("slots", slots, B)
     qr, Hq = None, 0
     if q is not None:
         Hq = q.shape[1]
-        qr = _rows("q", q, (B, Hq, n_new, D), k_new.dtype)
+        if q.shape != (B, Hq, n_new, D) or q.dtype is not dtype:
+            raise ValueError("q must have k_new's batch, rows, head_dim and dtype")
         if q_out is None:
-            q_out = torch.empty((B, Hq, n_new, D), dtype=q.dtype, device=q.device)
-        _need_cuda("q_out", q_out)
-        if tuple(q_out.shape) != (B, Hq, n_new, D) or q_out.dtype != q.dtype:
-            raise ValueError("q_out must have q's shape and dtype")
+            q_out = torch.empty((B, Hq, n_new, D), dtype=dtype, device=q.device)
+        else:
+            _dense("q_out", q_out, dtype, (B, Hq, n_new, D))
+        qr = C.byref(_rows("q", q))
     elif q_out is not None:
         raise ValueError("q_out without q")
-    _on_device(("cache", cache.planes["k"]["payload"]), ("table", table), ("k_new", k_new), ("v_new", v_new), ("q", q),
-               ("positions", positions), ("q_out", q_out))
-    rope = L.KvqRope(table.data_ptr(), table.shape[0], table.shape[1], int(bool(interleaved)), _ptr(positions))
-    return rope, k, v, qr, _DTYPES[k_new.dtype], Hq, n_new, q_out
+    dev = _here(("cache", cache.planes["k"]["payload"]), ("table", table), ("k_new", k_new), ("v_new", v_new), ("q", q),
+                ("positions", positions), ("slots", slots), ("q_out", q_out))
+    n_pos, rot_dim = table.shape
+    rope = L.KvqRope(table.data_ptr(), n_pos, rot_dim, 1 if interleaved else 0, _ptr(positions))
+    return (C.byref(cache.struct), C.byref(rope), C.byref(_rows("k_new", k_new)), C.byref(_rows("v_new", v_new)), qr,
+            _DTYPES[dtype], Hq, n_new), q_out, _stream_of(stream, dev)
 
 
 def rope_store(cache: KVCache, table: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, pos0: int,
@@ -595,10 +617,8 @@ def rope_store(cache: KVCache, table: torch.Tensor, k_new: torch.Tensor, v_new: 
     """store() of k_new rotated by the table and of v_new at slots [pos0, pos0 + n_new); returns q rotated
     ([B][H_q][n_new][D], contiguous, q's dtype). k_new, v_new and q may be strided views. positions: int32
     [B][n_new], the rotary positions where they are not the slots."""
-    rope, k, v, qr, dt, Hq, n_new, q_out = _rope_call(cache, table, k_new, v_new, q, positions, interleaved, q_out)
-    L.check(L.lib().kvq_rope_store(C.byref(cache.struct), C.byref(rope), C.byref(k), C.byref(v),
-                                   None if qr is None else C.byref(qr), dt, Hq, n_new, pos0, _ptr(q_out),
-                                   _stream(stream)), "kvq_rope_store")
+    args, q_out, st = _rope_call(cache, table, k_new, v_new, None, q, positions, interleaved, q_out, stream)
+    L.check(L.lib().kvq_rope_store(*args, pos0, _ptr(q_out), st), "kvq_rope_store")
     return q_out
 
 
@@ -606,61 +626,57 @@ def paged_rope_store(cache: PagedKVCache, table: torch.Tensor, k_new: torch.Tens
                      slots: torch.Tensor, q: torch.Tensor | None = None, positions: torch.Tensor | None = None,
                      interleaved: bool = False, q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
     """rope_store into a paged pool: sequence b's rows at slots [slots[b], slots[b] + n_new)."""
-    _i32_vec("slots", slots, cache.batch)
-    rope, k, v, qr, dt, Hq, n_new, q_out = _rope_call(cache, table, k_new, v_new, q, positions, interleaved, q_out)
-    _on_device(("slots", slots))
-    L.check(L.lib().kvq_paged_rope_store(C.byref(cache.struct), C.byref(rope), C.byref(k), C.byref(v),
-                                         None if qr is None else C.byref(qr), dt, Hq, n_new, slots.data_ptr(),
-                                         _ptr(q_out), _stream(stream)), "kvq_paged_rope_store")
+    args, q_out, st = _rope_call(cache, table, k_new, v_new, slots, q, positions, interleaved, q_out, stream)
+    L.check(L.lib().kvq_paged_rope_store(*args, slots.data_ptr(), _ptr(q_out), st), "kvq_paged_rope_store")
     return q_out
 
 
 # ------------------------------------------------------------------ a cache inside a budget
 def _scores(name: str, t: torch.Tensor, cache) -> int:
     """Checks running scores f32 [B][H_kv][stride] and returns the stride."""
-    _need_cuda(name, t)
-    if t.dtype != torch.float32 or t.dim() != 3 or tuple(t.shape[:2]) != (cache.batch, cache.n_kv_heads):
-        raise ValueError(f"{name} must be float32 [batch][n_kv_heads][tokens]")
-    return t.shape[2]
+    shape = t.shape
+    if t.dtype is not torch.float32 or len(shape) != 3 or shape[0] != cache.batch or shape[1] != cache.n_kv_heads or \
+            not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous float32 [batch][n_kv_heads][tokens]")
+    return shape[2]
 
 
 def attend_weights_workspace_bytes(cache: KVCache, n_q_heads: int, n_q: int, kv_len: int, chunk: int = 0) -> int:
-    return int(L.lib().kvq_attend_weights_workspace_bytes(C.byref(cache.struct), n_q_heads, n_q, kv_len, chunk))
+    return L.lib().kvq_attend_weights_workspace_bytes(C.byref(cache.struct), n_q_heads, n_q, kv_len, chunk)
 
 
 def paged_attend_weights_workspace_bytes(cache: PagedKVCache, n_q_heads: int, n_q: int, max_kv_len: int,
                                          chunk: int = 0) -> int:
-    return int(L.lib().kvq_paged_attend_weights_workspace_bytes(C.byref(cache.struct), n_q_heads, n_q, max_kv_len,
-                                                                chunk))
+    return L.lib().kvq_paged_attend_weights_workspace_bytes(C.byref(cache.struct), n_q_heads, n_q, max_kv_len, chunk)
 
 
-def _weights_call(cache, q, scores, scores_out, attn_scale, out, workspace, need):
-    """The buffers both calls share: (scores_out, stride, attn_scale, out, workspace)."""
-    B, Hq, n_q, D = q.shape
-    if B != cache.batch or D != cache.head_dim:
+def _weights_call(cache, need_fn, q, n, seq_lens, scores, scores_out, attn_scale, chunk, out, workspace, stream):
+    """The buffers both calls share: (out, scores_out, stride, attn_scale, workspace, its bytes, stream)."""
+    shape = q.shape
+    if len(shape) != 4 or shape[0] != cache.batch or shape[3] != cache.head_dim:
         raise ValueError("q shape does not match the cache")
-    if scores is None and scores_out is None:
-        raise ValueError("scores or scores_out is needed")
-    if scores is not None:
-        _scores("scores", scores, cache)
+    if q.dtype not in _DTYPES or not q.is_contiguous():
+        raise ValueError("q must be contiguous f32, bf16 or f16")
     if scores_out is None:
+        if scores is None:
+            raise ValueError("scores or scores_out is needed")
         scores_out = scores
     stride = _scores("scores_out", scores_out, cache)
-    if scores is not None and scores.shape != scores_out.shape:
+    if scores is not None and scores is not scores_out and _scores("scores", scores, cache) != stride:
         raise ValueError("scores and scores_out must have the same shape")
-    if attn_scale is None:
-        attn_scale = 1.0 / math.sqrt(D)
+    _ints("seq_lens", seq_lens, cache.batch)
     if out is None:
-        out = torch.empty((B, Hq, n_q, D), dtype=torch.float32, device=q.device)
-    _need_cuda("out", out)
-    if out.dtype != torch.float32 or out.shape != q.shape:
-        raise ValueError("out must be float32 of q's shape")
+        out = torch.empty(shape, dtype=torch.float32, device=q.device)
+    else:
+        _dense("out", out, torch.float32, shape)
     if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
-    _need_cuda("workspace", workspace)
-    _on_device(("cache", cache.planes["k"]["payload"]), ("q", q), ("scores", scores), ("scores_out", scores_out),
-               ("out", out), ("workspace", workspace))
-    return scores_out, stride, float(attn_scale), out, workspace
+        workspace = torch.empty(max(need_fn(cache, shape[1], shape[2], n, chunk), 256), dtype=torch.uint8, device=q.device)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    dev = _here(("cache", cache.planes["k"]["payload"]), ("q", q), ("scores", scores), ("scores_out", scores_out),
+                ("seq_lens", seq_lens), ("out", out), ("workspace", workspace))
+    return (out, scores_out, stride, 1.0 / math.sqrt(shape[3]) if attn_scale is None else attn_scale, workspace,
+            workspace.numel() * workspace.element_size(), _stream_of(stream, dev))
 
 
 def decode_attend_weights(cache: KVCache, q: torch.Tensor, kv_len: int, scores: torch.Tensor | None,
@@ -670,15 +686,12 @@ def decode_attend_weights(cache: KVCache, q: torch.Tensor, kv_len: int, scores: 
     """decode_attend that also updates the tokens' running attention weight: returns (out, scores_out) with
     scores_out[b][h][t] = decay * scores[b][h][t] + the weights of token t summed over the query rows of kv
     head h, t < kv_len. scores: f32 [B][H_kv][tokens >= kv_len] or None; scores_out defaults to scores."""
-    _need_cuda("q", q)
-    Hq, n_q = q.shape[1], q.shape[2]
-    need = 0 if workspace is not None else attend_weights_workspace_bytes(cache, Hq, n_q, kv_len, chunk)
-    scores_out, stride, attn_scale, out, workspace = _weights_call(cache, q, scores, scores_out, attn_scale, out,
-                                                                   workspace, need)
+    out, scores_out, stride, attn_scale, workspace, nbytes, st = _weights_call(
+        cache, attend_weights_workspace_bytes, q, kv_len, None, scores, scores_out, attn_scale, chunk, out, workspace, stream)
     L.check(L.lib().kvq_decode_attend_weights(
-        C.byref(cache.struct), q.data_ptr(), _DTYPES[q.dtype], Hq, n_q, kv_len, int(bool(causal)), q_pos0, attn_scale,
-        chunk, out.data_ptr(), _ptr(scores), scores_out.data_ptr(), stride, float(decay), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _stream(stream)), "kvq_decode_attend_weights")
+        C.byref(cache.struct), q.data_ptr(), _DTYPES[q.dtype], q.shape[1], q.shape[2], kv_len, 1 if causal else 0, q_pos0,
+        attn_scale, chunk, out.data_ptr(), _ptr(scores), scores_out.data_ptr(), stride, decay, workspace.data_ptr(),
+        nbytes, st), "kvq_decode_attend_weights")
     return out, scores_out
 
 
@@ -689,18 +702,13 @@ def paged_decode_attend_weights(cache: PagedKVCache, q: torch.Tensor, seq_lens: 
                                 workspace: torch.Tensor | None = None, stream=None):
     """paged_decode_attend that also updates the tokens' running attention weight (decode_attend_weights);
     scores of sequence b's tokens t < seq_lens[b] are written."""
-    _need_cuda("q", q)
-    _i32_vec("seq_lens", seq_lens, cache.batch)
-    Hq, n_q = q.shape[1], q.shape[2]
-    need = 0 if workspace is not None else paged_attend_weights_workspace_bytes(cache, Hq, n_q, max_kv_len, chunk)
-    scores_out, stride, attn_scale, out, workspace = _weights_call(cache, q, scores, scores_out, attn_scale, out,
-                                                                   workspace, need)
-    _on_device(("seq_lens", seq_lens))
+    out, scores_out, stride, attn_scale, workspace, nbytes, st = _weights_call(
+        cache, paged_attend_weights_workspace_bytes, q, max_kv_len, seq_lens, scores, scores_out, attn_scale, chunk, out,
+        workspace, stream)
     L.check(L.lib().kvq_paged_decode_attend_weights(
-        C.byref(cache.struct), q.data_ptr(), _DTYPES[q.dtype], Hq, n_q, seq_lens.data_ptr(), max_kv_len,
-        int(bool(causal)), attn_scale, chunk, out.data_ptr(), _ptr(scores), scores_out.data_ptr(), stride, float(decay),
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream)),
-        "kvq_paged_decode_attend_weights")
+        C.byref(cache.struct), q.data_ptr(), _DTYPES[q.dtype], q.shape[1], q.shape[2], seq_lens.data_ptr(), max_kv_len,
+        1 if causal else 0, attn_scale, chunk, out.data_ptr(), _ptr(scores), scores_out.data_ptr(), stride, decay,
+        workspace.data_ptr(), nbytes, st), "kvq_paged_decode_attend_weights")
     return out, scores_out
 
 
@@ -711,28 +719,28 @@ def evict_select(scores: torch.Tensor, kv_len: int, n_keep: int, n_sink: int = 0
     the last n_recent and the highest scores among the others, ties to the lowest index. seq_lens: int32 [B]
     lengths (else kv_len for all); sequences of at most n_keep tokens keep all, -1 fills their lists.
     new_lens: int32 [B], gets min(length, n_keep)."""
-    _need_cuda("scores", scores)
-    if scores.dtype != torch.float32 or scores.dim() != 3:
-        raise ValueError("scores must be float32 [batch][n_kv_heads][tokens]")
+    if scores.dtype is not torch.float32 or scores.dim() != 3 or not scores.is_contiguous():
+        raise ValueError("scores must be contiguous float32 [batch][n_kv_heads][tokens]")
     B, H, stride = scores.shape
     if keep is None:
         keep = torch.empty((B, H, max(n_keep, 1)), dtype=torch.int32, device=scores.device)
-    _i32_vec("keep", keep, B * H * max(n_keep, 1))
-    for name, t in (("seq_lens", seq_lens), ("new_lens", new_lens)):
-        if t is not None:
-            _i32_vec(name, t, B)
-    _on_device(("scores", scores), ("keep", keep), ("seq_lens", seq_lens), ("new_lens", new_lens))
+    else:
+        _ints("keep", keep, B * H * max(n_keep, 1))
+    _ints("seq_lens", seq_lens, B)
+    _ints("new_lens", new_lens, B)
+    dev = _here(("scores", scores), ("keep", keep), ("seq_lens", seq_lens), ("new_lens", new_lens))
     L.check(L.lib().kvq_evict_select(scores.data_ptr(), B, H, stride, kv_len, _ptr(seq_lens), n_keep, n_sink, n_recent,
-                                     keep.data_ptr(), _ptr(new_lens), _stream(stream)), "kvq_evict_select")
+                                     keep.data_ptr(), _ptr(new_lens), _stream_of(stream, dev)), "kvq_evict_select")
     return keep
 
 
 def _keep_list(keep: torch.Tensor, cache) -> int:
     """Checks a list of kept tokens int32 [B][H_kv][n_keep] and returns n_keep."""
-    _need_cuda("keep", keep)
-    if keep.dtype != torch.int32 or keep.dim() != 3 or tuple(keep.shape[:2]) != (cache.batch, cache.n_kv_heads):
-        raise ValueError("keep must be int32 [batch][n_kv_heads][n_keep]")
-    return keep.shape[2]
+    shape = keep.shape
+    if keep.dtype is not torch.int32 or len(shape) != 3 or shape[0] != cache.batch or shape[1] != cache.n_kv_heads or \
+            not keep.is_contiguous():
+        raise ValueError("keep must be contiguous int32 [batch][n_kv_heads][n_keep]")
+    return shape[2]
 
 
 def evict_compact(cache: KVCache, keep: torch.Tensor, kv_len: int, dst: KVCache | None = None,
@@ -743,11 +751,11 @@ def evict_compact(cache: KVCache, keep: torch.Tensor, kv_len: int, dst: KVCache 
     n_keep = _keep_list(keep, cache)
     stride = _scores("scores", scores, cache) if scores is not None else 0
     out_stride = _scores("scores_out", scores_out, cache) if scores_out is not None else stride
-    _on_device(("cache", cache.planes["k"]["payload"]), ("keep", keep), ("scores", scores), ("scores_out", scores_out),
-               ("dst", None if dst is None else dst.planes["k"]["payload"]))
+    dev = _here(("cache", cache.planes["k"]["payload"]), ("keep", keep), ("scores", scores), ("scores_out", scores_out),
+                ("dst", None if dst is None else dst.planes["k"]["payload"]))
     L.check(L.lib().kvq_evict_compact(C.byref(cache.struct), None if dst is None else C.byref(dst.struct),
                                       keep.data_ptr(), n_keep, kv_len, _ptr(scores), stride, _ptr(scores_out),
-                                      out_stride, _stream(stream)), "kvq_evict_compact")
+                                      out_stride, _stream_of(stream, dev)), "kvq_evict_compact")
     return min(kv_len, n_keep)
 
 
@@ -755,9 +763,9 @@ def paged_evict_compact(cache: PagedKVCache, keep: torch.Tensor, seq_lens: torch
                         scores: torch.Tensor | None = None, stream=None) -> None:
     """evict_compact in place in a paged pool, every sequence by its own length (seq_lens: the lengths before)."""
     n_keep = _keep_list(keep, cache)
-    _i32_vec("seq_lens", seq_lens, cache.batch)
+    _ints("seq_lens", seq_lens, cache.batch)
     stride = _scores("scores", scores, cache) if scores is not None else 0
-    _on_device(("cache", cache.planes["k"]["payload"]), ("keep", keep), ("seq_lens", seq_lens), ("scores", scores))
+    dev = _here(("cache", cache.planes["k"]["payload"]), ("keep", keep), ("seq_lens", seq_lens), ("scores", scores))
     L.check(L.lib().kvq_paged_evict_compact(C.byref(cache.struct), keep.data_ptr(), n_keep, seq_lens.data_ptr(),
-                                            max_kv_len, _ptr(scores), stride, _stream(stream)),
+                                            max_kv_len, _ptr(scores), stride, _stream_of(stream, dev)),
             "kvq_paged_evict_compact")

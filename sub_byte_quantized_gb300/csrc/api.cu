@@ -961,10 +961,13 @@ constexpr int kMaxEvictTokens = 1 << 27;
 // Chunk of an attention call that also scores the tokens, for chunk 0: the attention's own choice, with
 // two bounds. 2560 tokens: its float32 result carries the truncation of the tensor cores' accumulation,
 // which grows with the tokens a warp adds up (16 sequences of up to 16379 tokens in Q8_0: 9.1e-6 of the
-// output's norm at the automatic 4608 tokens). And on the tcgen05 kernel as many chunks as fill the SMs
-// (it takes at most eight by itself: 64 CTAs for 128 rows and 8 kv heads).
+// output's norm at the automatic 4608 tokens); 1536 where the sequences have lengths of their own, whose
+// chunks fill the SMs more evenly (the same batch: 83 us, at 2560 89 us, at 768 92 us). And on the tcgen05
+// kernel as many chunks as fill the SMs (it takes at most eight by itself: 64 CTAs for 128 rows and 8 kv
+// heads).
 int weights_chunk(const kvq::CacheView &c, int n_q_heads, int n_q, int kv_len, int auto_chunk) {
-  int chunk = auto_chunk < 2560 ? auto_chunk : 2560;
+  const int most = c.page_shift >= 0 ? 1536 : 2560;
+  int chunk = auto_chunk < most ? auto_chunk : most;
   const int rows = n_q_heads / c.H * n_q;
   if (kvq::tc_prefill_shape(c.layout, c.v_layout, c.D, rows)) {
     int dev = 0, sms = 148;

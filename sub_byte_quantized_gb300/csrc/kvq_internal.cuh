@@ -216,12 +216,18 @@ cudaError_t launch_rope_table(const RopeTurns &f, int rot, int pos0, int n_pos, 
 // Rotary append: rows [batch][heads][n_new][D] of k, v (and q, when Hq > 0) by their strides in
 // elements. Slots are pos0 + j, or slots[b] + j (device); rotary positions positions[b][j] (device),
 // or the slots when nullptr; a position outside the table is clamped into it. The launcher fills the
-// row counts and the row bytes.
+// divisors, the row counts and the row bytes.
 struct RowsIn {
   const void *data;
   long long batch, head, token;
 };
+// Division by a constant of the launch (dividends below 2^31).
+struct FastDiv {
+  unsigned mul;
+  int shift;
+};
 struct RopeStore {
+  FastDiv by_new, by_kv_heads, by_q_heads;
   RowsIn in[3];                // k, v, q
   int dtype, Hq, n_new, pos0;
   const int32_t *slots;

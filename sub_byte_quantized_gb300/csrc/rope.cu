@@ -4,7 +4,7 @@
 // angle has lost its fraction of a turn in float32 (p f = 1e5 leaves 2^-7 of a radian), so the angle is
 // counted in turns: f_i / 2 pi as a 64-bit binary fraction, and p times it in wrapping 64-bit integers,
 // which takes whole turns off exactly. The nearest quarter turn goes into signs and a swap; what is
-// left, in [-1/8, 1/8) of a turn, is rounded to float32 once and given to sinpif / cospif.
+// left, in [-1/8, 1/8) of a turn, is rounded to float32 once and goes into two short polynomials.
 //
 // Append with rotary positions. One launch reads q, k and v from wherever their projection left them
 // (any strides between batches, heads and tokens), rotates q and k, and writes q in its own type and k
@@ -23,32 +23,63 @@ namespace kvq {
 namespace {
 
 constexpr int kTableThreads = 256;
+constexpr int kTableRows = 8;        // positions per thread, a grid apart
 
-__global__ void __launch_bounds__(kTableThreads) rope_table_kernel(RopeTurns f, int half, int pos0, int n_pos, float mag,
+// sin(pi u) and cos(pi u) for |u| <= 1/4, by their Taylor polynomials in u^2 (remainders below 2^-29);
+// pi is split so that only u's own rounding and the last addition count.
+__device__ __forceinline__ void sincos_pi(float u, float &s, float &c) {
+  const float z = __fmul_rn(u, u);
+  float p = 0.08214588661112823f;                        // pi^9 / 9!
+  p = __fmaf_rn(p, z, -0.5992645293207921f);             // pi^7 / 7!
+  p = __fmaf_rn(p, z, 2.550164039877345f);               // pi^5 / 5!
+  p = __fmaf_rn(p, z, -5.16771278004997f);               // pi^3 / 3!
+  p = __fmaf_rn(p, z, -8.742277657347586e-08f);          // pi - fl(pi)
+  s = __fmaf_rn(u, 3.1415927410125732f, __fmul_rn(u, p));
+  float q = -0.025806891390014061f;                      // pi^10 / 10!
+  q = __fmaf_rn(q, z, 0.23533063035889321f);             // pi^8 / 8!
+  q = __fmaf_rn(q, z, -1.3352627688545895f);             // pi^6 / 6!
+  q = __fmaf_rn(q, z, 4.0587121264167682f);              // pi^4 / 4!
+  q = __fmaf_rn(q, z, -4.9348022005446793f);             // pi^2 / 2!
+  c = __fmaf_rn(q, z, 1.0f);
+}
+
+// Thread (frequency quad, first row) steps through its positions by adding rows * f to the angle: the
+// frequencies, read at an index of its own per lane, are loaded once per thread. 16-byte stores.
+__global__ void __launch_bounds__(kTableThreads) rope_table_kernel(RopeTurns f, int half, int pos0, int n_pos, int rows, float mag,
                                                                    float *__restrict__ table) {
-  // four neighbouring frequencies of one position per thread: 16-byte stores
   const int quads = half >> 2;
   const long long id = (long long)blockIdx.x * kTableThreads + threadIdx.x;
-  const long long p = id / quads;
-  if (p >= n_pos) return;
-  const int i0 = 4 * (int)(id - p * quads);
-  const unsigned long long pos = (unsigned long long)pos0 + (unsigned long long)p;
-  float c[4], s[4];
+  const long long first = id / quads;
+  if (first >= rows) return;
+  const int i0 = 4 * (int)(id - first * quads);
+  unsigned long long turn[4], step[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const unsigned long long t = pos * f.turn[i0 + k];            // the angle in 2^-64 turns, whole turns gone
-    const unsigned quarter = (unsigned)((t + (1ull << 61)) >> 62);   // nearest quarter turn (0 .. 3)
-    const long long rest = (long long)(t - ((unsigned long long)quarter << 62));   // [-2^61, 2^61)
-    const float half_turns = __ll2float_rn(rest) * 0x1.0p-63f;     // in units of pi
-    const float sr = sinpif(half_turns), cr = cospif(half_turns);
-    const float sv = (quarter & 1) ? cr : sr, cv = (quarter & 1) ? sr : cr;
-    s[k] = __fmul_rn((quarter & 2) ? -sv : sv, mag);
-    c[k] = __fmul_rn(((quarter + 1) & 2) ? -cv : cv, mag);         // cos is negative in quarters 1 and 2
+    const unsigned long long t = f.turn[i0 + k];
+    turn[k] = ((unsigned long long)pos0 + (unsigned long long)first) * t;   // in 2^-64 turns, whole turns gone
+    step[k] = (unsigned long long)rows * t;
   }
-  float *row = table + (size_t)p * (2 * half) + i0;
-  *reinterpret_cast<float4 *>(row) = make_float4(c[0], c[1], c[2], c[3]);
-  *reinterpret_cast<float4 *>(row + half) = make_float4(s[0], s[1], s[2], s[3]);
+  for (long long p = first; p < n_pos; p += rows) {
+    float c[4], s[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const unsigned quarter = (unsigned)((turn[k] + (1ull << 61)) >> 62);       // nearest quarter turn (0 .. 3)
+      const long long rest = (long long)(turn[k] - ((unsigned long long)quarter << 62));   // [-2^61, 2^61)
+      float sr, cr;
+      sincos_pi(__ll2float_rn(rest) * 0x1.0p-63f, sr, cr);       // in units of pi
+      const float sv = (quarter & 1) ? cr : sr, cv = (quarter & 1) ? sr : cr;
+      s[k] = __fmul_rn((quarter & 2) ? -sv : sv, mag);
+      c[k] = __fmul_rn(((quarter + 1) & 2) ? -cv : cv, mag);     // cos is negative in quarters 1 and 2
+      turn[k] += step[k];
+    }
+    float *row = table + (size_t)p * (2 * half) + i0;
+    *reinterpret_cast<float4 *>(row) = make_float4(c[0], c[1], c[2], c[3]);
+    *reinterpret_cast<float4 *>(row + half) = make_float4(s[0], s[1], s[2], s[3]);
+  }
 }
+
+// n / d for n < 2^31 by one high product: (n + umulhi(n, mul)) >> shift.
+__device__ __forceinline__ unsigned divide(unsigned n, const FastDiv &d) { return (n + __umulhi(n, d.mul)) >> d.shift; }
 
 // Which row a thread or warp works on: K rows first, then V, then q.
 struct RopeRow {
@@ -62,10 +93,10 @@ __device__ __forceinline__ RopeRow rope_row(const CacheView &c, const RopeStore 
   w.what = r < g.k_rows ? 0 : (r < g.k_rows + g.v_rows ? 1 : 2);
   r -= w.what == 0 ? 0 : (w.what == 1 ? g.k_rows : g.k_rows + g.v_rows);
   const int heads = w.what == 2 ? g.Hq : c.H;
-  if (r <= 0x7FFFFFFFLL) {                                // 32-bit divisions
-    const unsigned bh = (unsigned)r / (unsigned)g.n_new;
+  if (r <= 0x7FFFFFFFLL) {
+    const unsigned bh = divide((unsigned)r, g.by_new);
     w.j = (int)((unsigned)r - bh * (unsigned)g.n_new);
-    w.b = (int)(bh / (unsigned)heads);
+    w.b = (int)divide(bh, w.what == 2 ? g.by_q_heads : g.by_kv_heads);
     w.head = (int)(bh - (unsigned)w.b * (unsigned)heads);
   } else {
     const long long bh = r / g.n_new;
@@ -175,6 +206,7 @@ __global__ void __launch_bounds__(256) rope_store_block_kernel(CacheView c, Rope
   float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   if (valid) rope_load<8>(g, w, 8 * tr, y);
   if (valid && w.what == 2) write_q<8>(g, w, c.D, 8 * tr, y);
+  if (__all_sync(0xffffffffu, !valid || w.what == 2)) return;   // a warp of q rows has nothing to quantise
   quant_block<LAYOUT>(c, w.what == 1, w.crow, g.row_bytes, c.D / kBlock, tr >> 2, tr & 3, y, valid && w.what != 2);
 }
 
@@ -215,17 +247,29 @@ cudaError_t launch_plane(const CacheView &c, int layout, const RopeStore &g, cud
   return cudaGetLastError();
 }
 
+FastDiv fast_div(int d) {
+  FastDiv f = {0, 0};
+  while ((1ull << f.shift) < (unsigned long long)d) ++f.shift;
+  f.mul = (unsigned)((((1ull << f.shift) - (unsigned long long)d) << 32) / (unsigned long long)d + 1);
+  return f;
+}
+
 }  // namespace
 
 cudaError_t launch_rope_table(const RopeTurns &f, int rot, int pos0, int n_pos, float mag, float *table, cudaStream_t st) {
-  const long long threads = (long long)n_pos * (rot / 8);
+  // short tables: a position per thread
+  const int per = n_pos >= 32768 ? kTableRows : 1, rows = (n_pos + per - 1) / per;
+  const long long threads = (long long)rows * (rot / 8);
   rope_table_kernel<<<(unsigned)((threads + kTableThreads - 1) / kTableThreads), kTableThreads, 0, st>>>(
-      f, rot / 2, pos0, n_pos, mag, table);
+      f, rot / 2, pos0, n_pos, rows, mag, table);
   return cudaGetLastError();
 }
 
 cudaError_t launch_rope_store(const CacheView &c, RopeStore g, cudaStream_t st) {
   const long long rows = (long long)c.B * c.H * g.n_new;
+  g.by_new = fast_div(g.n_new);
+  g.by_kv_heads = fast_div(c.H);
+  g.by_q_heads = fast_div(g.Hq > 0 ? g.Hq : 1);
   g.k_rows = rows;
   g.v_rows = c.layout == c.v_layout ? rows : 0;
   g.q_rows = (long long)c.B * g.Hq * g.n_new;

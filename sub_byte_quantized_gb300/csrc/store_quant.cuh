@@ -23,11 +23,35 @@ __device__ __forceinline__ __half f16_sat(float x) {
   return __float2half_rn(fminf(fmaxf(x, -kF16Max), kF16Max));
 }
 
-// q = clamp(rint(x / s), lo, hi), or 0 when s == 0.
-__device__ __forceinline__ int sym_code(float x, float s, int lo, int hi) {
-  if (!(s > 0.0f)) return 0;
-  const float r = rintf(__fdiv_rn(x, s));
-  return (int)fminf(fmaxf(r, (float)lo), (float)hi);
+// Codes clamp(rint(x / s), LO, HI) of N values (0 when s == 0), x / s the correctly rounded quotient: as
+// bit fields of an unsigned word each, two's complement (the caller masks them).
+//
+// The quotient is taken as r = x * fl(1 / s), off by less than 2^-22 of itself, i.e. by less than 7e-5 for
+// |x / s| <= 256 (beyond, both clamp alike). It rounds like the correct quotient unless a half-integer lies
+// between the two, and then r is within 1e-4 of one: those rare threads divide. Rounding is the addition of
+// 1.5 * 2^23 (nearest even), whose low mantissa bits are the code. A scale below 2^-100 divides throughout
+// (its reciprocal could overflow).
+template <int LO, int HI, int N>
+__device__ __forceinline__ void round_codes(const float (&x)[N], float s, uint32_t (&code)[N]) {
+  constexpr float kMagic = 12582912.0f;
+  if (!(s > 0.0f)) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) code[i] = 0;
+    return;
+  }
+  const float inv = __frcp_rn(s);
+  bool divide = s < 0x1p-100f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float r = fminf(fmaxf(__fmul_rn(x[i], inv), -300.0f), 300.0f), m = __fadd_rn(r, kMagic);
+    divide |= fabsf(__fsub_rn(r, __fsub_rn(m, kMagic))) > 0.4999f;
+    code[i] = __float_as_uint(fminf(fmaxf(m, kMagic + LO), kMagic + HI));
+  }
+  if (divide) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      code[i] = (uint32_t)(int)fminf(fmaxf(rintf(__fdiv_rn(x[i], s)), (float)LO), (float)HI);
+  }
 }
 
 // Eight values (dims 32 blk + 8 lb + 0..7) of a row, in a thread whose three neighbours in the aligned
@@ -48,16 +72,13 @@ __device__ __forceinline__ void quant_block(const CacheView &c, int kv, long lon
     const __half sh = f16_sat(__fdiv_rn(__fsub_rn(mx, mn), 15.0f));
     const __half zh = f16_sat(mn);
     const float s = __half2float(sh), z = __half2float(zh);
-    uint32_t w = 0;
+    float x[8];
+    uint32_t q[8], w = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      int q = 0;
-      if (s > 0.0f) {
-        const float rr = rintf(__fdiv_rn(__fsub_rn(v[i], z), s));
-        q = (int)fminf(fmaxf(rr, 0.0f), 15.0f);
-      }
-      w |= (uint32_t)q << (4 * i);
-    }
+    for (int i = 0; i < 8; ++i) x[i] = __fsub_rn(v[i], z);
+    round_codes<0, 15>(x, s, q);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w |= (q[i] & 0xFu) << (4 * i);
     if (!valid) return;
     *reinterpret_cast<uint32_t *>(prow + blk * 16 + lb * 4) = w;
     if (lb == 0) {
@@ -74,20 +95,22 @@ __device__ __forceinline__ void quant_block(const CacheView &c, int kv, long lon
   if (LAYOUT == KVQ_Q4_0) {
     const __half sh = f16_sat(__fdiv_rn(amax, 8.0f));
     const float s = __half2float(sh);
-    uint32_t w = 0;
+    uint32_t q[8], w = 0;
+    round_codes<-8, 7>(v, s, q);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w |= ((uint32_t)sym_code(v[i], s, -8, 7) & 0xFu) << (4 * i);
+    for (int i = 0; i < 8; ++i) w |= (q[i] & 0xFu) << (4 * i);
     if (!valid) return;
     *reinterpret_cast<uint32_t *>(prow + blk * 16 + lb * 4) = w;
     if (lb == 0) srow[blk] = sh;
   } else if (LAYOUT == KVQ_Q8_0) {
     const __half sh = f16_sat(__fdiv_rn(amax, 128.0f));
     const float s = __half2float(sh);
-    uint32_t w0 = 0, w1 = 0;                   // byte i = value i (two's complement)
+    uint32_t q[8], w0 = 0, w1 = 0;             // byte i = value i (two's complement)
+    round_codes<-128, 127>(v, s, q);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      w0 |= ((uint32_t)sym_code(v[i], s, -128, 127) & 0xFFu) << (8 * i);
-      w1 |= ((uint32_t)sym_code(v[4 + i], s, -128, 127) & 0xFFu) << (8 * i);
+      w0 |= (q[i] & 0xFFu) << (8 * i);
+      w1 |= (q[4 + i] & 0xFFu) << (8 * i);
     }
     if (!valid) return;
     *reinterpret_cast<uint2 *>(prow + blk * 32 + lb * 8) = make_uint2(w0, w1);
@@ -95,12 +118,12 @@ __device__ __forceinline__ void quant_block(const CacheView &c, int kv, long lon
   } else {  // Q6_0
     const __half sh = f16_sat(__fdiv_rn(amax, 32.0f));
     const float s = __half2float(sh);
-    uint32_t lo = 0, hi = 0;
+    uint32_t q[8], lo = 0, hi = 0;
+    round_codes<-32, 31>(v, s, q);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const uint32_t u = (uint32_t)sym_code(v[i], s, -32, 31) & 0x3Fu;
-      lo |= (u & 0xFu) << (4 * i);
-      hi |= ((u >> 4) & 0x3u) << (2 * i);      // values 4k..4k+3 -> byte k, bits 0,2,4,6
+      lo |= (q[i] & 0xFu) << (4 * i);
+      hi |= ((q[i] >> 4) & 0x3u) << (2 * i);   // values 4k..4k+3 -> byte k, bits 0,2,4,6
     }
     if (!valid) return;
     uint8_t *bp = prow + blk * 24;
@@ -128,10 +151,10 @@ __device__ __forceinline__ void quant_had(const CacheView &c, int kv, long long 
   for (int m = 16; m; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
   constexpr int QMAX = BITS == 4 ? 7 : 1;
   const float s = __fdiv_rn(amax, (float)QMAX);
-  uint32_t w = 0;                                           // field i of the lane at bits BITS*i
+  uint32_t q[V], w = 0;                                     // field i of the lane at bits BITS*i
+  round_codes<-QMAX, QMAX>(x, s, q);
 #pragma unroll
-  for (int i = 0; i < V; ++i)
-    w |= ((uint32_t)sym_code(x[i], s, -QMAX, QMAX) & ((1u << BITS) - 1u)) << (BITS * i);
+  for (int i = 0; i < V; ++i) w |= (q[i] & ((1u << BITS) - 1u)) << (BITS * i);
   uint8_t *prow = (kv ? c.payload[1] : c.payload[0]) + (size_t)crow * row_bytes;
   if (V * BITS == 8) {
     prow[lane] = (uint8_t)w;
