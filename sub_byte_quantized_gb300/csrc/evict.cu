@@ -25,11 +25,10 @@ namespace {
 namespace cg = cooperative_groups;
 
 // ------------------------------------------------------------------------------------ selection
-constexpr int kSelThreads = 1024;
-constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kSelFixed = (3 * kBins + 2 * kSelWarps + 8) * 4;      // histograms, per-warp counts, results
-constexpr int kSelMaxKeys = (227 * 1024 - kSelFixed) / 4 / 4 * 4;   // keys one CTA can hold
+template <int THREADS>
+__host__ __device__ constexpr int select_fixed() { return (3 * kBins + 2 * (THREADS / 32) + 4) * 4; }   // histograms, per-warp counts, results
+constexpr int kSelMaxKeys = (227 * 1024 - select_fixed<1024>()) / 4 / 128 * 128;   // keys one CTA can hold
 
 // Keys compare like the scores: NaN counts as -infinity, -0 as +0.
 __device__ __forceinline__ uint32_t score_key(float x) {
@@ -39,13 +38,14 @@ __device__ __forceinline__ uint32_t score_key(float x) {
 }
 
 // RESIDENT: the slice's keys fit shared memory (else every pass reads the scores again).
-template <bool RESIDENT>
-__global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs a) {
+template <int THREADS, bool RESIDENT>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_select_kernel(SelectArgs a) {
+  constexpr int WARPS = THREADS / 32, OWN = kBins / THREADS;   // bins per thread, neighbouring
   extern __shared__ __align__(16) uint32_t sm[];
   uint32_t *hist = sm;                                   // [3][kBins]
-  uint32_t *wcount = sm + 3 * kBins;                     // [2][kSelWarps]: greater, equal
-  uint32_t *res = wcount + 2 * kSelWarps;                // digit, remaining, slice's greater and equal
-  uint32_t *keys = res + 8;
+  uint32_t *wcount = sm + 3 * kBins;                     // [2][WARPS]
+  uint32_t *res = wcount + 2 * WARPS;                    // digit, rank inside it
+  uint32_t *keys = res + 4;
   cg::cluster_group cl = cg::this_cluster();
   const int rank = (int)cl.block_rank(), ranks = (int)cl.num_blocks();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -54,11 +54,11 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
   int32_t *keep = a.keep + (size_t)bh * a.n_keep;
   if (a.new_lens && bh % a.H == 0 && rank == 0 && tid == 0) a.new_lens[b] = min(L, a.n_keep);
   if (L <= a.n_keep) {                                   // everything stays (the whole cluster takes this branch)
-    for (int i = rank * kSelThreads + tid; i < a.n_keep; i += ranks * kSelThreads) keep[i] = i < L ? i : -1;
+    for (int i = rank * THREADS + tid; i < a.n_keep; i += ranks * THREADS) keep[i] = i < L ? i : -1;
     return;
   }
   const int lo = a.n_sink, hi = L - a.n_recent;          // the tokens that compete; lo < hi since L > n_keep
-  for (int i = rank * kSelThreads + tid; i < a.n_sink + a.n_recent; i += ranks * kSelThreads) {
+  for (int i = rank * THREADS + tid; i < a.n_sink + a.n_recent; i += ranks * THREADS) {
     if (i < a.n_sink) keep[i] = i;
     else keep[a.n_keep - a.n_recent + (i - a.n_sink)] = hi + (i - a.n_sink);
   }
@@ -69,44 +69,71 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
   const int n = min(per, hi - s0);
   const float *score = a.scores + (size_t)bh * a.stride + s0;
   auto key_at = [&](int i) { return RESIDENT ? keys[i] : score_key(__ldg(score + i)); };
-
-  for (int i = tid; i < 3 * kBins; i += kSelThreads) hist[i] = 0;
+  if constexpr (RESIDENT) {
+#pragma unroll 8
+    for (int i = tid; i < n; i += THREADS) keys[i] = score_key(__ldg(score + i));
+  }
+  for (int i = tid; i < 3 * kBins; i += THREADS) hist[i] = 0;
   __syncthreads();
   uint32_t prefix = 0, mask = 0, want = (uint32_t)k;      // T's digits so far, and the rank inside them
+  uint32_t gt = 0, eq = 0;                               // keys over / equal to T in the slices before this one
 #pragma unroll
   for (int d = 0; d < 3; ++d) {
     const int shift = d == 0 ? 21 : (d == 1 ? 10 : 0);
     const uint32_t width = d == 2 ? 1024u : 2048u;
     uint32_t *h = hist + d * kBins;
-    for (int i0 = warp * 32; i0 < n; i0 += kSelThreads) {   // whole warps: the votes below need all lanes
-      const int i = i0 + lane;
-      uint32_t key = 0;
-      bool in = i < n;
-      if (in) {
-        key = d == 0 || !RESIDENT ? score_key(__ldg(score + i)) : keys[i];
-        if (RESIDENT && d == 0) keys[i] = key;
-        in = (key & mask) == prefix;
+    for (int i0 = warp * 128; i0 < n; i0 += 4 * THREADS) {  // whole warps: the votes below need all lanes
+      const int i = i0 + 4 * lane;                          // four keys per lane
+      uint32_t key[4];
+      if constexpr (RESIDENT) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(keys + i);   // (the keys' space is a multiple of 128)
+        key[0] = v.x; key[1] = v.y; key[2] = v.z; key[3] = v.w;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) key[j] = i + j < n ? key_at(i + j) : 0;
       }
-      const uint32_t digit = (key >> shift) & (width - 1);
-      // long runs of one score (zeros) would serialise on one counter: count such a warp at once
-      const unsigned who = __ballot_sync(0xffffffffu, in);
-      if (who == 0) continue;
-      const uint32_t first = __shfl_sync(0xffffffffu, digit, __ffs(who) - 1);
-      if (__all_sync(0xffffffffu, !in || digit == first)) {
-        if (lane == 0) atomicAdd(h + first, (uint32_t)__popc(who));
-      } else if (in) {
-        atomicAdd(h + digit, 1u);
+      bool in[4], any = false;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        in[j] = i + j < n && (key[j] & mask) == prefix;
+        any |= in[j];
+      }
+      if (!__any_sync(0xffffffffu, any)) continue;
+      // long runs of one score (zeros) would serialise on one counter: count such a group at once
+      const uint32_t first = __shfl_sync(0xffffffffu, (key[0] >> shift) & (width - 1), 0);
+      bool same = true;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        key[j] = (key[j] >> shift) & (width - 1);
+        same &= in[j] && key[j] == first;
+      }
+      if (__all_sync(0xffffffffu, same)) {
+        if (lane == 0) atomicAdd(h + first, 128u);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (in[j]) atomicAdd(h + key[j], 1u);
       }
     }
     cl.sync();                                           // every slice is counted
-    // thread t owns bins 2t and 2t + 1; counts above them by a suffix scan over warps
-    uint32_t c0 = 0, c1 = 0;
+    // thread t owns bins OWN t .. OWN t + OWN - 1; the counts above them by a suffix scan over warps
+    uint32_t c[OWN] = {}, before[OWN] = {};              // all slices; the slices before this one
     for (int r = 0; r < ranks; ++r) {
-      const uint2 v = *reinterpret_cast<const uint2 *>(cl.map_shared_rank(h, r) + 2 * tid);
-      c0 += v.x;
-      c1 += v.y;
+      const uint32_t *o = cl.map_shared_rank(h, r) + OWN * tid;
+#pragma unroll
+      for (int j = 0; j < OWN; j += 2) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(o + j);
+        c[j] += v.x;
+        c[j + 1] += v.y;
+        before[j] += r < rank ? v.x : 0;
+        before[j + 1] += r < rank ? v.y : 0;
+      }
     }
-    uint32_t suf = c0 + c1;
+    if (d == 2) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");   // the last remote reads
+    uint32_t own = 0;
+#pragma unroll
+    for (int j = 0; j < OWN; ++j) own += c[j];
+    uint32_t suf = own;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
       const uint32_t o = __shfl_down_sync(0xffffffffu, suf, m);
@@ -114,26 +141,50 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
     }
     if (lane == 0) wcount[warp] = suf;
     __syncthreads();
-    uint32_t above = 0;                                  // in the warps of higher bins
-    {
-      uint32_t w = lane > warp ? wcount[lane] : 0;
+    uint32_t above = lane > warp && lane < WARPS ? wcount[lane] : 0;   // in the warps of higher bins
 #pragma unroll
-      for (int m = 16; m; m >>= 1) w += __shfl_xor_sync(0xffffffffu, w, m);
-      above = w;
+    for (int m = 16; m; m >>= 1) above += __shfl_xor_sync(0xffffffffu, above, m);
+    above += suf - own;
+#pragma unroll
+    for (int j = OWN - 1; j >= 0; --j) {                 // above = keys in the bins over bin j
+      if (above < want && want <= above + c[j]) {
+        res[0] = OWN * tid + j;
+        res[1] = want - above;
+      }
+      above += c[j];
     }
-    const uint32_t above1 = above + suf - c0 - c1, above0 = above1 + c1;   // keys in bins over 2t + 1 / over 2t
-    if (above1 < want && want <= above1 + c1) { res[0] = 2 * tid + 1; res[1] = want - above1; }
-    if (above0 < want && want <= above0 + c0) { res[0] = 2 * tid; res[1] = want - above0; }
     __syncthreads();
-    prefix |= res[0] << shift;
-    mask |= (width - 1) << shift;
+    const uint32_t digit = res[0];
     want = res[1];
+    prefix |= digit << shift;
+    mask |= (width - 1) << shift;
+#pragma unroll
+    for (int j = 0; j < OWN; ++j) {
+      const uint32_t bin = OWN * tid + j;
+      if (bin > digit) gt += before[j];
+      if (d == 2 && bin == digit) eq += before[j];
+    }
     __syncthreads();                                     // res and wcount are written again
   }
-  // `want` of the keys equal to T stay. Count this slice's greater and equal keys by warp sub-slice.
-  const int sub = ((n + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
+  // block sums of gt and eq (each key counted by one thread)
+#pragma unroll
+  for (int m = 16; m; m >>= 1) {
+    gt += __shfl_xor_sync(0xffffffffu, gt, m);
+    eq += __shfl_xor_sync(0xffffffffu, eq, m);
+  }
+  if (lane == 0) {
+    wcount[warp] = gt;
+    wcount[WARPS + warp] = eq;
+  }
+  __syncthreads();
+  gt = lane < WARPS ? wcount[lane] : 0;
+  eq = lane < WARPS ? wcount[WARPS + lane] : 0;
+  __syncthreads();
+  // `want` of the keys equal to T stay. This slice's greater and equal keys by warp sub-slice.
+  const int sub = ((n + WARPS - 1) / WARPS + 31) / 32 * 32;
   const int w0 = min(n, warp * sub), w1 = min(n, w0 + sub);
   uint32_t ng = 0, ne = 0;
+#pragma unroll 4
   for (int i = w0 + lane; i < w1; i += 32) {
     const uint32_t key = key_at(i);
     ng += key > prefix;
@@ -146,27 +197,15 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
   }
   if (lane == 0) {
     wcount[warp] = ng;
-    wcount[kSelWarps + warp] = ne;
+    wcount[WARPS + warp] = ne;
   }
   __syncthreads();
-  uint32_t gt = lane < warp ? wcount[lane] : 0, eq = lane < warp ? wcount[kSelWarps + lane] : 0;
-  uint32_t gt_all = wcount[lane], eq_all = wcount[kSelWarps + lane];
+  gt += lane < warp ? wcount[lane] : 0;
+  eq += lane < warp ? wcount[WARPS + lane] : 0;
 #pragma unroll
   for (int m = 16; m; m >>= 1) {
     gt += __shfl_xor_sync(0xffffffffu, gt, m);
     eq += __shfl_xor_sync(0xffffffffu, eq, m);
-    gt_all += __shfl_xor_sync(0xffffffffu, gt_all, m);
-    eq_all += __shfl_xor_sync(0xffffffffu, eq_all, m);
-  }
-  if (tid == 0) {
-    res[2] = gt_all;
-    res[3] = eq_all;
-  }
-  cl.sync();
-  for (int r = 0; r < rank; ++r) {
-    const uint32_t *o = cl.map_shared_rank(res, r);
-    gt += o[2];
-    eq += o[3];
   }
   for (int i0 = w0; i0 < w1; i0 += 32) {
     const int i = i0 + lane;
@@ -180,91 +219,136 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
     gt += __popc(mg);
     eq += __popc(me);
   }
-  cl.sync();                                             // no CTA leaves while another reads its counts
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");   // no CTA leaves while another reads its counts
 }
 
 // ------------------------------------------------------------------------------------ compaction
 constexpr int kMoveThreads = 512;
 constexpr int kMoveUnits = 4;                            // units in flight per thread and round
 
-template <class U>
-__device__ __forceinline__ U load_unit(const uint8_t *p) { return __ldcg(reinterpret_cast<const U *>(p)); }
+// The rows of one plane (or of the scores) of one (batch, kv head), a column of each for this thread.
+template <bool PAGED>
+struct PlaneRows {
+  uint8_t *base;
+  int row_bytes;
+  const CacheView *c;
+  int b, kvh;
+  __device__ __forceinline__ uint8_t *at(int t) const {
+    if constexpr (PAGED) return base + (unsigned long long)cache_row_paged(*c, b, kvh, t) * (unsigned)row_bytes;
+    else return base + (unsigned long long)(unsigned)t * (unsigned)row_bytes;
+  }
+};
+template <bool PAGED>
+__device__ __forceinline__ PlaneRows<PAGED> rows_of(const CacheView &c, uint8_t *plane, int row_bytes, long long scores_stride,
+                                                    int b, int kvh, int col) {
+  PlaneRows<PAGED> r = {plane + col, row_bytes, &c, b, kvh};
+  if constexpr (!PAGED) {
+    const size_t head = (size_t)b * c.H + kvh;
+    r.base += head * (size_t)(scores_stride >= 0 ? scores_stride : c.cap) * row_bytes;
+  }
+  return r;
+}
 
-// One plane of one (batch, kv head): target rows [0, n_rows) in rounds of the whole cluster (IN_PLACE)
-// or of the CTAs of one grid row. U: the unit moved at once; a row is `upr` units.
-template <class U, bool IN_PLACE>
+// Source token of target row `row`: -1 = leave the row as it is, -2 = zero (scores behind the kept ones).
+template <bool IN_PLACE>
+__device__ __forceinline__ int source_of(const int32_t *keep, int row, int new_len, int n_rows, int L) {
+  if (row >= new_len) return row < n_rows ? -2 : -1;
+  const int t = __ldg(keep + row);
+  return (unsigned)t >= (unsigned)L || (IN_PLACE && t == row) ? -1 : t;
+}
+
+// Target rows [0, n_rows). A thread keeps its column of the row (row_bytes / sizeof(U) threads hold a row)
+// and steps through rows; U: the unit moved at once. Into another cache every CTA moves its own rounds. In
+// place the ranks' CTAs are one cluster whose rounds are ordered by its barrier; the sources of the round
+// after next are looked up, and the rows of the next one read, while this one waits.
+template <class U, bool IN_PLACE, bool PAGED>
 __device__ __forceinline__ void move_rows(const CompactArgs &a, const MovePart &p, int b, int kvh, int new_len, int n_rows,
-                                          int L, int rank, int ranks) {
-  const int upr = p.row_bytes / (int)sizeof(U);
+                                          int L, int rank) {
+  const int upr = p.row_bytes / (int)sizeof(U), rpp = kMoveThreads / upr;   // threads per row, rows per pass
+  const int own = (int)threadIdx.x / upr, col = ((int)threadIdx.x - own * upr) * (int)sizeof(U);
   const int32_t *keep = a.keep + ((size_t)b * a.src.H + kvh) * a.n_keep;
-  const size_t head = (size_t)b * a.src.H + kvh;
-  const unsigned total = (unsigned)n_rows * upr;         // at most 2^31 (the host checks)
-  const unsigned round = (unsigned)ranks * kMoveThreads * kMoveUnits;
-  auto src_row = [&](int t) -> const uint8_t * {
-    const size_t r = p.is_scores ? head * (size_t)a.scores_stride + t : cache_row(a.src, b, kvh, t);
-    return p.src + r * p.row_bytes;
-  };
-  auto dst_row = [&](int t) -> uint8_t * {
-    const size_t r = p.is_scores ? head * (size_t)a.out_stride + t : cache_row(a.dst, b, kvh, t);
-    return p.dst + r * p.row_bytes;
-  };
-  // unit u of the round that starts at `base`
-  auto unit_of = [&](unsigned base, int u) { return base + ((unsigned)u * ranks + rank) * kMoveThreads + threadIdx.x; };
-  // the source token of a unit: -1 = leave the target as it is, -2 = zero (scores behind the kept ones)
-  auto source = [&](unsigned id) -> int {
-    if (id >= total) return -1;
-    const int row = (int)(id / upr);
-    if (row >= new_len) return -2;
-    const int t = __ldg(keep + row);
-    if (t < 0 || t >= L || (IN_PLACE && t == row)) return -1;
-    return t;
-  };
-  U cur[kMoveUnits], nxt[kMoveUnits];
-  int st[kMoveUnits], sn[kMoveUnits];
-  auto gather = [&](unsigned base, int (&s)[kMoveUnits], U (&v)[kMoveUnits]) {
+  const auto src = rows_of<PAGED>(a.src, const_cast<uint8_t *>(p.src), p.row_bytes, p.is_scores ? a.scores_stride : -1, b, kvh, col);
+  const auto dst = rows_of<PAGED>(a.dst, p.dst, p.row_bytes, p.is_scores ? a.out_stride : -1, b, kvh, col);
+  const int step = a.ranks * rpp, round = step * kMoveUnits;   // rows between a thread's units, rows per round
+  const int row0 = own < rpp ? rank * rpp + own : n_rows;      // (threads beyond the last whole row idle)
+  if constexpr (!IN_PLACE) {
+    for (int base = row0; base < n_rows; base += round) {
+      int st[kMoveUnits];
+      U v[kMoveUnits];
 #pragma unroll
-    for (int u = 0; u < kMoveUnits; ++u) s[u] = source(unit_of(base, u));
+      for (int u = 0; u < kMoveUnits; ++u) st[u] = source_of<false>(keep, base + u * step, new_len, n_rows, L);
+#pragma unroll
+      for (int u = 0; u < kMoveUnits; ++u) {
+        v[u] = U{};
+        if (st[u] >= 0) v[u] = __ldcg(reinterpret_cast<const U *>(src.at(st[u])));
+      }
+#pragma unroll
+      for (int u = 0; u < kMoveUnits; ++u)
+        if (st[u] != -1) *reinterpret_cast<U *>(dst.at(base + u * step)) = v[u];
+    }
+  } else {
+    U cur[kMoveUnits], nxt[kMoveUnits];
+    int st[kMoveUnits], sn[kMoveUnits];                  // sources of this round and the next
 #pragma unroll
     for (int u = 0; u < kMoveUnits; ++u) {
-      v[u] = U{};
-      if (s[u] >= 0) v[u] = load_unit<U>(src_row(s[u]) + (size_t)(unit_of(base, u) % upr) * sizeof(U));
+      st[u] = source_of<true>(keep, row0 + u * step, new_len, n_rows, L);
+      sn[u] = source_of<true>(keep, row0 + round + u * step, new_len, n_rows, L);
     }
-  };
-  gather(0, st, cur);
-  for (unsigned base = 0; base < total; base += round) {
-    if constexpr (IN_PLACE) {
-      // this round's values have arrived (the register reads below wait for the loads) before any CTA
-      // of the cluster writes over their rows
+#pragma unroll
+    for (int u = 0; u < kMoveUnits; ++u) {
+      cur[u] = U{};
+      if (st[u] >= 0) cur[u] = __ldcg(reinterpret_cast<const U *>(src.at(st[u])));
+    }
+    for (int base = 0; base < n_rows; base += round) {
+      // This round's values have arrived (the register reads below wait for the loads) before any CTA of the
+      // cluster writes over their rows. That is all the barrier orders: nothing written before it is read
+      // after it, so the arrive needs no release of this thread's earlier stores.
 #pragma unroll
       for (int u = 0; u < kMoveUnits; ++u) asm volatile("" ::"r"(reinterpret_cast<const uint32_t *>(&cur[u])[0]) : "memory");
-      asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    }
-    if (round < total - base) gather(base + round, sn, nxt);
-    if constexpr (IN_PLACE) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+      asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+      const bool more = n_rows - base > round;
+      if (more) {
 #pragma unroll
-    for (int u = 0; u < kMoveUnits; ++u) {
-      const unsigned id = unit_of(base, u);
-      if (st[u] != -1) *reinterpret_cast<U *>(dst_row((int)(id / upr)) + (size_t)(id % upr) * sizeof(U)) = cur[u];
-      cur[u] = nxt[u];
-      st[u] = sn[u];
+        for (int u = 0; u < kMoveUnits; ++u) {
+          nxt[u] = U{};
+          if (sn[u] >= 0) nxt[u] = __ldcg(reinterpret_cast<const U *>(src.at(sn[u])));
+        }
+      }
+      asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+#pragma unroll
+      for (int u = 0; u < kMoveUnits; ++u)
+        if (st[u] != -1) *reinterpret_cast<U *>(dst.at(row0 + base + u * step)) = cur[u];
+      if (more) {
+#pragma unroll
+        for (int u = 0; u < kMoveUnits; ++u) {
+          cur[u] = nxt[u];
+          st[u] = sn[u];
+          sn[u] = source_of<true>(keep, row0 + base + 2 * round + u * step, new_len, n_rows, L);
+        }
+      }
     }
   }
 }
 
-template <bool IN_PLACE>
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(CompactArgs a) {
-  const int bh = blockIdx.x / a.ranks, b = bh / a.src.H, kvh = bh - b * a.src.H;
+template <bool IN_PLACE, bool PAGED>
+__device__ __forceinline__ void move_part(const CompactArgs &a, const MovePart &p, int b, int kvh, int new_len, int n_rows, int L,
+                                          int rank) {
+  switch (p.unit) {
+    case 16: move_rows<uint4, IN_PLACE, PAGED>(a, p, b, kvh, new_len, n_rows, L, rank); break;
+    case 8: move_rows<uint2, IN_PLACE, PAGED>(a, p, b, kvh, new_len, n_rows, L, rank); break;
+    default: move_rows<uint32_t, IN_PLACE, PAGED>(a, p, b, kvh, new_len, n_rows, L, rank); break;
+  }
+}
+
+template <bool IN_PLACE, bool PAGED>
+__global__ void __launch_bounds__(kMoveThreads, 2) evict_move_kernel(CompactArgs a) {
+  const int bh = blockIdx.x / a.ranks, b = bh / a.src.H, kvh = bh - b * a.src.H, rank = blockIdx.x - bh * a.ranks;
   const MovePart &p = a.part[blockIdx.y];
   const int L = a.seq_lens ? min(max(__ldg(a.seq_lens + b), 0), a.kv_len) : a.kv_len;
   const int new_len = min(L, a.n_keep);
-  // the scores behind the kept ones become zero, ready for the tokens appended next
-  const int n_rows = p.is_scores ? (int)min((long long)a.kv_len, a.out_stride) : new_len;
-  const int ranks = a.ranks, rank = blockIdx.x - bh * ranks;   // IN_PLACE: these CTAs are one cluster
-  switch (p.unit) {
-    case 16: move_rows<uint4, IN_PLACE>(a, p, b, kvh, new_len, n_rows, L, rank, ranks); break;
-    case 8: move_rows<uint2, IN_PLACE>(a, p, b, kvh, new_len, n_rows, L, rank, ranks); break;
-    default: move_rows<uint32_t, IN_PLACE>(a, p, b, kvh, new_len, n_rows, L, rank, ranks); break;
-  }
+  // the scores behind the kept ones become zero, ready for the tokens appended next; they are not paged
+  if (p.is_scores) move_rows<uint32_t, IN_PLACE, false>(a, p, b, kvh, new_len, (int)min((long long)a.kv_len, a.out_stride), L, rank);
+  else move_part<IN_PLACE, PAGED>(a, p, b, kvh, new_len, new_len, L, rank);
 }
 
 // The exact window: slot of token t is t mod R, and every kept window token moves back by the number of
@@ -308,15 +392,15 @@ int device_sms() {
   return sms;
 }
 
-template <bool RESIDENT>
-cudaError_t launch_select(const SelectArgs &a, int ranks, int smem, cudaStream_t st) {
+template <int THREADS, bool RESIDENT>
+cudaError_t launch_select(const SelectArgs &a, int ranks, int keys, cudaStream_t st) {
   static std::atomic<bool> done[kMaxDevices];
-  cudaError_t e = set_smem_once(done, evict_select_kernel<RESIDENT>, 227 * 1024);
+  cudaError_t e = set_smem_once(done, evict_select_kernel<THREADS, RESIDENT>, 227 * 1024);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ranks * a.B * a.H);
-  cfg.blockDim = dim3(kSelThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = select_fixed<THREADS>() + 4 * keys;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -324,7 +408,7 @@ cudaError_t launch_select(const SelectArgs &a, int ranks, int smem, cudaStream_t
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, evict_select_kernel<RESIDENT>, a);
+  return cudaLaunchKernelEx(&cfg, evict_select_kernel<THREADS, RESIDENT>, a);
 }
 
 }  // namespace
@@ -333,9 +417,10 @@ cudaError_t launch_evict_select(const SelectArgs &a, cudaStream_t st) {
   // CTAs per (batch, kv head): one per 8192 tokens, at most the portable cluster size of 8
   int ranks = 1;
   while (ranks < 8 && (long long)ranks * 8192 < a.kv_len) ranks *= 2;
-  const int per = (a.kv_len + ranks - 1) / ranks + 32;
-  if (per <= kSelMaxKeys) return launch_select<true>(a, ranks, kSelFixed + 4 * per, st);
-  return launch_select<false>(a, ranks, kSelFixed, st);
+  const int keys = ((a.kv_len + ranks - 1) / ranks + 31 + 127) / 128 * 128;
+  if (keys > kSelMaxKeys) return launch_select<1024, false>(a, ranks, 0, st);
+  // rows of one CTA: half the threads, two CTAs per SM
+  return ranks == 1 ? launch_select<512, true>(a, ranks, keys, st) : launch_select<1024, true>(a, ranks, keys, st);
 }
 
 cudaError_t launch_evict_compact(CompactArgs a, bool in_place, cudaStream_t st) {
@@ -344,10 +429,11 @@ cudaError_t launch_evict_compact(CompactArgs a, bool in_place, cudaStream_t st) 
   cfg.blockDim = dim3(kMoveThreads);
   cfg.stream = st;
   cudaError_t e;
-  // CTAs per plane of one (batch, kv head): about two per SM over the two payload planes; in place one
-  // cluster (at most the portable 8)
-  const int want = max(1, device_sms() / heads);
+  const int most = a.n_keep < a.kv_len ? a.n_keep : a.kv_len;
   if (in_place) {
+    // one cluster per plane of a (batch, kv head), at most the portable 8 CTAs: enough for two waves of two
+    // CTAs per SM over the two payload planes
+    const int want = (2 * device_sms() + heads - 1) / heads;
     a.ranks = 1;
     while (a.ranks < 8 && a.ranks < want) a.ranks *= 2;
     cfg.gridDim = dim3((unsigned)a.ranks * heads, a.n_parts);
@@ -357,11 +443,15 @@ cudaError_t launch_evict_compact(CompactArgs a, bool in_place, cudaStream_t st) 
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, evict_move_kernel<true>, a);
+    e = a.src.page_shift >= 0 ? cudaLaunchKernelEx(&cfg, evict_move_kernel<true, true>, a)
+                              : cudaLaunchKernelEx(&cfg, evict_move_kernel<true, false>, a);
   } else {
-    a.ranks = want;
-    cfg.gridDim = dim3((unsigned)want * heads, a.n_parts);
-    e = cudaLaunchKernelEx(&cfg, evict_move_kernel<false>, a);
+    // nothing waits: one round per CTA for the widest rows, the scheduler overlaps them
+    const int upr = (a.src.row_bytes > a.src.v_row_bytes ? a.src.row_bytes : a.src.v_row_bytes) / 16;
+    const int round = kMoveThreads / upr * kMoveUnits;
+    a.ranks = min((most + round - 1) / round, max(1, (1 << 16) / heads));
+    cfg.gridDim = dim3((unsigned)a.ranks * heads, a.n_parts);
+    e = cudaLaunchKernelEx(&cfg, evict_move_kernel<false, false>, a);
   }
   if (e != cudaSuccess || a.src.n_recent == 0) return e;
   evict_ring_kernel<<<dim3(heads, 2, a.src.D / 32), kRingThreads, 0, st>>>(a, in_place ? 1 : 0);

@@ -12,9 +12,9 @@
 // interleaved: dims (2 i, 2 i + 1); dims from rot_dim on stay as they are.
 //   y_a = x_a c - x_b s,   y_b = x_b c + x_a s
 // Each product and each sum is rounded to float32 by itself (this file is compiled with -fmad=false),
-// so the packed bytes follow from the table's entries exactly. Block layouts: one thread holds eight
-// dims of a row; its partners' eight (half layout) are a second 16-byte load of the same row, which the
-// L1 answers. Hadamard layouts: one warp per row, as in the plain append.
+// so the packed bytes follow from the table's entries exactly. A thread holds 16 dims of a row (block
+// layouts) or 8 (Hadamard); its partners' dims (half layout) are a second 16-byte load of the same row,
+// which the L1 answers.
 //
 // Bound by memory: 8192 tokens, 16 q and 8 kv heads of 256 dims (f16) move 148 MB.
 #include "store_quant.cuh"
@@ -84,7 +84,7 @@ __device__ __forceinline__ unsigned divide(unsigned n, const FastDiv &d) { retur
 // Which row a thread or warp works on: K rows first, then V, then q.
 struct RopeRow {
   int what;                 // 0 = K, 1 = V, 2 = q
-  int b, head, j, pos;      // batch, head (kv or query), row of the append, cache slot
+  int b, head, j, pos, at;  // batch, head (kv or query), row of the append, cache slot, table row
   long long crow;           // plane row (K and V)
   bool live;                // q, or a slot inside the cache
 };
@@ -108,55 +108,44 @@ __device__ __forceinline__ RopeRow rope_row(const CacheView &c, const RopeStore 
   const long long slot = (g.slots ? (long long)__ldg(g.slots + w.b) : (long long)g.pos0) + w.j;
   const bool inside = slot >= 0 && slot < c.cap;
   w.pos = (int)min(max(slot, (long long)INT_MIN), (long long)INT_MAX);   // also the default rotary position
+  w.at = min(max(g.positions ? __ldg(g.positions + (size_t)w.b * g.n_new + w.j) : w.pos, 0), g.n_pos - 1);
   w.live = w.what == 2 || inside;
   w.crow = w.what != 2 && inside ? (long long)cache_row(c, w.b, w.head, w.pos) : 0;
   return w;
 }
 
-// N (4 or 8) consecutive dims from d0 of one row, rotated when the row is K or q and d0 < rot_dim.
-template <int N>
-__device__ __forceinline__ void load_n(const void *base, int dtype, size_t e, float (&v)[N]) {
-  if constexpr (N == 8) load8_f32(base, dtype, e, v);
-  else load4_f32(base, dtype, e, v);
-}
-template <int N>
-__device__ __forceinline__ void rope_load(const RopeStore &g, const RopeRow &w, int d0, float (&y)[N]) {
-  const RowsIn &in = g.in[w.what];
-  const size_t e = (size_t)w.b * in.batch + (size_t)w.head * in.head + (size_t)w.j * in.token + d0;
-  float x[N];
-  load_n<N>(in.data, g.dtype, e, x);
+// Eight consecutive dims from d0 of one row, rotated when the row is K or q and d0 < rot_dim (a multiple of
+// 16: all eight are on the same side of rot_dim and of its half).
+__device__ __forceinline__ void rope_load(const RopeStore &g, const RopeRow &w, size_t row, int d0, float *y) {
+  const void *in = g.in[w.what].data;
+  float x[8];
+  load8_f32(in, g.dtype, row + d0, x);
   if (w.what == 1 || d0 >= g.rot) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) y[i] = x[i];
+    for (int i = 0; i < 8; ++i) y[i] = x[i];
     return;
   }
-  const int at = g.positions ? __ldg(g.positions + (size_t)w.b * g.n_new + w.j) : w.pos;
-  const float *row = g.table + (size_t)min(max(at, 0), g.n_pos - 1) * g.rot;
+  const float *t = g.table + (size_t)w.at * g.rot;
   const int half = g.rot >> 1;
   if (g.interleaved) {
-    float c[N / 2], s[N / 2];
-    if constexpr (N == 8) {
-      *reinterpret_cast<float4 *>(c) = __ldg(reinterpret_cast<const float4 *>(row + (d0 >> 1)));
-      *reinterpret_cast<float4 *>(s) = __ldg(reinterpret_cast<const float4 *>(row + half + (d0 >> 1)));
-    } else {
-      *reinterpret_cast<float2 *>(c) = __ldg(reinterpret_cast<const float2 *>(row + (d0 >> 1)));
-      *reinterpret_cast<float2 *>(s) = __ldg(reinterpret_cast<const float2 *>(row + half + (d0 >> 1)));
-    }
+    float c[4], s[4];
+    load4_f32(t, KVQ_F32, d0 >> 1, c);
+    load4_f32(t, KVQ_F32, half + (d0 >> 1), s);
 #pragma unroll
-    for (int i = 0; i < N / 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       y[2 * i] = __fsub_rn(__fmul_rn(x[2 * i], c[i]), __fmul_rn(x[2 * i + 1], s[i]));
       y[2 * i + 1] = __fadd_rn(__fmul_rn(x[2 * i + 1], c[i]), __fmul_rn(x[2 * i], s[i]));
     }
     return;
   }
-  const bool second = d0 >= half;                        // half is a multiple of 8: all N dims are on one side
+  const bool second = d0 >= half;
   const int i0 = second ? d0 - half : d0;
-  float p[N], c[N], s[N];
-  load_n<N>(in.data, g.dtype, second ? e - half : e + half, p);
-  load_n<N>(row, KVQ_F32, i0, c);
-  load_n<N>(row, KVQ_F32, half + i0, s);
+  float p[8], c[8], s[8];
+  load8_f32(in, g.dtype, row + (second ? i0 : d0 + half), p);
+  load8_f32(t, KVQ_F32, i0, c);
+  load8_f32(t, KVQ_F32, half + i0, s);
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
+  for (int i = 0; i < 8; ++i) {
     const float a = __fmul_rn(x[i], c[i]), b = __fmul_rn(p[i], s[i]);
     y[i] = second ? __fadd_rn(a, b) : __fsub_rn(a, b);
   }
@@ -171,77 +160,86 @@ __device__ __forceinline__ uint32_t pack2(int dtype, float lo, float hi) {
   return *reinterpret_cast<const uint32_t *>(&v);
 }
 // q rows are written [batch][n_q_heads][n_new][head_dim], rounded once to their type
-template <int N>
-__device__ __forceinline__ void write_q(const RopeStore &g, const RopeRow &w, int D, int d0, const float (&y)[N]) {
+__device__ __forceinline__ void write_q(const RopeStore &g, const RopeRow &w, int D, int d0, const float *y) {
   const size_t e = (((size_t)w.b * g.Hq + w.head) * g.n_new + w.j) * D + d0;
   if (g.dtype == KVQ_F32) {
     float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(g.q_out) + e);
     o[0] = make_float4(y[0], y[1], y[2], y[3]);
-    if constexpr (N == 8) o[1] = make_float4(y[4], y[5], y[6], y[7]);
-    return;
+    o[1] = make_float4(y[4], y[5], y[6], y[7]);
+  } else {
+    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(g.q_out) + e) =
+        make_uint4(pack2(g.dtype, y[0], y[1]), pack2(g.dtype, y[2], y[3]), pack2(g.dtype, y[4], y[5]), pack2(g.dtype, y[6], y[7]));
   }
-  uint16_t *o = static_cast<uint16_t *>(g.q_out) + e;
-  if constexpr (N == 8)
-    *reinterpret_cast<uint4 *>(o) = make_uint4(pack2(g.dtype, y[0], y[1]), pack2(g.dtype, y[2], y[3]),
-                                               pack2(g.dtype, y[4], y[5]), pack2(g.dtype, y[6], y[7]));
-  else
-    *reinterpret_cast<uint2 *>(o) = make_uint2(pack2(g.dtype, y[0], y[1]), pack2(g.dtype, y[2], y[3]));
 }
 
-// Neither kernel lets a dependent launch start early: the attention call that follows reads q_out, and
-// its query preparation does not wait for its predecessor.
+// Sixteen dims per thread (block layouts) or eight (Hadamard): rows per warp 4 or 2 at head_dim 128. Neither
+// kernel lets a dependent launch start early: the attention call that follows reads q_out, and its query
+// preparation does not wait for its predecessor.
 template <int LAYOUT>
 __global__ void __launch_bounds__(256) rope_store_block_kernel(CacheView c, RopeStore g) {
-  const int shift = c.D == 128 ? 4 : 5;                   // D / 8 threads per row
+  const int shift = c.D == 128 ? 3 : 4;                   // D / 16 threads per row
   const long long gt = (long long)blockIdx.x * blockDim.x + threadIdx.x;
   const long long r = gt >> shift;
   const int tr = (int)(gt & ((1 << shift) - 1));
-  // threads past the last row take part in the quad shuffles (full-warp masks) but load and store nothing
+  // threads past the last row take part in the shuffles (full-warp masks) but load and store nothing
   RopeRow w = {};
   bool valid = r < g.k_rows + g.v_rows + g.q_rows;
   if (valid) {
     w = rope_row(c, g, r);
     valid = w.live;
   }
-  float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (valid) rope_load<8>(g, w, 8 * tr, y);
-  if (valid && w.what == 2) write_q<8>(g, w, c.D, 8 * tr, y);
+  float y[16] = {};
+  if (valid) {
+    const RowsIn &in = g.in[w.what];
+    const size_t row = (size_t)w.b * in.batch + (size_t)w.head * in.head + (size_t)w.j * in.token;
+    rope_load(g, w, row, 16 * tr, y);
+    rope_load(g, w, row, 16 * tr + 8, y + 8);
+    if (w.what == 2) {
+      write_q(g, w, c.D, 16 * tr, y);
+      write_q(g, w, c.D, 16 * tr + 8, y + 8);
+    }
+  }
   if (__all_sync(0xffffffffu, !valid || w.what == 2)) return;   // a warp of q rows has nothing to quantise
-  quant_block<LAYOUT>(c, w.what == 1, w.crow, g.row_bytes, c.D / kBlock, tr >> 2, tr & 3, y, valid && w.what != 2);
+  quant_block<LAYOUT, 16>(c, w.what == 1, w.crow, g.row_bytes, c.D / kBlock, tr >> 1, tr & 1, y, valid && w.what != 2);
 }
 
-template <int V, int BITS>
+template <int LANES, int BITS>
 __global__ void __launch_bounds__(256) rope_store_had_kernel(CacheView c, RopeStore g) {
-  const int lane = threadIdx.x & 31;
-  const long long r = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  if (r >= g.k_rows + g.v_rows + g.q_rows) return;         // whole warp (one row)
-  const RopeRow w = rope_row(c, g, r);
-  if (!w.live) return;
-  float y[V];
-  rope_load<V>(g, w, V * lane, y);
-  if (w.what == 2) {
-    write_q<V>(g, w, 32 * V, V * lane, y);
-    return;
+  const long long gt = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  const long long r = gt / LANES;
+  const int lane = (int)(gt % LANES);
+  RopeRow w = {};
+  bool valid = r < g.k_rows + g.v_rows + g.q_rows;
+  if (valid) {
+    w = rope_row(c, g, r);
+    valid = w.live;
   }
-  quant_had<V, BITS>(c, w.what, w.crow, g.row_bytes, lane, y, c.n_recent > 0 && w.j >= g.n_new - c.n_recent,
-                     (long long)w.b * c.H + w.head, w.pos);
+  float y[8] = {};
+  if (valid) {
+    const RowsIn &in = g.in[w.what];
+    rope_load(g, w, (size_t)w.b * in.batch + (size_t)w.head * in.head + (size_t)w.j * in.token, 8 * lane, y);
+    if (w.what == 2) write_q(g, w, 8 * LANES, 8 * lane, y);
+  }
+  if (__all_sync(0xffffffffu, !valid || w.what == 2)) return;
+  quant_had<8, LANES, BITS>(c, w.what == 1, w.crow, g.row_bytes, lane, y, c.n_recent > 0 && w.j >= g.n_new - c.n_recent,
+                            (long long)w.b * c.H + w.head, w.pos, valid && w.what != 2);
 }
 
 cudaError_t launch_plane(const CacheView &c, int layout, const RopeStore &g, cudaStream_t st) {
   const long long rows = g.k_rows + g.v_rows + g.q_rows;
-  const unsigned blocks = (unsigned)((rows * (is_hadamard(layout) ? 32 : c.D / 8) + 255) / 256);
+  const unsigned blocks = (unsigned)((rows * (is_hadamard(layout) ? c.D / 8 : c.D / 16) + 255) / 256);
   switch (layout) {
     case KVQ_Q4_0: rope_store_block_kernel<KVQ_Q4_0><<<blocks, 256, 0, st>>>(c, g); break;
     case KVQ_Q6_0: rope_store_block_kernel<KVQ_Q6_0><<<blocks, 256, 0, st>>>(c, g); break;
     case KVQ_Q8_0: rope_store_block_kernel<KVQ_Q8_0><<<blocks, 256, 0, st>>>(c, g); break;
     case KVQ_ASYM4_G32: rope_store_block_kernel<KVQ_ASYM4_G32><<<blocks, 256, 0, st>>>(c, g); break;
     case KVQ_HAD_INT4:
-      if (c.D == 128) rope_store_had_kernel<4, 4><<<blocks, 256, 0, st>>>(c, g);
-      else rope_store_had_kernel<8, 4><<<blocks, 256, 0, st>>>(c, g);
+      if (c.D == 128) rope_store_had_kernel<16, 4><<<blocks, 256, 0, st>>>(c, g);
+      else rope_store_had_kernel<32, 4><<<blocks, 256, 0, st>>>(c, g);
       break;
     default:
-      if (c.D == 128) rope_store_had_kernel<4, 2><<<blocks, 256, 0, st>>>(c, g);
-      else rope_store_had_kernel<8, 2><<<blocks, 256, 0, st>>>(c, g);
+      if (c.D == 128) rope_store_had_kernel<16, 2><<<blocks, 256, 0, st>>>(c, g);
+      else rope_store_had_kernel<32, 2><<<blocks, 256, 0, st>>>(c, g);
       break;
   }
   return cudaGetLastError();

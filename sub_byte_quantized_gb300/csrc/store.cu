@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(256) store_block_kernel(CacheView c, const voi
 
   float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   if (valid) load8_f32(kv ? v_new : k_new, dtype, (size_t)in_row * g.D + (size_t)tr * 8, v);
-  quant_block<LAYOUT>(c, kv, crow, g.row_bytes, g.nb, blk, lb, v, valid);
+  quant_block<LAYOUT, 8>(c, kv, crow, g.row_bytes, g.nb, blk, lb, v, valid);
 }
 
 // Hadamard int4 (BITS 4: scale amax / 7, codes [-7, 7], two per byte) or int2 (BITS 2: scale
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(256) store_had_kernel(CacheView c, const void 
   }
   // Exact-f32 ring of the newest tokens: only the last min(n_new, n_recent) rows of this call,
   // so no two rows of one call write the same slot.
-  quant_had<V, BITS>(c, kv, crow, g.row_bytes, lane, x, c.n_recent > 0 && j >= g.n_new - c.n_recent, bh, pos);
+  quant_had<V, 32, BITS>(c, kv, crow, g.row_bytes, lane, x, c.n_recent > 0 && j >= g.n_new - c.n_recent, bh, pos, true);
 }
 
 }  // namespace

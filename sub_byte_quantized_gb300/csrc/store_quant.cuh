@@ -10,29 +10,20 @@ namespace kvq {
 
 constexpr float kF16Max = 65504.0f;
 
-__device__ __forceinline__ float quad_max(float v) {
-  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-}
-__device__ __forceinline__ float quad_min(float v) {
-  v = fminf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-  return fminf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-}
-
 __device__ __forceinline__ __half f16_sat(float x) {
   return __float2half_rn(fminf(fmaxf(x, -kF16Max), kF16Max));
 }
 
-// Codes clamp(rint(x / s), LO, HI) of N values (0 when s == 0), x / s the correctly rounded quotient: as
-// bit fields of an unsigned word each, two's complement (the caller masks them).
+// Codes clamp(rint(x / s), LO, HI) of N values (0 when s == 0), x / s the correctly rounded quotient, as
+// words whose low bits are the two's complement code (the caller masks them).
 //
-// The quotient is taken as r = x * fl(1 / s), off by less than 2^-22 of itself, i.e. by less than 7e-5 for
-// |x / s| <= 256 (beyond, both clamp alike). It rounds like the correct quotient unless a half-integer lies
-// between the two, and then r is within 1e-4 of one: those rare threads divide. Rounding is the addition of
-// 1.5 * 2^23 (nearest even), whose low mantissa bits are the code. A scale below 2^-100 divides throughout
-// (its reciprocal could overflow).
+// The quotient is taken as x * fl(1 / s), off by less than 2^-22 of itself, i.e. by less than 1e-4 for
+// |x / s| <= 300. It rounds like the correct quotient unless a half-integer lies between the two, and then
+// the product is within 2e-4 of one: those rare threads divide. Rounding is the addition of 1.5 * 2^23 in
+// one fma (nearest even), whose low mantissa bits are the code. `divide` sends a thread to the division at
+// once: where some |x / s| may pass 300, or fl(1 / s) may overflow.
 template <int LO, int HI, int N>
-__device__ __forceinline__ void round_codes(const float (&x)[N], float s, uint32_t (&code)[N]) {
+__device__ __forceinline__ void round_codes(const float (&x)[N], float s, bool divide, uint32_t (&code)[N]) {
   constexpr float kMagic = 12582912.0f;
   if (!(s > 0.0f)) {
 #pragma unroll
@@ -40,47 +31,67 @@ __device__ __forceinline__ void round_codes(const float (&x)[N], float s, uint32
     return;
   }
   const float inv = __frcp_rn(s);
-  bool divide = s < 0x1p-100f;
+  float off = 0.0f;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const float r = fminf(fmaxf(__fmul_rn(x[i], inv), -300.0f), 300.0f), m = __fadd_rn(r, kMagic);
-    divide |= fabsf(__fsub_rn(r, __fsub_rn(m, kMagic))) > 0.4999f;
+    const float m = __fmaf_rn(x[i], inv, kMagic), q = __fsub_rn(m, kMagic);
+    off = fmaxf(off, fabsf(__fmaf_rn(x[i], inv, -q)));
     code[i] = __float_as_uint(fminf(fmaxf(m, kMagic + LO), kMagic + HI));
   }
-  if (divide) {
+  if (divide || off > 0.4998f) {
 #pragma unroll
     for (int i = 0; i < N; ++i)
       code[i] = (uint32_t)(int)fminf(fmaxf(rintf(__fdiv_rn(x[i], s)), (float)LO), (float)HI);
   }
 }
+// N fields of BITS bits from codes, field i at BITS * i.
+template <int BITS, int N>
+__device__ __forceinline__ uint32_t pack_codes(const uint32_t *code) {
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) w |= (code[i] & ((1u << BITS) - 1u)) << (BITS * i);
+  return w;
+}
+// Maximum over aligned groups of 32 / N neighbouring lanes (the lanes of a 32-value block).
+template <int N>
+__device__ __forceinline__ float block_max(float v) {
+#pragma unroll
+  for (int m = 1; m < 32 / N; m <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, m));
+  return v;
+}
 
-// Eight values (dims 32 blk + 8 lb + 0..7) of a row, in a thread whose three neighbours in the aligned
-// group of four hold the rest of the block. LAYOUT: KVQ_Q4_0, KVQ_Q6_0, KVQ_Q8_0 or KVQ_ASYM4_G32.
+// N = 8 or 16 values (dims 32 blk + N lb + 0 ..) of a row, in a thread whose neighbours in the aligned
+// group of 32 / N hold the rest of the block. LAYOUT: KVQ_Q4_0, KVQ_Q6_0, KVQ_Q8_0 or KVQ_ASYM4_G32.
 // Every lane of the warp calls it (full-warp shuffles); one with valid == false stores nothing.
-template <int LAYOUT>
+template <int LAYOUT, int N>
 __device__ __forceinline__ void quant_block(const CacheView &c, int kv, long long crow, int row_bytes, int nb, int blk,
-                                            int lb, const float (&v)[8], bool valid) {
+                                            int lb, const float (&v)[N], bool valid) {
   uint8_t *prow = (kv ? c.payload[1] : c.payload[0]) + (size_t)crow * row_bytes;
   __half *srow = static_cast<__half *>((kv ? c.scale[1] : c.scale[0])) + (size_t)crow * nb;
+  uint32_t q[N];
 
   if (LAYOUT == KVQ_ASYM4_G32) {
     float mn = v[0], mx = v[0];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) { mn = fminf(mn, v[i]); mx = fmaxf(mx, v[i]); }
-    mn = quad_min(mn);
-    mx = quad_max(mx);
-    const __half sh = f16_sat(__fdiv_rn(__fsub_rn(mx, mn), 15.0f));
+    for (int i = 1; i < N; ++i) { mn = fminf(mn, v[i]); mx = fmaxf(mx, v[i]); }
+    mn = -block_max<N>(-mn);
+    mx = block_max<N>(mx);
+    const float span = __fsub_rn(mx, mn);
+    const __half sh = f16_sat(__fdiv_rn(span, 15.0f));
     const __half zh = f16_sat(mn);
     const float s = __half2float(sh), z = __half2float(zh);
-    float x[8];
-    uint32_t q[8], w = 0;
+    float x[N];
+    float top = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = __fsub_rn(v[i], z);
-    round_codes<0, 15>(x, s, q);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w |= (q[i] & 0xFu) << (4 * i);
+    for (int i = 0; i < N; ++i) {
+      x[i] = __fsub_rn(v[i], z);
+      top = fmaxf(top, fabsf(x[i]));
+    }
+    round_codes<0, 15>(x, s, !(top <= __fmul_rn(s, 290.0f)), q);
     if (!valid) return;
-    *reinterpret_cast<uint32_t *>(prow + blk * 16 + lb * 4) = w;
+    uint32_t *o = reinterpret_cast<uint32_t *>(prow + blk * 16 + lb * (N / 2));
+    if constexpr (N == 16) *reinterpret_cast<uint2 *>(o) = make_uint2(pack_codes<4, 8>(q), pack_codes<4, 8>(q + 8));
+    else *o = pack_codes<4, 8>(q);
     if (lb == 0) {
       srow[blk] = sh;
       (kv ? c.zero[1] : c.zero[0])[(size_t)crow * nb + blk] = zh;
@@ -90,57 +101,66 @@ __device__ __forceinline__ void quant_block(const CacheView &c, int kv, long lon
 
   float amax = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
-  amax = quad_max(amax);
+  for (int i = 0; i < N; ++i) amax = fmaxf(amax, fabsf(v[i]));
+  amax = block_max<N>(amax);
+  constexpr int TOP = LAYOUT == KVQ_Q4_0 ? 8 : (LAYOUT == KVQ_Q8_0 ? 128 : 32);
+  const __half sh = f16_sat(__fdiv_rn(amax, (float)TOP));
+  const float s = __half2float(sh);
+  round_codes<-TOP, TOP - 1>(v, s, !(amax <= __fmul_rn(s, 290.0f)), q);
+  if (!valid) return;
+  if (lb == 0) srow[blk] = sh;
   if (LAYOUT == KVQ_Q4_0) {
-    const __half sh = f16_sat(__fdiv_rn(amax, 8.0f));
-    const float s = __half2float(sh);
-    uint32_t q[8], w = 0;
-    round_codes<-8, 7>(v, s, q);
+    uint32_t *o = reinterpret_cast<uint32_t *>(prow + blk * 16 + lb * (N / 2));
+    if constexpr (N == 16) *reinterpret_cast<uint2 *>(o) = make_uint2(pack_codes<4, 8>(q), pack_codes<4, 8>(q + 8));
+    else *o = pack_codes<4, 8>(q);
+  } else if (LAYOUT == KVQ_Q8_0) {             // byte i = value i
+    uint8_t *o = prow + blk * 32 + lb * N;
+    if constexpr (N == 16)
+      *reinterpret_cast<uint4 *>(o) = make_uint4(pack_codes<8, 4>(q), pack_codes<8, 4>(q + 4), pack_codes<8, 4>(q + 8), pack_codes<8, 4>(q + 12));
+    else
+      *reinterpret_cast<uint2 *>(o) = make_uint2(pack_codes<8, 4>(q), pack_codes<8, 4>(q + 4));
+  } else {                                     // Q6_0: low nibbles, then values 4k .. 4k + 3 -> high byte k
+    uint32_t hi[N];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w |= (q[i] & 0xFu) << (4 * i);
-    if (!valid) return;
-    *reinterpret_cast<uint32_t *>(prow + blk * 16 + lb * 4) = w;
-    if (lb == 0) srow[blk] = sh;
-  } else if (LAYOUT == KVQ_Q8_0) {
-    const __half sh = f16_sat(__fdiv_rn(amax, 128.0f));
-    const float s = __half2float(sh);
-    uint32_t q[8], w0 = 0, w1 = 0;             // byte i = value i (two's complement)
-    round_codes<-128, 127>(v, s, q);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      w0 |= (q[i] & 0xFFu) << (8 * i);
-      w1 |= (q[4 + i] & 0xFFu) << (8 * i);
+    for (int i = 0; i < N; ++i) hi[i] = q[i] >> 4;
+    uint32_t *o = reinterpret_cast<uint32_t *>(prow + blk * 24 + lb * (N / 2));
+    if constexpr (N == 16) {
+      *reinterpret_cast<uint2 *>(o) = make_uint2(pack_codes<4, 8>(q), pack_codes<4, 8>(q + 8));   // rows of 24-byte blocks: 8-byte aligned
+      *reinterpret_cast<uint32_t *>(prow + blk * 24 + 16 + lb * 4) = pack_codes<2, 16>(hi);
+    } else {
+      *o = pack_codes<4, 8>(q);
+      *reinterpret_cast<uint16_t *>(prow + blk * 24 + 16 + lb * 2) = (uint16_t)pack_codes<2, 8>(hi);
     }
-    if (!valid) return;
-    *reinterpret_cast<uint2 *>(prow + blk * 32 + lb * 8) = make_uint2(w0, w1);
-    if (lb == 0) srow[blk] = sh;
-  } else {  // Q6_0
-    const __half sh = f16_sat(__fdiv_rn(amax, 32.0f));
-    const float s = __half2float(sh);
-    uint32_t q[8], lo = 0, hi = 0;
-    round_codes<-32, 31>(v, s, q);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      lo |= (q[i] & 0xFu) << (4 * i);
-      hi |= ((q[i] >> 4) & 0x3u) << (2 * i);   // values 4k..4k+3 -> byte k, bits 0,2,4,6
-    }
-    if (!valid) return;
-    uint8_t *bp = prow + blk * 24;
-    *reinterpret_cast<uint32_t *>(bp + lb * 4) = lo;
-    *reinterpret_cast<uint16_t *>(bp + 16 + lb * 2) = (uint16_t)hi;
-    if (lb == 0) srow[blk] = sh;
   }
 }
 
-// A whole row in one warp, V = D/32 consecutive values per lane, rotated here: BITS 4 (scale
-// amax / 7, codes [-7, 7], two per byte) or 2 (scale amax, codes [-1, 1], four per byte). in_ring:
-// the rotated float32 row also goes to slot pos mod n_recent of the window.
-template <int V, int BITS>
+// A whole row in LANES neighbouring lanes (a warp, or the half of one), V consecutive values per lane,
+// rotated here: BITS 4 (scale amax / 7, codes [-7, 7], two per byte) or 2 (scale amax, codes [-1, 1], four
+// per byte). in_ring: the rotated float32 row also goes to slot pos mod n_recent of the window. Every lane
+// of the warp calls it; those with valid == false store nothing.
+//
+// The rotation is the butterfly of warp_fwht in the same order: half-spans inside the lane, then lane bits;
+// a lane's partner value o gives o + x or o - x as one fma with the factor 1 or -1 (rounded once, like the
+// sum itself).
+template <int V, int LANES, int BITS>
 __device__ __forceinline__ void quant_had(const CacheView &c, int kv, long long crow, int row_bytes, int lane,
-                                          float (&x)[V], bool in_ring, long long bh, int pos) {
-  warp_fwht<V>(x, lane);
-  const float cD = inv_sqrt_dim(32 * V);
+                                          float (&x)[V], bool in_ring, long long bh, int pos, bool valid) {
+#pragma unroll
+  for (int h = 1; h < V; h <<= 1)
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if ((i & h) == 0) {
+        const float a = x[i], b = x[i + h];
+        x[i] = __fadd_rn(a, b);
+        x[i + h] = __fsub_rn(a, b);
+      }
+#pragma unroll
+  for (int m = 1; m < LANES; m <<= 1) {
+    const float sign = (lane & m) ? -1.0f : 1.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = __fmaf_rn(x[i], sign, __shfl_xor_sync(0xffffffffu, x[i], m));
+  }
+  const float cD = inv_sqrt_dim(LANES * V);
   float amax = 0.0f;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
@@ -148,13 +168,13 @@ __device__ __forceinline__ void quant_had(const CacheView &c, int kv, long long 
     amax = fmaxf(amax, fabsf(x[i]));
   }
 #pragma unroll
-  for (int m = 16; m; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
+  for (int m = LANES / 2; m; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
   constexpr int QMAX = BITS == 4 ? 7 : 1;
   const float s = __fdiv_rn(amax, (float)QMAX);
-  uint32_t q[V], w = 0;                                     // field i of the lane at bits BITS*i
-  round_codes<-QMAX, QMAX>(x, s, q);
-#pragma unroll
-  for (int i = 0; i < V; ++i) w |= (q[i] & ((1u << BITS) - 1u)) << (BITS * i);
+  uint32_t q[V];
+  round_codes<-QMAX, QMAX>(x, s, s < 0x1p-100f, q);        // |x / s| is at most a rounding above QMAX
+  if (!valid) return;
+  const uint32_t w = pack_codes<BITS, V>(q);
   uint8_t *prow = (kv ? c.payload[1] : c.payload[0]) + (size_t)crow * row_bytes;
   if (V * BITS == 8) {
     prow[lane] = (uint8_t)w;
@@ -165,7 +185,7 @@ __device__ __forceinline__ void quant_had(const CacheView &c, int kv, long long 
   }
   if (lane == 0) static_cast<float *>((kv ? c.scale[1] : c.scale[0]))[crow] = s;
   if (in_ring) {
-    float *dst = (kv ? c.ring[1] : c.ring[0]) + ((size_t)bh * c.n_recent + (size_t)(pos % c.n_recent)) * (32 * V) + lane * V;
+    float *dst = (kv ? c.ring[1] : c.ring[0]) + ((size_t)bh * c.n_recent + (size_t)(pos % c.n_recent)) * (LANES * V) + lane * V;
 #pragma unroll
     for (int i = 0; i < V; i += 4)
       *reinterpret_cast<float4 *>(dst + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
