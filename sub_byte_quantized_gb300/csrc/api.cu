@@ -1063,21 +1063,11 @@ kvq_status run_compact(const kvq::CacheView &src, const kvq::CacheView &dst, boo
   a.seq_lens = seq_lens;
   a.n_keep = n_keep;
   a.kv_len = kv_len;
-  a.n_parts = 0;
   a.ranks = 1;
+  a.scores = scores;
+  a.scores_out = scores_out;
   a.scores_stride = scores_stride;
   a.out_stride = out_stride;
-  auto part = [&](const void *from, void *to, int row_bytes, int is_scores) {
-    const int unit = row_bytes % 16 == 0 ? 16 : (row_bytes % 8 == 0 ? 8 : 4);
-    a.part[a.n_parts++] = {static_cast<const uint8_t *>(from), static_cast<uint8_t *>(to), row_bytes, unit, is_scores};
-  };
-  const int layouts[2] = {src.layout, src.v_layout}, bytes[2] = {src.row_bytes, src.v_row_bytes};
-  for (int t = 0; t < 2; ++t) part(src.payload[t], dst.payload[t], bytes[t], 0);
-  for (int t = 0; t < 2; ++t) {
-    part(src.scale[t], dst.scale[t], kvq::is_hadamard(layouts[t]) ? 4 : src.D / kvq::kBlock * 2, 0);
-    if (layouts[t] == KVQ_ASYM4_G32) part(src.zero[t], dst.zero[t], src.D / kvq::kBlock * 2, 0);
-  }
-  if (scores) part(scores, scores_out, 4, 1);
   const cudaError_t e = kvq::launch_evict_compact(a, in_place, s);
   if (e != cudaSuccess) return fail(KVQ_ECUDA, "compact launch: %s", cudaGetErrorString(e));
   return KVQ_OK;

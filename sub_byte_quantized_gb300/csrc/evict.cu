@@ -12,9 +12,12 @@
 //
 // Compaction: row keep[i] of every plane moves to row i. keep ascends, so keep[i] >= i: a round reads
 // the sources of the next block of target rows, everyone waits until all of the cluster's reads have
-// arrived, then writes. Reads of later rounds lie behind what this round writes, so they are issued
-// before the wait and stay in flight across it. One cluster per (batch, kv head, plane); into another
-// cache nothing can be overwritten too early, and the rounds need no barrier. Bound by memory.
+// arrived, then writes; reads of later rounds lie behind what it writes. One cluster per (batch, kv head,
+// plane); into another cache nothing can be overwritten too early, and the rounds need no barrier. Bound
+// by memory: scattered rows of 64 bytes and scales of 8 cost whole DRAM bursts (128K to 32K tokens in Q4_0,
+// 8 heads: 81 MB read for 41 that are needed). Reading the next round before this one's barrier cost
+// registers and was slower (16 ragged sequences in Q8_0, 58 instead of 46 us), as were clusters of two or
+// four CTAs where the planes alone fill the SMs (50 and 56 us).
 #include <cooperative_groups.h>
 
 #include "kvq_internal.cuh"
@@ -224,131 +227,174 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_select_kernel(S
 
 // ------------------------------------------------------------------------------------ compaction
 constexpr int kMoveThreads = 512;
-constexpr int kMoveUnits = 4;                            // units in flight per thread and round
+constexpr int kMoveUnits = 4;                            // 16-byte units of the payload per thread and round
 
-// The rows of one plane (or of the scores) of one (batch, kv head), a column of each for this thread.
+// Rows of one plane of one (batch, kv head).
 template <bool PAGED>
 struct PlaneRows {
-  uint8_t *base;
+  uint8_t *base;                                         // contiguous: row 0 of the (batch, kv head); else the pool
   int row_bytes;
-  const CacheView *c;
-  int b, kvh;
-  __device__ __forceinline__ uint8_t *at(int t) const {
-    if constexpr (PAGED) return base + (unsigned long long)cache_row_paged(*c, b, kvh, t) * (unsigned)row_bytes;
-    else return base + (unsigned long long)(unsigned)t * (unsigned)row_bytes;
+  template <class U>
+  __device__ __forceinline__ U *at(size_t row, int byte) const {
+    return reinterpret_cast<U *>(base + (unsigned long long)row * (unsigned)row_bytes + byte);
   }
 };
 template <bool PAGED>
-__device__ __forceinline__ PlaneRows<PAGED> rows_of(const CacheView &c, uint8_t *plane, int row_bytes, long long scores_stride,
-                                                    int b, int kvh, int col) {
-  PlaneRows<PAGED> r = {plane + col, row_bytes, &c, b, kvh};
-  if constexpr (!PAGED) {
-    const size_t head = (size_t)b * c.H + kvh;
-    r.base += head * (size_t)(scores_stride >= 0 ? scores_stride : c.cap) * row_bytes;
-  }
-  return r;
+__device__ __forceinline__ PlaneRows<PAGED> plane_rows(const CacheView &c, void *plane, int row_bytes, int b, int kvh) {
+  uint8_t *p = static_cast<uint8_t *>(plane);
+  if constexpr (!PAGED) p += ((size_t)b * c.H + kvh) * c.cap * row_bytes;
+  return {p, row_bytes};
+}
+// Row of token t in those planes.
+template <bool PAGED>
+__device__ __forceinline__ size_t plane_row(const CacheView &c, int b, int kvh, int t) {
+  if constexpr (PAGED) return cache_row_paged(c, b, kvh, t);
+  else return (unsigned)t;
 }
 
-// Source token of target row `row`: -1 = leave the row as it is, -2 = zero (scores behind the kept ones).
+// Source token of target row `row`, or -1: leave the row as it is.
 template <bool IN_PLACE>
-__device__ __forceinline__ int source_of(const int32_t *keep, int row, int new_len, int n_rows, int L) {
-  if (row >= new_len) return row < n_rows ? -2 : -1;
+__device__ __forceinline__ int source_of(const int32_t *keep, int row, int new_len, int L) {
+  if (row >= new_len) return -1;
   const int t = __ldg(keep + row);
   return (unsigned)t >= (unsigned)L || (IN_PLACE && t == row) ? -1 : t;
 }
 
-// Target rows [0, n_rows). A thread keeps its column of the row (row_bytes / sizeof(U) threads hold a row)
-// and steps through rows; U: the unit moved at once. Into another cache every CTA moves its own rounds. In
-// place the ranks' CTAs are one cluster whose rounds are ordered by its barrier; the sources of the round
-// after next are looked up, and the rows of the next one read, while this one waits.
+// What one thread moves in a round: up to four 16-byte units of the payload (its column of four rows, `step`
+// rows apart) and the scales and zero-points (U) of up to two whole rows of the same block.
+template <class U>
+struct Moved {
+  uint4 v[kMoveUnits];
+  U scale[2], zero[2];
+};
+
+// Target rows [0, new_len) of one plane. Rounds cover `step` * 4 rows of all the ranks' CTAs. Into another
+// cache every CTA moves its own rounds. In place the ranks' CTAs are one cluster whose rounds are ordered by
+// its barrier.
 template <class U, bool IN_PLACE, bool PAGED>
-__device__ __forceinline__ void move_rows(const CompactArgs &a, const MovePart &p, int b, int kvh, int new_len, int n_rows,
-                                          int L, int rank) {
-  const int upr = p.row_bytes / (int)sizeof(U), rpp = kMoveThreads / upr;   // threads per row, rows per pass
-  const int own = (int)threadIdx.x / upr, col = ((int)threadIdx.x - own * upr) * (int)sizeof(U);
+__device__ __forceinline__ void move_plane(const CompactArgs &a, int plane, int b, int kvh, int new_len, int L, int rank) {
+  const int bytes = plane ? a.src.v_row_bytes : a.src.row_bytes;
+  const int upr = bytes / 16, rpp = kMoveThreads / upr;  // threads per row, rows per pass
+  const int own = (int)threadIdx.x / upr, col = 16 * ((int)threadIdx.x - own * upr);
   const int32_t *keep = a.keep + ((size_t)b * a.src.H + kvh) * a.n_keep;
-  const auto src = rows_of<PAGED>(a.src, const_cast<uint8_t *>(p.src), p.row_bytes, p.is_scores ? a.scores_stride : -1, b, kvh, col);
-  const auto dst = rows_of<PAGED>(a.dst, p.dst, p.row_bytes, p.is_scores ? a.out_stride : -1, b, kvh, col);
-  const int step = a.ranks * rpp, round = step * kMoveUnits;   // rows between a thread's units, rows per round
-  const int row0 = own < rpp ? rank * rpp + own : n_rows;      // (threads beyond the last whole row idle)
-  if constexpr (!IN_PLACE) {
-    for (int base = row0; base < n_rows; base += round) {
-      int st[kMoveUnits];
-      U v[kMoveUnits];
+  const auto src = plane_rows<PAGED>(a.src, a.src.payload[plane], bytes, b, kvh);
+  const auto dst = plane_rows<PAGED>(a.dst, a.dst.payload[plane], bytes, b, kvh);
+  const auto src_s = plane_rows<PAGED>(a.src, a.src.scale[plane], sizeof(U), b, kvh);
+  const auto dst_s = plane_rows<PAGED>(a.dst, a.dst.scale[plane], sizeof(U), b, kvh);
+  const bool zeros = (plane ? a.src.v_layout : a.src.layout) == KVQ_ASYM4_G32;
+  const auto src_z = plane_rows<PAGED>(a.src, zeros ? a.src.zero[plane] : nullptr, sizeof(U), b, kvh);
+  const auto dst_z = plane_rows<PAGED>(a.dst, zeros ? a.dst.zero[plane] : nullptr, sizeof(U), b, kvh);
+  const int step = a.ranks * rpp, round = step * kMoveUnits;
+  constexpr int kFar = 1 << 30;                          // no such row
+  const int row0 = own < rpp ? rank * rpp + own : kFar;  // (threads beyond the last whole row idle)
+  // scale row k of this thread: row (tid + 512 k) of the CTA's rpp * 4 rows of a round
+  int srow[2];
 #pragma unroll
-      for (int u = 0; u < kMoveUnits; ++u) st[u] = source_of<false>(keep, base + u * step, new_len, n_rows, L);
+  for (int k = 0; k < 2; ++k) {
+    const int i = (int)threadIdx.x + kMoveThreads * k, pass = i / rpp;
+    srow[k] = pass < kMoveUnits ? pass * step + rank * rpp + (i - pass * rpp) : kFar;
+  }
+  auto look = [&](int base, int (&st)[kMoveUnits], int (&ss)[2]) {
 #pragma unroll
-      for (int u = 0; u < kMoveUnits; ++u) {
-        v[u] = U{};
-        if (st[u] >= 0) v[u] = __ldcg(reinterpret_cast<const U *>(src.at(st[u])));
+    for (int u = 0; u < kMoveUnits; ++u) st[u] = source_of<IN_PLACE>(keep, row0 + base + u * step, new_len, L);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) ss[k] = source_of<IN_PLACE>(keep, srow[k] + base, new_len, L);
+  };
+  auto read = [&](const int (&st)[kMoveUnits], const int (&ss)[2], Moved<U> &m) {
+#pragma unroll
+    for (int u = 0; u < kMoveUnits; ++u)
+      if (st[u] >= 0) m.v[u] = __ldcg(src.template at<uint4>(plane_row<PAGED>(a.src, b, kvh, st[u]), col));
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (ss[k] >= 0) {
+        const size_t r = plane_row<PAGED>(a.src, b, kvh, ss[k]);
+        m.scale[k] = __ldcg(src_s.template at<U>(r, 0));
+        if (zeros) m.zero[k] = __ldcg(src_z.template at<U>(r, 0));
       }
+  };
+  auto write = [&](int base, const int (&st)[kMoveUnits], const int (&ss)[2], const Moved<U> &m) {
 #pragma unroll
-      for (int u = 0; u < kMoveUnits; ++u)
-        if (st[u] != -1) *reinterpret_cast<U *>(dst.at(base + u * step)) = v[u];
+    for (int u = 0; u < kMoveUnits; ++u)
+      if (st[u] >= 0) *dst.template at<uint4>(plane_row<PAGED>(a.dst, b, kvh, row0 + base + u * step), col) = m.v[u];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (ss[k] >= 0) {
+        const size_t r = plane_row<PAGED>(a.dst, b, kvh, srow[k] + base);
+        *dst_s.template at<U>(r, 0) = m.scale[k];
+        if (zeros) *dst_z.template at<U>(r, 0) = m.zero[k];
+      }
+  };
+  if constexpr (!IN_PLACE) {
+    for (int base = 0; base < new_len; base += round) {
+      int st[kMoveUnits], ss[2];
+      Moved<U> m;
+      look(base, st, ss);
+      read(st, ss, m);
+      write(base, st, ss, m);
     }
   } else {
-    U cur[kMoveUnits], nxt[kMoveUnits];
-    int st[kMoveUnits], sn[kMoveUnits];                  // sources of this round and the next
-#pragma unroll
-    for (int u = 0; u < kMoveUnits; ++u) {
-      st[u] = source_of<true>(keep, row0 + u * step, new_len, n_rows, L);
-      sn[u] = source_of<true>(keep, row0 + round + u * step, new_len, n_rows, L);
-    }
-#pragma unroll
-    for (int u = 0; u < kMoveUnits; ++u) {
-      cur[u] = U{};
-      if (st[u] >= 0) cur[u] = __ldcg(reinterpret_cast<const U *>(src.at(st[u])));
-    }
-    for (int base = 0; base < n_rows; base += round) {
+    int st[kMoveUnits], ss[2];
+    Moved<U> m = {};
+    look(0, st, ss);
+    for (int base = 0; base < new_len; base += round) {
+      read(st, ss, m);
       // This round's values have arrived (the register reads below wait for the loads) before any CTA of the
       // cluster writes over their rows. That is all the barrier orders: nothing written before it is read
       // after it, so the arrive needs no release of this thread's earlier stores.
 #pragma unroll
-      for (int u = 0; u < kMoveUnits; ++u) asm volatile("" ::"r"(reinterpret_cast<const uint32_t *>(&cur[u])[0]) : "memory");
+      for (int u = 0; u < kMoveUnits; ++u) asm volatile("" ::"r"(m.v[u].x) : "memory");
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        asm volatile("" ::"r"(reinterpret_cast<const uint32_t *>(&m.scale[k])[0]), "r"(reinterpret_cast<const uint32_t *>(&m.zero[k])[0]) : "memory");
       asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-      const bool more = n_rows - base > round;
-      if (more) {
-#pragma unroll
-        for (int u = 0; u < kMoveUnits; ++u) {
-          nxt[u] = U{};
-          if (sn[u] >= 0) nxt[u] = __ldcg(reinterpret_cast<const U *>(src.at(sn[u])));
-        }
-      }
       asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-#pragma unroll
-      for (int u = 0; u < kMoveUnits; ++u)
-        if (st[u] != -1) *reinterpret_cast<U *>(dst.at(row0 + base + u * step)) = cur[u];
-      if (more) {
-#pragma unroll
-        for (int u = 0; u < kMoveUnits; ++u) {
-          cur[u] = nxt[u];
-          st[u] = sn[u];
-          sn[u] = source_of<true>(keep, row0 + base + 2 * round + u * step, new_len, n_rows, L);
-        }
-      }
+      write(base, st, ss, m);
+      look(base + round, st, ss);
     }
   }
 }
 
-template <bool IN_PLACE, bool PAGED>
-__device__ __forceinline__ void move_part(const CompactArgs &a, const MovePart &p, int b, int kvh, int new_len, int n_rows, int L,
-                                          int rank) {
-  switch (p.unit) {
-    case 16: move_rows<uint4, IN_PLACE, PAGED>(a, p, b, kvh, new_len, n_rows, L, rank); break;
-    case 8: move_rows<uint2, IN_PLACE, PAGED>(a, p, b, kvh, new_len, n_rows, L, rank); break;
-    default: move_rows<uint32_t, IN_PLACE, PAGED>(a, p, b, kvh, new_len, n_rows, L, rank); break;
+// The scores: moved likewise, and zero behind the kept ones, ready for the tokens appended next.
+template <bool IN_PLACE>
+__device__ __forceinline__ void move_scores(const CompactArgs &a, int b, int kvh, int new_len, int L, int rank) {
+  const size_t head = (size_t)b * a.src.H + kvh;
+  const int32_t *keep = a.keep + head * a.n_keep;
+  const float *src = a.scores + head * (size_t)a.scores_stride;
+  float *dst = a.scores_out + head * (size_t)a.out_stride;
+  const int n = (int)min((long long)a.kv_len, a.out_stride), step = a.ranks * kMoveThreads, round = step * kMoveUnits;
+  for (int base = 0; base < n; base += round) {
+    float v[kMoveUnits];
+    int st[kMoveUnits];
+#pragma unroll
+    for (int u = 0; u < kMoveUnits; ++u) {
+      st[u] = source_of<IN_PLACE>(keep, base + u * step + rank * kMoveThreads + (int)threadIdx.x, new_len, L);
+      v[u] = 0.0f;
+    }
+#pragma unroll
+    for (int u = 0; u < kMoveUnits; ++u)
+      if (st[u] >= 0) v[u] = __ldcg(src + st[u]);
+    if constexpr (IN_PLACE) {                            // as in move_plane
+#pragma unroll
+      for (int u = 0; u < kMoveUnits; ++u) asm volatile("" ::"f"(v[u]) : "memory");
+      asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+      asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    }
+#pragma unroll
+    for (int u = 0; u < kMoveUnits; ++u) {
+      const int row = base + u * step + rank * kMoveThreads + (int)threadIdx.x;
+      if (st[u] >= 0 || (row >= new_len && row < n)) dst[row] = v[u];
+    }
   }
 }
 
-template <bool IN_PLACE, bool PAGED>
+// Grid: (ranks * heads, K plane, V plane and scores).
+template <class U, bool IN_PLACE, bool PAGED>
 __global__ void __launch_bounds__(kMoveThreads, 2) evict_move_kernel(CompactArgs a) {
   const int bh = blockIdx.x / a.ranks, b = bh / a.src.H, kvh = bh - b * a.src.H, rank = blockIdx.x - bh * a.ranks;
-  const MovePart &p = a.part[blockIdx.y];
   const int L = a.seq_lens ? min(max(__ldg(a.seq_lens + b), 0), a.kv_len) : a.kv_len;
   const int new_len = min(L, a.n_keep);
-  // the scores behind the kept ones become zero, ready for the tokens appended next; they are not paged
-  if (p.is_scores) move_rows<uint32_t, IN_PLACE, false>(a, p, b, kvh, new_len, (int)min((long long)a.kv_len, a.out_stride), L, rank);
-  else move_part<IN_PLACE, PAGED>(a, p, b, kvh, new_len, new_len, L, rank);
+  if (blockIdx.y == 2) move_scores<IN_PLACE>(a, b, kvh, new_len, L, rank);
+  else move_plane<U, IN_PLACE, PAGED>(a, blockIdx.y, b, kvh, new_len, L, rank);
 }
 
 // The exact window: slot of token t is t mod R, and every kept window token moves back by the number of
@@ -423,38 +469,48 @@ cudaError_t launch_evict_select(const SelectArgs &a, cudaStream_t st) {
   return ranks == 1 ? launch_select<512, true>(a, ranks, keys, st) : launch_select<1024, true>(a, ranks, keys, st);
 }
 
-cudaError_t launch_evict_compact(CompactArgs a, bool in_place, cudaStream_t st) {
-  const int heads = a.src.B * a.src.H;
+namespace {
+
+template <class U>
+cudaError_t launch_move(CompactArgs &a, bool in_place, cudaStream_t st) {
+  const int heads = a.src.B * a.src.H, most = a.n_keep < a.kv_len ? a.n_keep : a.kv_len;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kMoveThreads);
   cfg.stream = st;
-  cudaError_t e;
-  const int most = a.n_keep < a.kv_len ? a.n_keep : a.kv_len;
-  if (in_place) {
-    // one cluster per plane of a (batch, kv head), at most the portable 8 CTAs: enough for two waves of two
-    // CTAs per SM over the two payload planes
-    const int want = (2 * device_sms() + heads - 1) / heads;
-    a.ranks = 1;
-    while (a.ranks < 8 && a.ranks < want) a.ranks *= 2;
-    cfg.gridDim = dim3((unsigned)a.ranks * heads, a.n_parts);
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = a.ranks;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = a.src.page_shift >= 0 ? cudaLaunchKernelEx(&cfg, evict_move_kernel<true, true>, a)
-                              : cudaLaunchKernelEx(&cfg, evict_move_kernel<true, false>, a);
-  } else {
+  const unsigned parts = a.scores ? 3 : 2;
+  if (!in_place) {
     // nothing waits: one round per CTA for the widest rows, the scheduler overlaps them
     const int upr = (a.src.row_bytes > a.src.v_row_bytes ? a.src.row_bytes : a.src.v_row_bytes) / 16;
     const int round = kMoveThreads / upr * kMoveUnits;
     a.ranks = min((most + round - 1) / round, max(1, (1 << 16) / heads));
-    cfg.gridDim = dim3((unsigned)a.ranks * heads, a.n_parts);
-    e = cudaLaunchKernelEx(&cfg, evict_move_kernel<false, false>, a);
+    cfg.gridDim = dim3((unsigned)a.ranks * heads, parts);
+    return cudaLaunchKernelEx(&cfg, evict_move_kernel<U, false, false>, a);
   }
+  // one cluster per plane of a (batch, kv head), at most the portable 8 CTAs, as many as are resident at once
+  // (two per SM over the two planes): a CTA's rounds overlap better than CTAs that follow one another
+  const int want = max(1, device_sms() / heads);
+  a.ranks = 1;
+  while (a.ranks < 8 && 2 * a.ranks <= want) a.ranks *= 2;
+  cfg.gridDim = dim3((unsigned)a.ranks * heads, parts);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = a.ranks;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return a.src.page_shift >= 0 ? cudaLaunchKernelEx(&cfg, evict_move_kernel<U, true, true>, a)
+                               : cudaLaunchKernelEx(&cfg, evict_move_kernel<U, true, false>, a);
+}
+
+}  // namespace
+
+cudaError_t launch_evict_compact(CompactArgs a, bool in_place, cudaStream_t st) {
+  // the scales of a row: one f32, or D / 32 f16
+  const cudaError_t e = is_hadamard(a.src.layout) ? launch_move<uint32_t>(a, in_place, st)
+                        : a.src.D == 128          ? launch_move<uint2>(a, in_place, st)
+                                                  : launch_move<uint4>(a, in_place, st);
   if (e != cudaSuccess || a.src.n_recent == 0) return e;
-  evict_ring_kernel<<<dim3(heads, 2, a.src.D / 32), kRingThreads, 0, st>>>(a, in_place ? 1 : 0);
+  evict_ring_kernel<<<dim3(a.src.B * a.src.H, 2, a.src.D / 32), kRingThreads, 0, st>>>(a, in_place ? 1 : 0);
   return cudaGetLastError();
 }
 

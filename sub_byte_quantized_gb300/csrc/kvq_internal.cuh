@@ -249,19 +249,14 @@ struct SelectArgs {
   int32_t *keep, *new_lens;
 };
 cudaError_t launch_evict_select(const SelectArgs &a, cudaStream_t st);
-// Compaction: the planes (and the scores) whose rows move; rows of row_bytes bytes in units of 16, 8
-// or 4 bytes. Planes are addressed as cache rows, the scores as [B][H][stride].
-struct MovePart {
-  const uint8_t *src;
-  uint8_t *dst;
-  int row_bytes, unit, is_scores;
-};
+// Compaction of src into dst (in place: the same view twice); the scores [B][H][stride] may be nullptr.
 struct CompactArgs {
   CacheView src, dst;
   const int32_t *keep, *seq_lens;
-  int n_keep, kv_len, n_parts, ranks;   // ranks: CTAs per plane of one (batch, kv head), set by the launcher
+  int n_keep, kv_len, ranks;   // ranks: CTAs per plane of one (batch, kv head), set by the launcher
+  const float *scores;
+  float *scores_out;
   long long scores_stride, out_stride;
-  MovePart part[7];            // payload, scale and zero-point of K and V, scores
 };
 cudaError_t launch_evict_compact(CompactArgs a, bool in_place, cudaStream_t st);
 // Per-token attention weight after an attention call that wrote a.lse: scores_out[t] = decay *

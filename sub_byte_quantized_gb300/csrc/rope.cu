@@ -81,17 +81,25 @@ __global__ void __launch_bounds__(kTableThreads) rope_table_kernel(RopeTurns f, 
 // n / d for n < 2^31 by one high product: (n + umulhi(n, mul)) >> shift.
 __device__ __forceinline__ unsigned divide(unsigned n, const FastDiv &d) { return (n + __umulhi(n, d.mul)) >> d.shift; }
 
-// Which row a thread or warp works on: K rows first, then V, then q.
+// The row a group of threads works on: K rows first, then V, then q.
 struct RopeRow {
   int what;                 // 0 = K, 1 = V, 2 = q
   int b, head, j, pos, at;  // batch, head (kv or query), row of the append, cache slot, table row
   long long crow;           // plane row (K and V)
-  bool live;                // q, or a slot inside the cache
 };
-__device__ __forceinline__ RopeRow rope_row(const CacheView &c, const RopeStore &g, long long r) {
-  RopeRow w;
-  w.what = r < g.k_rows ? 0 : (r < g.k_rows + g.v_rows ? 1 : 2);
-  r -= w.what == 0 ? 0 : (w.what == 1 ? g.k_rows : g.k_rows + g.v_rows);
+// Grid column y of a LONG launch (many rows per head): K, V or q, batch entry and head. Columns run fastest:
+// the heads of a token lie side by side in a fused projection's output.
+__device__ __forceinline__ void rope_column(const CacheView &c, const RopeStore &g, unsigned y, RopeRow &w) {
+  const unsigned kv = (unsigned)(c.B * c.H), k = g.k_rows ? kv : 0u, v = g.v_rows ? kv : 0u;
+  w.what = y < k ? 0 : (y < k + v ? 1 : 2);
+  const unsigned bh = y - (w.what == 0 ? 0u : (w.what == 1 ? k : k + v));
+  w.b = (int)divide(bh, w.what == 2 ? g.by_q_heads : g.by_kv_heads);
+  w.head = (int)(bh - (unsigned)w.b * (w.what == 2 ? (unsigned)g.Hq : (unsigned)c.H));
+}
+// Row r of a launch's rows in order: K, V or q, batch entry, head and row of the append.
+__device__ __forceinline__ void rope_split(const CacheView &c, const RopeStore &g, long long group, RopeRow &w) {
+  w.what = group < g.k_rows ? 0 : (group < g.k_rows + g.v_rows ? 1 : 2);
+  const long long r = group - (w.what == 0 ? 0 : (w.what == 1 ? g.k_rows : g.k_rows + g.v_rows));
   const int heads = w.what == 2 ? g.Hq : c.H;
   if (r <= 0x7FFFFFFFLL) {
     const unsigned bh = divide((unsigned)r, g.by_new);
@@ -104,22 +112,26 @@ __device__ __forceinline__ RopeRow rope_row(const CacheView &c, const RopeStore 
     w.b = (int)(bh / heads);
     w.head = (int)(bh - (long long)w.b * heads);
   }
+}
+// The rest of row w.j: its slot, plane row and table row; false when there is nothing to write.
+__device__ __forceinline__ bool rope_place(const CacheView &c, const RopeStore &g, RopeRow &w) {
   // a slot is 64-bit until it is known to lie inside the cache
   const long long slot = (g.slots ? (long long)__ldg(g.slots + w.b) : (long long)g.pos0) + w.j;
   const bool inside = slot >= 0 && slot < c.cap;
   w.pos = (int)min(max(slot, (long long)INT_MIN), (long long)INT_MAX);   // also the default rotary position
-  w.at = min(max(g.positions ? __ldg(g.positions + (size_t)w.b * g.n_new + w.j) : w.pos, 0), g.n_pos - 1);
-  w.live = w.what == 2 || inside;
-  w.crow = w.what != 2 && inside ? (long long)cache_row(c, w.b, w.head, w.pos) : 0;
-  return w;
+  if (w.what != 1) w.at = min(max(g.positions ? __ldg(g.positions + (size_t)w.b * g.n_new + w.j) : w.pos, 0), g.n_pos - 1);
+  if (w.what == 2) return true;
+  w.crow = inside ? (long long)cache_row(c, w.b, w.head, w.pos) : 0;
+  return inside;
 }
 
 // Eight consecutive dims from d0 of one row, rotated when the row is K or q and d0 < rot_dim (a multiple of
 // 16: all eight are on the same side of rot_dim and of its half).
+template <int DT>
 __device__ __forceinline__ void rope_load(const RopeStore &g, const RopeRow &w, size_t row, int d0, float *y) {
   const void *in = g.in[w.what].data;
   float x[8];
-  load8_f32(in, g.dtype, row + d0, x);
+  load8_f32(in, DT, row + d0, x);
   if (w.what == 1 || d0 >= g.rot) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = x[i];
@@ -141,7 +153,7 @@ __device__ __forceinline__ void rope_load(const RopeStore &g, const RopeRow &w, 
   const bool second = d0 >= half;
   const int i0 = second ? d0 - half : d0;
   float p[8], c[8], s[8];
-  load8_f32(in, g.dtype, row + (second ? i0 : d0 + half), p);
+  load8_f32(in, DT, row + (second ? i0 : d0 + half), p);
   load8_f32(t, KVQ_F32, i0, c);
   load8_f32(t, KVQ_F32, half + i0, s);
 #pragma unroll
@@ -151,8 +163,9 @@ __device__ __forceinline__ void rope_load(const RopeStore &g, const RopeRow &w, 
   }
 }
 
-__device__ __forceinline__ uint32_t pack2(int dtype, float lo, float hi) {
-  if (dtype == KVQ_BF16) {
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if constexpr (DT == KVQ_BF16) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&v);
   }
@@ -160,89 +173,117 @@ __device__ __forceinline__ uint32_t pack2(int dtype, float lo, float hi) {
   return *reinterpret_cast<const uint32_t *>(&v);
 }
 // q rows are written [batch][n_q_heads][n_new][head_dim], rounded once to their type
+template <int DT>
 __device__ __forceinline__ void write_q(const RopeStore &g, const RopeRow &w, int D, int d0, const float *y) {
   const size_t e = (((size_t)w.b * g.Hq + w.head) * g.n_new + w.j) * D + d0;
-  if (g.dtype == KVQ_F32) {
+  if constexpr (DT == KVQ_F32) {
     float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(g.q_out) + e);
     o[0] = make_float4(y[0], y[1], y[2], y[3]);
     o[1] = make_float4(y[4], y[5], y[6], y[7]);
   } else {
     *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(g.q_out) + e) =
-        make_uint4(pack2(g.dtype, y[0], y[1]), pack2(g.dtype, y[2], y[3]), pack2(g.dtype, y[4], y[5]), pack2(g.dtype, y[6], y[7]));
+        make_uint4(pack2<DT>(y[0], y[1]), pack2<DT>(y[2], y[3]), pack2<DT>(y[4], y[5]), pack2<DT>(y[6], y[7]));
   }
 }
 
 // Sixteen dims per thread (block layouts) or eight (Hadamard): rows per warp 4 or 2 at head_dim 128. Neither
 // kernel lets a dependent launch start early: the attention call that follows reads q_out, and its query
 // preparation does not wait for its predecessor.
-template <int LAYOUT>
-__global__ void __launch_bounds__(256) rope_store_block_kernel(CacheView c, RopeStore g) {
-  const int shift = c.D == 128 ? 3 : 4;                   // D / 16 threads per row
-  const long long gt = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-  const long long r = gt >> shift;
-  const int tr = (int)(gt & ((1 << shift) - 1));
-  // threads past the last row take part in the shuffles (full-warp masks) but load and store nothing
-  RopeRow w = {};
-  bool valid = r < g.k_rows + g.v_rows + g.q_rows;
-  if (valid) {
-    w = rope_row(c, g, r);
-    valid = w.live;
-  }
+// The threads of one row (TPR of them, `tr` this one's index): load, rotate, write q or quantise. Threads
+// without a row take part in the shuffles (full-warp masks) but load and store nothing.
+template <int LAYOUT, int D, int DT>
+__device__ __forceinline__ void rope_block_row(const CacheView &c, const RopeStore &g, RopeRow &w, bool valid, int tr) {
+  if (valid) valid = rope_place(c, g, w);
   float y[16] = {};
   if (valid) {
     const RowsIn &in = g.in[w.what];
     const size_t row = (size_t)w.b * in.batch + (size_t)w.head * in.head + (size_t)w.j * in.token;
-    rope_load(g, w, row, 16 * tr, y);
-    rope_load(g, w, row, 16 * tr + 8, y + 8);
+    rope_load<DT>(g, w, row, 16 * tr, y);
+    rope_load<DT>(g, w, row, 16 * tr + 8, y + 8);
     if (w.what == 2) {
-      write_q(g, w, c.D, 16 * tr, y);
-      write_q(g, w, c.D, 16 * tr + 8, y + 8);
+      write_q<DT>(g, w, D, 16 * tr, y);
+      write_q<DT>(g, w, D, 16 * tr + 8, y + 8);
     }
   }
   if (__all_sync(0xffffffffu, !valid || w.what == 2)) return;   // a warp of q rows has nothing to quantise
-  quant_block<LAYOUT, 16>(c, w.what == 1, w.crow, g.row_bytes, c.D / kBlock, tr >> 1, tr & 1, y, valid && w.what != 2);
+  quant_block<LAYOUT, 16>(c, w.what == 1, w.crow, g.row_bytes, D / kBlock, tr >> 1, tr & 1, y, valid && w.what != 2);
 }
-
-template <int LANES, int BITS>
-__global__ void __launch_bounds__(256) rope_store_had_kernel(CacheView c, RopeStore g) {
-  const long long gt = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-  const long long r = gt / LANES;
-  const int lane = (int)(gt % LANES);
-  RopeRow w = {};
-  bool valid = r < g.k_rows + g.v_rows + g.q_rows;
-  if (valid) {
-    w = rope_row(c, g, r);
-    valid = w.live;
-  }
+template <int LAYOUT, int D, int DT>
+__device__ __forceinline__ void rope_had_row(const CacheView &c, const RopeStore &g, RopeRow &w, bool valid, int lane) {
+  if (valid) valid = rope_place(c, g, w);
   float y[8] = {};
   if (valid) {
     const RowsIn &in = g.in[w.what];
-    rope_load(g, w, (size_t)w.b * in.batch + (size_t)w.head * in.head + (size_t)w.j * in.token, 8 * lane, y);
-    if (w.what == 2) write_q(g, w, 8 * LANES, 8 * lane, y);
+    rope_load<DT>(g, w, (size_t)w.b * in.batch + (size_t)w.head * in.head + (size_t)w.j * in.token, 8 * lane, y);
+    if (w.what == 2) write_q<DT>(g, w, D, 8 * lane, y);
   }
   if (__all_sync(0xffffffffu, !valid || w.what == 2)) return;
-  quant_had<8, LANES, BITS>(c, w.what == 1, w.crow, g.row_bytes, lane, y, c.n_recent > 0 && w.j >= g.n_new - c.n_recent,
-                            (long long)w.b * c.H + w.head, w.pos, valid && w.what != 2);
+  quant_had<8, D / 8, LAYOUT == KVQ_HAD_INT4 ? 4 : 2>(c, w.what == 1, w.crow, g.row_bytes, lane, y,
+                                                      c.n_recent > 0 && w.j >= g.n_new - c.n_recent,
+                                                      (long long)w.b * c.H + w.head, w.pos, valid && w.what != 2);
 }
 
-cudaError_t launch_plane(const CacheView &c, int layout, const RopeStore &g, cudaStream_t st) {
-  const long long rows = g.k_rows + g.v_rows + g.q_rows;
-  const unsigned blocks = (unsigned)((rows * (is_hadamard(layout) ? c.D / 8 : c.D / 16) + 255) / 256);
-  switch (layout) {
-    case KVQ_Q4_0: rope_store_block_kernel<KVQ_Q4_0><<<blocks, 256, 0, st>>>(c, g); break;
-    case KVQ_Q6_0: rope_store_block_kernel<KVQ_Q6_0><<<blocks, 256, 0, st>>>(c, g); break;
-    case KVQ_Q8_0: rope_store_block_kernel<KVQ_Q8_0><<<blocks, 256, 0, st>>>(c, g); break;
-    case KVQ_ASYM4_G32: rope_store_block_kernel<KVQ_ASYM4_G32><<<blocks, 256, 0, st>>>(c, g); break;
-    case KVQ_HAD_INT4:
-      if (c.D == 128) rope_store_had_kernel<16, 4><<<blocks, 256, 0, st>>>(c, g);
-      else rope_store_had_kernel<32, 4><<<blocks, 256, 0, st>>>(c, g);
-      break;
-    default:
-      if (c.D == 128) rope_store_had_kernel<16, 2><<<blocks, 256, 0, st>>>(c, g);
-      else rope_store_had_kernel<32, 2><<<blocks, 256, 0, st>>>(c, g);
-      break;
+// LONG: a block takes several passes of rows of one grid column, whose addresses are then the same but for
+// the row (8192 rows asymmetric, d256: one pass per block 67 us, four 60, eight 63; 255 rows Hadamard int4:
+// 16.0, at four 17.2); else the launch's rows are dealt out in order.
+template <int LAYOUT>
+constexpr int long_passes() { return is_hadamard(LAYOUT) ? 1 : 4; }
+template <int LAYOUT, int D, int DT, bool LONG>
+__global__ void __launch_bounds__(256, is_hadamard(LAYOUT) ? 6 : LONG ? 5 : 4) rope_store_kernel(CacheView c, RopeStore g) {
+  constexpr int TPR = is_hadamard(LAYOUT) ? D / 8 : D / 16, ROWS = 256 / TPR;   // threads per row, rows per pass
+  const int tr = threadIdx.x % TPR;
+  RopeRow w = {};
+  if constexpr (LONG) {
+    rope_column(c, g, blockIdx.x, w);
+    const int first = (int)blockIdx.y * (ROWS * long_passes<LAYOUT>());
+#pragma unroll 1
+    for (int k = 0; k < long_passes<LAYOUT>(); ++k) {
+      if (first + k * ROWS >= g.n_new) return;           // the whole block
+      w.j = first + k * ROWS + (int)threadIdx.x / TPR;
+      if constexpr (is_hadamard(LAYOUT)) rope_had_row<LAYOUT, D, DT>(c, g, w, w.j < g.n_new, tr);
+      else rope_block_row<LAYOUT, D, DT>(c, g, w, w.j < g.n_new, tr);
+    }
+  } else {
+    const long long group = (long long)blockIdx.x * ROWS + threadIdx.x / TPR;
+    const bool valid = group < g.k_rows + g.v_rows + g.q_rows;
+    if (valid) rope_split(c, g, group, w);
+    if constexpr (is_hadamard(LAYOUT)) rope_had_row<LAYOUT, D, DT>(c, g, w, valid, tr);
+    else rope_block_row<LAYOUT, D, DT>(c, g, w, valid, tr);
+  }
+}
+
+template <int LAYOUT, int D, int DT>
+cudaError_t launch_typed(const CacheView &c, const RopeStore &g, cudaStream_t st) {
+  constexpr int rows_per_pass = 256 / (is_hadamard(LAYOUT) ? D / 8 : D / 16), per_block = rows_per_pass * long_passes<LAYOUT>();
+  const long long rows = g.k_rows + g.v_rows + g.q_rows, columns = rows / g.n_new;
+  // at least a block of rows per head: a grid column per head
+  const long long blocks_per_head = (g.n_new + per_block - 1) / per_block;
+  if (g.n_new >= per_block && blocks_per_head <= 65535) {
+    rope_store_kernel<LAYOUT, D, DT, true><<<dim3((unsigned)columns, (unsigned)blocks_per_head), 256, 0, st>>>(c, g);
+  } else {
+    const unsigned blocks = (unsigned)((rows + rows_per_pass - 1) / rows_per_pass);
+    rope_store_kernel<LAYOUT, D, DT, false><<<blocks, 256, 0, st>>>(c, g);
   }
   return cudaGetLastError();
+}
+template <int LAYOUT>
+cudaError_t launch_layout(const CacheView &c, const RopeStore &g, cudaStream_t st) {
+  if (c.D == 128) {
+    if (g.dtype == KVQ_F32) return launch_typed<LAYOUT, 128, KVQ_F32>(c, g, st);
+    return g.dtype == KVQ_BF16 ? launch_typed<LAYOUT, 128, KVQ_BF16>(c, g, st) : launch_typed<LAYOUT, 128, KVQ_F16>(c, g, st);
+  }
+  if (g.dtype == KVQ_F32) return launch_typed<LAYOUT, 256, KVQ_F32>(c, g, st);
+  return g.dtype == KVQ_BF16 ? launch_typed<LAYOUT, 256, KVQ_BF16>(c, g, st) : launch_typed<LAYOUT, 256, KVQ_F16>(c, g, st);
+}
+cudaError_t launch_plane(const CacheView &c, int layout, const RopeStore &g, cudaStream_t st) {
+  switch (layout) {
+    case KVQ_Q4_0: return launch_layout<KVQ_Q4_0>(c, g, st);
+    case KVQ_Q6_0: return launch_layout<KVQ_Q6_0>(c, g, st);
+    case KVQ_Q8_0: return launch_layout<KVQ_Q8_0>(c, g, st);
+    case KVQ_ASYM4_G32: return launch_layout<KVQ_ASYM4_G32>(c, g, st);
+    case KVQ_HAD_INT4: return launch_layout<KVQ_HAD_INT4>(c, g, st);
+    default: return launch_layout<KVQ_HAD_INT2>(c, g, st);
+  }
 }
 
 FastDiv fast_div(int d) {

@@ -14,43 +14,53 @@ __device__ __forceinline__ __half f16_sat(float x) {
   return __float2half_rn(fminf(fmaxf(x, -kF16Max), kF16Max));
 }
 
-// Codes clamp(rint(x / s), LO, HI) of N values (0 when s == 0), x / s the correctly rounded quotient, as
-// words whose low bits are the two's complement code (the caller masks them).
+// Codes clamp(rint(x / s), LO, HI) of N values (0 when s == 0), x / s the correctly rounded quotient, each
+// as the float 1.5 * 2^23 + code - LO, whose bits are kCodeBase + (code - LO).
 //
-// The quotient is taken as x * fl(1 / s), off by less than 2^-22 of itself, i.e. by less than 1e-4 for
-// |x / s| <= 300. It rounds like the correct quotient unless a half-integer lies between the two, and then
-// the product is within 2e-4 of one: those rare threads divide. Rounding is the addition of 1.5 * 2^23 in
-// one fma (nearest even), whose low mantissa bits are the code. `divide` sends a thread to the division at
-// once: where some |x / s| may pass 300, or fl(1 / s) may overflow.
-template <int LO, int HI, int N>
-__device__ __forceinline__ void round_codes(const float (&x)[N], float s, bool divide, uint32_t (&code)[N]) {
-  constexpr float kMagic = 12582912.0f;
+// The quotient is taken as x * fl(1 / s), off by at most 2^-24 of itself like the correctly rounded one, so
+// both round alike unless a half-integer lies within 2^-23 of |x / s| <= kTop of them; a thread that finds
+// one of its products within four times that of a half-integer divides (one warp of 512 values in a hundred
+// for 4-bit codes). Rounding is the addition of 1.5 * 2^23 - LO in one fma (nearest even). `divide` sends a
+// thread to the division at once: where fl(1 / s) may overflow; |x| > top does the same for quotients
+// beyond kTop. LEAST: the lowest code, where only the division can fall below it.
+constexpr uint32_t kCodeBase = 0x4B400000u;              // the bits of 1.5 * 2^23
+template <int LO, int HI, int LEAST = LO, int N>
+__device__ __forceinline__ void round_codes(const float (&x)[N], float s, float top, bool divide, uint32_t (&code)[N]) {
+  constexpr float kBase = 12582912.0f, kZero = kBase - LO, kTop = 2.0f * (HI + 1);
   if (!(s > 0.0f)) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) code[i] = 0;
+    for (int i = 0; i < N; ++i) code[i] = kCodeBase + (uint32_t)(-LO);
     return;
   }
   const float inv = __frcp_rn(s);
   float off = 0.0f;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const float m = __fmaf_rn(x[i], inv, kMagic), q = __fsub_rn(m, kMagic);
+    const float m = __fmaf_rn(x[i], inv, kZero), q = __fsub_rn(m, kZero);
     off = fmaxf(off, fabsf(__fmaf_rn(x[i], inv, -q)));
-    code[i] = __float_as_uint(fminf(fmaxf(m, kMagic + LO), kMagic + HI));
+    code[i] = __float_as_uint(fminf(fmaxf(m, kBase), kBase + (HI - LO)));
   }
-  if (divide || off > 0.4998f) {
+  if (divide || off > 0.5f - kTop * 0x1p-21f || !(top <= __fmul_rn(s, kTop))) {
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      code[i] = (uint32_t)(int)fminf(fmaxf(rintf(__fdiv_rn(x[i], s)), (float)LO), (float)HI);
+      code[i] = kCodeBase + (uint32_t)(-LO) + (uint32_t)(int)fminf(fmaxf(rintf(__fdiv_rn(x[i], s)), (float)LEAST), (float)HI);
   }
 }
-// N fields of BITS bits from codes, field i at BITS * i.
-template <int BITS, int N>
+// N = 32 / BITS fields of BITS bits, field i at BITS * i: the two's complement codes of a signed layout
+// (LO = -2^(BITS - 1)), or the codes of an unsigned one. One shift-add per code; what the base's bits add up
+// to is taken off at the end, and the offset -LO comes out of the fields' top bits.
+template <int BITS, bool SIGNED, int N>
 __device__ __forceinline__ uint32_t pack_codes(const uint32_t *code) {
-  uint32_t w = 0;
+  static_assert(BITS * N <= 32, "one word");
+  uint32_t w = 0, base = 0, flip = 0;
 #pragma unroll
-  for (int i = 0; i < N; ++i) w |= (code[i] & ((1u << BITS) - 1u)) << (BITS * i);
-  return w;
+  for (int i = N - 1; i >= 0; --i) {
+    w = (w << BITS) + code[i];
+    base = (base << BITS) + kCodeBase;
+    flip = (flip << BITS) | (1u << (BITS - 1));
+  }
+  w -= base;
+  return SIGNED ? w ^ flip : w;
 }
 // Maximum over aligned groups of 32 / N neighbouring lanes (the lanes of a 32-value block).
 template <int N>
@@ -81,17 +91,14 @@ __device__ __forceinline__ void quant_block(const CacheView &c, int kv, long lon
     const __half zh = f16_sat(mn);
     const float s = __half2float(sh), z = __half2float(zh);
     float x[N];
-    float top = 0.0f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      x[i] = __fsub_rn(v[i], z);
-      top = fmaxf(top, fabsf(x[i]));
-    }
-    round_codes<0, 15>(x, s, !(top <= __fmul_rn(s, 290.0f)), q);
+    for (int i = 0; i < N; ++i) x[i] = __fsub_rn(v[i], z);
+    const float top = fmaxf(fabsf(__fsub_rn(mx, z)), fabsf(__fsub_rn(mn, z)));   // no |x| is larger
+    round_codes<0, 15>(x, s, top, false, q);
     if (!valid) return;
     uint32_t *o = reinterpret_cast<uint32_t *>(prow + blk * 16 + lb * (N / 2));
-    if constexpr (N == 16) *reinterpret_cast<uint2 *>(o) = make_uint2(pack_codes<4, 8>(q), pack_codes<4, 8>(q + 8));
-    else *o = pack_codes<4, 8>(q);
+    if constexpr (N == 16) *reinterpret_cast<uint2 *>(o) = make_uint2(pack_codes<4, false, 8>(q), pack_codes<4, false, 8>(q + 8));
+    else *o = pack_codes<4, false, 8>(q);
     if (lb == 0) {
       srow[blk] = sh;
       (kv ? c.zero[1] : c.zero[0])[(size_t)crow * nb + blk] = zh;
@@ -106,30 +113,35 @@ __device__ __forceinline__ void quant_block(const CacheView &c, int kv, long lon
   constexpr int TOP = LAYOUT == KVQ_Q4_0 ? 8 : (LAYOUT == KVQ_Q8_0 ? 128 : 32);
   const __half sh = f16_sat(__fdiv_rn(amax, (float)TOP));
   const float s = __half2float(sh);
-  round_codes<-TOP, TOP - 1>(v, s, !(amax <= __fmul_rn(s, 290.0f)), q);
+  round_codes<-TOP, TOP - 1>(v, s, amax, false, q);
   if (!valid) return;
   if (lb == 0) srow[blk] = sh;
   if (LAYOUT == KVQ_Q4_0) {
     uint32_t *o = reinterpret_cast<uint32_t *>(prow + blk * 16 + lb * (N / 2));
-    if constexpr (N == 16) *reinterpret_cast<uint2 *>(o) = make_uint2(pack_codes<4, 8>(q), pack_codes<4, 8>(q + 8));
-    else *o = pack_codes<4, 8>(q);
+    if constexpr (N == 16) *reinterpret_cast<uint2 *>(o) = make_uint2(pack_codes<4, true, 8>(q), pack_codes<4, true, 8>(q + 8));
+    else *o = pack_codes<4, true, 8>(q);
   } else if (LAYOUT == KVQ_Q8_0) {             // byte i = value i
     uint8_t *o = prow + blk * 32 + lb * N;
     if constexpr (N == 16)
-      *reinterpret_cast<uint4 *>(o) = make_uint4(pack_codes<8, 4>(q), pack_codes<8, 4>(q + 4), pack_codes<8, 4>(q + 8), pack_codes<8, 4>(q + 12));
+      *reinterpret_cast<uint4 *>(o) = make_uint4(pack_codes<8, true, 4>(q), pack_codes<8, true, 4>(q + 4), pack_codes<8, true, 4>(q + 8), pack_codes<8, true, 4>(q + 12));
     else
-      *reinterpret_cast<uint2 *>(o) = make_uint2(pack_codes<8, 4>(q), pack_codes<8, 4>(q + 4));
+      *reinterpret_cast<uint2 *>(o) = make_uint2(pack_codes<8, true, 4>(q), pack_codes<8, true, 4>(q + 4));
   } else {                                     // Q6_0: low nibbles, then values 4k .. 4k + 3 -> high byte k
-    uint32_t hi[N];
+    // u = code + 32 = (its low four bits) + 16 * (the high field with its sign bit flipped)
+    uint32_t lo[N], hi[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) hi[i] = q[i] >> 4;
-    uint32_t *o = reinterpret_cast<uint32_t *>(prow + blk * 24 + lb * (N / 2));
+    for (int i = 0; i < N; ++i) {
+      const uint32_t u = q[i] - kCodeBase;
+      lo[i] = kCodeBase + (u & 15u);
+      hi[i] = kCodeBase + (u >> 4);
+    }
+    uint32_t *o = reinterpret_cast<uint32_t *>(prow + blk * 24 + lb * (N / 2));   // (24-byte blocks: 8-byte aligned)
     if constexpr (N == 16) {
-      *reinterpret_cast<uint2 *>(o) = make_uint2(pack_codes<4, 8>(q), pack_codes<4, 8>(q + 8));   // rows of 24-byte blocks: 8-byte aligned
-      *reinterpret_cast<uint32_t *>(prow + blk * 24 + 16 + lb * 4) = pack_codes<2, 16>(hi);
+      *reinterpret_cast<uint2 *>(o) = make_uint2(pack_codes<4, false, 8>(lo), pack_codes<4, false, 8>(lo + 8));
+      *reinterpret_cast<uint32_t *>(prow + blk * 24 + 16 + lb * 4) = pack_codes<2, true, 16>(hi);
     } else {
-      *o = pack_codes<4, 8>(q);
-      *reinterpret_cast<uint16_t *>(prow + blk * 24 + 16 + lb * 2) = (uint16_t)pack_codes<2, 8>(hi);
+      *o = pack_codes<4, false, 8>(lo);
+      *reinterpret_cast<uint16_t *>(prow + blk * 24 + 16 + lb * 2) = (uint16_t)pack_codes<2, true, 8>(hi);
     }
   }
 }
@@ -172,9 +184,10 @@ __device__ __forceinline__ void quant_had(const CacheView &c, int kv, long long 
   constexpr int QMAX = BITS == 4 ? 7 : 1;
   const float s = __fdiv_rn(amax, (float)QMAX);
   uint32_t q[V];
-  round_codes<-QMAX, QMAX>(x, s, s < 0x1p-100f, q);        // |x / s| is at most a rounding above QMAX
+  // codes as offsets from -QMAX - 1, the fields' own offset
+  round_codes<-QMAX - 1, QMAX, -QMAX>(x, s, amax, s < 0x1p-100f, q);
   if (!valid) return;
-  const uint32_t w = pack_codes<BITS, V>(q);
+  const uint32_t w = pack_codes<BITS, true, V>(q);
   uint8_t *prow = (kv ? c.payload[1] : c.payload[0]) + (size_t)crow * row_bytes;
   if (V * BITS == 8) {
     prow[lane] = (uint8_t)w;
