@@ -268,7 +268,7 @@ struct WeightArgs {
   float *scores_out;
   long long stride;
   float decay;
-  int units;                   // many rows: 32-token units per CTA
+  int units;                   // many rows: 32-token units (tcgen05: 128-token tiles) per CTA
   int n_ctas;                  // CTAs over the body's tokens; the window's follow
 };
 cudaError_t launch_attend_weights(const AttendArgs &a, const float *scores_in, float *scores_out, long long stride,
