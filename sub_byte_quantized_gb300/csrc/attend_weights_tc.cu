@@ -13,10 +13,11 @@
 //
 // Bound by the exponentials: 32 query heads x 32 rows over 32749 tokens, 8 kv heads, take 33.5 M of them,
 // 7 us at 16 per clock and SM; the products take 2 us, the packed keys 3. One CTA per SM:
-//   warps 0-7   weights: two groups of four (TMEM lane quarters); accumulators go to the groups in turn
-//   warps 8-11  unpack: one token row per thread, packed row -> swizzled f16 tile (two buffers); the next
-//               tile's row is in flight in registers meanwhile
-//   warp  12    one lane issues the MMAs; the warp owns the TMEM allocation (four accumulators of 128 rows)
+//   warps 0-15  weights: four groups of four (TMEM lane quarters); accumulators go to the groups in turn (with
+//               two groups, a scheduler's two warps left every latency open: 28 instead of 19 us)
+//   warps 16-19 unpack: one token row per thread, packed row -> swizzled f16 tile (two buffers); rows of the
+//               tiles to come are prefetched into L2
+//   warp  20    one lane issues the MMAs; the warp owns the TMEM allocation (four accumulators of 128 rows)
 // Query rows beyond 256 (128 with f32 queries) are taken in further groups over the same tokens, whose sums
 // stay in shared memory. Every wait is bounded; a CTA whose wait gives up writes NaN scores.
 #include "attend_weights.cuh"
@@ -28,9 +29,12 @@ using namespace weights;
 constexpr int kD = 128, kTile = 128;     // head_dim; tokens per tile = TMEM lanes
 constexpr int kBlk = 128;                // query rows per accumulator
 constexpr int kMaxTiles = 16;            // tiles per CTA (sums in shared memory)
-constexpr int kEpiWarps = 8, kUnpWarp = 8, kUnpThreads = 128, kMmaWarp = 12, kWarps = 13, kThreads = 32 * kWarps;
+constexpr int kEpiWarps = 16, kUnpWarp = 16, kUnpThreads = 128, kMmaWarp = 20, kWarps = 21, kThreads = 32 * kWarps;
+constexpr int kAhead = 3;                // tiles that the unpack warps prefetch ahead
 constexpr int kAcc = 4, kTmemCols = kAcc * kBlk;
 constexpr int kOperand = kTile * kD * 2; // bytes of one f16 operand of 128 rows: two 64-dim column blocks
+
+constexpr int kWinRowsTc = 4 * kWarps;   // query rows at a time in a window CTA
 
 // HILO: the key values enter as hi + lo. QLO: so do the queries.
 template <bool HILO, bool QLO>
@@ -39,7 +43,7 @@ struct Smem {
   static constexpr int GROUP = QLO ? kBlk : 2 * kBlk;             // query rows at a time
   static constexpr int OFF_B = 2 * A, B = 2 * kOperand;
   static constexpr int OFF_ROW = OFF_B + B;                       // float2 (factor, lse) per row, then limits
-  static constexpr int OFF_SUM = OFF_ROW + 2 * kBlk * 12;         // [2 groups][tiles][128]
+  static constexpr int OFF_SUM = OFF_ROW + 2 * kBlk * 12;         // [accumulator of the group][tiles][128]
   static constexpr int OFF_BAR = OFF_SUM + 2 * kMaxTiles * kTile * 4;
   static constexpr int TOTAL = OFF_BAR + 128;
   static_assert(TOTAL <= 227 * 1024, "one CTA per SM");
@@ -93,6 +97,13 @@ struct TokenRow {
   uint4 w[RB / 16];
   uint2 scale, zero;
 };
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+template <int KL>
+__device__ __forceinline__ void prefetch_row(const CacheView &cv, size_t row) {
+  prefetch_l2(cv.payload[0] + row * TokenRow<KL>::RB);
+  prefetch_l2(static_cast<const uint8_t *>(cv.scale[0]) + row * (is_hadamard(KL) ? 4 : 8));
+  if constexpr (KL == KVQ_ASYM4_G32) prefetch_l2(reinterpret_cast<const uint8_t *>(cv.zero[0]) + row * 8);
+}
 template <int KL>
 __device__ __forceinline__ void load_row(const CacheView &cv, size_t row, TokenRow<KL> &t) {
   const uint4 *p = reinterpret_cast<const uint4 *>(cv.payload[0] + row * TokenRow<KL>::RB);
@@ -261,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_weights_tc_kernel(WeightAr
   if (is_hadamard(KL) && (int)blockIdx.x >= wa.n_ctas) {
     const int j = (int)blockIdx.x - wa.n_ctas;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (sl.n_body + j * kWinTokens < sl.kv_len) window_tokens<kD, kWarps>(wa, sl, bb, kvh, j, reinterpret_cast<float *>(sm));
+    if (sl.n_body + j * kWinTokens < sl.kv_len) window_tokens<kD, kWarps, kWinRowsTc>(wa, sl, bb, kvh, j, reinterpret_cast<float *>(sm));
     return;
   }
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -319,22 +330,24 @@ __global__ void __launch_bounds__(kThreads, 1) attend_weights_tc_kernel(WeightAr
     __syncthreads();
 
     if (warp < kEpiWarps) {
-      // ---------------- weights: group g takes every second accumulator
-      const int g = warp >> 2, lr = 32 * (warp & 3) + lane;
+      // ---------------- weights: group g takes every fourth accumulator
+      const int g = warp >> 2, lr = 32 * (warp & 3) + lane, items = n_tiles * nblk;
       const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-      for (int i = g; i < n_tiles * nblk && ok; i += 2) {
-        const int tile = nblk == 2 ? i >> 1 : i, blk = nblk == 2 ? i & 1 : 0, it = item_n + i;
+      auto tile_of = [&](int i) { return nblk == 2 ? i >> 1 : i; };
+      // what the scores of item i's token are multiplied by
+      auto unit_of = [&](int i) -> float {
+        const size_t row = token_row((first + tile_of(i)) * kTile + lr);
+        if constexpr (is_hadamard(KL)) return __ldg(static_cast<const float *>(cv.scale[0]) + row);
+        const uint2 s = __ldg(static_cast<const uint2 *>(cv.scale[0]) + row);
+        uint2 z = make_uint2(0u, 0u);
+        if constexpr (KL == KVQ_ASYM4_G32) z = __ldg(reinterpret_cast<const uint2 *>(cv.zero[0]) + row);
+        return token_unit(s, z, KL == KVQ_ASYM4_G32);
+      };
+      float f = g < items ? unit_of(g) : 0.0f;
+      for (int i = g; i < items && ok; i += 4) {
+        const int tile = tile_of(i), blk = nblk == 2 ? i & 1 : 0, it = item_n + i;
         const int t0 = (first + tile) * kTile, t = t0 + lr;
-        const size_t row = token_row(t);
-        float f;                                           // what a code's score is multiplied by
-        if constexpr (is_hadamard(KL)) {
-          f = __ldg(static_cast<const float *>(cv.scale[0]) + row);
-        } else {
-          const uint2 s = __ldg(static_cast<const uint2 *>(cv.scale[0]) + row);
-          uint2 z = make_uint2(0u, 0u);
-          if constexpr (KL == KVQ_ASYM4_G32) z = __ldg(reinterpret_cast<const uint2 *>(cv.zero[0]) + row);
-          f = token_unit(s, z, KL == KVQ_ASYM4_G32);
-        }
+        const float f_next = i + 4 < items ? unit_of(i + 4) : 0.0f;   // in flight while this item is summed
         const int cols = (min(n - blk * kBlk, kBlk) + 31) / 32 * 32;
         const float2 *pr = par + blk * kBlk;
         const bool masked = t0 + kTile - 1 > min_lim;
@@ -343,51 +356,48 @@ __global__ void __launch_bounds__(kThreads, 1) attend_weights_tc_kernel(WeightAr
         asm volatile("tcgen05.fence::after_thread_sync;");
         const uint32_t acc = tmem + lanes + (uint32_t)(it & (kAcc - 1)) * kBlk;
         float w[4] = {0.f, 0.f, 0.f, 0.f};
-        uint32_t cur[32], nxt[32];
-        tm_issue32(acc, cur);
-        tm_wait32(cur);
         for (int c = 0; c < cols; c += 32) {
-          if (c + 32 < cols) tm_issue32(acc + c + 32, nxt);   // in flight while this chunk is summed
+          uint32_t d[32];
+          tm_issue32(acc + c, d);
+          tm_wait32(d);
           if (!masked) {
 #pragma unroll
             for (int k = 0; k < 32; k += 2) {
               const float4 p = *reinterpret_cast<const float4 *>(pr + c + k);
-              w[k & 3] += ex2(fmaf(__uint_as_float(cur[k]) * f, p.x, -p.y));
-              w[(k & 3) + 1] += ex2(fmaf(__uint_as_float(cur[k + 1]) * f, p.z, -p.w));
+              w[k & 3] += ex2(fmaf(__uint_as_float(d[k]) * f, p.x, -p.y));
+              w[(k & 3) + 1] += ex2(fmaf(__uint_as_float(d[k + 1]) * f, p.z, -p.w));
             }
           } else {
 #pragma unroll
             for (int k = 0; k < 32; ++k) {
               const float2 p = pr[c + k];
-              const float e = ex2(fmaf(__uint_as_float(cur[k]) * f, p.x, -p.y));
+              const float e = ex2(fmaf(__uint_as_float(d[k]) * f, p.x, -p.y));
               w[k & 3] += t <= lim[blk * kBlk + c + k] ? e : 0.0f;
             }
-          }
-          if (c + 32 < cols) {
-            tm_wait32(nxt);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) cur[k] = nxt[k];
           }
         }
         asm volatile("tcgen05.fence::before_thread_sync;");   // the reads above precede the next MMAs
         bar_arrive(bar + B_DE + (it & (kAcc - 1)));
-        sums[(g * kMaxTiles + tile) * kTile + lr] += (w[0] + w[1]) + (w[2] + w[3]);
+        // an accumulator's rows of a tile belong to one thread at a time
+        sums[(blk * kMaxTiles + tile) * kTile + lr] += (w[0] + w[1]) + (w[2] + w[3]);
+        f = f_next;
       }
     } else if (warp >= kUnpWarp && warp < kMmaWarp) {
       // ---------------- unpack: one token row per thread
       const int lr = tid - 32 * kUnpWarp;
-      TokenRow<KL> cur;
-      load_row<KL>(cv, token_row(first * kTile + lr), cur);
+#pragma unroll
+      for (int k = 1; k < kAhead; ++k)
+        if (k < n_tiles) prefetch_row<KL>(cv, token_row((first + k) * kTile + lr));
+      TokenRow<KL> t;
       for (int j = 0; j < n_tiles && ok; ++j) {
         const int tn = tile_n + j, buf = tn & 1;
-        TokenRow<KL> nxt = cur;
-        if (j + 1 < n_tiles) load_row<KL>(cv, token_row((first + j + 1) * kTile + lr), nxt);
+        load_row<KL>(cv, token_row((first + j) * kTile + lr), t);
+        if (j + kAhead < n_tiles) prefetch_row<KL>(cv, token_row((first + j + kAhead) * kTile + lr));
         if (tn >= 2) ok = __all_sync(0xffffffffu, bar_wait(bar + B_AE + buf, ((tn >> 1) - 1) & 1));
         if (!ok) break;
-        unpack_token<KL>(cur, sm + buf * S::A, lr);
+        unpack_token<KL>(t, sm + buf * S::A, lr);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         bar_arrive(bar + B_AF + buf);
-        cur = nxt;
       }
     } else if (warp == kMmaWarp && lane == 0) {
       // ---------------- MMA issue (one thread)
@@ -407,11 +417,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_weights_tc_kernel(WeightAr
           const uint32_t id = (1u << 4) | ((cols >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);   // f16, f32 accumulate, K-major
 #pragma unroll
           for (int pass = 0; pass < (HILO ? (QLO ? 3 : 2) : 1); ++pass) {   // hi hi, lo hi, hi lo
-            const uint32_t pa = at + (pass == 1 ? kOperand : 0), pb = bt + (pass == 2 ? kOperand : 0);
+            // a k-step is 32 bytes, four to a column block: the start addresses differ by constants
+            const uint64_t da = sdesc(at + (pass == 1 ? kOperand : 0)), db = sdesc(bt + (pass == 2 ? kOperand : 0));
 #pragma unroll
             for (int ks = 0; ks < kD / 16; ++ks) {
-              const uint32_t o = (ks >> 2) * (kOperand / 2) + 32 * (ks & 3);
-              mma_f16(d, sdesc(pa + o), sdesc(pb + o), id, pass > 0 || ks > 0 ? 1u : 0u);
+              const uint64_t o = ((ks >> 2) * (kOperand / 2) + 32 * (ks & 3)) >> 4;
+              mma_f16(d, da + o, db + o, id, pass > 0 || ks > 0 ? 1u : 0u);
             }
           }
           mma_commit(bar + B_DF + ab);
@@ -443,7 +454,7 @@ template <int KL, bool QLO>
 cudaError_t launch_tc(WeightArgs &wa, cudaStream_t st) {
   static std::atomic<bool> done[kMaxDevices];
   constexpr int body = Smem<!is_hadamard(KL), QLO>::TOTAL;
-  constexpr int smem = is_hadamard(KL) ? max_of(body, window_smem<kD, kWarps>()) : body;
+  constexpr int smem = is_hadamard(KL) ? max_of(body, window_smem<kD, kWarps, kWinRowsTc>()) : body;
   cudaError_t e = set_smem_once(done, attend_weights_tc_kernel<KL, QLO>, smem);
   if (e != cudaSuccess) return e;
   int dev = 0, sms = 148;
