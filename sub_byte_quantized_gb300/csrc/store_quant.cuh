@@ -21,8 +21,8 @@ __device__ __forceinline__ __half f16_sat(float x) {
 // both round alike unless a half-integer lies within 2^-23 of |x / s| <= kTop of them; a thread that finds
 // one of its products within four times that of a half-integer divides (one warp of 512 values in a hundred
 // for 4-bit codes). Rounding is the addition of 1.5 * 2^23 - LO in one fma (nearest even). `divide` sends a
-// thread to the division at once: where fl(1 / s) may overflow; |x| > top does the same for quotients
-// beyond kTop. LEAST: the lowest code, where only the division can fall below it.
+// thread to the division at once: where fl(1 / s) may overflow or s is infinite; |x| > top does the same for
+// quotients beyond kTop. LEAST: the lowest code, where only the division can fall below it.
 constexpr uint32_t kCodeBase = 0x4B400000u;              // the bits of 1.5 * 2^23
 template <int LO, int HI, int LEAST = LO, int N>
 __device__ __forceinline__ void round_codes(const float (&x)[N], float s, float top, bool divide, uint32_t (&code)[N]) {
@@ -185,7 +185,7 @@ __device__ __forceinline__ void quant_had(const CacheView &c, int kv, long long 
   const float s = __fdiv_rn(amax, (float)QMAX);
   uint32_t q[V];
   // codes as offsets from -QMAX - 1, the fields' own offset
-  round_codes<-QMAX - 1, QMAX, -QMAX>(x, s, amax, s < 0x1p-100f, q);
+  round_codes<-QMAX - 1, QMAX, -QMAX>(x, s, amax, !(s >= 0x1p-100f && s <= 0x1p100f), q);
   if (!valid) return;
   const uint32_t w = pack_codes<BITS, true, V>(q);
   uint8_t *prow = (kv ? c.payload[1] : c.payload[0]) + (size_t)crow * row_bytes;
