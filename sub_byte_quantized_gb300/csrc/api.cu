@@ -812,7 +812,7 @@ kvq_status check_rows(const char *name, const kvq_rows *r, int dtype, kvq::RowsI
   const int64_t st[] = {r->batch_stride, r->head_stride, r->token_stride};
   for (int64_t x : st) {
     if (x < 0) return fail(KVQ_EINVAL, "%s has a negative stride", name);
-    if ((x * (int64_t)dtype_bytes(dtype)) % 16) return fail(KVQ_EALIGN, "%s: a stride is not a multiple of 16 bytes", name);
+    if (x % 16 * (int64_t)dtype_bytes(dtype) % 16) return fail(KVQ_EALIGN, "%s: a stride is not a multiple of 16 bytes", name);
   }
   if (!aligned(r->data, 16)) return fail(KVQ_EALIGN, "%s not 16-byte aligned", name);
   in = {r->data, r->batch_stride, r->head_stride, r->token_stride};

@@ -95,8 +95,8 @@ __device__ __forceinline__ int row_limit_of(const AttendArgs &a, const SeqLen &s
 __device__ __forceinline__ uint32_t lds32(const uint8_t *p) { return *reinterpret_cast<const uint32_t *>(p); }
 
 // SIGNED: V codes enter as exact signed values, no offset mass goes through the long P'V accumulation
-// (calls that also score the tokens, whose output is held to float32: error 4e-5 -> see the table of
-// value-path precision).
+// (calls that also score the tokens, whose output is held to float32: over 32K tokens of random keys its
+// error falls from 4e-5 of the output's norm to 1e-6).
 template <int D, bool PAGED, bool SIGNED>
 __global__ void __launch_bounds__(kThreads, kMmaQ6CtasPerSm(D)) attend_mma_q6_kernel(AttendArgs a) {
   using G = Geom<D>;

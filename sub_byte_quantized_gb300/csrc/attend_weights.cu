@@ -15,10 +15,11 @@
 // Decode calls need no second pass over K: their phase 1 leaves its masked scores behind (4 bytes per query
 // row and token, against 72 to 136 for a packed K row, and mostly still in L2), and one small kernel turns
 // them into weights. The others score K again:
-// up to eight query rows per kv head, bound by the K plane's bytes: each warp streams 32-token stages through a private cp.async ring, with the rows' operand fragments in
-// registers; more rows, bound by the tensor pipe and the exponentials; the rows' fragments sit in shared
-// memory (up to 128 rows at a time) and a warp applies each of them to the two tiles of 32 tokens that it
-// holds in registers, so a fragment is read from shared memory once per 32 tokens.
+//   up to eight query rows per kv head   bound by the K plane's bytes: each warp streams 32-token stages
+//       through a private cp.async ring, with the rows' operand fragments in registers
+//   more rows, head_dim 128              attend_weights_tc.cu
+//   more rows, head_dim 256              bound by the tensor pipe and the exponentials: the rows' fragments sit
+//       in shared memory, 64 rows at a time, and a warp applies them to 16 tokens that it holds in registers
 #include "attend_weights.cuh"
 
 namespace kvq {
@@ -30,9 +31,7 @@ constexpr int kManyWarps = 8;            // warps per CTA, more rows
 constexpr int kStage = 32;               // tokens of a stage or of a warp's unit
 constexpr int kRing = 3;                 // stages per warp in shared memory
 
-// Query rows in shared memory at a time.
-template <int D, bool SPLIT>
-__host__ __device__ constexpr int pass_rows() { return D == 128 && !SPLIT ? 128 : 64; }
+constexpr int kPassRows = 64;             // query rows in shared memory at a time, more rows
 // The rows' operand fragments (hi, then lo), block sums, alpha, lse and limit, and a row buffer per warp.
 template <int D, bool SPLIT, int ROWS, int WARPS>
 __host__ __device__ constexpr int rows_smem() { return ROWS * D * 2 * (SPLIT ? 2 : 1) + ROWS * (D / 32 + 3) * 4 + WARPS * D * 4; }
@@ -551,15 +550,13 @@ __global__ void __launch_bounds__(32 * kFewWarps, D == 128 && !SPLIT ? 5 : 1) at
   asm volatile("cp.async.wait_group 0;\n" ::: "memory");
 }
 
-// More than eight query rows. A CTA takes `units` groups of 32 tokens, dealt to its warps in turn.
+// More than eight query rows, head_dim 256. A CTA takes `units` groups of 32 tokens, dealt to its warps in turn.
 // PASSES: more rows than shared memory holds at a time; a warp then keeps the sums of its kManyUnits units
 // across the passes (and reads their packed rows again from the cache).
 constexpr int kManyUnits = 4;
-template <int KL, int D, bool SPLIT, bool PASSES>
+template <int KL, bool SPLIT, bool PASSES>
 __global__ void __launch_bounds__(32 * kManyWarps, 2) attend_weights_many_kernel(WeightArgs wa) {
-  constexpr int NB = D / 32, ROWS = pass_rows<D, SPLIT>();
-  // tiles a warp holds at once: 32 tokens, or 16 where their fragments would not fit the registers
-  constexpr int MT = D == 128 ? 2 : 1;
+  constexpr int D = 256, NB = D / 32, ROWS = kPassRows;
   extern __shared__ __align__(16) uint8_t smem[];
   const AttendArgs &a = wa.a;
   const CacheView &cv = a.cache;
@@ -615,15 +612,12 @@ __global__ void __launch_bounds__(32 * kManyWarps, 2) attend_weights_many_kernel
       float w[4] = {0.f, 0.f, 0.f, 0.f};
       const bool masked = t0 + kStage - 1 > min_lim;
 #pragma unroll 1
-      for (int half = 0; half < 2 / MT; ++half) {
-        Tile<KL, D> t[MT];
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          // a unit's second tile may lie behind the body: it then repeats the last token of the first
-          const int tt = t0 + 16 * (half + m);
-          load_global_tile<KL, D>(cv, bb, kvh, tt <= t_last ? tt : t0, t_last, g, c, t[m]);
-        }
-        float sum[MT][2] = {};
+      for (int half = 0; half < 2; ++half) {              // the fragments of 16 tokens fit the registers
+        Tile<KL, D> tl;
+        // a unit's second tile may lie behind the body: it then repeats the last token of the first
+        const int tt = t0 + 16 * half;
+        load_global_tile<KL, D>(cv, bb, kvh, tt <= t_last ? tt : t0, t_last, g, c, tl);
+        float sum[2] = {};
 #pragma unroll 1
         for (int nt = 0; nt < n_tiles; ++nt) {
           const uint4 *f = frag + nt * NB * 32 + lane;
@@ -632,26 +626,14 @@ __global__ void __launch_bounds__(32 * kManyWarps, 2) attend_weights_many_kernel
           int2 lim = make_int2(0, 0);
           if (masked) lim = *reinterpret_cast<const int2 *>(p.limit + 8 * nt + 2 * c);
           const float *q0 = qsum + (8 * nt + 2 * c) * NB;
-          uint4 B[(SPLIT ? 2 : 1) * NB];
-          if constexpr (MT > 1) {
-#pragma unroll
-            for (int b = 0; b < (SPLIT ? 2 : 1) * NB; ++b) B[b] = b < NB ? f[b * 32] : f[(ROWS / 8 * NB + b - NB) * 32];
-          }
-          auto get = [&](int b) {
-            if constexpr (MT > 1) return B[b];
-            else return b < NB ? f[b * 32] : f[(ROWS / 8 * NB + b - NB) * 32];
-          };
-#pragma unroll
-          for (int m = 0; m < MT; ++m)
-            add_rows<KL, D, SPLIT>(t[m], get, al, ls, lim, q0, q0 + NB, t0 + 16 * (half + m), masked, g, sum[m]);
+          auto get = [&](int b) { return b < NB ? f[b * 32] : f[(ROWS / 8 * NB + b - NB) * 32]; };
+          add_rows<KL, D, SPLIT>(tl, get, al, ls, lim, q0, q0 + NB, tt, masked, g, sum);
         }
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            if (MT > 1) w[2 * m + k] = sum[m][k];
-            else w[k] = half == 0 ? sum[0][k] : w[k], w[2 + k] = half == 1 ? sum[0][k] : w[2 + k];
-          }
+        for (int k = 0; k < 2; ++k) {
+          w[k] = half == 0 ? sum[k] : w[k];
+          w[2 + k] = half == 1 ? sum[k] : w[2 + k];
+        }
       }
       if constexpr (PASSES) {
 #pragma unroll
@@ -739,10 +721,10 @@ cudaError_t launch_scores_rows(WeightArgs &wa, cudaStream_t st) {
   return wa.a.s_rows == 4 ? launch_scores<4, D, HAD>(wa, st) : launch_scores<8, D, HAD>(wa, st);
 }
 
-template <int KL, int D, bool SPLIT, bool PASSES>
+template <int KL, bool SPLIT, bool PASSES>
 cudaError_t launch_many(WeightArgs &wa, cudaStream_t st) {
   static std::atomic<bool> done[kMaxDevices];
-  constexpr int rows = rows_smem<D, SPLIT, pass_rows<D, SPLIT>(), kManyWarps>();
+  constexpr int D = 256, rows = rows_smem<D, SPLIT, kPassRows, kManyWarps>();
   constexpr int smem = is_hadamard(KL) ? max_of(rows, window_smem<D, kManyWarps>()) : rows;
   // two CTAs per SM: the units of a head shared out over one wave (a warp keeps at most kManyUnits
   // across passes)
@@ -753,7 +735,7 @@ cudaError_t launch_many(WeightArgs &wa, cudaStream_t st) {
   if (PASSES) wa.units = min(wa.units, kManyUnits * kManyWarps);
   wa.units = max(wa.units, kManyWarps);
   wa.n_ctas = (n_units + wa.units - 1) / wa.units;
-  return launch_one<KL, D>(attend_weights_many_kernel<KL, D, SPLIT, PASSES>, wa, kManyWarps, smem, done, st);
+  return launch_one<KL, D>(attend_weights_many_kernel<KL, SPLIT, PASSES>, wa, kManyWarps, smem, done, st);
 }
 
 template <int KL, int D, bool SPLIT>
@@ -761,7 +743,7 @@ cudaError_t launch_rows(WeightArgs &wa, cudaStream_t st) {
   const int rows = wa.a.gqa * wa.a.n_q;
   if (rows <= 8) return launch_few<KL, D, SPLIT>(wa, st);
   if constexpr (D == 128) return launch_attend_weights_tc(wa, st);
-  else return rows <= pass_rows<D, SPLIT>() ? launch_many<KL, D, SPLIT, false>(wa, st) : launch_many<KL, D, SPLIT, true>(wa, st);
+  else return rows <= kPassRows ? launch_many<KL, SPLIT, false>(wa, st) : launch_many<KL, SPLIT, true>(wa, st);
 }
 
 template <int KL, int D>

@@ -1,0 +1,99 @@
+"""The cache-budget operators at sizes where their kernels change form: groups of query rows, tiles beyond one
+CTA's share, more heads than SMs, planes beyond 4 GB."""
+import numpy as np
+import pytest
+import torch
+
+import sub_byte_quantized_gb300 as kvq
+from oracle import rope as OR
+from tests.test_gpu_budget import LAYOUTS, _check
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("dtype,Hq,nq", [("bf16", 2, 150), ("f32", 2, 70), ("f16", 4, 33)])
+def test_weights_row_groups(layout, dtype, Hq, nq):
+    """300 rows of 16-bit queries, 140 of f32: a second group over the same tokens; 132 rows: two accumulators."""
+    w = 50 if "had" in layout else 0
+    _check(layout, 128, 1, Hq, 1, 290, nq, causal=True, dtype=dtype, n_recent=w)
+    _check(layout, 128, 1, Hq, 1, 131, nq, dtype=dtype, n_recent=w)
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_weights_row_passes_of_wide_heads(layout, dtype):
+    w = 33 if "had" in layout else 0
+    _check(layout, 256, 1, 8, 2, 300, 20, causal=True, dtype=dtype, n_recent=w)   # 80 rows
+    _check(layout, 256, 1, 2, 1, 100, 32, dtype=dtype, n_recent=w)                # 64: one pass
+
+
+def test_weights_more_heads_than_sms():
+    """Tiles (or units) of a head in as few CTAs as hold them."""
+    _check("q4_0", 128, 20, 24, 8, 2200, 3, causal=True)                          # 18 tiles: 16 and 2
+    _check("had_int4", 128, 20, 24, 8, 300, 3, causal=True, n_recent=40)
+    _check("q6_0", 256, 20, 40, 20, 500, 35, causal=True)                         # 70 rows, 16 units
+    _check("asym4_g32", 256, 20, 40, 20, 300, 2)
+
+
+@pytest.mark.parametrize("layout", ["q4_0", "q8_0", "had_int4"])
+@pytest.mark.parametrize("D", [128, 256])
+def test_weights_shortest(layout, D):
+    """One token under many rows, a window that holds every token, one that leaves one."""
+    for S, nq, w in ((1, 20, 0), (1, 1, 0), (5, 12, 8), (9, 3, 8)):
+        _check(layout, D, 1, 2, 1, S, nq, n_recent=w if "had" in layout else 0)
+        if nq <= S:
+            _check(layout, D, 1, 2, 1, S, nq, causal=True, q_pos0=0, n_recent=w if "had" in layout else 0)
+
+
+def test_planes_beyond_four_gigabytes():
+    """Rows of 128 bytes behind byte 2^32 of a plane: appended, weighed, selected and moved."""
+    H, D, far = 4, 128, 1 << 23
+    n = far + 5
+    dc = kvq.KVCache("q8_0", 1, H, D, n)
+    for p in dc.planes.values():
+        for t in p.values():
+            t.zero_()
+    g = torch.Generator().manual_seed(1)
+    k, v = (torch.randn((1, H, 5, D), generator=g) for _ in range(2))
+    f, _ = kvq.rope_frequencies(D)
+    table = kvq.rope_table(f, 5, pos0=far)
+    pos = torch.arange(5, dtype=torch.int32, device="cuda")[None]
+    kvq.rope_store(dc, table, k.cuda(), v.cuda(), far, positions=pos)
+    small = kvq.KVCache("q8_0", 1, H, D, 5)
+    kvq.store(small, torch.from_numpy(OR.rotate(k.numpy(), table.cpu().numpy()[None, None])).cuda(), v.cuda(), 0)
+    for t in ("k", "v"):
+        for name, x in small.planes[t].items():
+            assert torch.equal(dc.planes[t][name][:, :, far:], x)
+    # weights: the zero rows all score 0, the last five their own dot products; the sums of 2^23 exponentials
+    # are float32 with at most 2^13 additions in a row
+    q = torch.randn((1, H, 9, D), generator=g)
+    kd = small.planes["k"]["payload"].cpu().numpy().view(np.int8).reshape(H, 5, D // 32, 32).astype(np.float64)
+    kd = (kd * small.planes["k"]["scale"].cpu().numpy().astype(np.float64)[0][..., None]).reshape(H, 5, D)
+    for nq in (1, 9):
+        qq = q[:, :, :nq].contiguous()
+        alpha = 1.0                                              # (far above 1 / sqrt(D): the five stand out)
+        s = np.einsum("hrd,htd->hrt", qq[0].numpy().astype(np.float64), kd) * alpha
+        total = far + np.exp(s).sum(-1)
+        scores = torch.zeros((1, H, n), device="cuda")
+        kvq.decode_attend_weights(dc, qq.cuda(), n, None, scores_out=scores, attn_scale=alpha)
+        want = (np.exp(s) / total[..., None]).sum(1)
+        got = scores[0, :, far:].cpu().numpy()
+        assert (np.abs(got - want) <= 2.0 ** -10 * want).all()
+        rest = (1 / total).sum(1)
+        lo, hi = scores[0, :, :far].min(1).values.cpu().numpy(), scores[0, :, :far].max(1).values.cpu().numpy()
+        assert (np.abs(lo - rest) <= 2.0 ** -10 * rest).all() and (np.abs(hi - rest) <= 2.0 ** -10 * rest).all()
+    scores[0, :, ::1 << 20] = 2.0                                # eight far apart
+    keep = kvq.evict_select(scores, n, 13, n_recent=5)
+    want = torch.cat([torch.arange(0, far, 1 << 20), torch.arange(far, n)]).int().cuda()
+    assert torch.equal(keep, want.expand(1, H, 13))
+    dst = kvq.KVCache("q8_0", 1, H, D, 13)
+    so = torch.empty((1, H, 13), device="cuda")
+    last = scores[:, :, far:].clone()
+    kvq.evict_compact(dc, keep, n, dst=dst, scores=scores, scores_out=so)
+    kvq.evict_compact(dc, keep, n, scores=scores)
+    for c in (dc, dst):
+        for t in ("k", "v"):
+            for name, x in small.planes[t].items():
+                assert torch.equal(c.planes[t][name][:, :, 8:13], x) and not c.planes[t][name][:, :, :8].any()
+    assert torch.equal(so[:, :, 8:], last) and torch.equal(scores[:, :, :13], so) and not scores[:, :, 13:].any()
