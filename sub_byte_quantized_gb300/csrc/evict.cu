@@ -4,11 +4,11 @@
 // Selection, per (batch, kv head): of L tokens the first n_sink and the last n_recent stay; among the
 // others the k with the highest scores, ties going to the lowest index. That set is {score > T} and the
 // first few of {score == T}, T being the k-th highest score: a radix selection over order-preserving
-// 32-bit keys finds T in three digits (11, 11 and 10 bits), then one ordered pass writes the list in
+// 32-bit keys finds T in three digits (12, 10 and 10 bits), then one ordered pass writes the list in
 // ascending order. One cluster works on one (batch, kv head): every CTA keeps its slice of the keys in
-// shared memory, so the scores are read from memory once; the digits' histograms and the slices' counts
-// are summed over distributed shared memory. Bound by latency (load, three histogram rounds, the
-// ordered pass), not by its bytes.
+// shared memory, so the scores are read from memory once; the digits' counts are summed over distributed
+// shared memory. Bound by latency (load, three histogram rounds, the ordered pass), not by its bytes: SELECT_BIG
+// us for 32K of 128K tokens in 8 heads, SELECT_SMALL for 1021 of up to 4099 in 256 heads.
 //
 // Compaction: row keep[i] of every plane moves to row i. keep ascends, so keep[i] >= i: a round reads
 // the sources of the next block of target rows, everyone waits until all of the cluster's reads have
@@ -28,26 +28,71 @@ namespace {
 namespace cg = cooperative_groups;
 
 // ------------------------------------------------------------------------------------ selection
-constexpr int kBins = 2048;
-template <int THREADS>
-__host__ __device__ constexpr int select_fixed() { return (3 * kBins + 2 * (THREADS / 32) + 4) * 4; }   // histograms, per-warp counts, results
+// Digits of 12, 10 and 10 bits: the first one's histogram takes every key, and at 12 bits (sign, exponent and three
+// bits of the fraction) fewer of a warp's keys meet in one counter.
+__host__ __device__ constexpr int digit_shift(int d) { return d == 0 ? 20 : d == 1 ? 10 : 0; }
+__host__ __device__ constexpr int digit_bins(int d) { return d == 0 ? 4096 : 1024; }
+__host__ __device__ constexpr int digit_at(int d) { return d == 0 ? 0 : 4096 + 1024 * (d - 1); }   // its first counter
+constexpr int kBins = digit_at(3), kGroups = kBins / 32;   // counters; their sums in groups of 32
+template <int THREADS>                   // histograms, their groups' sums, per-warp counts, results
+__host__ __device__ constexpr int select_fixed() { return (kBins + kGroups + 2 * (THREADS / 32) + 4) * 4; }
 constexpr int kSelMaxKeys = (227 * 1024 - select_fixed<1024>()) / 4 / 128 * 128;   // keys one CTA can hold
 
-// Keys compare like the scores: NaN counts as -infinity, -0 as +0.
+// Keys compare like the scores: NaN counts as -infinity, -0 as +0. No score has a key below 2^22: key 0 stands for
+// "no token", and what it adds to the lowest counter is never reached.
 __device__ __forceinline__ uint32_t score_key(float x) {
   if (x != x) x = -INFINITY;
   const uint32_t u = __float_as_uint(x + 0.0f);
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+// One warp: among the bins of which each lane holds OWN neighbouring ones (`c`: their counts, all slices; `before`:
+// in the slices before this one), the bin of the key that has `want` - 1 keys over it, `above` of them in bins
+// over all of these. Sets `above` to what lies over that bin, adds the earlier slices' keys over it to `gt`, and
+// returns its index; `at` its earlier slices' count.
+template <int OWN>
+__device__ __forceinline__ int find_bin(const uint32_t (&c)[OWN], const uint32_t (&before)[OWN], uint32_t want, int lane,
+                                        uint32_t &above, uint32_t &gt, uint32_t &at) {
+  uint32_t own = 0;
+#pragma unroll
+  for (int j = 0; j < OWN; ++j) own += c[j];
+  uint32_t over = own;                                   // suffix sums: the counts of this lane and those above
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const uint32_t o = __shfl_down_sync(0xffffffffu, over, m);
+    if (lane + m < 32) over += o;
+  }
+  over += above - own;
+  int hit = -1;
+  uint32_t hit_over = 0;
+#pragma unroll
+  for (int j = OWN - 1; j >= 0; --j) {
+    if (over < want && want <= over + c[j]) hit = j, hit_over = over;
+    over += c[j];
+  }
+  const int from = __ffs(__ballot_sync(0xffffffffu, hit >= 0)) - 1;
+  const int bin = OWN * from + __shfl_sync(0xffffffffu, hit, from);
+  above = __shfl_sync(0xffffffffu, hit_over, from);
+  uint32_t more = 0, here = 0;
+#pragma unroll
+  for (int j = 0; j < OWN; ++j) {
+    if (OWN * lane + j > bin) more += before[j];
+    if (OWN * lane + j == bin) here = before[j];
+  }
+  gt += __reduce_add_sync(0xffffffffu, more);
+  at = __shfl_sync(0xffffffffu, here, from);
+  return bin;
+}
+
 // RESIDENT: the slice's keys fit shared memory (else every pass reads the scores again).
 template <int THREADS, bool RESIDENT>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_select_kernel(SelectArgs a) {
-  constexpr int WARPS = THREADS / 32, OWN = kBins / THREADS;   // bins per thread, neighbouring
+  constexpr int WARPS = THREADS / 32;
+  constexpr int RANKS = THREADS == 512 ? 1 : 8;          // CTAs of a cluster, at most
   extern __shared__ __align__(16) uint32_t sm[];
-  uint32_t *hist = sm;                                   // [3][kBins]
-  uint32_t *wcount = sm + 3 * kBins;                     // [2][WARPS]
-  uint32_t *res = wcount + 2 * WARPS;                    // digit, rank inside it
+  uint32_t *hist = sm, *group = hist + kBins;
+  uint32_t *wcount = group + kGroups;                    // [2][WARPS]
+  uint32_t *res = wcount + 2 * WARPS;                    // digit, rank inside it; earlier slices' keys over T, equal to T
   uint32_t *keys = res + 4;
   cg::cluster_group cl = cg::this_cluster();
   const int rank = (int)cl.block_rank(), ranks = (int)cl.num_blocks();
@@ -67,160 +112,193 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_select_kernel(S
   }
   const int k = a.n_keep - a.n_sink - a.n_recent;
   if (k == 0) return;                                    // the same for every CTA
-  const int per = ((hi - lo + ranks - 1) / ranks + 31) / 32 * 32;
-  const int s0 = (int)min((long long)hi, lo + (long long)rank * per);   // this CTA's slice [s0, s0 + n)
-  const int n = min(per, hi - s0);
+  // this CTA's slice [s0, s0 + n), from a multiple of four on; in shared memory np keys, a multiple of 128
+  const int lo4 = lo & ~3, per = ((hi - lo4 + ranks - 1) / ranks + 31) / 32 * 32;
+  const int s0 = (int)min((long long)hi, lo4 + (long long)rank * per);
+  const int n = min(per, hi - s0), np = (n + 127) / 128 * 128;
   const float *score = a.scores + (size_t)bh * a.stride + s0;
-  auto key_at = [&](int i) { return RESIDENT ? keys[i] : score_key(__ldg(score + i)); };
+  auto key_of = [&](int i, float x) { return i < n && s0 + i >= lo ? score_key(x) : 0u; };
+  auto four = [&](int i, uint32_t (&key)[4]) {
+    if constexpr (RESIDENT) {
+      const uint4 v = *reinterpret_cast<const uint4 *>(keys + i);
+      key[0] = v.x; key[1] = v.y; key[2] = v.z; key[3] = v.w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) key[j] = key_of(i + j, i + j < n ? __ldg(score + i + j) : 0.0f);
+    }
+  };
   if constexpr (RESIDENT) {
-#pragma unroll 8
-    for (int i = tid; i < n; i += THREADS) keys[i] = score_key(__ldg(score + i));
+    if (a.stride % 4 == 0) {                             // rows and slices begin at 16-byte boundaries
+#pragma unroll 1
+      for (int i0 = 4 * tid; i0 < np; i0 += 16 * THREADS) {   // four loads in flight
+        float4 v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int i = i0 + 4 * THREADS * u;
+          v[u] = i < n ? __ldg(reinterpret_cast<const float4 *>(score + i)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int i = i0 + 4 * THREADS * u;
+          if (i < np)
+            *reinterpret_cast<uint4 *>(keys + i) = make_uint4(key_of(i, v[u].x), key_of(i + 1, v[u].y), key_of(i + 2, v[u].z), key_of(i + 3, v[u].w));
+        }
+      }
+    } else {
+#pragma unroll 4
+      for (int i = tid; i < np; i += THREADS) keys[i] = key_of(i, i < n ? __ldg(score + i) : 0.0f);
+    }
   }
-  for (int i = tid; i < 3 * kBins; i += THREADS) hist[i] = 0;
+  for (int i = tid; i < kBins; i += THREADS) hist[i] = 0;
   __syncthreads();
-  uint32_t prefix = 0, mask = 0, want = (uint32_t)k;      // T's digits so far, and the rank inside them
+  uint32_t prefix = 0, want = (uint32_t)k;               // T's digits so far, and the rank inside them
   uint32_t gt = 0, eq = 0;                               // keys over / equal to T in the slices before this one
 #pragma unroll
   for (int d = 0; d < 3; ++d) {
-    const int shift = d == 0 ? 21 : (d == 1 ? 10 : 0);
-    const uint32_t width = d == 2 ? 1024u : 2048u;
-    uint32_t *h = hist + d * kBins;
-    for (int i0 = warp * 128; i0 < n; i0 += 4 * THREADS) {  // whole warps: the votes below need all lanes
-      const int i = i0 + 4 * lane;                          // four keys per lane
+    const int shift = digit_shift(d), bins = digit_bins(d);
+    uint32_t *h = hist + digit_at(d), *gr = group + digit_at(d) / 32;
+    for (int i0 = warp * 128; i0 < np; i0 += 4 * THREADS) { // whole warps: the votes below need all lanes
       uint32_t key[4];
-      if constexpr (RESIDENT) {
-        const uint4 v = *reinterpret_cast<const uint4 *>(keys + i);   // (the keys' space is a multiple of 128)
-        key[0] = v.x; key[1] = v.y; key[2] = v.z; key[3] = v.w;
-      } else {
+      four(i0 + 4 * lane, key);
+      bool in[4] = {true, true, true, true};
+      if (d > 0) {                                       // keys whose higher digits are T's
 #pragma unroll
-        for (int j = 0; j < 4; ++j) key[j] = i + j < n ? key_at(i + j) : 0;
+        for (int j = 0; j < 4; ++j) in[j] = key[j] >> digit_shift(d - 1) == prefix;
+        if (!__any_sync(0xffffffffu, in[0] || in[1] || in[2] || in[3])) continue;
       }
-      bool in[4], any = false;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        in[j] = i + j < n && (key[j] & mask) == prefix;
-        any |= in[j];
-      }
-      if (!__any_sync(0xffffffffu, any)) continue;
+      for (int j = 0; j < 4; ++j) key[j] = (key[j] >> shift) & (bins - 1);
       // long runs of one score (zeros) would serialise on one counter: count such a group at once
-      const uint32_t first = __shfl_sync(0xffffffffu, (key[0] >> shift) & (width - 1), 0);
-      bool same = true;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        key[j] = (key[j] >> shift) & (width - 1);
-        same &= in[j] && key[j] == first;
+      if (d == 0 || __all_sync(0xffffffffu, in[0] && in[1] && in[2] && in[3])) {
+        const uint32_t first = __shfl_sync(0xffffffffu, key[0], 0);
+        const uint32_t other = (key[0] ^ first) | (key[1] ^ first) | (key[2] ^ first) | (key[3] ^ first);
+        if (__all_sync(0xffffffffu, other == 0)) {
+          if (lane == 0) atomicAdd(h + first, 128u);
+          continue;
+        }
       }
-      if (__all_sync(0xffffffffu, same)) {
-        if (lane == 0) atomicAdd(h + first, 128u);
-      } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (in[j]) atomicAdd(h + key[j], 1u);
-      }
+      for (int j = 0; j < 4; ++j)
+        if (in[j]) atomicAdd(h + key[j], 1u);
+    }
+    __syncthreads();
+    // sums of the groups of 32 bins: the search below reads these and then 32 bins from every slice, not the
+    // whole histograms (8 KB from each of eight CTAs and digit over the cluster's network: 3 to 5 thousand cycles)
+    {
+      const int own = bins / THREADS;                    // neighbouring bins of a thread, a power of two
+      uint32_t c = 0;
+      for (int j = 0; j < own; ++j) c += h[own * tid + j];
+      for (int m = 1; m < 32 / own; m <<= 1) c += __shfl_xor_sync(0xffffffffu, c, m);
+      if (own * tid % 32 == 0) gr[own * tid / 32] = c;
     }
     cl.sync();                                           // every slice is counted
-    // thread t owns bins OWN t .. OWN t + OWN - 1; the counts above them by a suffix scan over warps
-    uint32_t c[OWN] = {}, before[OWN] = {};              // all slices; the slices before this one
-    for (int r = 0; r < ranks; ++r) {
-      const uint32_t *o = cl.map_shared_rank(h, r) + OWN * tid;
+    if (warp == 0) {
+      uint32_t above = 0, at;
+      int g;
+      // (the slices' words are asked for together: one latency, not eight)
+      if (d == 0) {
+        uint32_t c[4] = {}, b[4] = {};                   // 128 groups, else 32
+        uint4 v[RANKS];
 #pragma unroll
-      for (int j = 0; j < OWN; j += 2) {
-        const uint2 v = *reinterpret_cast<const uint2 *>(o + j);
-        c[j] += v.x;
-        c[j + 1] += v.y;
-        before[j] += r < rank ? v.x : 0;
-        before[j + 1] += r < rank ? v.y : 0;
+        for (int r = 0; r < RANKS; ++r) v[r] = reinterpret_cast<const uint4 *>(cl.map_shared_rank(gr, min(r, ranks - 1)))[lane];
+#pragma unroll
+        for (int r = 0; r < RANKS; ++r) {
+          const uint32_t w[4] = {v[r].x, v[r].y, v[r].z, v[r].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            c[j] += r < ranks ? w[j] : 0;
+            b[j] += r < rank ? w[j] : 0;
+          }
+        }
+        g = find_bin(c, b, want, lane, above, gt, at);
+      } else {
+        uint32_t c[1] = {}, b[1] = {}, v[RANKS];
+#pragma unroll
+        for (int r = 0; r < RANKS; ++r) v[r] = cl.map_shared_rank(gr, min(r, ranks - 1))[lane];
+#pragma unroll
+        for (int r = 0; r < RANKS; ++r) {
+          c[0] += r < ranks ? v[r] : 0;
+          b[0] += r < rank ? v[r] : 0;
+        }
+        g = find_bin(c, b, want, lane, above, gt, at);
       }
-    }
-    if (d == 2) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");   // the last remote reads
-    uint32_t own = 0;
+      uint32_t c[1] = {}, b[1] = {}, v[RANKS];
 #pragma unroll
-    for (int j = 0; j < OWN; ++j) own += c[j];
-    uint32_t suf = own;
+      for (int r = 0; r < RANKS; ++r) v[r] = cl.map_shared_rank(h, min(r, ranks - 1))[32 * g + lane];
 #pragma unroll
-    for (int m = 1; m < 32; m <<= 1) {
-      const uint32_t o = __shfl_down_sync(0xffffffffu, suf, m);
-      if (lane + m < 32) suf += o;
-    }
-    if (lane == 0) wcount[warp] = suf;
-    __syncthreads();
-    uint32_t above = lane > warp && lane < WARPS ? wcount[lane] : 0;   // in the warps of higher bins
-#pragma unroll
-    for (int m = 16; m; m >>= 1) above += __shfl_xor_sync(0xffffffffu, above, m);
-    above += suf - own;
-#pragma unroll
-    for (int j = OWN - 1; j >= 0; --j) {                 // above = keys in the bins over bin j
-      if (above < want && want <= above + c[j]) {
-        res[0] = OWN * tid + j;
+      for (int r = 0; r < RANKS; ++r) {
+        c[0] += r < ranks ? v[r] : 0;
+        b[0] += r < rank ? v[r] : 0;
+      }
+      const int bin = 32 * g + find_bin(c, b, want, lane, above, gt, at);
+      if (lane == 0) {
+        res[0] = bin;
         res[1] = want - above;
+        res[2] = gt;
+        res[3] = at;
       }
-      above += c[j];
     }
     __syncthreads();
-    const uint32_t digit = res[0];
+    if (d == 2) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");   // the last remote reads
+    prefix = d == 0 ? res[0] : prefix * bins + res[0];
     want = res[1];
-    prefix |= digit << shift;
-    mask |= (width - 1) << shift;
-#pragma unroll
-    for (int j = 0; j < OWN; ++j) {
-      const uint32_t bin = OWN * tid + j;
-      if (bin > digit) gt += before[j];
-      if (d == 2 && bin == digit) eq += before[j];
-    }
-    __syncthreads();                                     // res and wcount are written again
   }
-  // block sums of gt and eq (each key counted by one thread)
-#pragma unroll
-  for (int m = 16; m; m >>= 1) {
-    gt += __shfl_xor_sync(0xffffffffu, gt, m);
-    eq += __shfl_xor_sync(0xffffffffu, eq, m);
-  }
-  if (lane == 0) {
-    wcount[warp] = gt;
-    wcount[WARPS + warp] = eq;
-  }
-  __syncthreads();
-  gt = lane < WARPS ? wcount[lane] : 0;
-  eq = lane < WARPS ? wcount[WARPS + lane] : 0;
-  __syncthreads();
-  // `want` of the keys equal to T stay. This slice's greater and equal keys by warp sub-slice.
-  const int sub = ((n + WARPS - 1) / WARPS + 31) / 32 * 32;
-  const int w0 = min(n, warp * sub), w1 = min(n, w0 + sub);
+  gt = res[2];
+  eq = res[3];
+  // `want` of the keys equal to T stay, in order. Mostly a slice keeps all of its own or none: then what it keeps
+  // are its keys from a bound on. Warps take sub-slices in order: each counts what it keeps, and writes behind those
+  // before it.
+  const int sub = ((n + WARPS - 1) / WARPS + 127) / 128 * 128;
+  const int w0 = min(np, warp * sub), w1 = min(np, w0 + sub);
+  const uint32_t own = hist[digit_at(2) + (prefix & (digit_bins(2) - 1))];   // the slice's keys equal to T
+  const uint32_t stay = eq >= want ? 0 : min(own, want - eq);
+  const uint32_t bound = stay == 0 ? prefix + 1 : prefix;
+  const bool some = stay > 0 && stay < own;              // (the same for the whole CTA)
   uint32_t ng = 0, ne = 0;
-#pragma unroll 4
-  for (int i = w0 + lane; i < w1; i += 32) {
-    const uint32_t key = key_at(i);
-    ng += key > prefix;
-    ne += key == prefix;
-  }
+#pragma unroll 2
+  for (int i = w0 + 4 * lane; i < w1; i += 128) {
+    uint32_t key[4];
+    four(i, key);
 #pragma unroll
-  for (int m = 16; m; m >>= 1) {
-    ng += __shfl_xor_sync(0xffffffffu, ng, m);
-    ne += __shfl_xor_sync(0xffffffffu, ne, m);
+    for (int j = 0; j < 4; ++j) {
+      ng += key[j] >= bound;
+      if (some) ne += key[j] == prefix;
+    }
   }
+  ng = __reduce_add_sync(0xffffffffu, ng);
+  ne = __reduce_add_sync(0xffffffffu, ne);
   if (lane == 0) {
     wcount[warp] = ng;
     wcount[WARPS + warp] = ne;
   }
   __syncthreads();
-  gt += lane < warp ? wcount[lane] : 0;
-  eq += lane < warp ? wcount[WARPS + lane] : 0;
-#pragma unroll
-  for (int m = 16; m; m >>= 1) {
-    gt += __shfl_xor_sync(0xffffffffu, gt, m);
-    eq += __shfl_xor_sync(0xffffffffu, eq, m);
-  }
-  for (int i0 = w0; i0 < w1; i0 += 32) {
-    const int i = i0 + lane;
-    const uint32_t key = i < w1 ? key_at(i) : 0;
-    const bool g = i < w1 && key > prefix, e = i < w1 && key == prefix;
-    const unsigned mg = __ballot_sync(0xffffffffu, g), me = __ballot_sync(0xffffffffu, e);
-    const unsigned below = (1u << lane) - 1u;
-    const uint32_t eq_rank = eq + __popc(me & below);
-    if (g || (e && eq_rank < want))
-      keep[a.n_sink + gt + __popc(mg & below) + min(eq_rank, want)] = s0 + i;
-    gt += __popc(mg);
-    eq += __popc(me);
+  keep += a.n_sink;
+  uint32_t at = gt + min(eq, want) + __reduce_add_sync(0xffffffffu, lane < warp ? wcount[lane] : 0);
+  auto key_at = [&](int i) -> uint32_t {
+    if constexpr (RESIDENT) return keys[i];
+    else return key_of(i, i < n ? __ldg(score + i) : 0.0f);
+  };
+  const unsigned below = (1u << lane) - 1u;
+  if (!some) {
+#pragma unroll 4
+    for (int i = w0 + lane; i < w1; i += 32) {
+      const bool in = key_at(i) >= bound;
+      const unsigned m = __ballot_sync(0xffffffffu, in);
+      if (in) keep[at + __popc(m & below)] = s0 + i;
+      at += __popc(m);
+    }
+  } else {                                               // the first `stay` of the keys equal to T
+    uint32_t rank_eq = __reduce_add_sync(0xffffffffu, lane < warp ? wcount[WARPS + lane] : 0);
+    at -= rank_eq - min(rank_eq, stay);                   // (the counts took all of them)
+    for (int i = w0 + lane; i < w1; i += 32) {
+      const uint32_t key = key_at(i);
+      const unsigned me = __ballot_sync(0xffffffffu, key == prefix);
+      const bool in = key > prefix || (key == prefix && rank_eq + __popc(me & below) < stay);
+      const unsigned m = __ballot_sync(0xffffffffu, in);
+      if (in) keep[at + __popc(m & below)] = s0 + i;
+      at += __popc(m);
+      rank_eq += __popc(me);
+    }
   }
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");   // no CTA leaves while another reads its counts
 }

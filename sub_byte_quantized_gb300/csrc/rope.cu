@@ -3,8 +3,9 @@
 // Table. Row p holds cos(p f_i) m, i = 0 .. h-1, then sin(p f_i) m, h = rot_dim / 2. A far position's
 // angle has lost its fraction of a turn in float32 (p f = 1e5 leaves 2^-7 of a radian), so the angle is
 // counted in turns: f_i / 2 pi as a 64-bit binary fraction, and p times it in wrapping 64-bit integers,
-// which takes whole turns off exactly. The nearest quarter turn goes into signs and a swap; what is
-// left, in [-1/8, 1/8) of a turn, is rounded to float32 once and goes into two short polynomials.
+// which takes whole turns off exactly. The upper 32 bits, rounded, are the angle (off by 2^-33 of a turn: 7e-10
+// in the entry, an eightieth of a rounding of the entries near 1). The nearest quarter turn goes into signs and a
+// swap; what is left, in [-1/8, 1/8) of a turn, is rounded to float32 and goes into two short polynomials.
 //
 // Append with rotary positions. One launch reads q, k and v from wherever their projection left them
 // (any strides between batches, heads and tokens), rotates q and k, and writes q in its own type and k
@@ -56,17 +57,19 @@ __global__ void __launch_bounds__(kTableThreads) rope_table_kernel(RopeTurns f, 
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const unsigned long long t = f.turn[i0 + k];
-    turn[k] = ((unsigned long long)pos0 + (unsigned long long)first) * t;   // in 2^-64 turns, whole turns gone
+    // in 2^-64 turns, whole turns gone; the half of 2^-32 rounds the upper word, which is what is read
+    turn[k] = ((unsigned long long)pos0 + (unsigned long long)first) * t + (1ull << 31);
     step[k] = (unsigned long long)rows * t;
   }
   for (long long p = first; p < n_pos; p += rows) {
     float c[4], s[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const unsigned quarter = (unsigned)((turn[k] + (1ull << 61)) >> 62);       // nearest quarter turn (0 .. 3)
-      const long long rest = (long long)(turn[k] - ((unsigned long long)quarter << 62));   // [-2^61, 2^61)
+      const unsigned angle = (unsigned)(turn[k] >> 32);          // in 2^-32 turns
+      const unsigned quarter = (angle + (1u << 29)) >> 30;       // nearest quarter turn (0 .. 3)
+      const int rest = (int)(angle - (quarter << 30));           // [-2^29, 2^29)
       float sr, cr;
-      sincos_pi(__ll2float_rn(rest) * 0x1.0p-63f, sr, cr);       // in units of pi
+      sincos_pi(__int2float_rn(rest) * 0x1.0p-31f, sr, cr);      // in units of pi
       const float sv = (quarter & 1) ? cr : sr, cv = (quarter & 1) ? sr : cr;
       s[k] = __fmul_rn((quarter & 2) ? -sv : sv, mag);
       c[k] = __fmul_rn(((quarter + 1) & 2) ? -cv : cv, mag);     // cos is negative in quarters 1 and 2
