@@ -597,7 +597,7 @@ def _rope_call(cache, table, k_new, v_new, slots, q, positions, interleaved, q_o
         if q.shape != (B, Hq, n_new, D) or q.dtype is not dtype:
             raise ValueError("q must have k_new's batch, rows, head_dim and dtype")
         if q_out is None:
-            q_out = q.new_empty((B, Hq, n_new, D))
+            q_out = torch.empty((B, Hq, n_new, D), dtype=dtype, device=q.device)
         else:
             _dense("q_out", q_out, dtype, (B, Hq, n_new, D))
         qr = C.byref(_rows("q", q))
@@ -666,11 +666,11 @@ def _weights_call(cache, need_fn, q, n, seq_lens, scores, scores_out, attn_scale
         raise ValueError("scores and scores_out must have the same shape")
     _ints("seq_lens", seq_lens, cache.batch)
     if out is None:
-        out = q.new_empty(shape, dtype=torch.float32)
+        out = torch.empty(shape, dtype=torch.float32, device=q.device)
     else:
         _dense("out", out, torch.float32, shape)
     if workspace is None:
-        workspace = q.new_empty(max(need_fn(cache, shape[1], shape[2], n, chunk), 256), dtype=torch.uint8)
+        workspace = torch.empty(max(need_fn(cache, shape[1], shape[2], n, chunk), 256), dtype=torch.uint8, device=q.device)
     elif not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     dev = _here(("cache", cache.planes["k"]["payload"]), ("q", q), ("scores", scores), ("scores_out", scores_out),
@@ -723,7 +723,7 @@ def evict_select(scores: torch.Tensor, kv_len: int, n_keep: int, n_sink: int = 0
         raise ValueError("scores must be contiguous float32 [batch][n_kv_heads][tokens]")
     B, H, stride = scores.shape
     if keep is None:
-        keep = scores.new_empty((B, H, max(n_keep, 1)), dtype=torch.int32)
+        keep = torch.empty((B, H, max(n_keep, 1)), dtype=torch.int32, device=scores.device)
     else:
         _ints("keep", keep, B * H * max(n_keep, 1))
     _ints("seq_lens", seq_lens, B)
