@@ -17,11 +17,14 @@
 // layouts) or 8 (Hadamard); its partners' dims (half layout) are a second 16-byte load of the same row,
 // which the L1 answers.
 //
-// Bound by memory: 8192 tokens, 16 q and 8 kv heads of 256 dims (f16) move 148 MB.
+// Bound by memory: 8192 tokens, 16 q and 8 kv heads of 256 dims (f16, asymmetric) move 224 MB, 33 us at the copy
+// rate; 53.9 us.
+#include "mma_util.cuh"
 #include "store_quant.cuh"
 
 namespace kvq {
 namespace {
+using namespace mma;
 
 constexpr int kTableThreads = 256;
 constexpr int kTableRows = 8;        // positions per thread, a grid apart
@@ -128,13 +131,37 @@ __device__ __forceinline__ bool rope_place(const CacheView &c, const RopeStore &
   return inside;
 }
 
-// Eight consecutive dims from d0 of one row, rotated when the row is K or q and d0 < rot_dim (a multiple of
+// Eight elements from the e-th of `in`, in global memory or (SM) in shared memory.
+template <int DT, bool SM>
+__device__ __forceinline__ void load8(const void *in, size_t e, float (&v)[8]) {
+  if constexpr (!SM) {
+    load8_f32(in, DT, e, v);
+  } else if constexpr (DT == KVQ_F32) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) *reinterpret_cast<float4 *>(v + i) = *reinterpret_cast<const float4 *>(static_cast<const float *>(in) + e + i);
+  } else {
+    const uint4 w = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(in) + e);
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (DT == KVQ_BF16) {
+        v[2 * k] = bf16_bits_to_f32(u[k] & 0xFFFFu);
+        v[2 * k + 1] = bf16_bits_to_f32(u[k] >> 16);
+      } else {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&u[k]));
+        v[2 * k] = f.x;
+        v[2 * k + 1] = f.y;
+      }
+    }
+  }
+}
+
+// Eight consecutive dims from d0 of one row (at element `row` of `in`), rotated when the row is K or q and d0 < rot_dim (a multiple of
 // 16: all eight are on the same side of rot_dim and of its half).
-template <int DT>
-__device__ __forceinline__ void rope_load(const RopeStore &g, const RopeRow &w, size_t row, int d0, float *y) {
-  const void *in = g.in[w.what].data;
+template <int DT, bool SM>
+__device__ __forceinline__ void rope_load(const RopeStore &g, const RopeRow &w, const void *in, size_t row, int d0, float *y) {
   float x[8];
-  load8_f32(in, DT, row + d0, x);
+  load8<DT, SM>(in, row + d0, x);
   if (w.what == 1 || d0 >= g.rot) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = x[i];
@@ -156,7 +183,7 @@ __device__ __forceinline__ void rope_load(const RopeStore &g, const RopeRow &w, 
   const bool second = d0 >= half;
   const int i0 = second ? d0 - half : d0;
   float p[8], c[8], s[8];
-  load8_f32(in, DT, row + (second ? i0 : d0 + half), p);
+  load8<DT, SM>(in, row + (second ? i0 : d0 + half), p);
   load8_f32(t, KVQ_F32, i0, c);
   load8_f32(t, KVQ_F32, half + i0, s);
 #pragma unroll
@@ -194,15 +221,14 @@ __device__ __forceinline__ void write_q(const RopeStore &g, const RopeRow &w, in
 // preparation does not wait for its predecessor.
 // The threads of one row (TPR of them, `tr` this one's index): load, rotate, write q or quantise. Threads
 // without a row take part in the shuffles (full-warp masks) but load and store nothing.
-template <int LAYOUT, int D, int DT>
-__device__ __forceinline__ void rope_block_row(const CacheView &c, const RopeStore &g, RopeRow &w, bool valid, int tr) {
+template <int LAYOUT, int D, int DT, bool SM>
+__device__ __forceinline__ void rope_block_row(const CacheView &c, const RopeStore &g, RopeRow &w, bool valid, int tr,
+                                               const void *in, size_t row) {
   if (valid) valid = rope_place(c, g, w);
   float y[16] = {};
   if (valid) {
-    const RowsIn &in = g.in[w.what];
-    const size_t row = (size_t)w.b * in.batch + (size_t)w.head * in.head + (size_t)w.j * in.token;
-    rope_load<DT>(g, w, row, 16 * tr, y);
-    rope_load<DT>(g, w, row, 16 * tr + 8, y + 8);
+    rope_load<DT, SM>(g, w, in, row, 16 * tr, y);
+    rope_load<DT, SM>(g, w, in, row, 16 * tr + 8, y + 8);
     if (w.what == 2) {
       write_q<DT>(g, w, D, 16 * tr, y);
       write_q<DT>(g, w, D, 16 * tr + 8, y + 8);
@@ -211,13 +237,13 @@ __device__ __forceinline__ void rope_block_row(const CacheView &c, const RopeSto
   if (__all_sync(0xffffffffu, !valid || w.what == 2)) return;   // a warp of q rows has nothing to quantise
   quant_block<LAYOUT, 16>(c, w.what == 1, w.crow, g.row_bytes, D / kBlock, tr >> 1, tr & 1, y, valid && w.what != 2);
 }
-template <int LAYOUT, int D, int DT>
-__device__ __forceinline__ void rope_had_row(const CacheView &c, const RopeStore &g, RopeRow &w, bool valid, int lane) {
+template <int LAYOUT, int D, int DT, bool SM>
+__device__ __forceinline__ void rope_had_row(const CacheView &c, const RopeStore &g, RopeRow &w, bool valid, int lane,
+                                             const void *in, size_t row) {
   if (valid) valid = rope_place(c, g, w);
   float y[8] = {};
   if (valid) {
-    const RowsIn &in = g.in[w.what];
-    rope_load<DT>(g, w, (size_t)w.b * in.batch + (size_t)w.head * in.head + (size_t)w.j * in.token, 8 * lane, y);
+    rope_load<DT, SM>(g, w, in, row, 8 * lane, y);
     if (w.what == 2) write_q<DT>(g, w, D, 8 * lane, y);
   }
   if (__all_sync(0xffffffffu, !valid || w.what == 2)) return;
@@ -226,32 +252,62 @@ __device__ __forceinline__ void rope_had_row(const CacheView &c, const RopeStore
                                                       (long long)w.b * c.H + w.head, w.pos, valid && w.what != 2);
 }
 
-// LONG: a block takes several passes of rows of one grid column, whose addresses are then the same but for
-// the row (8192 rows asymmetric, d256: one pass per block 67 us, four 60, eight 63; 255 rows Hadamard int4:
-// 16.0, at four 17.2); else the launch's rows are dealt out in order.
+// LONG: a block takes the rows of one grid column, whose addresses are then the same but for the row; else the
+// launch's rows are dealt out in order. The block layouts take four passes, whose input is on its way into shared
+// memory (cp.async, each thread its own dims; partners are in the same warp) while the pass before is worked on:
+// 8192 rows asymmetric, d256: 53.9 us, against 58.8 with four passes that load as they go, 57.6 with two and 58.9
+// with eight. Hadamard, whose rotation hides its loads: one pass from memory, 255 rows of int4 15.2 us, against
+// 16.2 with two and 17.4 with four from shared memory.
 template <int LAYOUT>
 constexpr int long_passes() { return is_hadamard(LAYOUT) ? 1 : 4; }
 template <int LAYOUT, int D, int DT, bool LONG>
 __global__ void __launch_bounds__(256, is_hadamard(LAYOUT) ? 6 : LONG ? 5 : 4) rope_store_kernel(CacheView c, RopeStore g) {
   constexpr int TPR = is_hadamard(LAYOUT) ? D / 8 : D / 16, ROWS = 256 / TPR;   // threads per row, rows per pass
-  const int tr = threadIdx.x % TPR;
+  const int tr = threadIdx.x % TPR, own = threadIdx.x / TPR;
   RopeRow w = {};
-  if constexpr (LONG) {
+  constexpr int PASSES = long_passes<LAYOUT>();
+  if constexpr (LONG && PASSES > 1) {
+    constexpr int E = DT == KVQ_F32 ? 4 : 2, BYTES = D / TPR * E;   // of a thread's dims
+    __shared__ __align__(16) uint8_t ring[2][256 * BYTES];
     rope_column(c, g, blockIdx.x, w);
-    const int first = (int)blockIdx.y * (ROWS * long_passes<LAYOUT>());
+    const RowsIn &in = g.in[w.what];
+    const int first = (int)blockIdx.y * (ROWS * PASSES);
+    const uint8_t *src = static_cast<const uint8_t *>(in.data) + ((size_t)w.b * in.batch + (size_t)w.head * in.head) * E + tr * BYTES;
+    auto fetch = [&](int k) {
+      const int j = first + k * ROWS + own;
+      if (k < PASSES && j < g.n_new) {
+#pragma unroll
+        for (int i = 0; i < BYTES; i += 16)
+          cp_async16(smem_addr(ring[k & 1] + threadIdx.x * BYTES + i), src + (size_t)j * in.token * E + i, 16);
+      }
+      cp_async_commit();                                 // always one group per call
+    };
+    fetch(0);
 #pragma unroll 1
-    for (int k = 0; k < long_passes<LAYOUT>(); ++k) {
-      if (first + k * ROWS >= g.n_new) return;           // the whole block
-      w.j = first + k * ROWS + (int)threadIdx.x / TPR;
-      if constexpr (is_hadamard(LAYOUT)) rope_had_row<LAYOUT, D, DT>(c, g, w, w.j < g.n_new, tr);
-      else rope_block_row<LAYOUT, D, DT>(c, g, w, w.j < g.n_new, tr);
+    for (int k = 0; k < PASSES; ++k) {
+      if (first + k * ROWS >= g.n_new) return;           // the whole block; the groups still open are empty
+      fetch(k + 1);
+      cp_async_wait<1>();
+      __syncwarp();
+      w.j = first + k * ROWS + own;
+      rope_block_row<LAYOUT, D, DT, true>(c, g, w, w.j < g.n_new, tr, ring[k & 1], (size_t)own * D);
+      __syncwarp();                                      // the buffer is read; the next fetch fills it
     }
   } else {
-    const long long group = (long long)blockIdx.x * ROWS + threadIdx.x / TPR;
-    const bool valid = group < g.k_rows + g.v_rows + g.q_rows;
-    if (valid) rope_split(c, g, group, w);
-    if constexpr (is_hadamard(LAYOUT)) rope_had_row<LAYOUT, D, DT>(c, g, w, valid, tr);
-    else rope_block_row<LAYOUT, D, DT>(c, g, w, valid, tr);
+    bool valid;
+    if constexpr (LONG) {
+      rope_column(c, g, blockIdx.x, w);
+      w.j = (int)blockIdx.y * ROWS + own;
+      valid = w.j < g.n_new;
+    } else {
+      const long long group = (long long)blockIdx.x * ROWS + own;
+      valid = group < g.k_rows + g.v_rows + g.q_rows;
+      if (valid) rope_split(c, g, group, w);
+    }
+    const RowsIn &in = g.in[w.what];
+    const size_t row = (size_t)w.b * in.batch + (size_t)w.head * in.head + (size_t)w.j * in.token;
+    if constexpr (is_hadamard(LAYOUT)) rope_had_row<LAYOUT, D, DT, false>(c, g, w, valid, tr, in.data, row);
+    else rope_block_row<LAYOUT, D, DT, false>(c, g, w, valid, tr, in.data, row);
   }
 }
 

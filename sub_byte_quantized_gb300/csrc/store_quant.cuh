@@ -14,33 +14,33 @@ __device__ __forceinline__ __half f16_sat(float x) {
   return __float2half_rn(fminf(fmaxf(x, -kF16Max), kF16Max));
 }
 
-// Codes clamp(rint(x / s), LO, HI) of N values (0 when s == 0), x / s the correctly rounded quotient, each
+// Codes clamp(rint(x / s), LEAST, HI) of N values (0 when s == 0), x / s the correctly rounded quotient, each
 // as the float 1.5 * 2^23 + code - LO, whose bits are kCodeBase + (code - LO).
 //
-// The quotient is taken as x * fl(1 / s), off by at most 2^-24 of itself like the correctly rounded one, so
-// both round alike unless a half-integer lies within 2^-23 of |x / s| <= kTop of them; a thread that finds
-// one of its products within four times that of a half-integer divides (one warp of 512 values in a hundred
-// for 4-bit codes). Rounding is the addition of 1.5 * 2^23 - LO in one fma (nearest even). `divide` sends a
-// thread to the division at once: where fl(1 / s) may overflow or s is infinite; |x| > top does the same for
-// quotients beyond kTop. LEAST: the lowest code, where only the division can fall below it.
+// fl(1 / s) is off by at most 2^-24 of itself and the correctly rounded quotient by 2^-24 of its own, so both
+// lie between the products of x with fl(1 / s) made smaller and larger by 2^-22; where the two round to one
+// integer, so does the quotient. Rounding is the addition of 1.5 * 2^23 - LO in one fma (nearest even). A thread
+// with a value whose products round apart divides (one warp of 512 values in five hundred for 4-bit codes, in
+// sixty for 8-bit ones). `fast`: 1 / s is finite and normal, no x is NaN, and no quotient lies half a step or
+// more below LEAST or (TOP_CLAMP: it may round to HI + 1 there) above HI; else every thread divides.
 constexpr uint32_t kCodeBase = 0x4B400000u;              // the bits of 1.5 * 2^23
-template <int LO, int HI, int LEAST = LO, int N>
-__device__ __forceinline__ void round_codes(const float (&x)[N], float s, float top, bool divide, uint32_t (&code)[N]) {
-  constexpr float kBase = 12582912.0f, kZero = kBase - LO, kTop = 2.0f * (HI + 1);
+template <int LO, int HI, int LEAST, bool TOP_CLAMP, int N>
+__device__ __forceinline__ void round_codes(const float (&x)[N], float s, bool fast, uint32_t (&code)[N]) {
+  constexpr float kBase = 12582912.0f, kZero = kBase - LO;
   if (!(s > 0.0f)) {
 #pragma unroll
     for (int i = 0; i < N; ++i) code[i] = kCodeBase + (uint32_t)(-LO);
     return;
   }
-  const float inv = __frcp_rn(s);
-  float off = 0.0f;
+  const float inv = __frcp_rn(s), less = __fmul_rn(inv, 1.0f - 0x1p-22f), more = __fmul_rn(inv, 1.0f + 0x1p-22f);
+  uint32_t apart = 0;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const float m = __fmaf_rn(x[i], inv, kZero), q = __fsub_rn(m, kZero);
-    off = fmaxf(off, fabsf(__fmaf_rn(x[i], inv, -q)));
-    code[i] = __float_as_uint(fminf(fmaxf(m, kBase), kBase + (HI - LO)));
+    const float m = __fmaf_rn(x[i], less, kZero);
+    apart |= __float_as_uint(m) ^ __float_as_uint(__fmaf_rn(x[i], more, kZero));
+    code[i] = __float_as_uint(TOP_CLAMP ? fminf(m, kBase + (HI - LO)) : m);
   }
-  if (divide || off > 0.5f - kTop * 0x1p-21f || !(top <= __fmul_rn(s, kTop))) {
+  if (!fast || apart) {
 #pragma unroll
     for (int i = 0; i < N; ++i)
       code[i] = kCodeBase + (uint32_t)(-LO) + (uint32_t)(int)fminf(fmaxf(rintf(__fdiv_rn(x[i], s)), (float)LEAST), (float)HI);
@@ -62,11 +62,30 @@ __device__ __forceinline__ uint32_t pack_codes(const uint32_t *code) {
   w -= base;
   return SIGNED ? w ^ flip : w;
 }
-// Maximum over aligned groups of 32 / N neighbouring lanes (the lanes of a 32-value block).
-template <int N>
-__device__ __forceinline__ float block_max(float v) {
+// The larger of two values, NaN if one is NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+// Maximum of value(0 .. N - 1) and `start` over aligned groups of 32 / N neighbouring lanes (the lanes of a 32-value
+// block). NaN takes no part in it but clears `numbers`: it is looked for by a maximum that keeps it, and the
+// warp that has met one takes its maxima again.
+template <int N, class F>
+__device__ __forceinline__ float block_max(float start, F value, bool &numbers) {
+  float v = start;
 #pragma unroll
-  for (int m = 1; m < 32 / N; m <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, m));
+  for (int i = 0; i < N; ++i) v = max_nan(v, value(i));
+#pragma unroll
+  for (int m = 1; m < 32 / N; m <<= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, m));
+  numbers = v == v;
+  if (__any_sync(0xffffffffu, !numbers)) {
+    v = start;
+#pragma unroll
+    for (int i = 0; i < N; ++i) v = fmaxf(v, value(i));
+#pragma unroll
+    for (int m = 1; m < 32 / N; m <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, m));
+  }
   return v;
 }
 
@@ -81,11 +100,9 @@ __device__ __forceinline__ void quant_block(const CacheView &c, int kv, long lon
   uint32_t q[N];
 
   if (LAYOUT == KVQ_ASYM4_G32) {
-    float mn = v[0], mx = v[0];
-#pragma unroll
-    for (int i = 1; i < N; ++i) { mn = fminf(mn, v[i]); mx = fmaxf(mx, v[i]); }
-    mn = -block_max<N>(-mn);
-    mx = block_max<N>(mx);
+    bool numbers;
+    const float mn = -block_max<N>(-v[0], [&](int i) { return -v[i]; }, numbers);
+    const float mx = block_max<N>(v[0], [&](int i) { return v[i]; }, numbers);
     const float span = __fsub_rn(mx, mn);
     const __half sh = f16_sat(__fdiv_rn(span, 15.0f));
     const __half zh = f16_sat(mn);
@@ -93,8 +110,9 @@ __device__ __forceinline__ void quant_block(const CacheView &c, int kv, long lon
     float x[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] = __fsub_rn(v[i], z);
-    const float top = fmaxf(fabsf(__fsub_rn(mx, z)), fabsf(__fsub_rn(mn, z)));   // no |x| is larger
-    round_codes<0, 15>(x, s, top, false, q);
+    // the quotients' ends: half a step beyond the codes only where z or s are coarse beside the block's span
+    const bool fast = numbers && __fsub_rn(mx, z) <= __fmul_rn(s, 15.4375f) && __fsub_rn(mn, z) >= __fmul_rn(s, -0.4375f);
+    round_codes<0, 15, 0, false>(x, s, fast, q);
     if (!valid) return;
     uint32_t *o = reinterpret_cast<uint32_t *>(prow + blk * 16 + lb * (N / 2));
     if constexpr (N == 16) *reinterpret_cast<uint2 *>(o) = make_uint2(pack_codes<4, false, 8>(q), pack_codes<4, false, 8>(q + 8));
@@ -106,14 +124,12 @@ __device__ __forceinline__ void quant_block(const CacheView &c, int kv, long lon
     return;
   }
 
-  float amax = 0.0f;
-#pragma unroll
-  for (int i = 0; i < N; ++i) amax = fmaxf(amax, fabsf(v[i]));
-  amax = block_max<N>(amax);
+  bool numbers;
+  const float amax = block_max<N>(0.0f, [&](int i) { return fabsf(v[i]); }, numbers);
   constexpr int TOP = LAYOUT == KVQ_Q4_0 ? 8 : (LAYOUT == KVQ_Q8_0 ? 128 : 32);
   const __half sh = f16_sat(__fdiv_rn(amax, (float)TOP));
   const float s = __half2float(sh);
-  round_codes<-TOP, TOP - 1>(v, s, amax, false, q);
+  round_codes<-TOP, TOP - 1, -TOP, true>(v, s, numbers && amax <= __fmul_rn(s, TOP + 0.4375f), q);
   if (!valid) return;
   if (lb == 0) srow[blk] = sh;
   if (LAYOUT == KVQ_Q4_0) {
@@ -184,8 +200,9 @@ __device__ __forceinline__ void quant_had(const CacheView &c, int kv, long long 
   constexpr int QMAX = BITS == 4 ? 7 : 1;
   const float s = __fdiv_rn(amax, (float)QMAX);
   uint32_t q[V];
-  // codes as offsets from -QMAX - 1, the fields' own offset
-  round_codes<-QMAX - 1, QMAX, -QMAX>(x, s, amax, !(s >= 0x1p-100f && s <= 0x1p100f), q);
+  // codes as offsets from -QMAX - 1, the fields' own offset; the ends are QMAX s to a rounding of s (a NaN in the
+  // row makes every value NaN and s 0)
+  round_codes<-QMAX - 1, QMAX, -QMAX, false>(x, s, s >= 0x1p-100f && s <= 0x1p100f, q);
   if (!valid) return;
   const uint32_t w = pack_codes<BITS, true, V>(q);
   uint8_t *prow = (kv ? c.payload[1] : c.payload[0]) + (size_t)crow * row_bytes;
