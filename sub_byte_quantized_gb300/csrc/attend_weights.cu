@@ -56,11 +56,11 @@ __host__ __device__ constexpr int stage_bytes() {
 //   8-bit codes   columns 2b, 2b+1, dims 32b + 4c + 0..3 and 32b + 16 + 4c + 0..3: (0,1) (2,3) each
 //   2-bit codes   column = 64 dims, 16c + 0..15: k-step k takes (k, 8 + k) (4 + k, 12 + k)
 //   Q6_0          dims 32b + 8c + 0..7, as the 4-bit codes
-// 4- and 2-bit codes stay where they are in their f16 lane, as exact subnormals u 16^j 2^-24 or u 4^k 2^-24
-// of the offset code u = code + 8 or code + 2 (asymmetric: u = code): one lop3 per pair. The query
-// entries facing a shifted field are divided by it, the 2^-24 goes into the row's factor and the offset
-// times the query's block sum into the accumulator's initial value. 6- and 8-bit codes become exact signed
-// values, since their offsets (32, 128) would cost the scores' precision.
+// Hadamard codes stay where they are in their f16 lane, as exact subnormals u 16^j 2^-24 or u 4^k 2^-24 of the
+// offset code u = code + 8 or code + 2: one lop3 per pair. The query entries facing a shifted field are divided by
+// it, the 2^-24 goes into the row's factor and the offset times the query's sum into the accumulator's initial
+// value; all of it is exact in integers. The other layouts' codes become exact signed values (asymmetric: code - 8,
+// and the zero-point z + 8 s), since offsets would cost the scores' precision.
 template <int KL, int D>
 struct Words {
   static constexpr int NB = D / 32, N = KL == KVQ_Q6_0 ? 2 * NB : row_bytes<KL, D>() / 16;
@@ -107,7 +107,9 @@ __device__ __forceinline__ void unpack_row(const uint32_t (&w)[Words<KL, D>::N],
       } else if constexpr (KL == KVQ_Q6_0) {
         unpack8_s6(w[2 * b], w[2 * b + 1], o);
       } else {
-        unpack8_sub<KL == KVQ_ASYM4_G32>(w[b], o);
+        if constexpr (is_hadamard(KL)) unpack8_sub<false>(w[b], o);
+        else if constexpr (KL == KVQ_ASYM4_G32) unpack8_u4m8(w[b], o);
+        else unpack8_q4(w[b], o);
       }
       A[2 * b][h] = o[0];
       A[2 * b][2 + h] = o[1];
@@ -144,7 +146,11 @@ template <bool SMEM, int KL, int D>
 __device__ __forceinline__ void load_scales(const uint8_t *scale, const uint8_t *zero, int h, Tile<KL, D> &t) {
   if constexpr (is_hadamard(KL)) t.scale[h][0] = load_of<SMEM, float>(scale);
   else f16_scales<SMEM>(scale, t.scale[h]);
-  if constexpr (KL == KVQ_ASYM4_G32) f16_scales<SMEM>(zero, t.zero[h]);
+  if constexpr (KL == KVQ_ASYM4_G32) {
+    f16_scales<SMEM>(zero, t.zero[h]);
+#pragma unroll
+    for (int b = 0; b < D / 32; ++b) t.zero[h][b] = fmaf(8.0f, t.scale[h][b], t.zero[h][b]);
+  }
 }
 
 struct RowParams {
@@ -159,7 +165,7 @@ template <int KL, int D, bool SPLIT>
 __device__ __forceinline__ void prepare_row(const AttendArgs &a, int bb, int kvh, int r, int slot, int lane, float *buf,
                                             uint4 *frag, int lo_at, float *qsum, float *alpha_out) {
   constexpr int V = D / 32, KP = D / 32;                 // values per lane; pairs of k-steps
-  constexpr bool SUB = KL != KVQ_Q8_0 && KL != KVQ_Q6_0; // codes enter as subnormals
+  constexpr bool SUB = is_hadamard(KL);                  // codes enter as subnormals
   const bool live = r < a.gqa * a.n_q;
   const size_t row = live ? query_row_index(a, bb, kvh, r) : 0;
   float x[V];
@@ -223,15 +229,15 @@ __device__ __forceinline__ void prepare_row(const AttendArgs &a, int bb, int kvh
       f[lo_at] = make_uint4(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]), pack_f16x2(v[4], v[5]), pack_f16x2(v[6], v[7]));
     }
   }
-  if constexpr (SUB) {
+  if constexpr (SUB || KL == KVQ_ASYM4_G32) {
     s += __shfl_xor_sync(0xffffffffu, s, 1);
     s += __shfl_xor_sync(0xffffffffu, s, 2);
     if constexpr (is_hadamard(KL)) {                     // one accumulator: the whole row's sum in block 0
 #pragma unroll
       for (int m = 4; m < 32; m <<= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
     }
-    constexpr float kOffset = KL == KVQ_ASYM4_G32 ? 1.0f : KL == KVQ_HAD_INT2 ? -2.0f : -8.0f;
-    if (lane < D / 8 && c == 0) qsum[slot * KP + b] = s * (kOffset * 5.9604644775390625e-8f);
+    constexpr float kTerm = !SUB ? 1.0f : (KL == KVQ_HAD_INT2 ? -2.0f : -8.0f) * 5.9604644775390625e-8f;
+    if (lane < D / 8 && c == 0) qsum[slot * KP + b] = s * kTerm;
   }
   if (lane == 0) alpha_out[slot] = alpha;
   __syncwarp();
@@ -243,7 +249,6 @@ template <int KL, int D, bool SPLIT, class F>
 __device__ __forceinline__ void add_rows(const Tile<KL, D> &t, F frag, float2 al, float2 ls, int2 lim, const float *q0,
                                          const float *q1, int t0, bool masked, int g, float (&w)[2]) {
   constexpr int NB = D / 32;
-  constexpr bool OFFSET = KL == KVQ_Q4_0 || is_hadamard(KL);
   float x[4] = {0.f, 0.f, 0.f, 0.f};
   if constexpr (is_hadamard(KL)) {
     float d[2][4];                                       // two chains of the exact integer dot x 2^-24
@@ -267,8 +272,7 @@ __device__ __forceinline__ void add_rows(const Tile<KL, D> &t, F frag, float2 al
     for (int b = 0; b < NB; ++b) {
       float d[4];
       const uint4 f = frag(b);
-      const float i0 = OFFSET ? q0[b] : 0.0f, i1 = OFFSET ? q1[b] : 0.0f;
-      mma16816_c(d, t.A[2 * b], f.x, f.y, i0, i1, i0, i1);
+      mma16816_c(d, t.A[2 * b], f.x, f.y, 0.f, 0.f, 0.f, 0.f);
       mma16816(d, t.A[2 * b + 1], f.z, f.w);
       if constexpr (SPLIT) {
         const uint4 l = frag(NB + b);
@@ -510,7 +514,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, D == 128 && !SPLIT ? 5 : 1) at
   if (ls.x == INFINITY) al.x = 0.0f;                      // a row that sees nothing may hold any score
   if (ls.y == INFINITY) al.y = 0.0f;
   const int2 lim = *reinterpret_cast<const int2 *>(limit + 2 * c);
-  constexpr bool TERMS = KL != KVQ_Q8_0 && KL != KVQ_Q6_0;
+  constexpr bool TERMS = is_hadamard(KL) || KL == KVQ_ASYM4_G32;
   float q0[NB], q1[NB];
 #pragma unroll
   for (int b = 0; b < NB; ++b) {

@@ -20,8 +20,8 @@ __device__ __forceinline__ __half f16_sat(float x) {
 // fl(1 / s) is off by at most 2^-24 of itself and the correctly rounded quotient by 2^-24 of its own, so both
 // lie between the products of x with fl(1 / s) made smaller and larger by 2^-22; where the two round to one
 // integer, so does the quotient. Rounding is the addition of 1.5 * 2^23 - LO in one fma (nearest even). A thread
-// with a value whose products round apart divides (one warp of 512 values in five hundred for 4-bit codes, in
-// sixty for 8-bit ones). `fast`: 1 / s is finite and normal, no x is NaN, and no quotient lies half a step or
+// with a value whose products round apart divides (of random values about one warp of 512 in a thousand for 4-bit
+// codes, in a hundred for 8-bit ones). `fast`: 1 / s is finite and normal, no x is NaN, and no quotient lies half a step or
 // more below LEAST or (TOP_CLAMP: it may round to HI + 1 there) above HI; else every thread divides.
 constexpr uint32_t kCodeBase = 0x4B400000u;              // the bits of 1.5 * 2^23
 template <int LO, int HI, int LEAST, bool TOP_CLAMP, int N>

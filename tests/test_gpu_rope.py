@@ -191,3 +191,14 @@ def test_broadcast_and_refused_views():
         kvq.rope_store(dc, table, kb, kb, 0, positions=torch.zeros((2, 4), dtype=torch.int64, device="cuda"))
     with pytest.raises(ValueError):
         kvq.rope_store(dc, table.cpu(), kb, kb, 0)
+
+
+@pytest.mark.parametrize("layout", ["q4_0", "q6_0", "q8_0", "asym4_g32", "q8_0+q4_0"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rope_store_prompts(layout, dtype, interleaved):
+    """Rows enough for blocks of several passes: whole ones, and a last one that ends inside a pass."""
+    _check(layout, 128, 2, 4, 2, 301, 128, interleaved, dtype, 7, 320)
+    _check(layout, 128, 1, 2, 1, 128, 80, interleaved, dtype, 0, 128, fused=False)
+    _check(layout, 256, 1, 4, 2, 145, 256, interleaved, dtype, 3, 160)
+    _check(layout, 256, 1, 1, 1, 65, 112, interleaved, dtype, 0, 70, positions=np.arange(64, -1, -1)[None] * 3 % 200)
