@@ -958,20 +958,19 @@ namespace {
 
 constexpr int kMaxEvictTokens = 1 << 27;
 
-// Chunk of an attention call that also scores the tokens, for chunk 0: the attention's own choice, with
-// two bounds. 2560 tokens: its float32 result carries the truncation of the tensor cores' accumulation,
-// which grows with the tokens a warp adds up (16 sequences of up to 16379 tokens in Q8_0: 9.1e-6 of the
-// output's norm at the automatic 4608 tokens); 1536 where the sequences have lengths of their own, whose
-// chunks fill the SMs more evenly (the same batch: 83 us, at 2560 89 us, at 768 92 us). And on the tcgen05
-// kernel as many chunks as fill the SMs (it takes at most eight by itself: 64 CTAs for 128 rows and 8 kv
-// heads).
+// Chunk of an attention call that also scores the tokens, for chunk 0: the attention's own choice, but for two
+// kinds. Paged pools with up to two (sequence, kv head) per SM: at most 1536 tokens, since chunks that leave scores
+// behind take longer and the sequences' lengths differ (16 sequences of up to 16379 tokens, 8 kv heads: Q8_0 82 us
+// against 90 at the attention's 4608, asymmetric 99 against 136; 64 sequences of up to 4000, which fill the SMs by
+// themselves: 89 against 77). And the tcgen05 kernel: as many chunks as fill the SMs (it takes at most eight by
+// itself: 64 CTAs for 128 rows and 8 kv heads).
 int weights_chunk(const kvq::CacheView &c, int n_q_heads, int n_q, int kv_len, int auto_chunk) {
-  const int most = c.page_shift >= 0 ? 1536 : 2560;
-  int chunk = auto_chunk < most ? auto_chunk : most;
+  int dev = 0, sms = 148;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  int chunk = auto_chunk;
+  if (c.page_shift >= 0 && (long long)c.B * c.H <= 2LL * sms && chunk > 1536) chunk = 1536;
   const int rows = n_q_heads / c.H * n_q;
   if (kvq::tc_prefill_shape(c.layout, c.v_layout, c.D, rows)) {
-    int dev = 0, sms = 148;
-    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     const long long units = (long long)((rows + kvq::kTcRows - 1) / kvq::kTcRows) * c.B * c.H;
     const long long n = sms / units, body = kv_len > c.n_recent ? kv_len - c.n_recent : 1;
     if (n > 1) {
