@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import sub_byte_quantized_gb300 as kvq
-from oracle import rope as OR
+from oracle import attention as OA, budget as OB, rope as OR
 from tests.test_gpu_budget import LAYOUTS, _check
 
 pytestmark = pytest.mark.gpu
@@ -97,3 +97,38 @@ def test_planes_beyond_four_gigabytes():
             for name, x in small.planes[t].items():
                 assert torch.equal(c.planes[t][name][:, :, 8:13], x) and not c.planes[t][name][:, :, :8].any()
     assert torch.equal(so[:, :, 8:], last) and torch.equal(scores[:, :, :13], so) and not scores[:, :, 13:].any()
+
+
+@pytest.mark.parametrize("layout", ["q4_0", "q8_0", "q4_0+q8_0", "had_int4", "had_int2", "asym4_g32", "q6_0"])
+@pytest.mark.parametrize("first", [0, 100, 470, 511])
+def test_weights_with_values_of_any_size(layout, first):
+    """Values of up to 4e4 from one token on (their scales reach far beyond 2), small ones before it: the output
+    stays within float32's reach of the sum of |weight * value|."""
+    S, D = 512, 128
+    rng = np.random.default_rng(first)
+    k, v = (rng.standard_normal((1, 2, S, D)).astype(np.float32) for _ in range(2))
+    v[:, :, :first] *= 1e-3
+    v[:, :, first:] *= 1e4
+    q = rng.standard_normal((1, 4, 1, D)).astype(np.float32)
+    dc, oc = kvq.KVCache(layout, 1, 2, D, S), OA.OracleCache(layout, 1, 2, D, S)
+    kvq.store(dc, torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda(), 0)
+    oc.store(k, v, 0)
+    alpha = np.float32(0.3)
+    out, _ = kvq.decode_attend_weights(dc, torch.from_numpy(q).cuda(), S, None, scores_out=torch.zeros((1, 2, S), device="cuda"),
+                                       attn_scale=float(alpha))
+    ref = oc.attend(q, alpha, S)
+    ref = ref[0] if isinstance(ref, tuple) else ref
+    s, _ = OB.scores_dense(oc, q, alpha, S)
+    p = np.exp(s - s.max(-1, keepdims=True))
+    l = p.sum(-1, keepdims=True)
+    av = np.abs(oc.dequantized("v", S))[:, [0, 0, 1, 1]]
+    mass = np.einsum("bhqt,bhtd->bhqd", p / l, av)
+    # Beside a scale of 2 or more the probabilities p <= 1 and P' = p * scale are held as two f16 parts without the
+    # factor 2^12: the lo parts are multiples of 2^-24, off by at most 2^-25 each. Per token that is 2^-25 |v| from
+    # p's and 2^-25 |code| from P', over l.
+    code = 128 if "q8" in layout else 32 if layout == "q6_0" else 15
+    low = 2.0 ** -25 * (av.sum(2, keepdims=True) + S * code) / l
+    if "had" in layout:                                         # the rotation back adds up every dim
+        mass, low = (np.broadcast_to(x.sum(-1, keepdims=True) / np.sqrt(D), x.shape) for x in (mass, low))
+    # probabilities: the scores' float32 (|s| < 64: 2^-18); products and sums: 2^-20 of the mass
+    assert (np.abs(out.cpu().numpy() - ref) <= 2.0 ** -17 * mass + low).all()
