@@ -398,13 +398,15 @@ __global__ void __launch_bounds__(kScoreThreads) attend_weights_scores_kernel(We
   const float *in = wa.scores_in ? wa.scores_in + (size_t)bh * wa.stride : nullptr;
   float *out = wa.scores_out + (size_t)bh * wa.stride;
   float x[PER][V], old[PER];
+  uint64_t last;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(last));
 #pragma unroll
   for (int k = 0; k < PER; ++k) {
     const int i = k * kScoreThreads + (int)threadIdx.x, t = t0 + i / LPT;
     if (t < end) {
       const float *p = ps + (size_t)t * RP + (i % LPT) * V;
-      if constexpr (V == 4) *reinterpret_cast<float4 *>(x[k]) = __ldcg(reinterpret_cast<const float4 *>(p));
-      else *reinterpret_cast<float2 *>(x[k]) = __ldcg(reinterpret_cast<const float2 *>(p));
+      if constexpr (V == 4) asm volatile("ld.global.L2::cache_hint.v4.f32 {%0, %1, %2, %3}, [%4], %5;" : "=f"(x[k][0]), "=f"(x[k][1]), "=f"(x[k][2]), "=f"(x[k][3]) : "l"(p), "l"(last) : "memory");
+      else asm volatile("ld.global.L2::cache_hint.v2.f32 {%0, %1}, [%2], %3;" : "=f"(x[k][0]), "=f"(x[k][1]) : "l"(p), "l"(last) : "memory");
     } else {
 #pragma unroll
       for (int v = 0; v < V; ++v) x[k][v] = -INFINITY;

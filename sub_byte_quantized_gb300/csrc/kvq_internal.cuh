@@ -188,8 +188,13 @@ __host__ __device__ constexpr int score_rows(int kl, int vl, int D, int rows) {
 __device__ __forceinline__ void keep_scores(const AttendArgs &a, int bh, int t, int r, const float (&s)[4], int end) {
   if (r < a.s_rows) {
     float *p = a.part_s + ((size_t)bh * a.s_tokens + t) * a.s_rows + r;
-    if (t < end) *reinterpret_cast<float2 *>(p) = make_float2(s[0], s[1]);
-    if (t + 8 < end) *reinterpret_cast<float2 *>(p + 8 * a.s_rows) = make_float2(s[2], s[3]);
+    uint64_t keep;                                       // they are read once more, by the next kernel but one
+    asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
+    auto put = [&](float *q, float x, float y) {
+      asm volatile("st.global.L2::cache_hint.v2.f32 [%0], {%1, %2}, %3;" ::"l"(q), "f"(x), "f"(y), "l"(keep) : "memory");
+    };
+    if (t < end) put(p, s[0], s[1]);
+    if (t + 8 < end) put(p + 8 * a.s_rows, s[2], s[3]);
   }
 }
 // Row index (b, hq, qi) of query row r (of the gqa * n_q rows of kv head kvh).
