@@ -1,6 +1,7 @@
 // C ABI of the library: host-side validation, workspace layout and kernel launches.
 // Nothing here allocates, synchronises or prints; failures return a kvq_status and record a
 // one-line reason readable through kvq_last_error().
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstdarg>
@@ -962,8 +963,8 @@ constexpr int kMaxEvictTokens = 1 << 27;
 // kinds. Paged pools with up to two (sequence, kv head) per SM: at most 1536 tokens, since chunks that leave scores
 // behind take longer and the sequences' lengths differ (16 sequences of up to 16379 tokens, 8 kv heads: Q8_0 82 us
 // against 90 at the attention's 4608, asymmetric 99 against 136; 64 sequences of up to 4000, which fill the SMs by
-// themselves: 89 against 77). And the tcgen05 kernel: as many chunks as fill the SMs (it takes at most eight by
-// itself: 64 CTAs for 128 rows and 8 kv heads).
+// themselves: 89 against 77). And the tcgen05 kernel: as many chunks as fill the SMs beside the window's CTAs (it
+// takes at most eight by itself: 64 CTAs for 128 rows and 8 kv heads; window CTAs in a second wave cost 13 us).
 int weights_chunk(const kvq::CacheView &c, int n_q_heads, int n_q, int kv_len, int auto_chunk) {
   int dev = 0, sms = 148;
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -972,7 +973,8 @@ int weights_chunk(const kvq::CacheView &c, int n_q_heads, int n_q, int kv_len, i
   const int rows = n_q_heads / c.H * n_q;
   if (kvq::tc_prefill_shape(c.layout, c.v_layout, c.D, rows)) {
     const long long units = (long long)((rows + kvq::kTcRows - 1) / kvq::kTcRows) * c.B * c.H;
-    const long long n = sms / units, body = kv_len > c.n_recent ? kv_len - c.n_recent : 1;
+    const long long win = (long long)c.B * c.H * ((std::min(c.n_recent, kv_len) + kvq::kWinChunk - 1) / kvq::kWinChunk);
+    const long long n = (sms - win) / units, body = kv_len > c.n_recent ? kv_len - c.n_recent : 1;
     if (n > 1) {
       const long long fill = ((body + n - 1) / n + 63) / 64 * 64;
       if (fill < chunk) chunk = (int)fill;

@@ -45,6 +45,12 @@
 // partial (m, l, O) is exact softmax algebra for any reference, so the result does not depend on
 // when m moves; what tau saves is the wait for the tensor core on almost every stage.
 //
+// ALT (at most 128 query rows, calls that also score the tokens): with one row block the softmax of a stage and the
+// MMAs around it would follow one another, so both blocks hold the same rows and take the stages in turn, block
+// b the stages j with j % 2 == b; at the end block 0 combines the two (m, l, O). The second block's query codes
+// leave room for a fourth tile buffer. 32 query rows of 4 heads over 32K tokens, 8 kv heads: ALT_FIGURES. (Other
+// calls keep the order of their sums.)
+//
 // The int8 query codes and scales, and the rotated f32 query rows, come from the query-preparation
 // kernel launched just before (one pass over the rows instead of one per chunk). The exact-f32
 // recent window is scored by more CTAs of the same grid, after the body CTAs in launch order
@@ -66,7 +72,7 @@ static_assert(kCtaRows == kTcRows, "the chunk planner's rows per CTA");
 constexpr int kStage = 64;              // tokens per stage
 constexpr int kD = 128;
 constexpr int kRing = 3;                // raw stage slots
-constexpr int kTB = 3;                  // code tile buffers (the unpackers run up to two stages ahead)
+constexpr int kTB = 3, kTBAlt = 4;      // code tile buffers (the unpackers run up to two stages ahead)
 constexpr int kWCopy = 8, kWMma = 9, kWUnp = 10, kUnpThreads = 64;
 // Tensor memory (columns of 32 bits, lane = query row of the block): per block b, S at 64 b, O at
 // 128 + 128 b, and P' at 384 + 64 b (the f16 hi parts of the stage's 64 tokens in 32 columns, then
@@ -84,21 +90,25 @@ constexpr int kSQ = 0;                          // Q codes f16 per block: two 64
 constexpr int kQBlk = 32768;
 constexpr int kST = kSQ + kBlk * kQBlk;         // kTB tile buffers of K (16 KB) + V (16 KB)
 constexpr int kTileBuf = 32768;
-constexpr int kSTsc = kST + kTB * kTileBuf;     // kTB x (s_k[64], s_v[64]) f32
-constexpr int kSRaw = kSTsc + kTB * 512;       // raw ring
+constexpr int kSTAlt = kSQ + kQBlk;             // kTBAlt of them
+constexpr int kSTsc = kST + kTB * kTileBuf;     // per tile buffer (s_k[64], s_v[64]) f32
+static_assert(kSTAlt + kTBAlt * kTileBuf == kSTsc, "the fourth buffer takes the second block's query codes");
+constexpr int kSRaw = kSTsc + kTBAlt * 512;     // raw ring
 template <int L>
 struct RawGeo {
   static constexpr int RB = L == KVQ_HAD_INT2 ? 32 : 64;     // payload bytes per token row
   static constexpr int OFF_V = kStage * RB, OFF_SK = 2 * kStage * RB, OFF_SV = OFF_SK + 4 * kStage;
   static constexpr int SLOT = OFF_SV + 4 * kStage;
+  // Where 16-byte piece q of a stage's rows lies in the slot: eight rows' pieces p in eight different bank groups
+  static __device__ __forceinline__ int raw_piece(int q) { return q ^ ((q >> 3) & (RB / 16 - 1)); }
   static constexpr int SVMAX = kSRaw + kRing * SLOT;          // per tile buffer: the stage's largest s_v, two halves
-  static constexpr int BAR = SVMAX + 8 * kTB;                 // mbarriers
+  static constexpr int BAR = SVMAX + 8 * kTBAlt;                 // mbarriers
   static constexpr int SMEM = BAR + 256;
   static_assert(SMEM <= 227 * 1024, "fits one CTA per SM");
 };
-static_assert(kST % 1024 == 0, "swizzled tiles on 1 KB boundaries");
+static_assert(kST % 1024 == 0 && kSTAlt % 1024 == 0, "swizzled tiles on 1 KB boundaries");
 // mbarriers (SF, PF, PVD: one per row block)
-enum { B_RAWF = 0, B_RAWE = kRing, B_TF = 2 * kRing, B_TE = B_TF + kTB, B_SF = B_TE + kTB, B_PF = B_SF + kBlk,
+enum { B_RAWF = 0, B_RAWE = kRing, B_TF = 2 * kRing, B_TE = B_TF + kTBAlt, B_SF = B_TE + kTBAlt, B_PF = B_SF + kBlk,
        B_PVD = B_PF + kBlk, B_DR = B_PVD + kBlk, N_BAR = B_DR + 1 };
 static_assert(N_BAR * 8 <= 256, "mbarriers fit");
 // Shared-memory matrix descriptor, 128-byte swizzle: start, leading and stride byte offsets.
@@ -471,12 +481,15 @@ __device__ __forceinline__ void window_chunk(const AttendArgs &a, uint8_t *sm, i
   }
 }
 
-template <int L, bool PAGED, bool CAP>
+template <int L, bool PAGED, bool CAP, bool ALT>
 __global__ void __launch_bounds__(kThreads, 1) attend_prefill_tc_kernel(AttendArgs a) {
   using RG = RawGeo<L>;
   static_assert(!CAP || !PAGED, "score capture: contiguous cache");
+  static_assert(!CAP || !ALT, "score capture: the rows' own order");
+  constexpr int TB = ALT ? kTBAlt : kTB, ST = ALT ? kSTAlt : kST;
   extern __shared__ __align__(1024) uint8_t sm[];
   __shared__ uint32_t tmem_base;
+  __shared__ float alt_state[ALT ? 2 : 1][kRows];       // ALT: (m, l) of block 1's rows
 #if defined(__CUDA_ARCH__) && __CUDA_ARCH__ >= 900
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the query codes come from the preceding kernel
@@ -509,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_tc_kernel(AttendAr
       bar_init(bar + B_RAWF + i, 32);                   // the copy lanes' cp.async completions
       bar_init(bar + B_RAWE + i, kUnpThreads);
     }
-    for (int i = 0; i < kTB; ++i) {
+    for (int i = 0; i < TB; ++i) {
       bar_init(bar + B_TF + i, kUnpThreads);
       bar_init(bar + B_TE + i, 1);
     }
@@ -523,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_tc_kernel(AttendAr
   }
   // ---- query codes of the CTA's rows as exact f16 in the tiles' dim order: each unit is one
   // 8-dim group of one row (16 int8 -> one 16-byte store of four (dim i, dim i + 4) pairs)
-  for (int u = tid; u < kCtaRows * 16; u += kThreads) {
+  for (int u = tid; u < (ALT ? kRows : kCtaRows) * 16; u += kThreads) {
     const int cr = u >> 4, gi = u & 15, r = row0 + cr;
     uint32_t w[4] = {0u, 0u, 0u, 0u};
     if (r < R) {
@@ -560,9 +573,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_tc_kernel(AttendAr
 #pragma unroll
       for (int k = 0; k < kStage * RG::RB / 16 / 32; ++k) {
         const int q = lane + 32 * k;                     // 16-byte piece q of the stage's rows
+        const int to = 16 * RG::raw_piece(q);
         const bool in = ts + q / (RG::RB / 16) < t_end;
-        cp_async16(smem_addr(raw + 16 * q), kp + (in ? 16 * q : 0), in ? 16 : 0);
-        cp_async16(smem_addr(raw + RG::OFF_V + 16 * q), vp + (in ? 16 * q : 0), in ? 16 : 0);
+        cp_async16(smem_addr(raw + to), kp + (in ? 16 * q : 0), in ? 16 : 0);
+        cp_async16(smem_addr(raw + RG::OFF_V + to), vp + (in ? 16 * q : 0), in ? 16 : 0);
       }
       const float *skp = static_cast<const float *>(cv.scale[0]) + r0;
       const float *svp = static_cast<const float *>(cv.scale[1]) + r0;
@@ -577,36 +591,43 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_tc_kernel(AttendAr
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp >= kWUnp) {
-    // ---------------- unpack: raw slot -> tile buffer j % kTB (each thread 16 (row, 8-dim group) units per plane)
+    // ---------------- unpack: raw slot -> tile buffer j % TB (a token row of both planes per thread)
     const int ut = tid - kWUnp * 32;
     for (int j = 0; j < n_st && ok; ++j) {
-      const int slot = j % kRing, tb = j % kTB;
+      const int slot = j % kRing, tb = j % TB;
       ok = bar_wait_relaxed(bar + B_RAWF + slot, (j / kRing) & 1);
-      if (ok && j >= kTB) ok = bar_wait_relaxed(bar + B_TE + tb, ((j - kTB) / kTB) & 1);   // P'V of stage j - kTB done
+      if (ok && j >= TB) ok = bar_wait_relaxed(bar + B_TE + tb, ((j - TB) / TB) & 1);   // P'V of stage j - TB done
       if (!ok) break;
       const uint8_t *raw = sm + kSRaw + slot * RG::SLOT;
-      uint8_t *tk = sm + kST + tb * kTileBuf, *tv = tk + 16384;
+      uint8_t *tk = sm + ST + tb * kTileBuf, *tv = tk + 16384;
+      static_assert(kUnpThreads == kStage, "a token row per unpack thread");
+      uint4 kr[RG::RB / 16], vr[RG::RB / 16];
 #pragma unroll
-      for (int k = 0; k < kStage * 16 / kUnpThreads; ++k) {
-        const int u = ut + kUnpThreads * k;
-        const int row = u >> 4, gi = u & 15;
-        const uint32_t off = (uint32_t)(gi >> 3) * 8192 + sw128(row, 16 * (gi & 7));
+      for (int p = 0; p < RG::RB / 16; ++p) {
+        const int at = 16 * RG::raw_piece(ut * (RG::RB / 16) + p);
+        kr[p] = *reinterpret_cast<const uint4 *>(raw + at);
+        vr[p] = *reinterpret_cast<const uint4 *>(raw + RG::OFF_V + at);
+      }
+      auto word_of = [](const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; };
+#pragma unroll
+      for (int gi = 0; gi < 16; ++gi) {                  // 8-dim groups
+        const uint32_t off = (uint32_t)(gi >> 3) * 8192 + sw128(ut, 16 * (gi & 7));
         uint32_t o[4];
         if constexpr (L == KVQ_HAD_INT2) {
-          unpack8_s2(*reinterpret_cast<const uint16_t *>(raw + row * RG::RB + 2 * gi), o);
+          const uint32_t kw = word_of(kr[gi >> 3], (gi >> 1) & 3), vw = word_of(vr[gi >> 3], (gi >> 1) & 3);
+          unpack8_s2((gi & 1) ? kw >> 16 : kw & 0xFFFFu, o);
           *reinterpret_cast<uint4 *>(tk + off) = make_uint4(o[0], o[1], o[2], o[3]);
-          unpack8_s2(*reinterpret_cast<const uint16_t *>(raw + RG::OFF_V + row * RG::RB + 2 * gi), o);
+          unpack8_s2((gi & 1) ? vw >> 16 : vw & 0xFFFFu, o);
           *reinterpret_cast<uint4 *>(tv + off) = make_uint4(o[0], o[1], o[2], o[3]);
         } else {
-          unpack8_q4(*reinterpret_cast<const uint32_t *>(raw + row * RG::RB + 4 * gi), o);
+          unpack8_q4(word_of(kr[gi >> 2], gi & 3), o);
           *reinterpret_cast<uint4 *>(tk + off) = make_uint4(o[0], o[1], o[2], o[3]);
-          unpack8_q4(*reinterpret_cast<const uint32_t *>(raw + RG::OFF_V + row * RG::RB + 4 * gi), o);
+          unpack8_q4(word_of(vr[gi >> 2], gi & 3), o);
           *reinterpret_cast<uint4 *>(tv + off) = make_uint4(o[0], o[1], o[2], o[3]);
         }
       }
       // per-stage scales: s_k[0..63], s_v[0..63]; each unpack warp also records the largest s_v of
       // its 32 tokens (non-negative floats order like their bit patterns)
-      static_assert(kUnpThreads == kStage, "one key and one value scale per unpack thread");
       const float sck = *reinterpret_cast<const float *>(raw + RG::OFF_SK + 4 * ut);
       const float scv = *reinterpret_cast<const float *>(raw + RG::OFF_SV + 4 * ut);
       reinterpret_cast<float *>(sm + kSTsc + tb * 512)[ut] = sck;
@@ -625,30 +646,31 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_tc_kernel(AttendAr
     if (lane == 0) {
       constexpr uint32_t id_s = idesc(kRows, kStage, false), id_o = idesc(kRows, kD, true);
       auto pv = [&](int b, int i) {
-        ok = ok && bar_wait(bar + B_PF + b, i & 1);
+        const int ib = ALT ? i >> 1 : i;                  // the block's own count of stages
+        ok = ok && bar_wait(bar + B_PF + b, ib & 1);
         if (!ok) return;
         asm volatile("tcgen05.fence::after_thread_sync;");
-        const uint32_t vt = smem_addr(sm + kST + (i % kTB) * kTileBuf + 16384);
+        const uint32_t vt = smem_addr(sm + ST + (i % TB) * kTileBuf + 16384);
 #pragma unroll
         for (int ks = 0; ks < kStage / 16; ++ks) {
           const uint64_t db = sdesc(vt + 2048 * ks, 8192, 1024);
           const uint32_t pa = tmem + tm_p(b) + 8 * ks;    // 16 tokens = 8 columns
-          mma_f16_ta(tmem + tm_o(b), pa, db, id_o, (i > 0 || ks > 0) ? 1u : 0u);
+          mma_f16_ta(tmem + tm_o(b), pa, db, id_o, (ib > 0 || ks > 0) ? 1u : 0u);
           mma_f16_ta(tmem + tm_o(b), pa + 32, db, id_o, 1u);
         }
         mma_commit(bar + B_PVD + b);                    // O holds stage i; P' free
-        if (b == nblk - 1) mma_commit(bar + B_TE + (i % kTB));   // tile buffer free
+        if (ALT || b == nblk - 1) mma_commit(bar + B_TE + (i % TB));   // tile buffer free
       };
       for (int j = 0; j < n_st && ok; ++j) {
-        const int tb = j % kTB;
-        ok = bar_wait(bar + B_TF + tb, (j / kTB) & 1);
+        const int tb = j % TB;
+        ok = bar_wait(bar + B_TF + tb, (j / TB) & 1);
         if (!ok) break;
         asm volatile("tcgen05.fence::after_thread_sync;");
-        const uint32_t kt = smem_addr(sm + kST + tb * kTileBuf);
-        for (int b = 0; b < nblk && ok; ++b) {
-          if (j >= 1) pv(b, j - 1);
+        const uint32_t kt = smem_addr(sm + ST + tb * kTileBuf);
+        for (int b = ALT ? j & 1 : 0; b < (ALT ? (j & 1) + 1 : nblk) && ok; ++b) {
+          if (j >= (ALT ? 2 : 1)) pv(b, j - (ALT ? 2 : 1));
           if (!ok) break;
-          const uint32_t qt = smem_addr(sm + kSQ + b * kQBlk);
+          const uint32_t qt = smem_addr(sm + kSQ + (ALT ? 0 : b * kQBlk));
 #pragma unroll
           for (int kb = 0; kb < kD / 16; ++kb) {
             const uint64_t da = sdesc(qt + (kb >> 2) * 16384 + 32 * (kb & 3), 16, 1024);
@@ -658,14 +680,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_tc_kernel(AttendAr
           mma_commit(bar + B_SF + b);
         }
       }
-      for (int b = 0; b < nblk && ok; ++b) pv(b, n_st - 1);
+      if constexpr (ALT) {
+        for (int i = max(n_st - 2, 0); i < n_st && ok; ++i) pv(i & 1, i);
+      } else {
+        for (int b = 0; b < nblk && ok; ++b) pv(b, n_st - 1);
+      }
       mma_commit(bar + B_DR);                           // drain: every MMA issued above completes
       if (!bar_wait(bar + B_DR, 0)) ok = false;
     }
-  } else if ((warp >> 2) < nblk) {
+  } else if (ALT || (warp >> 2) < nblk) {
     // ---------------- softmax: block b = warp / 4, row lr = TMEM lane, whole rows (64 scores per stage)
     const int b = warp >> 2, q4 = warp & 3;
-    const int lr = 32 * q4 + lane, r = row0 + kRows * b + lr;
+    const int lr = 32 * q4 + lane, r = row0 + (ALT ? 0 : kRows * b) + lr;
     const bool live = r < R;
     const int lim = live ? row_limit(a, sl, r % a.n_q) : -1;
     const size_t qrow = live ? query_row_index(a, bb, kvh, r) : 0;
@@ -678,9 +704,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_tc_kernel(AttendAr
     if (CAP && live && chunk_id == 0) a.cap_sq[qrow] = a.s_q[qrow];
     const uint32_t lane_base = (uint32_t)(32 * q4) << 16;
     float m = -INFINITY, l = 0.0f;
-    for (int j = 0; j < n_st && ok; ++j) {
-      const int tb = j % kTB, ts = t0 + j * kStage;
-      ok = __all_sync(0xffffffffu, bar_wait(bar + B_TF + tb, (j / kTB) & 1) && bar_wait(bar + B_SF + b, j & 1));
+    for (int j = ALT ? b : 0; j < n_st && ok; j += ALT ? 2 : 1) {
+      const int tb = j % TB, ts = t0 + j * kStage, jb = ALT ? j >> 1 : j;   // jb: the block's own count
+      ok = __all_sync(0xffffffffu, bar_wait(bar + B_TF + tb, (j / TB) & 1) && bar_wait(bar + B_SF + b, jb & 1));
       if (!ok) break;
       asm volatile("tcgen05.fence::after_thread_sync;");
       const float *tsc = reinterpret_cast<const float *>(sm + kSTsc + tb * 512);
@@ -730,9 +756,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_tc_kernel(AttendAr
       const float m_new = bump ? mx : m;
       const float mu = m_new == -INFINITY ? 0.0f : m_new;
       const float corr = bump ? ex2(m - mu) : 1.0f;     // m = -inf -> 0
-      if (j >= 1) {
-        // P'V of stage j - 1 has read P' and updated O (it precedes S of stage j on the tensor core)
-        ok = __all_sync(0xffffffffu, bar_wait(bar + B_PVD + b, (j - 1) & 1));
+      if (jb >= 1) {
+        // P'V of the block's stage before has read P' and updated O (it precedes S of this one on the tensor core)
+        ok = __all_sync(0xffffffffu, bar_wait(bar + B_PVD + b, (jb - 1) & 1));
         if (!ok) break;
         asm volatile("tcgen05.fence::after_thread_sync;");
         if (__any_sync(0xffffffffu, bump && m != -INFINITY)) {   // rescale the block's O rows
@@ -779,8 +805,26 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_tc_kernel(AttendAr
       asm volatile("tcgen05.fence::before_thread_sync;");   // the TMEM stores above precede the MMAs
       bar_arrive(bar + B_PF + b);
     }
-    if (ok) ok = __all_sync(0xffffffffu, bar_wait(bar + B_PVD + b, (n_st - 1) & 1));
-    if (ok) {                                           // warp-uniform: the TMEM loads need the whole warp
+    const int n_b = ALT ? (n_st - b + 1) >> 1 : n_st;     // the block's stages (ALT: block 1 may have none)
+    if (ok && n_b > 0) ok = __all_sync(0xffffffffu, bar_wait(bar + B_PVD + b, (n_b - 1) & 1));
+    float w0 = 1.0f, w1 = 0.0f;                          // ALT: the weights of the two blocks' O
+    if constexpr (ALT) {
+      if (b == 1) {
+        alt_state[0][lr] = m;
+        alt_state[1][lr] = l;
+      }
+      asm volatile("tcgen05.fence::before_thread_sync;");
+      asm volatile("bar.sync 1, %0;" ::"n"(2 * kRows) : "memory");   // every softmax warp comes here, failed or not
+      asm volatile("tcgen05.fence::after_thread_sync;");
+      if (b == 0) {
+        const float m1 = alt_state[0][lr], top = fmaxf(m, m1);
+        w0 = m == -INFINITY ? 0.0f : ex2(m - top);
+        w1 = m1 == -INFINITY ? 0.0f : ex2(m1 - top);
+        l = l * w0 + alt_state[1][lr] * w1;
+        m = top;
+      }
+    }
+    if (ok && (!ALT || b == 0)) {                       // warp-uniform: the TMEM loads need the whole warp
       asm volatile("tcgen05.fence::after_thread_sync;");
       const bool write = live && t0 <= lim;
       const int hq = kvh * a.gqa + r / a.n_q, qi = r % a.n_q;
@@ -790,6 +834,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_tc_kernel(AttendAr
       for (int c = 0; c < kD; c += 32) {
         float o[32];
         tm_ld32(tmem + lane_base + tm_o(b) + c, o);
+        if constexpr (ALT) {
+          if (n_st > 1) {
+            float o1[32];
+            tm_ld32(tmem + lane_base + tm_o(1) + c, o1);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = o[i] * w0 + o1[i] * w1;
+          }
+        }
         if (write) {
 #pragma unroll
           for (int g8 = 0; g8 < 4; ++g8) {              // position 8 g8 + p holds dim 8 g8 + perm8(p)
@@ -824,10 +876,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_tc_kernel(AttendAr
   if (warp == kWMma) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemCols));
 }
 
-template <int L, bool PAGED, bool CAP>
+template <int L, bool PAGED, bool CAP, bool ALT>
 cudaError_t launch_tc(const AttendArgs &a, cudaStream_t st) {
   static std::atomic<bool> configured[kMaxDevices];
-  cudaError_t e = set_smem_once(configured, attend_prefill_tc_kernel<L, PAGED, CAP>, tc_smem<L>());
+  cudaError_t e = set_smem_once(configured, attend_prefill_tc_kernel<L, PAGED, CAP, ALT>, tc_smem<L>());
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   // body CTAs (row block, chunk, head), then the window CTAs in extra z slices
@@ -842,14 +894,15 @@ cudaError_t launch_tc(const AttendArgs &a, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attend_prefill_tc_kernel<L, PAGED, CAP>, a);
+  return cudaLaunchKernelEx(&cfg, attend_prefill_tc_kernel<L, PAGED, CAP, ALT>, a);
 }
 
 template <int L>
 cudaError_t launch_layout(const AttendArgs &a, cudaStream_t st) {
   const bool paged = a.cache.page_shift >= 0;
-  if (a.cap_scores) return paged ? cudaErrorNotSupported : launch_tc<L, false, true>(a, st);
-  return paged ? launch_tc<L, true, false>(a, st) : launch_tc<L, false, false>(a, st);
+  if (a.cap_scores) return paged ? cudaErrorNotSupported : launch_tc<L, false, true, false>(a, st);
+  if (a.lse && a.gqa * a.n_q <= kRows) return paged ? launch_tc<L, true, false, true>(a, st) : launch_tc<L, false, false, true>(a, st);
+  return paged ? launch_tc<L, true, false, false>(a, st) : launch_tc<L, false, false, false>(a, st);
 }
 
 }  // namespace

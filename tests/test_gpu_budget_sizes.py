@@ -132,3 +132,15 @@ def test_weights_with_values_of_any_size(layout, first):
         mass, low = (np.broadcast_to(x.sum(-1, keepdims=True) / np.sqrt(D), x.shape) for x in (mass, low))
     # probabilities: the scores' float32 (|s| < 64: 2^-18); products and sums: 2^-20 of the mass
     assert (np.abs(out.cpu().numpy() - ref) <= 2.0 ** -17 * mass + low).all()
+
+
+@pytest.mark.parametrize("layout", ["had_int4", "had_int2"])
+@pytest.mark.parametrize("Hq,nq", [(5, 13), (4, 24), (4, 32), (3, 43)])
+def test_weights_of_an_observation_window(layout, Hq, nq):
+    """65 to 129 rows per kv head over a Hadamard body of one stage of 64 tokens, of two, three and many, with rows
+    that see a part of the last ones only."""
+    for S, w, causal in ((50, 0, True), (64 + 40, 40, True), (129, 0, False), (161, 30, True), (1000, 64, True), (2600, 0, True)):
+        if nq <= S:
+            _check(layout, 128, 2, 2 * Hq, 2, S, nq, causal=causal, n_recent=w)
+    _check(layout, 128, 1, Hq, 1, 700, nq, causal=True, q_pos0=0, n_recent=20, chunk=192)
+    _check(layout, 128, 1, Hq, 1, 700, nq, causal=True, q_pos0=100, chunk=64)
