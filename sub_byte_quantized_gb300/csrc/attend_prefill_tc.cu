@@ -48,10 +48,9 @@
 // ALT (at most 128 query rows, calls that also score the tokens): with one row block the softmax of a stage and the
 // MMAs around it would follow one another, so both blocks hold the same rows and take the stages in turn, block
 // b the stages j with j % 2 == b; at the end block 0 combines the two (m, l, O). The second block's query codes
-// leave room for a fourth tile buffer. 32 query rows of 4 heads over 32K tokens, 8 kv heads: 44 us for the body's
-// CTAs instead of 54; what bounds them is the unpacking (1270 of 2130 cycles a stage, the rest its wait for a free
-// buffer). Issuing S two stages ahead of P'V, or whatever is ready first, did not help (73 and 71 us for the call,
-// 70.6 as it is). (Other calls keep the order of their sums.)
+// leave room for a fourth tile buffer. 32 query rows of 4 heads over 32K tokens, 8 kv heads: the call takes 70.2 us
+// instead of 89.6, the body's CTAs 44; what bounds them is the unpacking (1270 of 2130 cycles a stage, the rest its
+// wait for a free buffer). Issuing S two stages ahead of P'V, or whatever is ready first, did not help (73 and 71 us). (Other calls keep the order of their sums.)
 //
 // The int8 query codes and scales, and the rotated f32 query rows, come from the query-preparation
 // kernel launched just before (one pass over the rows instead of one per chunk). The exact-f32
