@@ -6,7 +6,7 @@ import torch
 
 import sub_byte_quantized_gb300 as kvq
 from oracle import attention as OA, budget as OB, rope as OR
-from tests.test_gpu_budget import LAYOUTS, _check
+from tests.test_gpu_budget import LAYOUTS, _check, test_paged_weights as paged_weights
 
 pytestmark = pytest.mark.gpu
 
@@ -144,3 +144,10 @@ def test_weights_of_an_observation_window(layout, Hq, nq):
             _check(layout, 128, 2, 2 * Hq, 2, S, nq, causal=causal, n_recent=w)
     _check(layout, 128, 1, Hq, 1, 700, nq, causal=True, q_pos0=0, n_recent=20, chunk=192)
     _check(layout, 128, 1, Hq, 1, 700, nq, causal=True, q_pos0=100, chunk=64)
+
+
+@pytest.mark.parametrize("layout,n_recent", [("had_int4", 40), ("had_int4", 0), ("had_int2", 130), ("q8_0", 0)])
+@pytest.mark.parametrize("nq", [30, 42, 100])
+def test_paged_weights_of_an_observation_window(layout, n_recent, nq):
+    """90, 126 and 300 rows over sequences of their own lengths: an empty one, some shorter than the rows' reach."""
+    paged_weights(layout, 128, n_recent, nq)
