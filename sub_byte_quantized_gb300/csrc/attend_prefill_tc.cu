@@ -49,8 +49,9 @@
 // MMAs around it would follow one another, so both blocks hold the same rows and take the stages in turn, block
 // b the stages j with j % 2 == b; at the end block 0 combines the two (m, l, O). The second block's query codes
 // leave room for a fourth tile buffer. 32 query rows of 4 heads over 32K tokens, 8 kv heads: the call takes 70.2 us
-// instead of 89.6, the body's CTAs 44; what bounds them is the unpacking (1270 of 2130 cycles a stage, the rest its
-// wait for a free buffer). Issuing S two stages ahead of P'V, or whatever is ready first, did not help (73 and 71 us). (Other calls keep the order of their sums.)
+// instead of 89.6, the body's CTAs 44: 2130 cycles a stage, of which the unpacking takes 1270 and a block's softmax,
+// with its wait for P'V and S, twice 2130. None of these helped: four unpacking warps (registers moved between the
+// roles: 71 us), S issued two stages ahead of P'V (73), whatever is ready first (71). (Other calls keep the order of their sums.)
 //
 // The int8 query codes and scales, and the rotated f32 query rows, come from the query-preparation
 // kernel launched just before (one pass over the rows instead of one per chunk). The exact-f32
