@@ -405,8 +405,8 @@ kvq_status kvq_paged_rope_store(const kvq_paged_cache *cache, const kvq_rope *ro
  * A cache inside a budget (no counterpart on the pages): running attention weight per token, the
  * selection of the tokens to keep, and the compaction of their rows.
  *
- * kvq_decode_attend (arguments as there; for chunk 0 its own choice, never longer than that of
- * kvq_decode_attend) that also updates every token's score:
+ * kvq_decode_attend (arguments as there; for chunk 0 its own choice) that also updates every token's
+ * score:
  *   scores_out[b][kv head][t] = decay * scores_in[b][kv head][t] + the softmax weights of token t
  *                               summed over the query rows of its kv head,  0 <= t < kv_len
  *   scores_in, scores_out  device f32 [batch][n_kv_heads][scores_stride], scores_stride >= kv_len;

@@ -959,40 +959,57 @@ namespace {
 
 constexpr int kMaxEvictTokens = 1 << 27;
 
-// Chunk of an attention call that also scores the tokens, for chunk 0: the attention's own choice, but for two
-// kinds. Paged pools with up to two (sequence, kv head) per SM: at most 1536 tokens, since chunks that leave scores
-// behind take longer and the sequences' lengths differ (16 sequences of up to 16379 tokens, 8 kv heads: Q8_0 82 us
-// against 90 at the attention's 4608, asymmetric 99 against 136; 64 sequences of up to 4000, which fill the SMs by
-// themselves: 89 against 77). And the tcgen05 kernel: as many chunks as fill the SMs beside the window's CTAs (it
-// takes at most eight by itself: 64 CTAs for 128 rows and 8 kv heads; window CTAs in a second wave cost 13 us).
-int weights_chunk(const kvq::CacheView &c, int n_q_heads, int n_q, int kv_len, int auto_chunk) {
+// Chunk of an attention call that also scores the tokens, for chunk 0: the attention's own choice, but for four
+// kinds.
+//   Paged pools with up to two (sequence, kv head) per SM: at most 1536 tokens, since chunks that leave scores
+//     behind take longer and the sequences' lengths differ (16 sequences of up to 16379 tokens, 8 kv heads: Q8_0
+//     82 us against 90 at the attention's 4608, asymmetric 99 against 136; 64 sequences of up to 4000, which fill
+//     the SMs by themselves: 89 against 77).
+//   The tcgen05 kernel: as many chunks as fill the SMs beside the window's CTAs (it takes at most eight by itself:
+//     64 CTAs for 128 rows and 8 kv heads; window CTAs in a second wave cost 13 us).
+//   The row-side kernel with more rows than its decode form: whole waves of two CTAs per SM (the attention's own
+//     four to six waves: Q4_0, 128 rows, 8 kv heads of 8000 tokens 69 against 108 us, Hadamard int4, 16 rows, 12
+//     kv heads of 4517 42 against 69) and at most 512 tokens: its result carries the truncation of the tensor
+//     cores' sums, which grows with the chunk (1.2e-5 of the output's norm at 3456 tokens). Many heads: Q4_0,
+//     16 rows, 128 kv heads of 4096 tokens 202 against 221; Q8_0, 256 rows, 8 of 32768 397 against 380.
+//   The CUDA-core kernel, whose time goes with the chunk: 64 tokens where chunks of 128 leave SMs idle (Q4_0, d256,
+//     4 kv heads of 5947 tokens: 29 against 44 us).
+int weights_chunk(const kvq::CacheView &c, int n_q_heads, int n_q, int kv_len, int auto_chunk, bool f32_queries) {
   int dev = 0, sms = 148;
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   int chunk = auto_chunk;
-  if (c.page_shift >= 0 && (long long)c.B * c.H <= 2LL * sms && chunk > 1536) chunk = 1536;
+  const long long heads = (long long)c.B * c.H;
+  if (c.page_shift >= 0 && heads <= 2LL * sms && chunk > 1536) chunk = 1536;
   const int rows = n_q_heads / c.H * n_q;
+  const bool had = kvq::is_hadamard(c.layout), decode = kvq::decode_kernel(c.layout, c.v_layout);
+  const int window = had ? std::min(c.n_recent, kv_len) : 0;
+  const long long body = kv_len > window ? kv_len - window : 1;
+  const long long n_win = (window + kvq::kWinChunk - 1) / kvq::kWinChunk;
+  auto split = [&](long long n) { return (int)std::min(8192LL, ((body + n - 1) / n + 63) / 64 * 64); };   // into n chunks
   if (kvq::tc_prefill_shape(c.layout, c.v_layout, c.D, rows)) {
-    const long long units = (long long)((rows + kvq::kTcRows - 1) / kvq::kTcRows) * c.B * c.H;
-    const long long win = (long long)c.B * c.H * ((std::min(c.n_recent, kv_len) + kvq::kWinChunk - 1) / kvq::kWinChunk);
-    const long long n = (sms - win) / units, body = kv_len > c.n_recent ? kv_len - c.n_recent : 1;
-    if (n > 1) {
-      const long long fill = ((body + n - 1) / n + 63) / 64 * 64;
-      if (fill < chunk) chunk = (int)fill;
+    const long long n = (sms - heads * n_win) / ((rows + kvq::kTcRows - 1) / kvq::kTcRows * heads);
+    if (n > 1) chunk = std::min(chunk, split(n));
+  } else if (kvq::prefill_shape(c.layout, c.v_layout, c.D, rows) && (had || !f32_queries)) {
+    if (rows > 16 || decode) {
+      const long long wave = std::max(1LL, 2LL * sms / ((rows + kvq::kPrefillRows - 1) / kvq::kPrefillRows * heads) - n_win);
+      chunk = split(((body + 511) / 512 + wave - 1) / wave * wave);
     }
+  } else if (!(decode && c.D == 128 && rows <= 8) && !(c.layout == KVQ_Q6_0 && c.v_layout == c.layout && kvq::mma_q6_shape(c.D, rows))) {
+    if (heads * ((body + 127) / 128) < 2LL * sms) chunk = 64;
   }
   return chunk;
 }
-int contiguous_chunk(const kvq_cache *cache, int n_q_heads, int n_q, int kv_len, int chunk) {
+int contiguous_chunk(const kvq_cache *cache, int n_q_heads, int n_q, int kv_len, int chunk, bool f32_queries) {
   kvq::AttendArgs a;
   size_t need = 0;
   if (chunk || resolve_attend(cache, n_q_heads, n_q, kv_len, 0, 0, 0, a, need, nullptr) != KVQ_OK) return chunk;
-  return weights_chunk(a.cache, n_q_heads, n_q, kv_len, a.chunk);
+  return weights_chunk(a.cache, n_q_heads, n_q, kv_len, a.chunk, f32_queries);
 }
-int paged_chunk(const kvq_paged_cache *cache, int n_q_heads, int n_q, int max_kv_len, int chunk) {
+int paged_chunk(const kvq_paged_cache *cache, int n_q_heads, int n_q, int max_kv_len, int chunk, bool f32_queries) {
   kvq::AttendArgs a;
   size_t need = 0;
   if (chunk || resolve_paged(cache, n_q_heads, n_q, max_kv_len, 0, 0, a, need, nullptr) != KVQ_OK) return chunk;
-  return weights_chunk(a.cache, n_q_heads, n_q, max_kv_len, a.chunk);
+  return weights_chunk(a.cache, n_q_heads, n_q, max_kv_len, a.chunk, f32_queries);
 }
 
 // A weights call's workspace behind the attention's: the rows' log-sum-exp, then the scores that phase 1
@@ -1078,20 +1095,28 @@ kvq_status run_compact(const kvq::CacheView &src, const kvq::CacheView &dst, boo
 
 size_t kvq_attend_weights_workspace_bytes(const kvq_cache *cache, int32_t n_q_heads, int32_t n_q, int32_t kv_len,
                                           int32_t chunk) {
-  kvq::AttendArgs a;
-  size_t need = 0;
-  chunk = contiguous_chunk(cache, n_q_heads, n_q, kv_len, chunk);
-  if (resolve_attend(cache, n_q_heads, n_q, kv_len, 0, 0, chunk, a, need, nullptr) != KVQ_OK) return 0;
-  return weights_space(a, need).total;
+  size_t most = 0;
+  for (const bool f32_queries : {false, true}) {         // the queries' type is not known here
+    kvq::AttendArgs a;
+    size_t need = 0;
+    const int ch = contiguous_chunk(cache, n_q_heads, n_q, kv_len, chunk, f32_queries);
+    if (resolve_attend(cache, n_q_heads, n_q, kv_len, 0, 0, ch, a, need, nullptr) != KVQ_OK) return 0;
+    most = std::max(most, weights_space(a, need).total);
+  }
+  return most;
 }
 
 size_t kvq_paged_attend_weights_workspace_bytes(const kvq_paged_cache *cache, int32_t n_q_heads, int32_t n_q,
                                                 int32_t max_kv_len, int32_t chunk) {
-  kvq::AttendArgs a;
-  size_t need = 0;
-  chunk = paged_chunk(cache, n_q_heads, n_q, max_kv_len, chunk);
-  if (resolve_paged(cache, n_q_heads, n_q, max_kv_len, 0, chunk, a, need, nullptr) != KVQ_OK) return 0;
-  return weights_space(a, need).total;
+  size_t most = 0;
+  for (const bool f32_queries : {false, true}) {
+    kvq::AttendArgs a;
+    size_t need = 0;
+    const int ch = paged_chunk(cache, n_q_heads, n_q, max_kv_len, chunk, f32_queries);
+    if (resolve_paged(cache, n_q_heads, n_q, max_kv_len, 0, ch, a, need, nullptr) != KVQ_OK) return 0;
+    most = std::max(most, weights_space(a, need).total);
+  }
+  return most;
 }
 
 kvq_status kvq_decode_attend_weights(const kvq_cache *cache, const void *q, int32_t q_dtype, int32_t n_q_heads,
@@ -1101,7 +1126,7 @@ kvq_status kvq_decode_attend_weights(const kvq_cache *cache, const void *q, int3
                                      kvq_stream_t stream) {
   g_last_error[0] = 0;
   kvq::AttendArgs a;
-  chunk = contiguous_chunk(cache, n_q_heads, n_q, kv_len, chunk);
+  chunk = contiguous_chunk(cache, n_q_heads, n_q, kv_len, chunk, q_dtype == KVQ_F32);
   kvq_status st = prepare_attend(cache, q, q_dtype, n_q_heads, n_q, kv_len, causal, q_pos0, attn_scale, chunk, out,
                                  workspace, workspace_bytes, a);
   if (st == KVQ_OK) st = check_scores(scores_in, scores_out, scores_stride, kv_len, decay);
@@ -1118,7 +1143,7 @@ kvq_status kvq_paged_decode_attend_weights(const kvq_paged_cache *cache, const v
                                            void *workspace, size_t workspace_bytes, kvq_stream_t stream) {
   g_last_error[0] = 0;
   kvq::AttendArgs a;
-  chunk = paged_chunk(cache, n_q_heads, n_q, max_kv_len, chunk);
+  chunk = paged_chunk(cache, n_q_heads, n_q, max_kv_len, chunk, q_dtype == KVQ_F32);
   kvq_status st = prepare_paged(cache, q, q_dtype, n_q_heads, n_q, seq_lens, max_kv_len, causal, attn_scale, chunk, out,
                                 workspace, workspace_bytes, a);
   if (st == KVQ_OK) st = check_scores(scores_in, scores_out, scores_stride, max_kv_len, decay);
