@@ -15,9 +15,9 @@
 // arrived, then writes; reads of later rounds lie behind what it writes. One cluster per (batch, kv head,
 // plane); into another cache nothing can be overwritten too early, and the rounds need no barrier. Bound
 // by memory: scattered rows of 64 bytes and scales of 8 cost whole DRAM bursts (128K to 32K tokens in Q4_0,
-// 8 heads: 81 MB read for 41 that are needed). Reading the next round before this one's barrier cost
-// registers and was slower (16 ragged sequences in Q8_0, 58 instead of 46 us), as were clusters of two or
-// four CTAs where the planes alone fill the SMs (50 and 56 us).
+// 8 heads: 81 MB read for 41 that are needed, 22.3 us; 16 ragged sequences in Q8_0 in place 53.5 us). Before the
+// barrier's arrival the loads must have returned: a relaxed arrival does not wait for them (and took 46.7 us, now and
+// then with rows that another CTA had already written over).
 #include <cooperative_groups.h>
 
 #include "kvq_internal.cuh"
@@ -416,15 +416,8 @@ __device__ __forceinline__ void move_plane(const CompactArgs &a, int plane, int 
     look(0, st, ss);
     for (int base = 0; base < new_len; base += round) {
       read(st, ss, m);
-      // This round's values have arrived (the register reads below wait for the loads) before any CTA of the
-      // cluster writes over their rows. That is all the barrier orders: nothing written before it is read
-      // after it, so the arrive needs no release of this thread's earlier stores.
-#pragma unroll
-      for (int u = 0; u < kMoveUnits; ++u) asm volatile("" ::"r"(m.v[u].x) : "memory");
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-        asm volatile("" ::"r"(reinterpret_cast<const uint32_t *>(&m.scale[k])[0]), "r"(reinterpret_cast<const uint32_t *>(&m.zero[k])[0]) : "memory");
-      asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+      // This round's values have been read before any CTA of the cluster writes over their rows.
+      asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
       asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
       write(base, st, ss, m);
       look(base + round, st, ss);
@@ -452,9 +445,7 @@ __device__ __forceinline__ void move_scores(const CompactArgs &a, int b, int kvh
     for (int u = 0; u < kMoveUnits; ++u)
       if (st[u] >= 0) v[u] = __ldcg(src + st[u]);
     if constexpr (IN_PLACE) {                            // as in move_plane
-#pragma unroll
-      for (int u = 0; u < kMoveUnits; ++u) asm volatile("" ::"f"(v[u]) : "memory");
-      asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+      asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
       asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     }
 #pragma unroll

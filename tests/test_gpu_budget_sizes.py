@@ -151,3 +151,35 @@ def test_weights_of_an_observation_window(layout, Hq, nq):
 def test_paged_weights_of_an_observation_window(layout, n_recent, nq):
     """90, 126 and 300 rows over sequences of their own lengths: an empty one, some shorter than the rows' reach."""
     paged_weights(layout, 128, n_recent, nq)
+
+
+@pytest.mark.parametrize("layout,D", [("q6_0", 128), ("q8_0", 256), ("asym4_g32", 128), ("had_int2", 256)])
+@pytest.mark.parametrize("H,n,n_keep", [(1, 7000, 5000), (2, 2500, 2400), (8, 900, 431)])
+def test_compact_in_place_again_and_again(layout, D, H, n, n_keep):
+    """Rows are read before another CTA of the cluster writes over them, every time: shifts of a few rows to
+    thousands, 40 random lists."""
+    g = torch.Generator("cuda").manual_seed(n)
+    dc = kvq.KVCache(layout, 2, H, D, n)
+    for p in dc.planes.values():
+        p["payload"].copy_(torch.randint(0, 256, p["payload"].shape, dtype=torch.uint8, device="cuda", generator=g))
+        for name in ("scale", "zero"):
+            if name in p:
+                p[name].copy_(torch.rand(p[name].shape, device="cuda", generator=g))
+    first = {t: {name: x.clone() for name, x in p.items()} for t, p in dc.planes.items()}
+    scores = torch.rand((2, H, n), device="cuda", generator=g)
+    for i in range(40):
+        keep = torch.rand((2, H, n), device="cuda", generator=g)
+        keep[..., : n // 2] *= (i % 4) / 3                       # few early cuts, or many
+        keep = keep.topk(n_keep, -1).indices.sort(-1).values
+        for t, p in dc.planes.items():
+            for name, x in p.items():
+                x.copy_(first[t][name])
+        sc = scores.clone()
+        kvq.evict_compact(dc, keep.int(), n, scores=sc)
+        for t, p in dc.planes.items():
+            for name, x in p.items():
+                if x.dim() < 3 or x.shape[2] != n:
+                    continue
+                at = keep if x.dim() == 3 else keep[..., None].expand(-1, -1, -1, x.shape[-1])
+                assert torch.equal(x[:, :, :n_keep], first[t][name].gather(2, at)), (i, t, name)
+        assert torch.equal(sc[..., :n_keep], scores.gather(2, keep)) and not sc[..., n_keep:].any()
