@@ -1,10 +1,13 @@
 """Thin torch-facing wrappers over the C ABI: they check tensor placement/shape, pass raw
 pointers and the current CUDA stream, and nothing else. Every computation runs in libkvq.so.
 
-torch is used for device memory (cache planes, workspace) and streams only.
+torch is used for device memory (cache planes, workspace) and streams only. A call given a `stream` makes the
+buffers that the caller leaves to it (workspace, outputs) on that stream; a caller that reads such an output on
+another stream orders the two, as for any tensor.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import math
 
@@ -58,6 +61,18 @@ def _ptr(t: torch.Tensor | None) -> int | None:
 def _stream(stream) -> int | None:
     s = stream if stream is not None else torch.cuda.current_stream()
     return s.cuda_stream if isinstance(s, torch.cuda.Stream) else int(s)
+
+
+_CURRENT = contextlib.nullcontext()
+
+
+def _made_on(stream):
+    """Context in which a call makes its own buffers: the stream it launches on. The allocator orders a buffer's
+    memory by the stream that it was made on, so one made on the current stream could still be in use there when
+    another stream's kernels write it, and a workspace, dropped on return, be handed out again while they run."""
+    if stream is None:
+        return _CURRENT
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
 
 
 def _need_cuda(name: str, t: torch.Tensor) -> None:
@@ -152,11 +167,13 @@ def decode_attend(cache: KVCache, q: torch.Tensor, kv_len: int, causal: bool = F
     if attn_scale is None:
         attn_scale = 1.0 / math.sqrt(D)
     if out is None:
-        out = torch.empty((B, Hq, n_q, D), dtype=torch.float32, device=q.device)
+        with _made_on(stream):
+            out = torch.empty((B, Hq, n_q, D), dtype=torch.float32, device=q.device)
     _need_cuda("out", out)
     need = attend_workspace_bytes(cache, Hq, n_q, kv_len, chunk)
     if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        with _made_on(stream):
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
     _need_cuda("workspace", workspace)
     L.check(L.lib().kvq_decode_attend(C.byref(cache.struct), q.data_ptr(), _DTYPES[q.dtype], Hq, n_q, kv_len,
                                       int(bool(causal)), q_pos0, float(attn_scale), chunk, out.data_ptr(),
@@ -184,11 +201,13 @@ def append_decode_attend(cache: KVCache, k_new: torch.Tensor, v_new: torch.Tenso
     if attn_scale is None:
         attn_scale = 1.0 / math.sqrt(D)
     if out is None:
-        out = torch.empty((B, Hq, n_q, D), dtype=torch.float32, device=q.device)
+        with _made_on(stream):
+            out = torch.empty((B, Hq, n_q, D), dtype=torch.float32, device=q.device)
     _need_cuda("out", out)
     need = attend_workspace_bytes(cache, Hq, n_q, kv_len, chunk)
     if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        with _made_on(stream):
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
     _need_cuda("workspace", workspace)
     L.check(L.lib().kvq_append_decode_attend(
         C.byref(cache.struct), k_new.data_ptr(), v_new.data_ptr(), _DTYPES[k_new.dtype], n_new, pos0, q.data_ptr(),
@@ -213,7 +232,8 @@ def decode_attend_static(cache: KVCache, q: torch.Tensor, kv_len: int, causal: b
     if attn_scale is None:
         attn_scale = 1.0 / math.sqrt(D)
     if out is None:
-        out = torch.empty((B, Hq, n_q, D), dtype=torch.float32, device=q.device)
+        with _made_on(stream):
+            out = torch.empty((B, Hq, n_q, D), dtype=torch.float32, device=q.device)
     _need_cuda("out", out)
     L.check(L.lib().kvq_decode_attend_static(C.byref(cache.struct), q.data_ptr(), _DTYPES[q.dtype], Hq, n_q,
                                              kv_len, int(bool(causal)), q_pos0, float(attn_scale), chunk,
@@ -226,8 +246,9 @@ def debug_scores_i32(cache: KVCache, q: torch.Tensor, kv_len: int, stream=None):
     _need_cuda("q", q)
     B, Hq, n_q, D = q.shape
     n_body = kv_len - min(cache.n_recent, kv_len)
-    buf = torch.empty(B * Hq * n_q * max(n_body, 1), dtype=torch.int32, device=q.device)
-    s_q = torch.empty((B, Hq, n_q), dtype=torch.float32, device=q.device)
+    with _made_on(stream):
+        buf = torch.empty(B * Hq * n_q * max(n_body, 1), dtype=torch.int32, device=q.device)
+        s_q = torch.empty((B, Hq, n_q), dtype=torch.float32, device=q.device)
     L.check(L.lib().kvq_debug_scores_i32(C.byref(cache.struct), q.data_ptr(), _DTYPES[q.dtype], Hq, n_q, kv_len,
                                          buf.data_ptr(), s_q.data_ptr(), _stream(stream)),
             "kvq_debug_scores_i32")
@@ -246,11 +267,12 @@ def debug_attend_scores_i32(cache: KVCache, q: torch.Tensor, kv_len: int, causal
     if attn_scale is None:
         attn_scale = 1.0 / math.sqrt(D)
     n_body = kv_len - min(cache.n_recent, kv_len)
-    out = torch.empty((B, Hq, n_q, D), dtype=torch.float32, device=q.device)
-    scores = torch.full((B * Hq * n_q * max(n_body, 1),), fill, dtype=torch.int32, device=q.device)
-    s_q = torch.zeros((B, Hq, n_q), dtype=torch.float32, device=q.device)
     need = attend_workspace_bytes(cache, Hq, n_q, kv_len, chunk)
-    workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+    with _made_on(stream):
+        out = torch.empty((B, Hq, n_q, D), dtype=torch.float32, device=q.device)
+        scores = torch.full((B * Hq * n_q * max(n_body, 1),), fill, dtype=torch.int32, device=q.device)
+        s_q = torch.zeros((B, Hq, n_q), dtype=torch.float32, device=q.device)
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
     L.check(L.lib().kvq_debug_attend_scores_i32(
         C.byref(cache.struct), q.data_ptr(), _DTYPES[q.dtype], Hq, n_q, kv_len, int(bool(causal)), q_pos0,
         float(attn_scale), chunk, out.data_ptr(), workspace.data_ptr(), workspace.numel(), scores.data_ptr(),
@@ -354,16 +376,18 @@ def paged_attend_plan_chunk(cache: PagedKVCache, n_q_heads: int, n_q: int, seq_l
                                                    lens.ctypes.data))
 
 
-def _paged_out_ws(cache, q, max_kv_len, chunk, out, workspace):
+def _paged_out_ws(cache, q, max_kv_len, chunk, out, workspace, stream):
     B, Hq, n_q, D = q.shape
     if B != cache.batch or D != cache.head_dim:
         raise ValueError("q shape does not match the cache")
     if out is None:
-        out = torch.empty((B, Hq, n_q, D), dtype=torch.float32, device=q.device)
+        with _made_on(stream):
+            out = torch.empty((B, Hq, n_q, D), dtype=torch.float32, device=q.device)
     _need_cuda("out", out)
     need = paged_attend_workspace_bytes(cache, Hq, n_q, max_kv_len, chunk)
     if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        with _made_on(stream):
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
     _need_cuda("workspace", workspace)
     return out, workspace
 
@@ -379,7 +403,7 @@ def paged_decode_attend(cache: PagedKVCache, q: torch.Tensor, seq_lens: torch.Te
     Hq, n_q, D = q.shape[1], q.shape[2], q.shape[3]
     if attn_scale is None:
         attn_scale = 1.0 / math.sqrt(D)
-    out, workspace = _paged_out_ws(cache, q, max_kv_len, chunk, out, workspace)
+    out, workspace = _paged_out_ws(cache, q, max_kv_len, chunk, out, workspace, stream)
     L.check(L.lib().kvq_paged_decode_attend(
         C.byref(cache.struct), q.data_ptr(), _DTYPES[q.dtype], Hq, n_q, seq_lens.data_ptr(), max_kv_len,
         int(bool(causal)), float(attn_scale), chunk, out.data_ptr(), workspace.data_ptr(),
@@ -404,7 +428,7 @@ def paged_append_decode_attend(cache: PagedKVCache, k_new: torch.Tensor, v_new: 
     Hq, n_q, D = q.shape[1], q.shape[2], q.shape[3]
     if attn_scale is None:
         attn_scale = 1.0 / math.sqrt(D)
-    out, workspace = _paged_out_ws(cache, q, max_kv_len, chunk, out, workspace)
+    out, workspace = _paged_out_ws(cache, q, max_kv_len, chunk, out, workspace, stream)
     L.check(L.lib().kvq_paged_append_decode_attend(
         C.byref(cache.struct), k_new.data_ptr(), v_new.data_ptr(), _DTYPES[k_new.dtype], n_new, q.data_ptr(),
         _DTYPES[q.dtype], Hq, n_q, seq_lens.data_ptr(), max_kv_len, int(bool(causal)), float(attn_scale), chunk,
@@ -420,7 +444,7 @@ def _need_host(name: str, t: torch.Tensor) -> None:
         raise ValueError(f"{name} must be contiguous")
 
 
-def _host_out_ws(q, device, need, out, workspace):
+def _host_out_ws(q, device, need, out, workspace, stream):
     B, Hq, n_q, D = q.shape
     if out is None:
         out = torch.empty((B, Hq, n_q, D), dtype=torch.float32, pin_memory=True)
@@ -428,7 +452,8 @@ def _host_out_ws(q, device, need, out, workspace):
     if out.dtype != torch.float32 or tuple(out.shape) != (B, Hq, n_q, D):
         raise ValueError("out must be a float32 host tensor of q's shape")
     if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+        with _made_on(stream):
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
     _need_cuda("workspace", workspace)
     return out, workspace
 
@@ -458,7 +483,7 @@ def append_decode_attend_host(cache: KVCache, k_new: torch.Tensor, v_new: torch.
         attn_scale = 1.0 / math.sqrt(D)
     need = 0 if workspace is not None else \
         append_decode_attend_host_workspace_bytes(cache, k_new.dtype, n_new, q.dtype, Hq, n_q, kv_len, chunk)
-    out, workspace = _host_out_ws(q, cache.planes["k"]["payload"].device, need, out, workspace)
+    out, workspace = _host_out_ws(q, cache.planes["k"]["payload"].device, need, out, workspace, stream)
     L.check(L.lib().kvq_append_decode_attend_host(
         C.byref(cache.struct), k_new.data_ptr(), v_new.data_ptr(), _DTYPES[k_new.dtype], n_new, pos0, q.data_ptr(),
         _DTYPES[q.dtype], Hq, n_q, kv_len, int(bool(causal)), q_pos0, float(attn_scale), chunk, out.data_ptr(),
@@ -494,7 +519,7 @@ def paged_append_decode_attend_host(cache: PagedKVCache, k_new: torch.Tensor, v_
         attn_scale = 1.0 / math.sqrt(D)
     need = 0 if workspace is not None else \
         paged_append_decode_attend_host_workspace_bytes(cache, k_new.dtype, n_new, q.dtype, Hq, n_q, max_kv_len, chunk)
-    out, workspace = _host_out_ws(q, cache.planes["k"]["payload"].device, need, out, workspace)
+    out, workspace = _host_out_ws(q, cache.planes["k"]["payload"].device, need, out, workspace, stream)
     L.check(L.lib().kvq_paged_append_decode_attend_host(
         C.byref(cache.struct), k_new.data_ptr(), v_new.data_ptr(), _DTYPES[k_new.dtype], n_new, q.data_ptr(),
         _DTYPES[q.dtype], Hq, n_q, seq_lens.data_ptr(), max_kv_len, int(bool(causal)), float(attn_scale), chunk,
@@ -559,7 +584,8 @@ def rope_table(inv_freq: torch.Tensor, n_pos: int, pos0: int = 0, magnitude: flo
         raise ValueError("inv_freq must be a contiguous host float64 vector")
     rot_dim = 2 * inv_freq.numel()
     if out is None:
-        out = torch.empty((max(n_pos, 0), rot_dim), dtype=torch.float32, device=device)
+        with _made_on(stream):
+            out = torch.empty((max(n_pos, 0), rot_dim), dtype=torch.float32, device=device)
     dev = _here(("out", out))
     _dense("out", out, torch.float32, (n_pos, rot_dim))
     L.check(L.lib().kvq_rope_table(inv_freq.data_ptr(), rot_dim, pos0, n_pos, magnitude, out.data_ptr(),
@@ -597,7 +623,8 @@ def _rope_call(cache, table, k_new, v_new, slots, q, positions, interleaved, q_o
         if q.shape != (B, Hq, n_new, D) or q.dtype is not dtype:
             raise ValueError("q must have k_new's batch, rows, head_dim and dtype")
         if q_out is None:
-            q_out = torch.empty((B, Hq, n_new, D), dtype=dtype, device=q.device)
+            with _made_on(stream):
+                q_out = torch.empty((B, Hq, n_new, D), dtype=dtype, device=q.device)
         else:
             _dense("q_out", q_out, dtype, (B, Hq, n_new, D))
         qr = C.byref(_rows("q", q))
@@ -666,11 +693,13 @@ def _weights_call(cache, need_fn, q, n, seq_lens, scores, scores_out, attn_scale
         raise ValueError("scores and scores_out must have the same shape")
     _ints("seq_lens", seq_lens, cache.batch)
     if out is None:
-        out = torch.empty(shape, dtype=torch.float32, device=q.device)
+        with _made_on(stream):
+            out = torch.empty(shape, dtype=torch.float32, device=q.device)
     else:
         _dense("out", out, torch.float32, shape)
     if workspace is None:
-        workspace = torch.empty(max(need_fn(cache, shape[1], shape[2], n, chunk), 256), dtype=torch.uint8, device=q.device)
+        with _made_on(stream):
+            workspace = torch.empty(max(need_fn(cache, shape[1], shape[2], n, chunk), 256), dtype=torch.uint8, device=q.device)
     elif not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     dev = _here(("cache", cache.planes["k"]["payload"]), ("q", q), ("scores", scores), ("scores_out", scores_out),
@@ -723,7 +752,8 @@ def evict_select(scores: torch.Tensor, kv_len: int, n_keep: int, n_sink: int = 0
         raise ValueError("scores must be contiguous float32 [batch][n_kv_heads][tokens]")
     B, H, stride = scores.shape
     if keep is None:
-        keep = torch.empty((B, H, max(n_keep, 1)), dtype=torch.int32, device=scores.device)
+        with _made_on(stream):
+            keep = torch.empty((B, H, max(n_keep, 1)), dtype=torch.int32, device=scores.device)
     else:
         _ints("keep", keep, B * H * max(n_keep, 1))
     _ints("seq_lens", seq_lens, B)
