@@ -834,11 +834,11 @@ kvq_status check_rope_store(const kvq::CacheView &v, const kvq_rope *rope, const
     return fail(KVQ_EALIGN, "rotary table/positions not 16-byte aligned");
   if ((q != nullptr) != (n_q_heads > 0)) return fail(KVQ_EINVAL, "q and n_q_heads go together");
   if (n_q_heads % v.H) return fail(KVQ_ESHAPE, "n_q_heads %d not a multiple of n_kv_heads %d", n_q_heads, v.H);
-  if (q && !q_out) return fail(KVQ_EINVAL, "q_out is NULL");
-  if (q && !aligned(q_out, 16)) return fail(KVQ_EALIGN, "q_out not 16-byte aligned");
   if ((long double)v.B * (2.0L * v.H + n_q_heads) * n_new * 32 > 256.0L * INT_MAX)
     return fail(KVQ_ESHAPE, "too many rows for one launch");
-  if (n_new == 0) return KVQ_OK;
+  if (n_new == 0) return KVQ_OK;                         // (buffers of no rows have no address)
+  if (q && !q_out) return fail(KVQ_EINVAL, "q_out is NULL");
+  if (q && !aligned(q_out, 16)) return fail(KVQ_EALIGN, "q_out not 16-byte aligned");
   st = check_rows("k_new", k_new, dtype, g.in[0]);
   if (st == KVQ_OK) st = check_rows("v_new", v_new, dtype, g.in[1]);
   g.in[2] = {nullptr, 0, 0, 0};

@@ -1,0 +1,35 @@
+"""Rotary appends at the ends of what they are documented for."""
+import pytest
+import torch
+
+import sub_byte_quantized_gb300 as kvq
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("queries", [False, True])
+@pytest.mark.parametrize("layout", ["q4_0", "had_int4", "q4_0+q8_0"])
+def test_an_append_of_no_rows(layout, queries, paged):
+    B, H, D, cap = 2, 2, 128, 128
+    n_recent = 16 if layout.startswith("had") else 0
+    x = torch.randn((B, H, 3, D), device="cuda").bfloat16()
+    f, _ = kvq.rope_frequencies(D)
+    table = kvq.rope_table(f, cap)
+    if paged:
+        c = kvq.PagedKVCache(layout, B, H, D, 64, 4, 2, n_recent=n_recent)
+        c.set_block_table(torch.arange(4).view(2, 2))
+        at, call = torch.tensor([5, 9], dtype=torch.int32, device="cuda"), kvq.paged_rope_store
+    else:
+        c, at, call = kvq.KVCache(layout, B, H, D, cap, n_recent=n_recent), cap, kvq.rope_store
+    for p in c.planes.values():
+        for t in p.values():
+            t.copy_(torch.randint(0, 100, t.shape, device="cuda"))
+    before = {(k, n): t.clone() for k, p in c.planes.items() for n, t in p.items()}
+    none = x[:, :, :0]
+    got = call(c, table, none, none, at, q=none if queries else None,
+               positions=torch.empty((B, 0), dtype=torch.int32, device="cuda"))
+    assert got.shape == (B, H, 0, D) if queries else got is None
+    torch.cuda.synchronize()
+    for (k, n), t in before.items():
+        assert torch.equal(c.planes[k][n], t)
