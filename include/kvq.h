@@ -388,7 +388,8 @@ typedef struct kvq_rows {
  *   y_a = x_a c - x_b s,  y_b = x_b c + x_a s   per pair (a, b), each product and sum rounded to f32
  * (so the packed bytes are those of kvq_store on the f32 rotated keys, bit for bit).
  *   k_new, v_new, q  in `dtype`; q NULL: no queries (n_q_heads 0, q_out NULL)
- *   q_out            device [batch][n_q_heads][n_new][head_dim] in `dtype`; overlaps no input
+ *   q_out            device [batch][n_q_heads][n_new][head_dim] in `dtype`; refused where it reaches into
+ *                    the memory from an input's first row to its last
  * One kernel launch (mixed K/V layouts: one per plane). n_new == 0 is a no-op.
  */
 kvq_status kvq_rope_store(const kvq_cache *cache, const kvq_rope *rope, const kvq_rows *k_new, const kvq_rows *v_new,
@@ -410,9 +411,9 @@ kvq_status kvq_paged_rope_store(const kvq_paged_cache *cache, const kvq_rope *ro
  *   scores_out[b][kv head][t] = decay * scores_in[b][kv head][t] + the softmax weights of token t
  *                               summed over the query rows of its kv head,  0 <= t < kv_len
  *   scores_in, scores_out  device f32 [batch][n_kv_heads][scores_stride], scores_stride >= kv_len;
- *                          they may be the same buffer, else they do not overlap. scores_in NULL or
- *                          decay 0: no earlier scores are read. Entries t >= kv_len are left as they
- *                          were. A row that sees no token adds nothing.
+ *                          they may be the same buffer; entries that overlap in another way are
+ *                          refused. scores_in NULL or decay 0: no earlier scores are read. Entries
+ *                          t >= kv_len are left as they were. A row that sees no token adds nothing.
  *   workspace              at least kvq_attend_weights_workspace_bytes (shared with no call in flight)
  * Deterministic: no atomics.
  */
@@ -441,9 +442,9 @@ kvq_status kvq_paged_decode_attend_weights(const kvq_paged_cache *cache, const v
  *   seq_lens  device i32 [batch], each clamped into [0, kv_len], or NULL: every length is kv_len
  *   keep      device i32 [batch][n_kv_heads][n_keep]: ascending; a sequence of at most n_keep tokens
  *             keeps all of them, and -1 fills the rest
- *   new_lens  device i32 [batch]: min(length, n_keep), or NULL; not seq_lens itself (every head reads
- *             the old lengths, and so does kvq_paged_evict_compact)
- * n_sink + n_recent <= n_keep; 1 <= kv_len <= 2^27. One launch.
+ *   new_lens  device i32 [batch]: min(length, n_keep), or NULL; no entry of seq_lens itself (every
+ *             head reads the old lengths, and so does kvq_paged_evict_compact)
+ * keep and scores do not overlap; n_sink + n_recent <= n_keep; 1 <= kv_len <= 2^27. One launch.
  */
 kvq_status kvq_evict_select(const float *scores, int32_t batch, int32_t n_kv_heads, int64_t scores_stride,
                             int32_t kv_len, const int32_t *seq_lens, int32_t n_keep, int32_t n_sink,
@@ -457,8 +458,8 @@ kvq_status kvq_evict_select(const float *scores, int32_t batch, int32_t n_kv_hea
  *   dst     NULL (or the cache itself): in place. Else another cache of the same layout, batch,
  *           n_kv_heads, head_dim and n_recent with room for min(kv_len, n_keep) tokens, no plane shared.
  *   scores  device f32 [batch][n_kv_heads][scores_stride] or NULL: moved likewise, in place, or (with
- *           another dst) to scores_out [batch][n_kv_heads][out_stride]; entries behind the kept ones up
- *           to min(stride, kv_len) become 0, ready for new tokens.
+ *           another dst) to scores_out [batch][n_kv_heads][out_stride], which overlaps them nowhere;
+ *           entries behind the kept ones up to min(stride, kv_len) become 0, ready for new tokens.
  * HAD_INT4 / HAD_INT2 with n_recent > 0: the list has to keep the last n_recent tokens (n_keep >=
  * n_recent), and the window ring is turned so that they stay at (new index mod n_recent).
  * 1 <= kv_len <= 2^27. Two launches at most.

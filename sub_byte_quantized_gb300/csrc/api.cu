@@ -6,6 +6,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <cstdlib>
 #include <cstring>
 #include <mutex>
 
@@ -27,6 +28,12 @@ kvq_status fail(kvq_status st, const char *fmt, ...) {
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+// Whether two runs of bytes share one (NULL: no run).
+bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && na && nb && (x <= y ? y - x < na : x - y < nb);
+}
 
 size_t row_bytes_of(int layout, int D) {
   if (D != 128 && D != 256) return 0;
@@ -853,6 +860,20 @@ kvq_status check_rope_store(const kvq::CacheView &v, const kvq_rope *rope, const
   return KVQ_OK;
 }
 
+// q_out is written while other rows, and the other halves of its own, are still to be read: it lies outside the run
+// of bytes from an input's first row to its last.
+kvq_status check_q_out(const kvq::CacheView &v, const kvq::RopeStore &g) {
+  const size_t size = dtype_bytes(g.dtype), out = (size_t)v.B * g.Hq * g.n_new * v.D * size;
+  const char *const names[] = {"k_new", "v_new", "q"};
+  for (int i = 0; i < 3; ++i) {
+    const kvq::RowsIn &in = g.in[i];
+    const int heads = i == 2 ? g.Hq : v.H;
+    const size_t last = (size_t)(v.B - 1) * in.batch + (size_t)(heads - 1) * in.head + (size_t)(g.n_new - 1) * in.token;
+    if (overlap(g.q_out, out, in.data, (last + v.D) * size)) return fail(KVQ_EINVAL, "q_out overlaps %s", names[i]);
+  }
+  return KVQ_OK;
+}
+
 }  // namespace
 
 kvq_status kvq_rope_frequencies(const kvq_rope_config *config, double *inv_freq, float *magnitude) {
@@ -929,6 +950,7 @@ kvq_status kvq_rope_store(const kvq_cache *cache, const kvq_rope *rope, const kv
   if (pos0 < 0) return fail(KVQ_EINVAL, "pos0 must be >= 0");
   if ((long long)pos0 + n_new > v.cap) return fail(KVQ_ECAPACITY, "pos0 + n_new = %lld > capacity %d", (long long)pos0 + n_new, v.cap);
   if (n_new == 0) return KVQ_OK;
+  if ((st = check_q_out(v, g)) != KVQ_OK) return st;
   g.pos0 = pos0;
   const cudaError_t e = kvq::launch_rope_store(v, g, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(KVQ_ECUDA, "rope store launch: %s", cudaGetErrorString(e));
@@ -948,6 +970,7 @@ kvq_status kvq_paged_rope_store(const kvq_paged_cache *cache, const kvq_rope *ro
   if (n_new == 0) return KVQ_OK;
   if (!slots) return fail(KVQ_EINVAL, "slots is NULL");
   if (!aligned(slots, 16)) return fail(KVQ_EALIGN, "slots not 16-byte aligned");
+  if ((st = check_q_out(v, g)) != KVQ_OK) return st;
   g.slots = slots;
   const cudaError_t e = kvq::launch_rope_store(v, g, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(KVQ_ECUDA, "rope store launch: %s", cudaGetErrorString(e));
@@ -1029,11 +1052,20 @@ WeightsSpace weights_space(const kvq::AttendArgs &a, size_t attend_need) {
   return w;
 }
 
-kvq_status check_scores(const float *scores_in, const float *scores_out, int64_t stride, int kv_len, float decay) {
+// `rows`: of scores, batch * n_kv_heads
+kvq_status check_scores(const float *scores_in, const float *scores_out, int64_t stride, int kv_len, float decay,
+                        int64_t rows) {
   if (!scores_out) return fail(KVQ_EINVAL, "scores_out is NULL");
   if (!aligned(scores_in, 16) || !aligned(scores_out, 16)) return fail(KVQ_EALIGN, "scores not 16-byte aligned");
   if (stride < kv_len) return fail(KVQ_ESHAPE, "scores_stride %lld < kv_len %d", (long long)stride, kv_len);
   if (!std::isfinite(decay)) return fail(KVQ_EINVAL, "decay must be finite");
+  if (scores_in && scores_in != scores_out && decay != 0.0f) {
+    // scores_out starts k rows and r entries behind scores_in: one of its rows meets row k or row k + 1 of scores_in
+    const int64_t d = (int64_t)((intptr_t)scores_out - (intptr_t)scores_in) / (int64_t)sizeof(float);
+    const int64_t k = d >= 0 ? d / stride : -((stride - 1 - d) / stride), r = d - k * stride;
+    if ((r < kv_len && std::abs(k) < rows) || (stride - r < kv_len && std::abs(k + 1) < rows))
+      return fail(KVQ_EINVAL, "scores_in and scores_out overlap without being the same");
+  }
   return KVQ_OK;
 }
 
@@ -1073,6 +1105,10 @@ kvq_status run_compact(const kvq::CacheView &src, const kvq::CacheView &dst, boo
     if (!aligned(scores, 16) || !aligned(scores_out, 16)) return fail(KVQ_EALIGN, "scores not 16-byte aligned");
     if (scores_stride < kv_len) return fail(KVQ_ESHAPE, "scores_stride %lld < kv_len %d", (long long)scores_stride, kv_len);
     if (out_stride < most) return fail(KVQ_ESHAPE, "out_stride %lld < %d kept tokens", (long long)out_stride, most);
+    const size_t rows = (size_t)src.B * src.H - 1;
+    if (scores_out != scores && overlap(scores, (rows * scores_stride + kv_len) * sizeof(float), scores_out,
+                                        (rows * out_stride + std::min<int64_t>(out_stride, kv_len)) * sizeof(float)))
+      return fail(KVQ_EINVAL, "scores and scores_out overlap");
   }
   kvq::CompactArgs a;
   a.src = src;
@@ -1129,7 +1165,7 @@ kvq_status kvq_decode_attend_weights(const kvq_cache *cache, const void *q, int3
   chunk = contiguous_chunk(cache, n_q_heads, n_q, kv_len, chunk, q_dtype == KVQ_F32);
   kvq_status st = prepare_attend(cache, q, q_dtype, n_q_heads, n_q, kv_len, causal, q_pos0, attn_scale, chunk, out,
                                  workspace, workspace_bytes, a);
-  if (st == KVQ_OK) st = check_scores(scores_in, scores_out, scores_stride, kv_len, decay);
+  if (st == KVQ_OK) st = check_scores(scores_in, scores_out, scores_stride, kv_len, decay, (int64_t)a.cache.B * a.cache.H);
   if (st != KVQ_OK) return st;
   const size_t need = kvq_attend_workspace_bytes(cache, n_q_heads, n_q, kv_len, chunk);   // of the same chunk
   return run_weights(a, need, workspace, workspace_bytes, scores_in, scores_out, scores_stride, decay,
@@ -1146,7 +1182,7 @@ kvq_status kvq_paged_decode_attend_weights(const kvq_paged_cache *cache, const v
   chunk = paged_chunk(cache, n_q_heads, n_q, max_kv_len, chunk, q_dtype == KVQ_F32);
   kvq_status st = prepare_paged(cache, q, q_dtype, n_q_heads, n_q, seq_lens, max_kv_len, causal, attn_scale, chunk, out,
                                 workspace, workspace_bytes, a);
-  if (st == KVQ_OK) st = check_scores(scores_in, scores_out, scores_stride, max_kv_len, decay);
+  if (st == KVQ_OK) st = check_scores(scores_in, scores_out, scores_stride, max_kv_len, decay, (int64_t)a.cache.B * a.cache.H);
   if (st != KVQ_OK) return st;
   const size_t need = kvq_paged_attend_workspace_bytes(cache, n_q_heads, n_q, max_kv_len, chunk);
   return run_weights(a, need, workspace, workspace_bytes, scores_in, scores_out, scores_stride, decay,
@@ -1161,12 +1197,16 @@ kvq_status kvq_evict_select(const float *scores, int32_t batch, int32_t n_kv_hea
   if (st != KVQ_OK) return st;
   if (!scores) return fail(KVQ_EINVAL, "scores is NULL");
   if (!aligned(scores, 16) || !aligned(new_lens, 16)) return fail(KVQ_EALIGN, "scores/new_lens not 16-byte aligned");
-  if (new_lens && new_lens == seq_lens) return fail(KVQ_EINVAL, "new_lens must not be seq_lens");
   if (batch < 1 || n_kv_heads < 1) return fail(KVQ_EINVAL, "batch and n_kv_heads must be >= 1");
   if ((long long)batch * n_kv_heads > 1 << 24) return fail(KVQ_ESHAPE, "batch * n_kv_heads > 2^24");
   if (scores_stride < kv_len) return fail(KVQ_ESHAPE, "scores_stride %lld < kv_len %d", (long long)scores_stride, kv_len);
   if (n_sink < 0 || n_recent < 0 || (long long)n_sink + n_recent > n_keep)
     return fail(KVQ_EINVAL, "n_sink and n_recent must be >= 0 and together at most n_keep");
+  if (overlap(new_lens, batch * sizeof(int32_t), seq_lens, batch * sizeof(int32_t)))
+    return fail(KVQ_EINVAL, "new_lens must not be seq_lens");
+  const size_t rows = (size_t)batch * n_kv_heads;
+  if (overlap(keep, rows * n_keep * sizeof(int32_t), scores, ((rows - 1) * scores_stride + kv_len) * sizeof(float)))
+    return fail(KVQ_EINVAL, "keep overlaps the scores");
   kvq::SelectArgs a = {batch, n_kv_heads, kv_len, n_keep, n_sink, n_recent, scores_stride, scores, seq_lens, keep, new_lens};
   const cudaError_t e = kvq::launch_evict_select(a, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(KVQ_ECUDA, "select launch: %s", cudaGetErrorString(e));

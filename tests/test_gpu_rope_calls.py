@@ -33,3 +33,28 @@ def test_an_append_of_no_rows(layout, queries, paged):
     torch.cuda.synchronize()
     for (k, n), t in before.items():
         assert torch.equal(c.planes[k][n], t)
+
+
+def test_rotated_queries_beside_the_projection_in_one_buffer():
+    """q_out right before and right behind the inputs' memory is no overlap; anywhere inside it is refused."""
+    B, n, Hq, H, D = 2, 3, 4, 2, 128
+    size, out = B * n * (Hq + 2 * H) * D, B * Hq * n * D
+    buf = torch.randn(size + 2 * out, device="cuda").bfloat16()
+    x = buf[out:out + size].view(B, n, Hq + 2 * H, D).transpose(1, 2)
+    q, k, v = x[:, :Hq], x[:, Hq:Hq + H], x[:, Hq + H:]
+    f, _ = kvq.rope_frequencies(D)
+    table = kvq.rope_table(f, 16)
+    c = kvq.KVCache("q4_0", B, H, D, 16)
+    want = kvq.rope_store(c, table, k, v, 2, q=q)
+    first = {(t, m): y.clone() for t, p in c.planes.items() for m, y in p.items()}
+    for at in (0, out + size):
+        got = buf[at:at + out].view(B, Hq, n, D)
+        assert kvq.rope_store(c, table, k, v, 2, q=q, q_out=got) is got and torch.equal(got, want)
+        for (t, m), y in first.items():
+            assert torch.equal(c.planes[t][m], y)
+    for at in (8, out, out + 8 * D, size + out - 8):
+        with pytest.raises(kvq.KvqError, match="overlaps"):
+            kvq.rope_store(c, table, k, v, 2, q=q, q_out=buf[at:at + out].view(B, Hq, n, D))
+    same = q[:1, :, :1]
+    with pytest.raises(kvq.KvqError, match="overlaps"):
+        kvq.rope_store(kvq.KVCache("q4_0", 1, H, D, 16), table, k[:1, :, :1], v[:1, :, :1], 2, q=same, q_out=same)
