@@ -413,7 +413,8 @@ kvq_status kvq_paged_rope_store(const kvq_paged_cache *cache, const kvq_rope *ro
  *   scores_in, scores_out  device f32 [batch][n_kv_heads][scores_stride], scores_stride >= kv_len;
  *                          they may be the same buffer; entries that overlap in another way are
  *                          refused. scores_in NULL or decay 0: no earlier scores are read. Entries
- *                          t >= kv_len are left as they were. A row that sees no token adds nothing.
+ *                          t >= kv_len are left as they were. A row that sees no token adds nothing; one
+ *                          whose output is NaN makes its tokens' scores NaN.
  *   workspace              at least kvq_attend_weights_workspace_bytes (shared with no call in flight)
  * Deterministic: no atomics.
  */

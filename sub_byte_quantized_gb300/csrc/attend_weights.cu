@@ -426,6 +426,7 @@ __global__ void __launch_bounds__(kScoreThreads) attend_weights_scores_kernel(We
     float w = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) w += ex2(x[k][v] - lse2[v]);   // a row that adds nothing has lse2 = +infinity
+    if (t >= end) w = 0.0f;                              // (a failed row's lse2 is NaN)
     if constexpr (LPT == 2) w += __shfl_xor_sync(0xffffffffu, w, 1);
     if (i % LPT == 0 && t < sl.n_body) out[t] = in ? fmaf(wa.decay, old[k], w) : w;
   }

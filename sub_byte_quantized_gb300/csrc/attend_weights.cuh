@@ -17,12 +17,13 @@ __host__ __device__ constexpr int max_of(int a, int b) { return a > b ? a : b; }
 template <int D, int WARPS, int ROWS = 2 * WARPS>
 __host__ __device__ constexpr int window_smem() { return (kWinTokens * (D + 4) + ROWS * D + WARPS * kWinTokens + 2 * ROWS) * 4; }
 
-// What the attention's second phase left for query row r; rows past the last add nothing.
+// What the attention's second phase left for query row r; rows past the last and rows that see nothing add nothing.
+// NaN (a phase 1 whose wait gave up) goes on into the weights of the tokens the row sees.
 __device__ __forceinline__ void row_result(const AttendArgs &a, const SeqLen &sl, int bb, int kvh, int r, float &lse2, int &limit) {
   const bool live = r < a.gqa * a.n_q;
   const float lse = live ? a.lse[query_row_index(a, bb, kvh, r)] : -INFINITY;
-  lse2 = lse > -INFINITY ? lse * kLog2e : INFINITY;
-  limit = live && lse > -INFINITY ? row_limit(a, sl, r % a.n_q) : -1;
+  lse2 = lse == -INFINITY ? INFINITY : lse * kLog2e;
+  limit = lse == -INFINITY ? -1 : row_limit(a, sl, r % a.n_q);
 }
 
 // Window tokens [n_body + 32 j, ..) of one kv head: lanes are tokens, warps are query rows (PW of them at a

@@ -169,7 +169,7 @@ struct AttendArgs {
   // cap_scores [B][Hq][n_q][n_body] and each row's int8 query scale to cap_sq [B][Hq][n_q].
   int32_t *cap_scores;
   float *cap_sq;
-  // natural log of each row's sum of exponentials [B][Hq][n_q] (-infinity: the row sees nothing),
+  // natural log of each row's sum of exponentials [B][Hq][n_q] (-infinity: the row sees nothing; NaN: phase 1 failed),
   // written by phase 2 when not nullptr
   float *lse;
   // masked scores in base 2, [B][H_kv][s_tokens][s_rows] (query rows of the kv head, tokens of the body),

@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kWarps * 32) attend_reduce_kernel(AttendArgs a
     for (int i = 0; i < VPL; ++i) x[i] = fmaf(sm_o[w][HAD ? lane * VPL + i : lane], wt, x[i]);
   }
   const float inv = Lt > 0.0f ? 1.0f / Lt : 0.0f;
-  if (a.lse && lane == 0 && d0 == 0) a.lse[row] = Lt > 0.0f ? Mt + logf(Lt) : -INFINITY;
+  if (a.lse && lane == 0 && d0 == 0) a.lse[row] = Lt == 0.0f ? -INFINITY : Mt + logf(Lt);   // NaN stays NaN
 #pragma unroll
   for (int i = 0; i < VPL; ++i) x[i] *= inv;
   if (HAD) {
@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kWarps * 32, KB >= 8 ? 1 : (D == 128 ? 8 - KB 
     M = bm;
   }
   const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-  if (a.lse && lane == 0) a.lse[row] = L > 0.0f ? M + logf(L) : -INFINITY;
+  if (a.lse && lane == 0) a.lse[row] = L == 0.0f ? -INFINITY : M + logf(L);   // NaN stays NaN
 #pragma unroll
   for (int i = 0; i < VPL; ++i) O[i] *= inv;
   if (HAD) {
