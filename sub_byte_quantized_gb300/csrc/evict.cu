@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_select_kernel(S
   int32_t *keep = a.keep + (size_t)bh * a.n_keep;
   if (a.new_lens && bh % a.H == 0 && rank == 0 && tid == 0) a.new_lens[b] = min(L, a.n_keep);
   if (L <= a.n_keep) {                                   // everything stays (the whole cluster takes this branch)
-    for (int i = rank * THREADS + tid; i < a.n_keep; i += ranks * THREADS) keep[i] = i < L ? i : -1;
+    for (long long i = rank * THREADS + tid; i < a.n_keep; i += ranks * THREADS) keep[i] = i < L ? (int)i : -1;   // (n_keep up to 2^31 - 1)
     return;
   }
   const int lo = a.n_sink, hi = L - a.n_recent;          // the tokens that compete; lo < hi since L > n_keep
