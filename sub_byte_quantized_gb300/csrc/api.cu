@@ -1243,7 +1243,7 @@ kvq_status kvq_evict_compact(const kvq_cache *cache, const kvq_cache *dst, const
     if (scores_out && scores_out != scores) return fail(KVQ_EINVAL, "in place the scores move in place too");
     scores_out = scores;
     out_stride = scores_stride;
-  } else if (scores && (!scores_out || scores_out == scores)) {
+  } else if (scores ? !scores_out || scores_out == scores : scores_out != nullptr) {
     return fail(KVQ_EINVAL, "with another dst the scores go to a scores_out of their own");
   }
   return run_compact(v, d, in_place, keep, n_keep, kv_len, nullptr, scores, scores_stride, scores_out, out_stride,

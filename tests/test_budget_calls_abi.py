@@ -67,3 +67,12 @@ def test_select_and_compact_refuse_overlaps(L):
     for d in (-16, 16, 64 * 4):
         assert L.kvq_evict_compact(C.byref(A._cache()), C.byref(other), P, 20, 60, F, 64, F + d, 32, None) == A.EINVAL
         assert b"overlap" in L.kvq_last_error()
+
+
+def test_compact_refuses_a_scores_out_without_scores(L):
+    """It would have been left unwritten, in place and into another cache."""
+    import tests.test_budget_abi as A
+    other = A._cache(ptr=2 * P)
+    for dst in (None, C.byref(other)):
+        assert L.kvq_evict_compact(C.byref(A._cache()), dst, P, 20, 60, None, 0, F, 32, None) == A.EINVAL
+        assert b"scores" in L.kvq_last_error()
