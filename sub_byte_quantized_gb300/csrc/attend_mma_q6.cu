@@ -96,7 +96,9 @@ __device__ __forceinline__ uint32_t lds32(const uint8_t *p) { return *reinterpre
 
 // SIGNED: V codes enter as exact signed values, no offset mass goes through the long P'V accumulation
 // (calls that also score the tokens, whose output is held to float32: over 32K tokens of random keys its
-// error falls from 4e-5 of the output's norm to 1e-6).
+// error falls from 4e-5 of the output's norm to 1e-6). Their probabilities are taken 2^12 larger, so that P' and
+// its lo part stay above f16's subnormals for small scales and tokens of little weight (4096 tokens with values of
+// 0.01: 4e-5 of the output's norm without); see kLift.
 template <int D, bool PAGED, bool SIGNED>
 __global__ void __launch_bounds__(kThreads, kMmaQ6CtasPerSm(D)) attend_mma_q6_kernel(AttendArgs a) {
   using G = Geom<D>;
@@ -334,10 +336,14 @@ __global__ void __launch_bounds__(kThreads, kMmaQ6CtasPerSm(D)) attend_mma_q6_ke
         mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, k));
       }
       const float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
-      const float mu0 = mn0 == -INFINITY ? 0.0f : mn0, mu1 = mn1 == -INFINITY ? 0.0f : mn1;
+      float mu0 = mn0 == -INFINITY ? 0.0f : mn0, mu1 = mn1 == -INFINITY ? 0.0f : mn1;
       const float corr0 = ex2(m0 - mu0), corr1 = ex2(m1 - mu1);
       m0 = mn0;
       m1 = mn1;
+      if constexpr (SIGNED) {
+        mu0 -= kLift;
+        mu1 -= kLift;
+      }
       const float p0 = ex2(s[0] - mu0), p1 = ex2(s[1] - mu1), p2 = ex2(s[2] - mu0), p3 = ex2(s[3] - mu1);
       l0 = fmaf(l0, corr0, p0 + p2);
       l1 = fmaf(l1, corr1, p1 + p3);
@@ -367,8 +373,8 @@ __global__ void __launch_bounds__(kThreads, kMmaQ6CtasPerSm(D)) attend_mma_q6_ke
     float *cm = reinterpret_cast<float *>(smem);
     float *cl = cm + 16;
     if (g == 0 && c < 2) {
-      cm[tw * 4 + r0] = m0;
-      cm[tw * 4 + r1] = m1;
+      cm[tw * 4 + r0] = m0 - (SIGNED ? kLift : 0.0f);
+      cm[tw * 4 + r1] = m1 - (SIGNED ? kLift : 0.0f);
       cl[tw * 4 + r0] = l0;
       cl[tw * 4 + r1] = l1;
     }
@@ -387,6 +393,7 @@ __global__ void __launch_bounds__(kThreads, kMmaQ6CtasPerSm(D)) attend_mma_q6_ke
     const uint32_t sel_v = (uint32_t)(g & 3) | ((uint32_t)(4 + (g & 3)) << 8);
     const uint32_t sel_h = (g & 1) ? 0x7632u : 0x5410u;
     const int gb = min(g, NB - 1);
+    bool lifted = SIGNED;                                // P' carries 2^kLift (the same for the whole warp)
 
     for (int i = 0; i <= n_stages; ++i) {
       cp_async_wait<1>();
@@ -397,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, kMmaQ6CtasPerSm(D)) attend_mma_q6_ke
       const int ts = t0 + j * kStage + tr;
       if (j < 0 || ts >= t_end) continue;
       const uint8_t *xs = xch + ((tw * 2 + (j & 1)) * 32 + lane) * 32;
-      const uint4 pb = *reinterpret_cast<const uint4 *>(xs);
+      uint4 pb = *reinterpret_cast<const uint4 *>(xs);
       const float2 cr = *reinterpret_cast<const float2 *>(xs + 16);
       if (__any_sync(0xffffffffu, cr.x != 1.0f || cr.y != 1.0f)) {
         Dw[0] *= cr.x;
@@ -430,6 +437,23 @@ __global__ void __launch_bounds__(kThreads, kMmaQ6CtasPerSm(D)) attend_mma_q6_ke
         const uint2 x8 = *reinterpret_cast<const uint2 *>(sa + 8 * G::SB), x9 = *reinterpret_cast<const uint2 *>(sa + 9 * G::SB);
         s2c[0] = x0.x; s2c[1] = x0.y; s2c1[0] = x1.x; s2c1[1] = x1.y;
         s2c8[0] = x8.x; s2c8[1] = x8.y; s2c9[0] = x9.x; s2c9[1] = x9.y;
+      }
+      if constexpr (SIGNED) {
+        if (lifted) {
+          uint32_t big = 0;                              // the top exponent bit of the tile's V scales
+#pragma unroll
+          for (int k = 0; k < NB / 2; ++k) big |= s2c[k] | s2c1[k] | s2c8[k] | s2c9[k];
+          if (__any_sync(0xffffffffu, big & kTopExponent)) {
+            lifted = false;
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) O[b][h][k] *= kUnlift;
+          }
+        }
+        if (!lifted) pb = unlift(pb);
       }
       // W term: rows g < NB of its A operand hold block g's V scales
       if constexpr (!SIGNED) {
@@ -482,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, kMmaQ6CtasPerSm(D)) attend_mma_q6_ke
     float *co = reinterpret_cast<float *>(smem) + 32;     // [tile][4][D] after cm/cl
     // value = u * s_v - 32 s_v: even dims entered as u * 2^-24, odd dims as 16 u * 2^-24 (SIGNED: the
     // codes themselves, Dw stays 0)
-    constexpr float kEven = SIGNED ? 1.0f : 16777216.0f, kOdd = SIGNED ? 1.0f : 1048576.0f;
+    const float kEven = SIGNED ? (lifted ? 1.0f : 1.0f / kUnlift) : 16777216.0f, kOdd = SIGNED ? kEven : 1048576.0f;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       const float w0 = 32.0f * __shfl_sync(0xffffffffu, Dw[0], 4 * b + c);

@@ -123,6 +123,16 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   return d;
 }
 
+// Calls that also score the tokens are held to float32: their probabilities are taken 2^kLift times larger (up to
+// 2^12 instead of 1), so that P' = p * scale and its lo part stay above f16's subnormals. What those still cost is
+// 2^-25 for each of the two in P', 2^-37 of the largest probability times the code. A scale of 2 or more could
+// take P' out of f16's range: a warp that meets one goes on without the factor.
+constexpr float kLift = 12.0f, kUnlift = 0x1p-12f;
+constexpr uint32_t kTopExponent = 0x40004000u;           // set in f16 values of 2 and more (NaN and infinity too)
+__device__ __forceinline__ uint4 unlift(const uint4 &p) {  // f16 pairs times 2^-12
+  return make_uint4(hmul2(p.x, 0x0C000C00u), hmul2(p.y, 0x0C000C00u), hmul2(p.z, 0x0C000C00u), hmul2(p.w, 0x0C000C00u));
+}
+
 // f16x2 constants (bit patterns): 1/16, -1032, -72 in both halves.
 constexpr uint32_t kH16th = 0x2C002C00u, kHm1032 = 0xE408E408u, kHm72 = 0xD480D480u;
 

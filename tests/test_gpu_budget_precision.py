@@ -1,0 +1,82 @@
+"""The output of scoring attention calls is held to float32 for values of any size and for rows whose weight lies
+on one token: its error, as a share of the output's norm, against the oracle in 64 bits."""
+import numpy as np
+import pytest
+import torch
+
+import sub_byte_quantized_gb300 as kvq
+from oracle import attention as OA, budget as OB
+
+pytestmark = pytest.mark.gpu
+S, H = 4096, 2
+TOP_CODE = {"q8_0": 128, "q6_0": 32, "asym4_g32": 15, "q4_0": 8, "had_int4": 7, "had_int2": 1}
+
+
+def _inputs(std, sink, rows, nq, D):
+    """Keys and queries of scores near 0.01, values of zero mean (std: of all tokens, or of each); or (sink) scores
+    near 0.1 and a first token without value that takes 2^14 times the others' weight."""
+    rng = np.random.default_rng(11)
+    alpha = np.float32((0.1 if sink else 0.01) / np.sqrt(D))
+    Hq = H * rows // nq
+    k = rng.standard_normal((1, H, S, D)).astype(np.float32)
+    v = (np.broadcast_to(np.asarray(std), (S,))[:, None] * rng.standard_normal((1, H, S, D))).astype(np.float32)
+    q = rng.standard_normal((1, Hq, nq, D)).astype(np.float32)
+    if sink:
+        q0 = rng.standard_normal((1, H, 1, D)).astype(np.float32)
+        q = np.repeat(q0, Hq // H, 1) + 0.05 * q
+        k[:, :, :1] = q0 * np.float32(14 * np.log(2)) / (alpha * (q0 * q0).sum(-1, keepdims=True))
+        v[:, :, 0] = 0
+    return k, v, torch.from_numpy(q).to(torch.bfloat16), alpha
+
+
+def _sums(layout, D, rows, chunk):
+    """What the tensor cores' additions may cost of a sum over a chunk. Each may truncate 2^-23 of the running sum."""
+    return chunk // 64 * 2.0 ** -23                         # four warps take its 16-token tiles in turn, hi and lo apart
+
+
+def _check(layout, rows, nq, std, sink=False, chunk=256, D=128, lift=12):
+    """The values' signs are random and independent of every rounding of the weights, so an error of at most e in
+    each token's weight moves the output by at most e of its norm in the mean square; 1.5 covers the spread over
+    dims and rows. e: the score's and the exponent's own, for the token and once more for the sum of all (as in
+    oracle.budget.weights); P' = p * scale as two f16 parts, 2^-21; the sums. Added to it what f16's subnormals
+    cost: two roundings of 2^-25 in P', p being 2^lift times larger, times the code."""
+    k, v, qd, alpha = _inputs(std, sink, rows, nq, D)
+    q = qd.float().numpy()
+    dc, oc = kvq.KVCache(layout, 1, H, D, S), OA.OracleCache(layout, 1, H, D, S)
+    kvq.store(dc, torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda(), 0)
+    oc.store(k, v, 0)
+    out, _ = kvq.decode_attend_weights(dc, qd.cuda(), S, None, scores_out=torch.zeros((1, H, S), device="cuda"),
+                                       attn_scale=float(alpha), chunk=chunk)
+    s, mass = OB.scores_dense(oc, q, alpha, S)
+    err = 2 * (float(mass.max()) * ((D // 16 + D // 32 + 4) * 2.0 ** -23 + 2.0 ** -22)
+               + 3 * 2.0 ** -24 * 1.5 * float(s.max() - s.min()) + 2.0 ** -22)
+    l = np.exp(s - s.max(-1, keepdims=True)).sum(-1)
+    low = 2 * 2.0 ** -(25 + lift) * TOP_CODE[layout.split("+")[-1]] * np.sqrt(S * D * ((1 / l) ** 2).sum())
+    ref = oc.attend(q, alpha, S)
+    ref = ref[0] if isinstance(ref, tuple) else ref
+    norm = np.linalg.norm(ref)
+    tol = 1.5 * (err + 2.0 ** -21 + _sums(layout, D, rows, chunk)) * norm + low
+    got = np.linalg.norm(out.cpu().numpy().astype(np.float64) - ref)
+    print(f"{layout} d{D} {rows} rows, std {std if np.isscalar(std) else 'mixed'}, sink {sink}, chunk {chunk}: "
+          f"{got / norm:.2e} of {tol / norm:.2e}")
+    assert got <= tol
+
+
+CASES = [("q6_0", 128, 1, 1), ("q6_0", 128, 8, 1), ("q6_0", 256, 1, 1), ("q6_0", 256, 32, 8)]
+
+
+@pytest.mark.parametrize("layout,D,rows,nq", CASES)
+@pytest.mark.parametrize("std", [1.0, 0.1, 0.01, 0.001])
+def test_output_with_values_of_any_size(layout, D, rows, nq, std):
+    _check(layout, rows, nq, std, D=D)
+
+
+@pytest.mark.parametrize("layout,D,rows,nq", CASES)
+def test_output_of_rows_whose_weight_lies_on_one_token(layout, D, rows, nq):
+    _check(layout, rows, nq, 1.0, sink=True, D=D)
+
+
+@pytest.mark.parametrize("layout,D,rows,nq", CASES)
+def test_output_with_values_that_grow_in_the_middle(layout, D, rows, nq):
+    """Scales beyond 2 from some token of a chunk on: probabilities without the factor from there."""
+    _check(layout, rows, nq, np.where(np.arange(S) < 150, 1e-3, 1e3), D=D, lift=0)
