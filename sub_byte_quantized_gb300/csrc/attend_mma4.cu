@@ -73,7 +73,11 @@ __device__ __forceinline__ uint32_t swz(int row, int j) {
 // SCORES: the masked scores go to a.part_s, for the kernel that sums the tokens' weights. CENTRED: K codes enter as
 // exact u - 8 and zero-points as z + 8 s, so that a score's terms are as small as the keys (f32 and f16 queries of
 // such calls: the weights' error over 7900 tokens falls from 1.2e-6 to 4e-7; bf16 products are short and lose
-// little either way). 128K tokens, f16: 80.5 -> 82.9 us.
+// little either way). 128K tokens, f16: 80.5 -> 82.9 us with the contiguous caches' chunk of that time.
+// SCORES also holds the output to float32: the probabilities are taken 2^kLift larger (4096 tokens with values of
+// 0.001: 1e-4 of the output's norm without), and each tile's products are summed by themselves, the small ones
+// first, and reach the output by a rounded addition (the tensor core truncates its sums: 128K tokens, 56 tiles per
+// warp, 1.8e-5 -> 1.2e-6 of the norm, 62.8 -> 64.7 us; with every other tile so 8.8e-6 and 63.7).
 template <int LAYOUT, bool QSPLIT, bool PAGED, bool SCORES, bool CENTRED>
 __global__ void __launch_bounds__(kThreads, kMma4CtasPerSm) attend_mma4_kernel(AttendArgs a) {
   using G = Geo4<LAYOUT>;
@@ -407,10 +411,14 @@ __global__ void __launch_bounds__(kThreads, kMma4CtasPerSm) attend_mma4_kernel(A
         mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, k));
       }
       const float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
-      const float mu0 = mn0 == -INFINITY ? 0.0f : mn0, mu1 = mn1 == -INFINITY ? 0.0f : mn1;
+      float mu0 = mn0 == -INFINITY ? 0.0f : mn0, mu1 = mn1 == -INFINITY ? 0.0f : mn1;
       const float corr0 = ex2(m0 - mu0), corr1 = ex2(m1 - mu1);
       m0 = mn0;
       m1 = mn1;
+      if constexpr (SCORES) {
+        mu0 -= kLift;
+        mu1 -= kLift;
+      }
       float p0 = ex2(s[0] - mu0), p1 = ex2(s[1] - mu1), p2 = ex2(s[2] - mu0), p3 = ex2(s[3] - mu1);
       l0 = fmaf(l0, corr0, p0 + p2);
       l1 = fmaf(l1, corr1, p1 + p3);
@@ -448,8 +456,8 @@ __global__ void __launch_bounds__(kThreads, kMma4CtasPerSm) attend_mma4_kernel(A
     float *cm = reinterpret_cast<float *>(smem);
     float *cl = cm + 32;
     if (g == 0) {
-      cm[tw * 8 + r0] = m0;
-      cm[tw * 8 + r1] = m1;
+      cm[tw * 8 + r0] = m0 - (SCORES ? kLift : 0.0f);
+      cm[tw * 8 + r1] = m1 - (SCORES ? kLift : 0.0f);
       cl[tw * 8 + r0] = l0;
       cl[tw * 8 + r1] = l1;
     }
@@ -460,6 +468,7 @@ __global__ void __launch_bounds__(kThreads, kMma4CtasPerSm) attend_mma4_kernel(A
     // (hi part in rows b, lo part in rows b + 8), from one small mma per tile
     float Dw[4] = {0.f, 0.f, 0.f, 0.f};
     const uint32_t wsel = (g & 1) ? 0x7632u : 0x5410u;
+    bool lifted = SCORES;                                // P' carries 2^kLift (the same for the whole warp)
 #pragma unroll
     for (int b = 0; b < 4; ++b)
 #pragma unroll
@@ -479,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, kMma4CtasPerSm) attend_mma4_kernel(A
       const int tile = kTPW * tw + tt;
       // (a tile past t_end is zero-filled and fully masked: it contributes nothing)
       const uint8_t *xs = xch + ((tile * 2 + (j & 1)) * 32 + lane) * 32;
-      const uint4 pb = *reinterpret_cast<const uint4 *>(xs);
+      uint4 pb = *reinterpret_cast<const uint4 *>(xs);
       const float2 cr = *reinterpret_cast<const float2 *>(xs + 16);
       if (__any_sync(0xffffffffu, cr.x != 1.0f || cr.y != 1.0f)) {
         Dw[0] *= cr.x;
@@ -528,6 +537,24 @@ __global__ void __launch_bounds__(kThreads, kMma4CtasPerSm) attend_mma4_kernel(A
                                __byte_perm(sa.y, sbv.y, 0x5410), __byte_perm(sa.y, sbv.y, 0x7632)};
       const uint32_t sp1[4] = {__byte_perm(sc.x, sd.x, 0x5410), __byte_perm(sc.x, sd.x, 0x7632),
                                __byte_perm(sc.y, sd.y, 0x5410), __byte_perm(sc.y, sd.y, 0x7632)};
+      if constexpr (SCORES) {
+        static_assert(!HAD, "the probabilities of a Hadamard body carry their value scales");
+        if (lifted) {
+          const uint32_t big = sa.x | sa.y | sbv.x | sbv.y | sc.x | sc.y | sd.x | sd.y;
+          if (__any_sync(0xffffffffu, big & kTopExponent)) {
+            lifted = false;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) Dw[k] *= kUnlift;
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) O[b][h][k] *= kUnlift;
+          }
+        }
+        if (!lifted) pb = unlift(pb);
+      }
       if (ASYM) {
         // W operand (group midpoints): rows g < 4 hold the hi part of block g's x = z_v + 8 s_v for
         // tokens (2c, 2c+1), (2c+8, 2c+9), rows g + 8 its lo part. With the codes centred (n - 8)
@@ -549,8 +576,16 @@ __global__ void __launch_bounds__(kThreads, kMma4CtasPerSm) attend_mma4_kernel(A
         midpoint_split(z1, s1, h1, l1);
         if (g >= 4) h0 = l0 = h1 = l1 = 0u;
         const uint32_t Aw[4] = {h0, l0, h1, l1};
-        mma16816(Dw, Aw, pb.x, pb.y);
-        mma16816(Dw, Aw, pb.z, pb.w);
+        if constexpr (SCORES) {
+          float d[4];
+          mma16816_c(d, Aw, pb.z, pb.w, 0.f, 0.f, 0.f, 0.f);
+          mma16816(d, Aw, pb.x, pb.y);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) Dw[k] += d[k];
+        } else {
+          mma16816(Dw, Aw, pb.x, pb.y);
+          mma16816(Dw, Aw, pb.z, pb.w);
+        }
       }
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
@@ -569,10 +604,22 @@ __global__ void __launch_bounds__(kThreads, kMma4CtasPerSm) attend_mma4_kernel(A
         }
         const uint32_t A0[4] = {ua[0], ua[1], ub[0], ub[1]};   // dims 4g+0 (row g), 4g+1 (row g+8)
         const uint32_t A1[4] = {ua[2], ua[3], ub[2], ub[3]};   // dims 4g+2, 4g+3
-        mma16816(O[b][0], A0, hi0, hi1);
-        mma16816(O[b][0], A0, lo0, lo1);
-        mma16816(O[b][1], A1, hi0, hi1);
-        mma16816(O[b][1], A1, lo0, lo1);
+        if constexpr (SCORES) {
+          float d[2][4];
+          mma16816_c(d[0], A0, lo0, lo1, 0.f, 0.f, 0.f, 0.f);
+          mma16816(d[0], A0, hi0, hi1);
+          mma16816_c(d[1], A1, lo0, lo1, 0.f, 0.f, 0.f, 0.f);
+          mma16816(d[1], A1, hi0, hi1);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) O[b][h][k] += d[h][k];
+        } else {
+          mma16816(O[b][0], A0, hi0, hi1);
+          mma16816(O[b][0], A0, lo0, lo1);
+          mma16816(O[b][1], A1, hi0, hi1);
+          mma16816(O[b][1], A1, lo0, lo1);
+        }
       }
       }
     }
@@ -581,6 +628,7 @@ __global__ void __launch_bounds__(kThreads, kMma4CtasPerSm) attend_mma4_kernel(A
     // O holds s_v * code (asymmetric: s_v (n - 8)); asymmetric values add the midpoint term,
     // s_v n + z_v = s_v (n - 8) + (z_v + 8 s_v).
     float *co = reinterpret_cast<float *>(smem) + 64;    // [tile][8][128] after cm/cl
+    const float up = SCORES && !lifted ? 1.0f / kUnlift : 1.0f;
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
       float w0 = 0.0f, w1 = 0.0f;
@@ -591,8 +639,8 @@ __global__ void __launch_bounds__(kThreads, kMma4CtasPerSm) attend_mma4_kernel(A
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int d = 32 * b + 4 * g + 2 * h;
-        *reinterpret_cast<float2 *>(co + (tw * 8 + r0) * kD + d) = make_float2(O[b][h][0] + w0, O[b][h][2] + w0);
-        *reinterpret_cast<float2 *>(co + (tw * 8 + r1) * kD + d) = make_float2(O[b][h][1] + w1, O[b][h][3] + w1);
+        *reinterpret_cast<float2 *>(co + (tw * 8 + r0) * kD + d) = make_float2((O[b][h][0] + w0) * up, (O[b][h][2] + w0) * up);
+        *reinterpret_cast<float2 *>(co + (tw * 8 + r1) * kD + d) = make_float2((O[b][h][1] + w1) * up, (O[b][h][3] + w1) * up);
       }
     }
   }

@@ -30,8 +30,12 @@ def _inputs(std, sink, rows, nq, D):
 
 
 def _sums(layout, D, rows, chunk):
-    """What the tensor cores' additions may cost of a sum over a chunk. Each may truncate 2^-23 of the running sum."""
-    return chunk // 64 * 2.0 ** -23                         # four warps take its 16-token tiles in turn, hi and lo apart
+    """What the tensor cores' additions may cost of a sum over a chunk. Each may truncate 2^-23 of the running sum;
+    n roundings of 2^-24 to nearest are independent."""
+    n = chunk // 64                                         # four warps take its 16-token tiles in turn
+    if layout == "asym4_g32" and rows <= 8:                 # two products of a tile by themselves, then one rounded addition
+        return 2 * 2.0 ** -23 + np.sqrt(n) * 2.0 ** -24
+    return n * 2.0 ** -23                                   # (Q6_0) hi and lo apart
 
 
 def _check(layout, rows, nq, std, sink=False, chunk=256, D=128, lift=12):
@@ -62,7 +66,8 @@ def _check(layout, rows, nq, std, sink=False, chunk=256, D=128, lift=12):
     assert got <= tol
 
 
-CASES = [("q6_0", 128, 1, 1), ("q6_0", 128, 8, 1), ("q6_0", 256, 1, 1), ("q6_0", 256, 32, 8)]
+CASES = [("q6_0", 128, 1, 1), ("q6_0", 128, 8, 1), ("q6_0", 256, 1, 1), ("q6_0", 256, 32, 8),
+         ("asym4_g32", 128, 1, 1), ("asym4_g32", 128, 8, 1), ("asym4_g32", 128, 6, 2)]
 
 
 @pytest.mark.parametrize("layout,D,rows,nq", CASES)
@@ -80,3 +85,9 @@ def test_output_of_rows_whose_weight_lies_on_one_token(layout, D, rows, nq):
 def test_output_with_values_that_grow_in_the_middle(layout, D, rows, nq):
     """Scales beyond 2 from some token of a chunk on: probabilities without the factor from there."""
     _check(layout, rows, nq, np.where(np.arange(S) < 150, 1e-3, 1e3), D=D, lift=0)
+
+
+@pytest.mark.parametrize("layout,D,rows,nq", [c for c in CASES if c[0] != "q6_0"])
+def test_output_of_long_chunks(layout, D, rows, nq):
+    """One chunk of all tokens."""
+    _check(layout, rows, nq, 1.0, chunk=S, D=D)
