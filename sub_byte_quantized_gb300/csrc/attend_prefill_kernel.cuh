@@ -109,6 +109,9 @@ struct PGeo {
   static_assert(SMEM <= BUDGET, "shared memory fits the CTAs per SM");
 };
 constexpr float kLog2e = 1.4426950408889634f;
+// Output tiles (8 dims) that a scoring call's pass sums at a time.
+template <int KL, int VL>
+constexpr int kScoreTiles = PGeo<KL, VL>::HAD ? 4 : 8;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // Byte offset of (token row, 16-byte chunk) in an f16 code tile. Within each 128-byte half of the
@@ -229,7 +232,12 @@ __device__ __forceinline__ int row_limit_of(const AttendArgs &a, const SeqLen &s
 // one warp scoring every token while the other three only unpack.
 // CAP: score capture (Hadamard layouts, contiguous cache): every exact integer body score the CTA
 // computes and each row's int8 query scale also go to a.cap_scores / a.cap_sq.
-template <int KL, int VL, bool PAGED, bool DEC, bool CAP = false>
+// SCORES: calls that also score the tokens, whose output is held to float32. Probabilities are taken 2^kLift larger
+// (4096 tokens in Hadamard int4 with values of 0.001: 6e-5 of the output's norm without; beside a token of 2^14
+// times the others' weight 6e-5 to 2e-4 in every layout), and a pass's products with V are summed by themselves, the
+// small ones first, and reach the output by a rounded addition (the tensor core truncates its sums: 1.4e-5 of the
+// norm in a chunk of 4096 tokens, so chunks may be as long as the grid wants them).
+template <int KL, int VL, bool PAGED, bool DEC, bool CAP = false, bool SCORES = false>
 __global__ void __launch_bounds__(kWarps * 32, PGeo<KL, VL>::CTAS) attend_prefill_kernel(AttendArgs a) {
   using G = PGeo<KL, VL>;
   constexpr int NTJ = DEC ? 2 : 4;                       // 8-token score tiles per pass
@@ -393,6 +401,7 @@ __global__ void __launch_bounds__(kWarps * 32, PGeo<KL, VL>::CTAS) attend_prefil
     warp_min = min(warp_min, __shfl_xor_sync(0xffffffffu, warp_min, k));
   }
   float m_g = -INFINITY, m_g8 = -INFINITY, l_g = 0.0f, l_g8 = 0.0f;
+  float lift = SCORES ? kLift : 0.0f;                    // of the body's P, in base 2
 
   if constexpr (HAD) {
   if (win) {
@@ -644,10 +653,29 @@ __global__ void __launch_bounds__(kWarps * 32, PGeo<KL, VL>::CTAS) attend_prefil
       mx_g8 = fmaxf(mx_g8, __shfl_xor_sync(0xffffffffu, mx_g8, 1));
       mx_g8 = fmaxf(mx_g8, __shfl_xor_sync(0xffffffffu, mx_g8, 2));
       const float mn_g = fmaxf(m_g, mx_g), mn_g8 = fmaxf(m_g8, mx_g8);
-      const float mu_g = mn_g == -INFINITY ? 0.0f : mn_g, mu_g8 = mn_g8 == -INFINITY ? 0.0f : mn_g8;
-      const float corr_g = ex2(m_g - mu_g), corr_g8 = ex2(m_g8 - mu_g8);
+      float mu_g = mn_g == -INFINITY ? 0.0f : mn_g, mu_g8 = mn_g8 == -INFINITY ? 0.0f : mn_g8;
+      float corr_g = ex2(m_g - mu_g), corr_g8 = ex2(m_g8 - mu_g8);
       m_g = mn_g;
       m_g8 = mn_g8;
+      if constexpr (SCORES) {
+        if constexpr (HAD) {                             // P' = p * s_v: without the factor from a scale of 2 on
+          if (lift > 0.0f) {
+            uint32_t big = 0;                            // the top exponent bit of the pass's V scales
+#pragma unroll
+            for (int j = 0; j < NTJ; ++j) {
+              const uint2 sv = *reinterpret_cast<const uint2 *>(svf + pass_tok(hh) + 8 * j + 2 * c);
+              big |= sv.x | sv.y;
+            }
+            if (__any_sync(0xffffffffu, big & 0x40000000u)) {
+              lift = 0.0f;
+              corr_g *= kUnlift;
+              corr_g8 *= kUnlift;
+            }
+          }
+        }
+        mu_g -= lift;                                    // (block layouts: P is an operand by itself)
+        mu_g8 -= lift;
+      }
       if (__any_sync(0xffffffffu, corr_g != 1.0f || corr_g8 != 1.0f)) {
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
@@ -678,6 +706,54 @@ __global__ void __launch_bounds__(kWarps * 32, PGeo<KL, VL>::CTAS) attend_prefil
       l_g8 = fmaf(l_g8, corr_g8, ls_g8);
 
       // O += P' . V, two 16-token steps
+      if constexpr (SCORES) {
+        uint32_t ah[NKK][4], al[NKK][4];                 // as below
+#pragma unroll
+        for (int kk = 0; kk < NKK; ++kk)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = 2 * kk + (e >> 1), xx = (e & 1) ? 2 : 0;
+            ah[kk][e] = pack_f16x2(s[j][xx], s[j][xx + 1]);
+            const float2 f = __half22float2(u32_as_h2(ah[kk][e]));
+            al[kk][e] = pack_f16x2(s[j][xx] - f.x, s[j][xx + 1] - f.y);
+          }
+        constexpr int GT = kScoreTiles<KL, VL>;          // output tiles at a time
+#pragma unroll
+        for (int t0g = 0; t0g < 16; t0g += GT) {
+          float d[GT][4];
+#pragma unroll
+          for (int kk = 0; kk < NKK; ++kk) {
+            const uint32_t vrow = vbase + (pass_tok(hh) + 16 * kk) * kTileRow;
+            uint32_t vw[GT / 2][4];
+            auto add = [&](const uint32_t (&x)[4], bool first) {
+#pragma unroll
+              for (int p = 0; p < GT / 2; ++p) {
+                if (first) {
+                  mma16816_c(d[2 * p], x, vw[p][0], vw[p][1], 0.f, 0.f, 0.f, 0.f);
+                  mma16816_c(d[2 * p + 1], x, vw[p][2], vw[p][3], 0.f, 0.f, 0.f, 0.f);
+                } else {
+                  mma16816(d[2 * p], x, vw[p][0], vw[p][1]);
+                  mma16816(d[2 * p + 1], x, vw[p][2], vw[p][3]);
+                }
+              }
+            };
+            if constexpr (!HAD) {                        // P_hi . V_lo
+#pragma unroll
+              for (int p = 0; p < GT / 2; ++p) ldsm_x4_t(vrow + 2 * kTile + vofs(t0g / 2 + p), vw[p]);
+              add(ah[kk], kk == 0);
+            }
+#pragma unroll
+            for (int p = 0; p < GT / 2; ++p) ldsm_x4_t(vrow + vofs(t0g / 2 + p), vw[p]);
+            add(al[kk], HAD && kk == 0);
+            add(ah[kk], false);
+          }
+#pragma unroll
+          for (int j = 0; j < GT; ++j)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) O[t0g + j][k] += d[j][k];
+        }
+        continue;
+      }
 #pragma unroll
       for (int kk = 0; kk < NKK; ++kk) {
         // A: a0 = (row g, tokens 2c..), a1 = (row g+8, tokens 2c..), a2 = (row g, tokens 8+2c..),
@@ -737,8 +813,8 @@ __global__ void __launch_bounds__(kWarps * 32, PGeo<KL, VL>::CTAS) attend_prefil
     float *xo = xl + kWarps * 16;                             // [warp][row][dim] O
     static_assert((2 * kWarps * 16 + kWarps * 16 * kD) * 4 <= G::REGION, "merge area fits the tile region");
     if (c == 0) {
-      xm[warp * 16 + g] = m_g;
-      xm[warp * 16 + g + 8] = m_g8;
+      xm[warp * 16 + g] = m_g - lift;
+      xm[warp * 16 + g + 8] = m_g8 - lift;
       xl[warp * 16 + g] = l_g;
       xl[warp * 16 + g + 8] = l_g8;
     }
@@ -789,17 +865,17 @@ __global__ void __launch_bounds__(kWarps * 32, PGeo<KL, VL>::CTAS) attend_prefil
       po[8 * j + 4 + c] = O[j][2 * half + 1];
     }
     if (c == 0) {
-      a.part_m[pi] = (half ? m_g8 : m_g) * kLn2;         // natural-log units, like the other kernels
+      a.part_m[pi] = ((half ? m_g8 : m_g) - lift) * kLn2;   // natural-log units, like the other kernels
       a.part_l[pi] = half ? l_g8 : l_g;
     }
   }
 }
 
-template <int KL, int VL, bool PAGED, bool DEC, bool CAP = false>
+template <int KL, int VL, bool PAGED, bool DEC, bool CAP = false, bool SCORES = false>
 cudaError_t launch_t(const AttendArgs &a, cudaStream_t st) {
   using G = PGeo<KL, VL>;
   static std::atomic<bool> configured[kMaxDevices];
-  cudaError_t e = set_smem_once(configured, attend_prefill_kernel<KL, VL, PAGED, DEC, CAP>, G::SMEM);
+  cudaError_t e = set_smem_once(configured, attend_prefill_kernel<KL, VL, PAGED, DEC, CAP, SCORES>, G::SMEM);
   if (e != cudaSuccess) return e;
   const int R = a.gqa * a.n_q;
   cudaLaunchConfig_t cfg = {};
@@ -814,11 +890,20 @@ cudaError_t launch_t(const AttendArgs &a, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attend_prefill_kernel<KL, VL, PAGED, DEC, CAP>, a);
+  return cudaLaunchKernelEx(&cfg, attend_prefill_kernel<KL, VL, PAGED, DEC, CAP, SCORES>, a);
 }
 
 // The launch for a layout pair: contiguous or paged; DEC for one row block when the pair has no
 // decode kernel of its own (the only shapes such pairs send here with few rows).
+template <int KL, int VL, bool SCORES>
+cudaError_t launch_kind(const AttendArgs &a, cudaStream_t st) {
+  const bool paged = a.cache.page_shift >= 0;
+  if constexpr (!decode_kernel(KL, VL)) {
+    if (a.gqa * a.n_q <= 16)
+      return paged ? launch_t<KL, VL, true, true, false, SCORES>(a, st) : launch_t<KL, VL, false, true, false, SCORES>(a, st);
+  }
+  return paged ? launch_t<KL, VL, true, false, false, SCORES>(a, st) : launch_t<KL, VL, false, false, false, SCORES>(a, st);
+}
 template <int KL, int VL>
 cudaError_t launch_pair(const AttendArgs &a, cudaStream_t st) {
   const bool paged = a.cache.page_shift >= 0;
@@ -831,11 +916,7 @@ cudaError_t launch_pair(const AttendArgs &a, cudaStream_t st) {
       return cudaErrorNotSupported;
     }
   }
-  if constexpr (!decode_kernel(KL, VL)) {
-    if (a.gqa * a.n_q <= 16)
-      return paged ? launch_t<KL, VL, true, true>(a, st) : launch_t<KL, VL, false, true>(a, st);
-  }
-  return paged ? launch_t<KL, VL, true, false>(a, st) : launch_t<KL, VL, false, false>(a, st);
+  return a.lse ? launch_kind<KL, VL, true>(a, st) : launch_kind<KL, VL, false>(a, st);
 }
 
 }  // namespace

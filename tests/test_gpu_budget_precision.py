@@ -33,9 +33,14 @@ def _sums(layout, D, rows, chunk):
     """What the tensor cores' additions may cost of a sum over a chunk. Each may truncate 2^-23 of the running sum;
     n roundings of 2^-24 to nearest are independent."""
     n = chunk // 64                                         # four warps take its 16-token tiles in turn
-    if layout == "asym4_g32" and rows <= 8:                 # two products of a tile by themselves, then one rounded addition
-        return 2 * 2.0 ** -23 + np.sqrt(n) * 2.0 ** -24
-    return n * 2.0 ** -23                                   # (Q6_0) hi and lo apart
+    if D == 128 and layout != "q6_0" and rows <= 8 and "+" not in layout or layout == "q4_0+q8_0" and rows <= 8:
+        if layout == "asym4_g32":                           # two products of a tile by themselves, then one rounded addition
+            return 2 * 2.0 ** -23 + np.sqrt(n) * 2.0 ** -24
+        return (2 + n) * 2.0 ** -23 + np.sqrt(n) * 2.0 ** -24   # every other tile so
+    if D == 128 and (rows > 8 or "+" in layout):
+        # 32 tokens by themselves (six products), or four warps and 16 tokens (three), then one rounded addition
+        return 6 * 2.0 ** -23 + np.sqrt(chunk // 32) * 2.0 ** -24
+    return n * 2.0 ** -23                                   # (Q6_0's own kernel) hi and lo apart
 
 
 def _check(layout, rows, nq, std, sink=False, chunk=256, D=128, lift=12):
@@ -68,6 +73,9 @@ def _check(layout, rows, nq, std, sink=False, chunk=256, D=128, lift=12):
 
 CASES = [("q6_0", 128, 1, 1), ("q6_0", 128, 8, 1), ("q6_0", 256, 1, 1), ("q6_0", 256, 32, 8),
          ("asym4_g32", 128, 1, 1), ("asym4_g32", 128, 8, 1), ("asym4_g32", 128, 6, 2)]
+CASES += [(layout, 128, rows, 1) for layout in ("q4_0", "q8_0", "q4_0+q8_0", "had_int4", "had_int2") for rows in (1, 8)]
+CASES += [(layout, 128, 32, 8) for layout in ("q4_0", "q6_0", "q8_0", "asym4_g32", "had_int4", "had_int2", "q4_0+q8_0")]
+CASES += [(layout, 128, rows, nq) for layout in ("asym4_g32+q8_0", "had_int2+had_int4") for rows, nq in ((1, 1), (12, 3), (40, 5))]
 
 
 @pytest.mark.parametrize("layout,D,rows,nq", CASES)
@@ -87,7 +95,7 @@ def test_output_with_values_that_grow_in_the_middle(layout, D, rows, nq):
     _check(layout, rows, nq, np.where(np.arange(S) < 150, 1e-3, 1e3), D=D, lift=0)
 
 
-@pytest.mark.parametrize("layout,D,rows,nq", [c for c in CASES if c[0] != "q6_0"])
+@pytest.mark.parametrize("layout,D,rows,nq", [c for c in CASES if c[:2] != ("q6_0", 256)])
 def test_output_of_long_chunks(layout, D, rows, nq):
     """One chunk of all tokens."""
     _check(layout, rows, nq, 1.0, chunk=S, D=D)
