@@ -416,6 +416,9 @@ kvq_status kvq_paged_rope_store(const kvq_paged_cache *cache, const kvq_rope *ro
  *                          t >= kv_len are left as they were. A row that sees no token adds nothing; one
  *                          whose output is NaN makes its tokens' scores NaN.
  *   workspace              at least kvq_attend_weights_workspace_bytes (shared with no call in flight)
+ *                          : the partials of the attention (4 (head_dim + 2) bytes per query row and
+ *                          chunk; chunk 0 keeps them near those of kvq_decode_attend's own chunk) and, up
+ *                          to eight query rows per kv head, 8 to 32 bytes per token and kv head
  * Deterministic: no atomics.
  */
 size_t kvq_attend_weights_workspace_bytes(const kvq_cache *cache, int32_t n_q_heads, int32_t n_q, int32_t kv_len,

@@ -984,17 +984,19 @@ constexpr int kMaxEvictTokens = 1 << 27;
 
 // Chunk of an attention call that also scores the tokens, for chunk 0: the attention's own choice, but for four
 // kinds.
-//   Paged pools with up to two (sequence, kv head) per SM: at most 1536 tokens, since chunks that leave scores
+//   Paged pools with up to two (sequence, kv head) per SM: up to 128 rows (whose partials are then at most 43 bytes
+//     per token and kv head, less than a third of its packed row) at most 1536 tokens, since chunks that leave scores
 //     behind take longer and the sequences' lengths differ (16 sequences of up to 16379 tokens, 8 kv heads: Q8_0
 //     82 us against 90 at the attention's 4608, asymmetric 99 against 136; 64 sequences of up to 4000, which fill
 //     the SMs by themselves: 89 against 77).
 //   The tcgen05 kernel: as many chunks as fill the SMs beside the window's CTAs (it takes at most eight by itself:
-//     64 CTAs for 128 rows and 8 kv heads; window CTAs in a second wave cost 13 us).
-//   The row-side kernel with more rows than its decode form: whole waves of two CTAs per SM (the attention's own
-//     four to six waves: Q4_0, 128 rows, 8 kv heads of 8000 tokens 69 against 108 us, Hadamard int4, 16 rows, 12
-//     kv heads of 4517 42 against 69) and at most 512 tokens: its result carries the truncation of the tensor
-//     cores' sums, which grows with the chunk (1.2e-5 of the output's norm at 3456 tokens). Many heads: Q4_0,
-//     16 rows, 128 kv heads of 4096 tokens 202 against 221; Q8_0, 256 rows, 8 of 32768 397 against 380.
+//     64 CTAs for 128 rows and 8 kv heads; window CTAs in a second wave cost 13 us). Sequences of a paged batch count
+//     as five eighths of the longest, here and below (4 of up to 16379 tokens, 256 rows, 8 kv heads 175 us; 210 without).
+//   The row-side kernel with more rows than its decode form: the fewest waves of two CTAs per SM times the tokens of
+//     a chunk and 256 more for what a CTA costs beside them, over one to four whole waves, so that the partials of a
+//     call stay bounded whatever its length (four waves of 64 rows, or chunks of 8192 tokens). Q4_0, 128 rows, 8 kv
+//     heads of 8000 tokens 70 us (the attention's own four to six waves: 108); Q8_0, 256 rows, 8 of 32768 333 (380;
+//     chunks of 512 tokens 412); Q4_0, 256 rows, 8 of 131072 1114 (1475 at 512); 16 rows, 128 of 4096 174 (221).
 //   The CUDA-core kernel, whose time goes with the chunk: 64 tokens where chunks of 128 leave SMs idle (Q4_0, d256,
 //     4 kv heads of 5947 tokens: 29 against 44 us).
 int weights_chunk(const kvq::CacheView &c, int n_q_heads, int n_q, int kv_len, int auto_chunk, bool f32_queries) {
@@ -1002,20 +1004,31 @@ int weights_chunk(const kvq::CacheView &c, int n_q_heads, int n_q, int kv_len, i
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   int chunk = auto_chunk;
   const long long heads = (long long)c.B * c.H;
-  if (c.page_shift >= 0 && heads <= 2LL * sms && chunk > 1536) chunk = 1536;
   const int rows = n_q_heads / c.H * n_q;
+  if (c.page_shift >= 0 && heads <= 2LL * sms && rows <= 128) chunk = std::min(chunk, 1536);
   const bool had = kvq::is_hadamard(c.layout), decode = kvq::decode_kernel(c.layout, c.v_layout);
   const int window = had ? std::min(c.n_recent, kv_len) : 0;
   const long long body = kv_len > window ? kv_len - window : 1;
   const long long n_win = (window + kvq::kWinChunk - 1) / kvq::kWinChunk;
   auto split = [&](long long n) { return (int)std::min(8192LL, ((body + n - 1) / n + 63) / 64 * 64); };   // into n chunks
+  // CTAs of `per` query rows that one chunk of every sequence takes
+  auto units = [&](int per) {
+    const long long n = (long long)((rows + per - 1) / per) * heads;
+    return c.page_shift >= 0 && c.B > 1 ? (5 * n + 7) / 8 : n;
+  };
   if (kvq::tc_prefill_shape(c.layout, c.v_layout, c.D, rows)) {
-    const long long n = (sms - heads * n_win) / ((rows + kvq::kTcRows - 1) / kvq::kTcRows * heads);
+    const long long n = (sms - heads * n_win) / units(kvq::kTcRows);
     if (n > 1) chunk = std::min(chunk, split(n));
   } else if (kvq::prefill_shape(c.layout, c.v_layout, c.D, rows) && (had || !f32_queries)) {
     if (rows > 16 || decode) {
-      const long long wave = std::max(1LL, 2LL * sms / ((rows + kvq::kPrefillRows - 1) / kvq::kPrefillRows * heads) - n_win);
-      chunk = split(((body + 511) / 512 + wave - 1) / wave * wave);
+      const long long slots = 2LL * sms, ctas = units(kvq::kPrefillRows);
+      auto cost = [&](long long n) { return (ctas * (n + n_win) + slots - 1) / slots * (split(n) + 256); };
+      long long best = (body + 8191) / 8192;
+      for (long long waves = 1; waves <= 4; ++waves) {
+        const long long n = waves * slots / ctas - n_win;
+        if (n > (body + 8191) / 8192 && cost(n) < cost(best)) best = n;
+      }
+      chunk = split(best);
     }
   } else if (!(decode && c.D == 128 && rows <= 8) && !(c.layout == KVQ_Q6_0 && c.v_layout == c.layout && kvq::mma_q6_shape(c.D, rows))) {
     if (heads * ((body + 127) / 128) < 2LL * sms) chunk = 64;

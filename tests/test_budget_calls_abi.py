@@ -76,3 +76,27 @@ def test_compact_refuses_a_scores_out_without_scores(L):
     for dst in (None, C.byref(other)):
         assert L.kvq_evict_compact(C.byref(A._cache()), dst, P, 20, 60, None, 0, F, 32, None) == A.EINVAL
         assert b"scores" in L.kvq_last_error()
+
+
+@pytest.mark.parametrize("layout", [0, 1, 2, 3, 4])
+@pytest.mark.parametrize("paged", [False, True])
+def test_the_workspace_of_a_scoring_call_stays_near_the_attentions(L, layout, paged):
+    """Long prompts under wide observation windows: the partials of the automatic chunk follow the grid, not rows
+    times tokens (512 rows per kv head over 131072 tokens: 68 MB, not 1091). Allowed beside the attention's own
+    chunks: four waves of two CTAs of 64 rows on 152 SMs, 4 * 304 * 64 rows of 130 floats, or chunks of 1536 tokens
+    of up to 128 rows in a paged pool that the sequences do not fill."""
+    import tests.test_budget_abi as A
+    for nq in (4, 16, 64, 128, 256):
+        for kv in (8000, 131072, 1 << 20):
+            if paged:
+                c = A._paged(layout, page=1 << 16, pages=16)
+                c.n_kv_heads = 8
+                plain = L.kvq_paged_attend_workspace_bytes(C.byref(c), 32, nq, kv, 0)
+                need = L.kvq_paged_attend_weights_workspace_bytes(C.byref(c), 32, nq, kv, 0)
+            else:
+                c = A._cache(layout, cap=kv, heads=8)
+                plain = L.kvq_attend_workspace_bytes(C.byref(c), 32, nq, kv, 0)
+                need = L.kvq_attend_weights_workspace_bytes(C.byref(c), 32, nq, kv, 0)
+            longest = 32 * nq * (kv // 8192 + 1) * 130 * 4
+            few = 32 * nq * (kv // 1536 + 1) * 130 * 4 if paged and 4 * nq <= 128 else 0
+            assert 0 < need <= max(plain, longest, few) + 4 * 304 * 64 * 130 * 4 + (1 << 20), (nq, kv, need, plain)
