@@ -44,6 +44,11 @@
 // stage's largest V scale so that p * s_v < 2^15 stays well inside the f16 range (tau <= 8). The
 // partial (m, l, O) is exact softmax algebra for any reference, so the result does not depend on
 // when m moves; what tau saves is the wait for the tensor core on almost every stage.
+// Calls that also score the tokens are held to float32: their m is set up to 2^12 below the maximum (tau <= 20), so
+// that P' and its lo part stay above f16's subnormals (4096 tokens in Hadamard int4: with values of 0.001 4e-5 of the
+// output's norm without and 5e-7 with it, beside a token of 2^14 times the others' weight 1e-4 and 7e-7). What is left
+// is the truncation of the sums in tensor memory: 2.4e-6 of the norm in a chunk of 4096 tokens, 4.8e-6 with more than
+// 128 rows, whose tokens all go into one accumulator.
 //
 // ALT (at most 128 query rows, calls that also score the tokens): with one row block the softmax of a stage and the
 // MMAs around it would follow one another, so both blocks hold the same rows and take the stages in turn, block
@@ -705,6 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_tc_kernel(AttendAr
     const float fabs_row = fabsf(arow);
     if (CAP && live && chunk_id == 0) a.cap_sq[qrow] = a.s_q[qrow];
     const uint32_t lane_base = (uint32_t)(32 * q4) << 16;
+    const int most = a.lse ? 20 : 8;                    // log2 of the largest p
     float m = -INFINITY, l = 0.0f;
     for (int j = ALT ? b : 0; j < n_st && ok; j += ALT ? 2 : 1) {
       const int tb = j % TB, ts = t0 + j * kStage, jb = ALT ? j >> 1 : j;   // jb: the block's own count
@@ -749,13 +755,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_tc_kernel(AttendAr
       for (int i = 0; i < 4; ++i) mx16[i] = fmaxf(fmaxf(mx16[i], mx16[i + 4]), fmaxf(mx16[i + 8], mx16[i + 12]));
       const float ztop = fmaxf(fmaxf(mx16[0], mx16[1]), fmaxf(mx16[2], mx16[3]));
       const float mx = ztop == -INFINITY ? -INFINITY : fabs_row * ztop;   // the stage's row maximum
-      // tau: p * s_v < 2^15 for p <= 2^tau (svmax < 2^(e + 1))
+      // tau: p * s_v < 2^15 for p <= 2^tau (svmax < 2^(e + 1)); the reference is set `lift` below the maximum
       const float *svm = reinterpret_cast<const float *>(sm + RG::SVMAX) + 2 * tb;
       const float svmax = fmaxf(svm[0], svm[1]);
       const int e = (int)((__float_as_uint(svmax) >> 23) & 0xFF) - 127;
-      const float tau = (float)min(8, max(0, 14 - e));
+      const int room = max(0, 14 - e);
+      const float tau = (float)min(most, room), lift = (float)max(0, min(most - 8, room - 4));
       const bool bump = mx > m + tau;                   // m = -inf: the first visible stage
-      const float m_new = bump ? mx : m;
+      const float m_new = bump ? mx - lift : m;
       const float mu = m_new == -INFINITY ? 0.0f : m_new;
       const float corr = bump ? ex2(m - mu) : 1.0f;     // m = -inf -> 0
       if (jb >= 1) {

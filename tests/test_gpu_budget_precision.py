@@ -33,6 +33,8 @@ def _sums(layout, D, rows, chunk):
     """What the tensor cores' additions may cost of a sum over a chunk. Each may truncate 2^-23 of the running sum;
     n roundings of 2^-24 to nearest are independent."""
     n = chunk // 64                                         # four warps take its 16-token tiles in turn
+    if layout in ("had_int4", "had_int2") and rows > 64:    # all tokens in one accumulator, hi and lo
+        return chunk // 16 * 2 * 2.0 ** -23
     if D == 128 and layout != "q6_0" and rows <= 8 and "+" not in layout or layout == "q4_0+q8_0" and rows <= 8:
         if layout == "asym4_g32":                           # two products of a tile by themselves, then one rounded addition
             return 2 * 2.0 ** -23 + np.sqrt(n) * 2.0 ** -24
@@ -76,6 +78,7 @@ CASES = [("q6_0", 128, 1, 1), ("q6_0", 128, 8, 1), ("q6_0", 256, 1, 1), ("q6_0",
 CASES += [(layout, 128, rows, 1) for layout in ("q4_0", "q8_0", "q4_0+q8_0", "had_int4", "had_int2") for rows in (1, 8)]
 CASES += [(layout, 128, 32, 8) for layout in ("q4_0", "q6_0", "q8_0", "asym4_g32", "had_int4", "had_int2", "q4_0+q8_0")]
 CASES += [(layout, 128, rows, nq) for layout in ("asym4_g32+q8_0", "had_int2+had_int4") for rows, nq in ((1, 1), (12, 3), (40, 5))]
+CASES += [(layout, 128, rows, 20) for layout in ("had_int4", "had_int2") for rows in (80, 160)]
 
 
 @pytest.mark.parametrize("layout,D,rows,nq", CASES)
