@@ -986,9 +986,10 @@ constexpr int kMaxEvictTokens = 1 << 27;
 // kinds.
 //   Paged pools with up to two (sequence, kv head) per SM: up to 128 rows (whose partials are then at most 43 bytes
 //     per token and kv head, less than a third of its packed row) at most 1536 tokens, since chunks that leave scores
-//     behind take longer and the sequences' lengths differ (16 sequences of up to 16379 tokens, 8 kv heads: Q8_0
-//     82 us against 90 at the attention's 4608, asymmetric 99 against 136; 64 sequences of up to 4000, which fill
-//     the SMs by themselves: 89 against 77).
+//     behind take longer and the sequences' lengths differ (16 sequences of up to 16379 tokens, 8 kv heads: Q8_0 81 us
+//     against 93 at the attention's 4608, asymmetric 101 against 140 at 8192; 64 sequences of 1000 to 4000, which fill
+//     the SMs by themselves: 117 against 97). One long sequence, or equal ones, would gain by longer chunks, but what
+//     the call knows is an upper bound of the lengths.
 //   The tcgen05 kernel: as many chunks as fill the SMs beside the window's CTAs (it takes at most eight by itself:
 //     64 CTAs for 128 rows and 8 kv heads; window CTAs in a second wave cost 13 us). Sequences of a paged batch count
 //     as five eighths of the longest, here and below (4 of up to 16379 tokens, 256 rows, 8 kv heads 175 us; 210 without).

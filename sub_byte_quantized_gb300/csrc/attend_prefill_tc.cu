@@ -53,8 +53,8 @@
 // ALT (at most 128 query rows, calls that also score the tokens): with one row block the softmax of a stage and the
 // MMAs around it would follow one another, so both blocks hold the same rows and take the stages in turn, block
 // b the stages j with j % 2 == b; at the end block 0 combines the two (m, l, O). The second block's query codes
-// leave room for a fourth tile buffer. 32 query rows of 4 heads over 32K tokens, 8 kv heads: the call takes 70.2 us
-// instead of 89.6, the body's CTAs 44: 2130 cycles a stage, of which the unpacking takes 1270 and a block's softmax,
+// leave room for a fourth tile buffer. 32 query rows of 4 heads over 32K tokens, 8 kv heads: the call took 70.2 us
+// instead of 89.6 (71.7 with the reference below the maximum), the body's CTAs 44: 2130 cycles a stage, of which the unpacking takes 1270 and a block's softmax,
 // with its wait for P'V and S, twice 2130. None of these helped: four unpacking warps (registers moved between the
 // roles: 71 us), S issued two stages ahead of P'V (73), whatever is ready first (71). (Other calls keep the order of their sums.)
 //

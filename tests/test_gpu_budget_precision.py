@@ -38,7 +38,9 @@ def _sums(layout, D, rows, chunk):
     if D == 128 and layout != "q6_0" and rows <= 8 and "+" not in layout or layout == "q4_0+q8_0" and rows <= 8:
         if layout == "asym4_g32":                           # two products of a tile by themselves, then one rounded addition
             return 2 * 2.0 ** -23 + np.sqrt(n) * 2.0 ** -24
-        return (2 + n) * 2.0 ** -23 + np.sqrt(n) * 2.0 ** -24   # every other tile so
+        if layout.startswith("had"):                        # two products of every tile into the running sum
+            return 2 * n * 2.0 ** -23
+        return (2 + n) * 2.0 ** -23 + np.sqrt(n) * 2.0 ** -24   # every other tile by itself
     if D == 128 and (rows > 8 or "+" in layout):
         # 32 tokens by themselves (six products), or four warps and 16 tokens (three), then one rounded addition
         return 6 * 2.0 ** -23 + np.sqrt(chunk // 32) * 2.0 ** -24
