@@ -3,7 +3,7 @@ pointers and the current CUDA stream, and nothing else. Every computation runs i
 
 torch is used for device memory (cache planes, workspace) and streams only. A call given a `stream` makes the
 buffers that the caller leaves to it (workspace, outputs) on that stream; a caller that reads such an output on
-another stream orders the two, as for any tensor.
+the current stream orders the two, and may then drop it like any tensor of that stream.
 """
 from __future__ import annotations
 
@@ -73,6 +73,17 @@ def _made_on(stream):
     if stream is None:
         return _CURRENT
     return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+
+
+def _output(stream, shape, dtype, device) -> torch.Tensor:
+    """A buffer for a call's output, made on its stream. The caller reads it on the current stream as a rule and may
+    drop it there while that is still to come: its memory waits for both."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _made_on(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(t.device))
+    return t
 
 
 def _need_cuda(name: str, t: torch.Tensor) -> None:
@@ -167,8 +178,7 @@ def decode_attend(cache: KVCache, q: torch.Tensor, kv_len: int, causal: bool = F
     if attn_scale is None:
         attn_scale = 1.0 / math.sqrt(D)
     if out is None:
-        with _made_on(stream):
-            out = torch.empty((B, Hq, n_q, D), dtype=torch.float32, device=q.device)
+        out = _output(stream, (B, Hq, n_q, D), torch.float32, q.device)
     _need_cuda("out", out)
     need = attend_workspace_bytes(cache, Hq, n_q, kv_len, chunk)
     if workspace is None:
@@ -201,8 +211,7 @@ def append_decode_attend(cache: KVCache, k_new: torch.Tensor, v_new: torch.Tenso
     if attn_scale is None:
         attn_scale = 1.0 / math.sqrt(D)
     if out is None:
-        with _made_on(stream):
-            out = torch.empty((B, Hq, n_q, D), dtype=torch.float32, device=q.device)
+        out = _output(stream, (B, Hq, n_q, D), torch.float32, q.device)
     _need_cuda("out", out)
     need = attend_workspace_bytes(cache, Hq, n_q, kv_len, chunk)
     if workspace is None:
@@ -232,8 +241,7 @@ def decode_attend_static(cache: KVCache, q: torch.Tensor, kv_len: int, causal: b
     if attn_scale is None:
         attn_scale = 1.0 / math.sqrt(D)
     if out is None:
-        with _made_on(stream):
-            out = torch.empty((B, Hq, n_q, D), dtype=torch.float32, device=q.device)
+        out = _output(stream, (B, Hq, n_q, D), torch.float32, q.device)
     _need_cuda("out", out)
     L.check(L.lib().kvq_decode_attend_static(C.byref(cache.struct), q.data_ptr(), _DTYPES[q.dtype], Hq, n_q,
                                              kv_len, int(bool(causal)), q_pos0, float(attn_scale), chunk,
@@ -246,9 +254,8 @@ def debug_scores_i32(cache: KVCache, q: torch.Tensor, kv_len: int, stream=None):
     _need_cuda("q", q)
     B, Hq, n_q, D = q.shape
     n_body = kv_len - min(cache.n_recent, kv_len)
-    with _made_on(stream):
-        buf = torch.empty(B * Hq * n_q * max(n_body, 1), dtype=torch.int32, device=q.device)
-        s_q = torch.empty((B, Hq, n_q), dtype=torch.float32, device=q.device)
+    buf = _output(stream, B * Hq * n_q * max(n_body, 1), torch.int32, q.device)
+    s_q = _output(stream, (B, Hq, n_q), torch.float32, q.device)
     L.check(L.lib().kvq_debug_scores_i32(C.byref(cache.struct), q.data_ptr(), _DTYPES[q.dtype], Hq, n_q, kv_len,
                                          buf.data_ptr(), s_q.data_ptr(), _stream(stream)),
             "kvq_debug_scores_i32")
@@ -268,10 +275,12 @@ def debug_attend_scores_i32(cache: KVCache, q: torch.Tensor, kv_len: int, causal
         attn_scale = 1.0 / math.sqrt(D)
     n_body = kv_len - min(cache.n_recent, kv_len)
     need = attend_workspace_bytes(cache, Hq, n_q, kv_len, chunk)
+    out = _output(stream, (B, Hq, n_q, D), torch.float32, q.device)
+    scores = _output(stream, B * Hq * n_q * max(n_body, 1), torch.int32, q.device)
+    s_q = _output(stream, (B, Hq, n_q), torch.float32, q.device)
     with _made_on(stream):
-        out = torch.empty((B, Hq, n_q, D), dtype=torch.float32, device=q.device)
-        scores = torch.full((B * Hq * n_q * max(n_body, 1),), fill, dtype=torch.int32, device=q.device)
-        s_q = torch.zeros((B, Hq, n_q), dtype=torch.float32, device=q.device)
+        scores.fill_(fill)
+        s_q.zero_()
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
     L.check(L.lib().kvq_debug_attend_scores_i32(
         C.byref(cache.struct), q.data_ptr(), _DTYPES[q.dtype], Hq, n_q, kv_len, int(bool(causal)), q_pos0,
@@ -381,8 +390,7 @@ def _paged_out_ws(cache, q, max_kv_len, chunk, out, workspace, stream):
     if B != cache.batch or D != cache.head_dim:
         raise ValueError("q shape does not match the cache")
     if out is None:
-        with _made_on(stream):
-            out = torch.empty((B, Hq, n_q, D), dtype=torch.float32, device=q.device)
+        out = _output(stream, (B, Hq, n_q, D), torch.float32, q.device)
     _need_cuda("out", out)
     need = paged_attend_workspace_bytes(cache, Hq, n_q, max_kv_len, chunk)
     if workspace is None:
@@ -584,8 +592,7 @@ def rope_table(inv_freq: torch.Tensor, n_pos: int, pos0: int = 0, magnitude: flo
         raise ValueError("inv_freq must be a contiguous host float64 vector")
     rot_dim = 2 * inv_freq.numel()
     if out is None:
-        with _made_on(stream):
-            out = torch.empty((max(n_pos, 0), rot_dim), dtype=torch.float32, device=device)
+        out = _output(stream, (max(n_pos, 0), rot_dim), torch.float32, device)
     dev = _here(("out", out))
     _dense("out", out, torch.float32, (n_pos, rot_dim))
     L.check(L.lib().kvq_rope_table(inv_freq.data_ptr(), rot_dim, pos0, n_pos, magnitude, out.data_ptr(),
@@ -623,8 +630,7 @@ def _rope_call(cache, table, k_new, v_new, slots, q, positions, interleaved, q_o
         if q.shape != (B, Hq, n_new, D) or q.dtype is not dtype:
             raise ValueError("q must have k_new's batch, rows, head_dim and dtype")
         if q_out is None:
-            with _made_on(stream):
-                q_out = torch.empty((B, Hq, n_new, D), dtype=dtype, device=q.device)
+            q_out = _output(stream, (B, Hq, n_new, D), dtype, q.device)
         else:
             _dense("q_out", q_out, dtype, (B, Hq, n_new, D))
         qr = C.byref(_rows("q", q))
@@ -693,8 +699,7 @@ def _weights_call(cache, need_fn, q, n, seq_lens, scores, scores_out, attn_scale
         raise ValueError("scores and scores_out must have the same shape")
     _ints("seq_lens", seq_lens, cache.batch)
     if out is None:
-        with _made_on(stream):
-            out = torch.empty(shape, dtype=torch.float32, device=q.device)
+        out = _output(stream, shape, torch.float32, q.device)
     else:
         _dense("out", out, torch.float32, shape)
     if workspace is None:
@@ -752,8 +757,7 @@ def evict_select(scores: torch.Tensor, kv_len: int, n_keep: int, n_sink: int = 0
         raise ValueError("scores must be contiguous float32 [batch][n_kv_heads][tokens]")
     B, H, stride = scores.shape
     if keep is None:
-        with _made_on(stream):
-            keep = torch.empty((B, H, max(n_keep, 1)), dtype=torch.int32, device=scores.device)
+        keep = _output(stream, (B, H, max(n_keep, 1)), torch.int32, scores.device)
     else:
         _ints("keep", keep, B * H * max(n_keep, 1))
     _ints("seq_lens", seq_lens, B)

@@ -124,3 +124,29 @@ def test_a_workspace_made_inside_a_capture_is_the_graphs():
     want, ws = kvq.decode_attend_weights(c, q, N, None, scores_out=torch.zeros_like(scores))
     assert torch.equal(out, want) and torch.equal(scores, ws)
     assert np.isfinite(out.cpu().numpy()).all()
+
+
+def test_an_output_dropped_while_it_is_read_on_the_current_stream():
+    """Its memory goes to nobody, on the call's stream either, before that read is over."""
+    calls = _calls()
+    s, here = torch.cuda.Stream(), torch.cuda.current_stream()
+    for name, f in calls.items():
+        if name.endswith("_host"):                          # (its output is the host's)
+            continue
+        want = [t.clone() for t in _tensors(f(None))]
+        s.wait_stream(here)
+        got = [t for t in _tensors(f(s))]
+        here.wait_stream(s)
+        torch.cuda._sleep(40_000_000)
+        kept = [(t.data_ptr(), t.numel() * t.element_size()) for t in got]
+        copies = [t.clone() for t in got]
+        own = [i for i, t in enumerate(got) if not (name.endswith("weights") and i == 1)]   # (scores_out is the caller's)
+        del got
+        with torch.cuda.stream(s):
+            for i in own:
+                t = torch.empty(kept[i][1], dtype=torch.uint8, device="cuda")
+                assert t.data_ptr() + t.numel() <= kept[i][0] or kept[i][0] + kept[i][1] <= t.data_ptr(), name
+                t.zero_()
+        torch.cuda.synchronize()
+        for a, b in zip(copies, want):
+            assert torch.equal(a, b), name
