@@ -84,7 +84,8 @@ __global__ void __launch_bounds__(kTableThreads) rope_table_kernel(RopeTurns f, 
   }
 }
 
-// n / d for n < 2^31 by one high product: (n + umulhi(n, mul)) >> shift.
+// n / d for n < 2^31 by one high product, (n + umulhi(n, mul)) >> shift, with the multiplier of Granlund and Montgomery
+// ("Division by invariant integers using multiplication", 1994): 2^32 + mul = floor(2^(32 + shift) / d) + 1.
 __device__ __forceinline__ unsigned divide(unsigned n, const FastDiv &d) { return (n + __umulhi(n, d.mul)) >> d.shift; }
 
 // The row a group of threads works on: K rows first, then V, then q.
