@@ -479,6 +479,51 @@ kvq_status kvq_paged_evict_compact(const kvq_paged_cache *cache, const int32_t *
                                    int64_t scores_stride, kvq_stream_t stream);
 
 /* ------------------------------------------------------------------------------------------
+ * Steps of a serving batch planned on the device (no counterpart on the pages): the pages and the slot
+ * map of a step from the requests' lengths, and the append of its ragged run of tokens by that map.
+ *
+ * Request b holds L = seq_lens[b] tokens (clamped into [0, max_pages_per_seq * page_size]) in its first
+ * ceil(L / page_size) table entries, and asks for n = new_lens[b] more; n < 0: it has ended.
+ *   - The pages of ended requests go behind the free ones, request by request, first page first (what the
+ *     list of n_pool entries has no room for is dropped).
+ *   - Then, in the requests' order, those are served that the table has room for (L + n); of these, those
+ *     whose pages, with those of all before them in this group, the free ones last for (a request that needs
+ *     none is always one); of these, those whose tokens, with those of all before them in this group,
+ *     max_tokens has room for. The others keep what they have: nothing granted.
+ *   - The pages taken are the last of the free ones, the last one first; they become the entries behind the
+ *     request's ceil(L / page_size). Other entries are left as they were.
+ *   block_table  device i32 [batch][max_pages_per_seq], read and written
+ *   free_pages   device i32 [n_pool], read and written; n_free device i32 [1]: how many are free
+ *   lens_out     device i32 [batch]: L + granted, 0 for one that has ended; may be seq_lens
+ *   granted      device i32 [batch]: n or 0; may be new_lens
+ *   n_free_out   device i32 [1]; may be n_free
+ *   cu_new       device i32 [batch + 1]: sums of granted, from 0
+ *   slots        device i64 [max_tokens]: the pool row (page * page_size + row) of the step's i-th token, the
+ *                requests' granted tokens one after the other; -1 behind the last
+ *   positions    device i32 [max_tokens]: its position in its sequence; -1 behind the last
+ * No other two buffers may overlap. A request's pages may be shared with no other request. Two launches at
+ * most. page_size as for a paged cache; 1 <= batch <= 2^20, 0 <= max_tokens <= 2^30 (0: slots and positions
+ * are not written).
+ */
+kvq_status kvq_page_plan(int32_t batch, int32_t page_size, int32_t max_pages_per_seq, const int32_t *seq_lens,
+                         const int32_t *new_lens, int32_t *block_table, int32_t *free_pages, int32_t n_pool,
+                         const int32_t *n_free, int32_t max_tokens, int32_t *lens_out, int32_t *granted,
+                         int32_t *n_free_out, int32_t *cu_new, int64_t *slots, int32_t *positions,
+                         kvq_stream_t stream);
+
+/*
+ * Append a ragged run of tokens to a paged pool: token t's row of every kv head goes to pool row slots[t].
+ *   k_new, v_new  [n_tokens][n_kv_heads][head_dim] in `dtype` by token_stride and head_stride (kvq_rows;
+ *                 batch_stride is not used)
+ *   slots         device i64 [n_tokens], as kvq_page_plan writes them; a token whose slot lies outside
+ *                 [0, n_pages * page_size) is not written. A slot that occurs twice gets either row.
+ * Quantisation as kvq_paged_store. The block table is not read. Hadamard caches with a window are refused
+ * (its ring goes by sequence). One launch (mixed K/V layouts: one per plane). n_tokens == 0 is a no-op.
+ */
+kvq_status kvq_paged_store_slots(const kvq_paged_cache *cache, const kvq_rows *k_new, const kvq_rows *v_new,
+                                 int32_t dtype, int32_t n_tokens, const int64_t *slots, kvq_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
  * Host-buffer forms of the two append + attend calls, for callers whose new rows and queries are
  * in host memory and who want the result there (no counterpart on the pages: the steps are
  * those of the device-buffer calls above, with the copies around them).

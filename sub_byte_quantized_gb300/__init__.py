@@ -12,5 +12,6 @@ from .api import (  # noqa: F401
     rope_frequencies, rope_table, rope_store, paged_rope_store,
     decode_attend_weights, paged_decode_attend_weights, attend_weights_workspace_bytes,
     paged_attend_weights_workspace_bytes, evict_select, evict_compact, paged_evict_compact,
+    PagePlan, page_plan, paged_store_slots,
 )
 from ._lib import KvqError, LAYOUT_IDS, EXPORTS  # noqa: F401

@@ -43,7 +43,8 @@ EXPORTS = ("kvq_row_bytes", "kvq_cache_bytes", "kvq_store_q4_0", "kvq_store_q6_0
            "kvq_rope_frequencies", "kvq_rope_table", "kvq_rope_store", "kvq_paged_rope_store",
            "kvq_attend_weights_workspace_bytes", "kvq_decode_attend_weights",
            "kvq_paged_attend_weights_workspace_bytes", "kvq_paged_decode_attend_weights",
-           "kvq_evict_select", "kvq_evict_compact", "kvq_paged_evict_compact")
+           "kvq_evict_select", "kvq_evict_compact", "kvq_paged_evict_compact",
+           "kvq_page_plan", "kvq_paged_store_slots")
 ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "banded": 3, "yarn": 4}   # kvq_rope_scaling
 STATIC_SCRATCH_BYTES = 16 * 1024 * 1024   # KVQ_STATIC_SCRATCH_BYTES in include/kvq.h
 
@@ -157,7 +158,9 @@ def lib() -> C.CDLL:
                                                  P]),
             ("kvq_evict_select", [P, I32, I32, I64, I32, P, I32, I32, I32, P, P, P]),
             ("kvq_evict_compact", [cache_p, cache_p, P, I32, I32, P, I64, P, I64, P]),
-            ("kvq_paged_evict_compact", [paged_p, P, I32, P, I32, P, I64, P])):
+            ("kvq_paged_evict_compact", [paged_p, P, I32, P, I32, P, I64, P]),
+            ("kvq_page_plan", [I32, I32, I32, P, P, P, P, I32, P, I32, P, P, P, P, P, P, P]),
+            ("kvq_paged_store_slots", [paged_p, rows_p, rows_p, I32, I32, P, P])):
         f = getattr(L, name)
         f.argtypes, f.restype = args, I32
     L.kvq_attend_weights_workspace_bytes.argtypes = [cache_p, I32, I32, I32, I32]

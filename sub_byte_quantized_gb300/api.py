@@ -10,6 +10,7 @@ from __future__ import annotations
 import contextlib
 import ctypes as C
 import math
+from typing import NamedTuple
 
 import torch
 
@@ -803,3 +804,69 @@ def paged_evict_compact(cache: PagedKVCache, keep: torch.Tensor, seq_lens: torch
     L.check(L.lib().kvq_paged_evict_compact(C.byref(cache.struct), keep.data_ptr(), n_keep, seq_lens.data_ptr(),
                                             max_kv_len, _ptr(scores), stride, _stream_of(stream, dev)),
             "kvq_paged_evict_compact")
+
+
+# ------------------------------------------------------------------ steps planned on the device
+class PagePlan(NamedTuple):
+    """What page_plan writes: int32 lens [batch], granted [batch], n_free [1], cu_new [batch + 1], positions
+    [max_tokens] and int64 slots [max_tokens]."""
+    lens: torch.Tensor
+    granted: torch.Tensor
+    n_free: torch.Tensor
+    cu_new: torch.Tensor
+    slots: torch.Tensor
+    positions: torch.Tensor
+
+
+def page_plan(seq_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor, page_size: int,
+              free_pages: torch.Tensor, n_free: torch.Tensor, max_tokens: int, lens_out: torch.Tensor | None = None,
+              granted: torch.Tensor | None = None, n_free_out: torch.Tensor | None = None,
+              cu_new: torch.Tensor | None = None, slots: torch.Tensor | None = None,
+              positions: torch.Tensor | None = None, stream=None) -> PagePlan:
+    """Pages, table entries and slot map of a step: request b holds seq_lens[b] tokens and asks for new_lens[b]
+    more (negative: it has ended, its pages go back to free_pages). In the requests' order, those are granted that
+    the table, the free pages and max_tokens have room for. block_table (int32 [batch][max_pages_per_seq]) and
+    free_pages (int32, n_free [1] of them free) are updated in place; lens_out, granted and n_free_out may be
+    seq_lens, new_lens and n_free. Token i of the step goes to pool row slots[i], at positions[i] of its sequence
+    (-1 behind the last of cu_new[batch] tokens)."""
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be int32 [batch][max_pages_per_seq]")
+    B, per = block_table.shape
+    dev = seq_lens.device
+    made = {"lens_out": (lens_out, B, torch.int32), "granted": (granted, B, torch.int32), "n_free_out": (n_free_out, 1, torch.int32),
+            "cu_new": (cu_new, B + 1, torch.int32), "slots": (slots, max(max_tokens, 0), torch.int64),
+            "positions": (positions, max(max_tokens, 0), torch.int32)}
+    out = {name: _output(stream, n, dtype, dev) if t is None else t for name, (t, n, dtype) in made.items()}
+    for name, (t, n, dtype) in made.items():
+        _dense(name, out[name], dtype)
+        if out[name].numel() != n:
+            raise ValueError(f"{name} must have {n} entries")
+    _ints("seq_lens", seq_lens, B)
+    _ints("new_lens", new_lens, B)
+    _ints("n_free", n_free, 1)
+    _dense("block_table", block_table, torch.int32)
+    _dense("free_pages", free_pages, torch.int32)
+    here = _here(("seq_lens", seq_lens), ("new_lens", new_lens), ("block_table", block_table), ("free_pages", free_pages),
+                 ("n_free", n_free), *out.items())
+    L.check(L.lib().kvq_page_plan(B, page_size, per, seq_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(),
+                                  free_pages.data_ptr(), free_pages.numel(), n_free.data_ptr(), max_tokens,
+                                  *(out[name].data_ptr() for name in made), _stream_of(stream, here)), "kvq_page_plan")
+    return PagePlan(*out.values())
+
+
+def paged_store_slots(cache: PagedKVCache, k_new: torch.Tensor, v_new: torch.Tensor, slots: torch.Tensor, stream=None) -> None:
+    """Append a ragged run of tokens k_new / v_new [n_tokens][H_kv][D] (strided views allowed): token t's rows go to
+    pool row slots[t] (int64, as page_plan writes them; -1: nowhere)."""
+    shape, dtype = k_new.shape, k_new.dtype
+    if len(shape) != 3 or shape[1] != cache.n_kv_heads or shape[2] != cache.head_dim:
+        raise ValueError("k_new must be [n_tokens][n_kv_heads][head_dim] of the cache")
+    if dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {dtype}")
+    if v_new.shape != shape or v_new.dtype is not dtype:
+        raise ValueError("k_new and v_new must have the same shape and dtype")
+    if slots.dtype is not torch.int64 or slots.numel() != shape[0] or not slots.is_contiguous():
+        raise ValueError(f"slots must be a contiguous int64 tensor of {shape[0]} entries")
+    dev = _here(("cache", cache.planes["k"]["payload"]), ("k_new", k_new), ("v_new", v_new), ("slots", slots))
+    k, v = (_rows(name, t.transpose(0, 1).unsqueeze(0)) for name, t in (("k_new", k_new), ("v_new", v_new)))
+    L.check(L.lib().kvq_paged_store_slots(C.byref(cache.struct), C.byref(k), C.byref(v), _DTYPES[dtype], shape[0],
+                                          slots.data_ptr(), _stream_of(stream, dev)), "kvq_paged_store_slots")

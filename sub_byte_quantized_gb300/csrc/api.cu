@@ -105,6 +105,13 @@ kvq_status check_cache(const kvq_cache *c, kvq::CacheView &v) {
   return KVQ_OK;
 }
 
+// log2 of a paged cache's page size; -1 when it is none.
+int page_shift_of(int page_size) {
+  for (int k = kvq::kMinPageShift; k <= 20; ++k)
+    if (page_size == (1 << k)) return k;
+  return -1;
+}
+
 // Validation of a paged pool and its block table.
 kvq_status check_paged_cache(const kvq_paged_cache *c, kvq::CacheView &v) {
   if (!c) return fail(KVQ_EINVAL, "cache is NULL");
@@ -112,9 +119,7 @@ kvq_status check_paged_cache(const kvq_paged_cache *c, kvq::CacheView &v) {
   if (st != KVQ_OK) return st;
   if (c->batch < 1 || c->n_kv_heads < 1 || c->n_pages < 1 || c->max_pages_per_seq < 1)
     return fail(KVQ_EINVAL, "batch, n_kv_heads, n_pages and max_pages_per_seq must be >= 1");
-  int shift = -1;
-  for (int k = kvq::kMinPageShift; k <= 20; ++k)
-    if (c->page_size == (1 << k)) shift = k;
+  const int shift = page_shift_of(c->page_size);
   if (shift < 0) return fail(KVQ_ESHAPE, "page_size %d is not a power of two in [64, 2^20]", c->page_size);
   if ((long long)c->max_pages_per_seq * c->page_size > INT_MAX)
     return fail(KVQ_ECAPACITY, "max_pages_per_seq * page_size exceeds INT_MAX tokens");
@@ -1276,6 +1281,69 @@ kvq_status kvq_paged_evict_compact(const kvq_paged_cache *cache, const int32_t *
   if (max_kv_len > v.cap) return fail(KVQ_ECAPACITY, "max_kv_len %d > capacity %d", max_kv_len, v.cap);
   return run_compact(v, v, true, keep, n_keep, max_kv_len, seq_lens, scores, scores_stride, scores, scores_stride,
                      reinterpret_cast<cudaStream_t>(stream));
+}
+
+// ------------------------------------------------------------------ steps planned on the device
+kvq_status kvq_page_plan(int32_t batch, int32_t page_size, int32_t max_pages_per_seq, const int32_t *seq_lens,
+                         const int32_t *new_lens, int32_t *block_table, int32_t *free_pages, int32_t n_pool,
+                         const int32_t *n_free, int32_t max_tokens, int32_t *lens_out, int32_t *granted,
+                         int32_t *n_free_out, int32_t *cu_new, int64_t *slots, int32_t *positions, kvq_stream_t stream) {
+  g_last_error[0] = 0;
+  if (batch < 1 || batch > 1 << 20) return fail(KVQ_EINVAL, "batch %d not in [1, 2^20]", batch);
+  if (max_pages_per_seq < 1 || n_pool < 1) return fail(KVQ_EINVAL, "max_pages_per_seq and n_pool must be >= 1");
+  if (max_tokens < 0 || max_tokens > 1 << 30) return fail(KVQ_EINVAL, "max_tokens %d not in [0, 2^30]", max_tokens);
+  const int shift = page_shift_of(page_size);
+  if (shift < 0) return fail(KVQ_ESHAPE, "page_size %d is not a power of two in [64, 2^20]", page_size);
+  if ((long long)max_pages_per_seq * page_size > INT_MAX)
+    return fail(KVQ_ECAPACITY, "max_pages_per_seq * page_size exceeds INT_MAX tokens");
+  const size_t n = sizeof(int32_t), b = batch;
+  const struct { const char *name; const void *p; size_t bytes; } bufs[] = {
+      {"seq_lens", seq_lens, n * b}, {"new_lens", new_lens, n * b}, {"n_free", n_free, n},
+      {"block_table", block_table, n * b * max_pages_per_seq}, {"free_pages", free_pages, n * n_pool},
+      {"lens_out", lens_out, n * b}, {"granted", granted, n * b}, {"n_free_out", n_free_out, n}, {"cu_new", cu_new, n * (b + 1)},
+      {"slots", slots, sizeof(int64_t) * max_tokens}, {"positions", positions, n * max_tokens}};
+  constexpr int kInputs = 3, kAll = sizeof(bufs) / sizeof(bufs[0]);
+  for (const auto &x : bufs) {
+    if (!x.p && x.bytes) return fail(KVQ_EINVAL, "%s is NULL", x.name);
+    if (!aligned(x.p, 16)) return fail(KVQ_EALIGN, "%s not 16-byte aligned", x.name);
+  }
+  for (int i = kInputs; i < kAll; ++i)
+    for (int j = 0; j < i; ++j) {
+      // in place: lens_out = seq_lens, granted = new_lens, n_free_out = n_free
+      if (j < kInputs && i == j + 5 && bufs[i].p == bufs[j].p) continue;
+      if (overlap(bufs[i].p, bufs[i].bytes, bufs[j].p, bufs[j].bytes))
+        return fail(KVQ_EINVAL, "%s overlaps %s", bufs[i].name, bufs[j].name);
+    }
+  const kvq::PlanArgs a = {batch, shift, max_pages_per_seq, n_pool, max_tokens, seq_lens, new_lens, n_free,
+                           block_table, free_pages, lens_out, granted, n_free_out, cu_new, slots, positions};
+  const cudaError_t e = kvq::launch_page_plan(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(KVQ_ECUDA, "page plan launch: %s", cudaGetErrorString(e));
+  return KVQ_OK;
+}
+
+kvq_status kvq_paged_store_slots(const kvq_paged_cache *cache, const kvq_rows *k_new, const kvq_rows *v_new, int32_t dtype,
+                                 int32_t n_tokens, const int64_t *slots, kvq_stream_t stream) {
+  g_last_error[0] = 0;
+  kvq::CacheView v;
+  kvq_status st = check_paged_cache(cache, v);
+  if (st != KVQ_OK) return st;
+  if (v.n_recent > 0) return fail(KVQ_EUNSUPPORTED, "a slot map has no sequences: a cache with a window takes kvq_paged_store");
+  if (dtype < KVQ_F32 || dtype > KVQ_F16) return fail(KVQ_EINVAL, "unknown dtype %d", dtype);
+  if (n_tokens < 0) return fail(KVQ_EINVAL, "n_tokens must be >= 0");
+  if ((long double)v.H * n_tokens * 2 * 32 > 256.0L * INT_MAX) return fail(KVQ_ESHAPE, "too many rows for one launch");
+  if (n_tokens == 0) return KVQ_OK;
+  kvq::SlotRows g;
+  st = check_rows("k_new", k_new, dtype, g.k);
+  if (st == KVQ_OK) st = check_rows("v_new", v_new, dtype, g.v);
+  if (st != KVQ_OK) return st;
+  if (!slots) return fail(KVQ_EINVAL, "slots is NULL");
+  if (!aligned(slots, 16)) return fail(KVQ_EALIGN, "slots not 16-byte aligned");
+  g.dtype = dtype;
+  g.n_tokens = n_tokens;
+  g.slots = reinterpret_cast<const long long *>(slots);
+  const cudaError_t e = kvq::launch_store_slots(v, g, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(KVQ_ECUDA, "store launch: %s", cudaGetErrorString(e));
+  return KVQ_OK;
 }
 
 // ------------------------------------------------------------------ host-buffer calls

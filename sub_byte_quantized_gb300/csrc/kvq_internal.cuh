@@ -244,6 +244,24 @@ struct RopeStore {
   int row_bytes;
 };
 cudaError_t launch_rope_store(const CacheView &c, RopeStore g, cudaStream_t st);
+// Append of a ragged run of tokens: row (t, h) of k and v (strides in elements) goes to pool row slots[t] (device;
+// one outside the pool: nowhere).
+struct SlotRows {
+  RowsIn k, v;
+  int dtype, n_tokens;
+  const long long *slots;
+};
+cudaError_t launch_store_slots(const CacheView &c, const SlotRows &g, cudaStream_t st);
+// A step's pages and slots. Everything on the device; in place (lens_out = seq_lens, granted = new_lens, n_free_out =
+// n_free) every value is read before it is written.
+struct PlanArgs {
+  int batch, page_shift, max_pages, n_pool, max_tokens;
+  const int32_t *seq_lens, *new_lens, *n_free;
+  int32_t *table, *free_pages, *lens_out, *granted, *n_free_out, *cu_new;
+  int64_t *slots;
+  int32_t *positions;
+};
+cudaError_t launch_page_plan(const PlanArgs &a, cudaStream_t st);
 // Selection of the tokens a cache keeps (scores [B][H][stride], keep [B][H][n_keep], new_lens [B] or
 // nullptr; seq_lens [B] on the device, each clamped into [0, kv_len], or nullptr).
 struct SelectArgs {
