@@ -84,7 +84,22 @@ typedef enum {
    * scale s = amax(|y|) per token, codes rint(y / s) in [-1, 1], four per byte (value 4j+i at
    * bits 2i of byte j, read back as (v ^ 2) - 2; D/4 bytes per token), the same optional ring
    * of the newest n_recent rotated rows in exact f32. Meant for a wide window. */
-  KVQ_HAD_INT2 = 5
+  KVQ_HAD_INT2 = 5,
+  /* 8-bit codes with one f32 scale per block of 64 tokens, head and plane (no counterpart on the pages): D code
+   * bytes per token (byte i = value i: int8 in [-127, 127], or e4m3), value = code * scale. An append of rows into a
+   * block, with need = amax(the new rows of the block) / 127 (e4m3: / 448), gives it
+   *   - the scale need, where the append begins at the block's row 0 (or the block's scale is 0);
+   *   - its scale s as it was, where need <= s;
+   *   - else s 2^k with the smallest k >= 1 that s 2^k >= need, and the codes of the block's rows in front of the new
+   *     ones are rounded again: round(code 2^-k), half to even.
+   * New codes are round(x / scale) by that scale (int8 half to even, e4m3 to nearest even, saturating; an infinity
+   * counts as the largest finite value); all 0 where it is 0. Rows
+   * behind the new ones are not touched, but what they stand for may change with the scale: an append ends its block.
+   * A row kept through several growths is off by at most one step of the last scale more. Contiguous caches: capacity
+   * a multiple of 64. One block layout in both planes; not provided by the rotary appends, the calls with token
+   * weights and the compaction. */
+  KVQ_INT8_B64 = 6,
+  KVQ_E4M3_B64 = 7
 } kvq_layout;
 
 /* Mixed K/V precision ([OTQ] Section 5: value quantisation costs more output quality than key
@@ -102,6 +117,7 @@ typedef enum { KVQ_F32 = 0, KVQ_BF16 = 1, KVQ_F16 = 2 } kvq_dtype;
  *   payload  u8  [batch][n_kv_heads][capacity][kvq_row_bytes(layout, head_dim)]
  *   scale    f16 [batch][n_kv_heads][capacity][head_dim/32]      (Q4_0, Q6_0, Q8_0, ASYM4_G32)
  *            f32 [batch][n_kv_heads][capacity]                   (HAD_INT4, HAD_INT2)
+ *            f32 [batch][n_kv_heads][capacity/64]                (INT8_B64, E4M3_B64)
  *   zero     f16 [batch][n_kv_heads][capacity][head_dim/32]      (ASYM4_G32 only, else NULL)
  *   recent   f32 [batch][n_kv_heads][n_recent][head_dim]         (HAD_INT4 / HAD_INT2 with
  *                                                                 n_recent > 0, else NULL)
@@ -135,7 +151,8 @@ kvq_status kvq_cache_bytes(int32_t layout, int32_t batch, int32_t n_kv_heads, in
 /*
  * Store (append) n_new tokens per (batch, kv head) at positions [pos0, pos0 + n_new).
  *   k_new, v_new: device [batch][n_kv_heads][n_new][head_dim] in `dtype` (f32, bf16 or f16).
- * Quantisation is exact and deterministic: re-storing a token writes identical bytes.
+ * Quantisation is exact and deterministic: re-storing a token writes identical bytes (block layouts: by
+ * the block's scale, see KVQ_INT8_B64).
  * HAD_INT4 / HAD_INT2 with n_recent > 0 also write the rotated f32 rows of the last
  * min(n_new, n_recent) tokens to ring slot (position mod n_recent); attention with the window
  * therefore expects kv_len equal to the end of the latest store.
@@ -221,6 +238,7 @@ kvq_status kvq_append_decode_attend(const kvq_cache *cache, const void *k_new, c
  *   payload  u8  [n_pages][n_kv_heads][page_size][kvq_row_bytes(layout, head_dim)]
  *   scale    f16 [n_pages][n_kv_heads][page_size][head_dim/32]   (Q4_0, Q6_0, ASYM4_G32)
  *            f32 [n_pages][n_kv_heads][page_size]                (HAD_INT4, HAD_INT2)
+ *            f32 [n_pages][n_kv_heads][page_size/64]             (INT8_B64, E4M3_B64)
  *   zero     f16 [n_pages][n_kv_heads][page_size][head_dim/32]   (ASYM4_G32 only, else NULL)
  *   recent   f32 [batch][n_kv_heads][n_recent][head_dim]         (HAD_INT4 / HAD_INT2 with
  *                                                                 n_recent > 0: one ring per
@@ -261,7 +279,8 @@ kvq_status kvq_paged_cache_bytes(int32_t layout, int32_t n_pages, int32_t n_kv_h
  *   positions:    device i32 [batch].
  * Quantisation as kvq_store_* for the cache's layout (any layout; bit-identical rows). The
  * positions are read on the device: a row whose position falls outside [0, max_pages_per_seq *
- * page_size) is not written. HAD_INT4 / HAD_INT2 with n_recent > 0 also write the rotated f32 rows of the
+ * page_size) is not written (block layouts: the first row that is written begins the append). HAD_INT4 /
+ * HAD_INT2 with n_recent > 0 also write the rotated f32 rows of the
  * last min(n_new, n_recent) tokens to the sequence's ring slot (position mod n_recent).
  * One kernel launch covers K and V. n_new == 0 is a no-op.
  */
@@ -516,9 +535,11 @@ kvq_status kvq_page_plan(int32_t batch, int32_t page_size, int32_t max_pages_per
  *   k_new, v_new  [n_tokens][n_kv_heads][head_dim] in `dtype` by token_stride and head_stride (kvq_rows;
  *                 batch_stride is not used)
  *   slots         device i64 [n_tokens], as kvq_page_plan writes them; a token whose slot lies outside
- *                 [0, n_pages * page_size) is not written. A slot that occurs twice gets either row.
- * Quantisation as kvq_paged_store. The block table is not read. Hadamard caches with a window are refused
- * (its ring goes by sequence). One launch (mixed K/V layouts: one per plane). n_tokens == 0 is a no-op.
+ *                 [0, n_pages * page_size) is not written. A slot that occurs twice gets either row
+ *                 (block layouts: as below).
+ * Quantisation as kvq_paged_store. Block layouts: consecutive slots of a block (64 pool rows) are one append to
+ * it, and several such runs that follow each other in the call (up to 64 tokens without a slot between them) are
+ * appended in their order; the values of a block that is met again behind other blocks are unspecified. The block table is not read. Hadamard caches with a window are refused (its ring goes by sequence). One launch (mixed K/V layouts: one per plane). n_tokens == 0 is a no-op.
  */
 kvq_status kvq_paged_store_slots(const kvq_paged_cache *cache, const kvq_rows *k_new, const kvq_rows *v_new,
                                  int32_t dtype, int32_t n_tokens, const int64_t *slots, kvq_stream_t stream);

@@ -12,10 +12,12 @@ import os
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkvq.so")
 
 KVQ_Q4_0, KVQ_Q6_0, KVQ_HAD_INT4, KVQ_ASYM4_G32, KVQ_Q8_0, KVQ_HAD_INT2 = 0, 1, 2, 3, 4, 5
+KVQ_INT8_B64, KVQ_E4M3_B64 = 6, 7
 KVQ_F32, KVQ_BF16, KVQ_F16 = 0, 1, 2
 LAYOUT_IDS = {"q4_0": KVQ_Q4_0, "q6_0": KVQ_Q6_0, "had_int4": KVQ_HAD_INT4, "asym4_g32": KVQ_ASYM4_G32,
-              "q8_0": KVQ_Q8_0, "had_int2": KVQ_HAD_INT2}
+              "q8_0": KVQ_Q8_0, "had_int2": KVQ_HAD_INT2, "int8_b64": KVQ_INT8_B64, "e4m3_b64": KVQ_E4M3_B64}
 HADAMARD_IDS = (KVQ_HAD_INT4, KVQ_HAD_INT2)
+BLOCK_IDS = (KVQ_INT8_B64, KVQ_E4M3_B64)      # one f32 scale per 64 tokens
 
 
 def mixed(k: int, v: int) -> int:

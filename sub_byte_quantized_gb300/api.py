@@ -39,6 +39,8 @@ def _plane_tensors(layout: int, lead: tuple, head_dim: int, dev, n_recent: int, 
         pl["scale"] = torch.zeros(lead, dtype=torch.float32, device=dev)
         if n_recent:
             pl["recent"] = torch.zeros(ring_lead + (n_recent, head_dim), dtype=torch.float32, device=dev)
+    elif layout in L.BLOCK_IDS:
+        pl["scale"] = torch.zeros(lead[:-1] + (lead[-1] // 64,), dtype=torch.float32, device=dev)
     else:
         pl["scale"] = torch.zeros(lead + (nb,), dtype=torch.float16, device=dev)
         if layout == L.KVQ_ASYM4_G32:
@@ -52,6 +54,8 @@ def _plane_read_bytes(layout: int, head_dim: int, n_tokens: int, n_recent: int) 
     if layout in L.HADAMARD_IDS:
         n_w = min(n_recent, n_tokens)
         return (n_tokens - n_w) * (per_tok + 4) + n_w * head_dim * 4
+    if layout in L.BLOCK_IDS:
+        return n_tokens * per_tok + (n_tokens + 63) // 64 * 4
     return n_tokens * (per_tok + 2 * (head_dim // 32) * (2 if layout == L.KVQ_ASYM4_G32 else 1))
 
 
@@ -109,7 +113,7 @@ class KVCache:
     """Device planes of one layer's packed cache plus the C struct describing them.
 
     Planes (K and V each): payload u8 [B][H_kv][cap][row_bytes]; scale f16 [B][H_kv][cap][D/32]
-    (f32 [B][H_kv][cap] for had_int4 / had_int2); zero f16 (asym4_g32); recent f32 [B][H_kv][n_recent][D]
+    (f32 [B][H_kv][cap] for had_int4 / had_int2, f32 [B][H_kv][cap/64] for int8_b64 / e4m3_b64); zero f16 (asym4_g32); recent f32 [B][H_kv][n_recent][D]
     (the Hadamard layouts with n_recent > 0).
     """
 
@@ -295,7 +299,8 @@ class PagedKVCache:
     """Device planes of one layer's paged pool, its block table and the C struct describing them.
 
     Planes (K and V each): payload u8 [n_pages][H_kv][page_size][row_bytes]; scale f16
-    [n_pages][H_kv][page_size][D/32] (f32 [n_pages][H_kv][page_size] for had_int4); zero f16
+    [n_pages][H_kv][page_size][D/32] (f32 [n_pages][H_kv][page_size] for had_int4, f32
+    [n_pages][H_kv][page_size/64] for int8_b64 / e4m3_b64); zero f16
     (asym4_g32); recent f32 [batch][H_kv][n_recent][D] (had_int4 with n_recent > 0, one ring per
     sequence). block_table: int32 [batch][max_pages_per_seq] (pool page of each logical page),
     owned by this object; the caller fills it (set_block_table) before storing.

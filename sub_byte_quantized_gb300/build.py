@@ -22,7 +22,7 @@ LIB = os.path.join(PKG, "libkvq.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
                  "-I", INCLUDE, "-I", CSRC, "--expt-relaxed-constexpr"]
-PER_FILE = {"store.cu": ["-fmad=false"], "rope.cu": ["-fmad=false"]}
+PER_FILE = {"store.cu": ["-fmad=false"], "rope.cu": ["-fmad=false"], "store_b64.cu": ["-fmad=false"]}
 
 
 def nvcc() -> str:

@@ -45,6 +45,8 @@ size_t row_bytes_of(int layout, int D) {
     case KVQ_HAD_INT2: return (size_t)D / 4;
     case KVQ_Q8_0: return 32 * (size_t)nb;
     case KVQ_ASYM4_G32: return 16 * (size_t)nb;
+    case KVQ_INT8_B64:
+    case KVQ_E4M3_B64: return (size_t)D;
     default: return 0;
   }
 }
@@ -55,7 +57,14 @@ bool split_layout(int32_t layout, int &k, int &v) {
   v = (layout >> 8) ? (layout >> 8) - 1 : k;
   if ((layout >> 8) > kvq::kLastLayout + 1 || layout < 0) return false;
   if (k > kvq::kLastLayout || v > kvq::kLastLayout) return false;
+  if (kvq::is_b64(k) || kvq::is_b64(v)) return k == v;   // their kernels take one layout in both planes
   return kvq::is_hadamard(k) == kvq::is_hadamard(v);
+}
+
+// Bytes of `rows` token rows' scales in a plain layout (the block layouts': whole blocks of 64 rows).
+size_t scale_bytes_of(int layout, size_t rows, int D) {
+  if (kvq::is_b64(layout)) return rows / 64 * sizeof(float);
+  return kvq::is_hadamard(layout) ? rows * sizeof(float) : rows * (D / kvq::kBlock) * 2;
 }
 
 // Layout checks shared by the contiguous and paged caches: both planes' layouts, head_dim, the
@@ -89,6 +98,7 @@ kvq_status check_cache(const kvq_cache *c, kvq::CacheView &v) {
   if (st != KVQ_OK) return st;
   if (c->batch < 1 || c->n_kv_heads < 1 || c->capacity < 1)
     return fail(KVQ_EINVAL, "batch, n_kv_heads and capacity must be >= 1");
+  if (kvq::is_b64(v.layout) && c->capacity % 64) return fail(KVQ_ESHAPE, "capacity %d not a multiple of 64 (block layouts)", c->capacity);
   const void *ptrs[] = {c->k_payload, c->v_payload, c->k_scale, c->v_scale};
   for (const void *p : ptrs) {
     if (!p) return fail(KVQ_EINVAL, "payload/scale pointer is NULL");
@@ -185,7 +195,11 @@ int auto_chunk(const kvq::CacheView &c, int rows, int n_body, int n_heads, long 
   const bool total_given = work > 0;
   if (!total_given) work = (long long)(n_body > 0 ? n_body : 1) * n_heads;
   long long chunk;
-  if (c.layout == KVQ_Q6_0 && kvq::mma_q6_shape(c.D, rows) && !kvq::prefill_shape(c.layout, c.v_layout, c.D, rows)) {
+  if (kvq::is_b64(c.layout)) {
+    // one chunk per resident CTA; each group of eight query rows has its own CTAs
+    const long long ctas = (long long)sms * kvq::kB64CtasPerSm(c.D), groups = (rows + 7) / 8;
+    chunk = ((work * groups + ctas - 1) / ctas + 63) / 64 * 64;
+  } else if (c.layout == KVQ_Q6_0 && kvq::mma_q6_shape(c.D, rows) && !kvq::prefill_shape(c.layout, c.v_layout, c.D, rows)) {
     // one chunk per resident CTA; each group of four query rows has its own CTAs
     const long long ctas = (long long)sms * kvq::kMmaQ6CtasPerSm(c.D);
     const long long groups = (rows + 3) / 4;
@@ -338,10 +352,11 @@ kvq_status kvq_cache_bytes(int32_t layout, int32_t batch, int32_t n_kv_heads, in
   if (layout < KVQ_Q4_0 || layout > kvq::kLastLayout) return fail(KVQ_EINVAL, "unknown layout %d", layout);
   if (!rb) return fail(KVQ_ESHAPE, "head_dim %d not 128/256", head_dim);
   if (batch < 1 || n_kv_heads < 1 || capacity < 1 || n_recent < 0) return fail(KVQ_EINVAL, "bad sizes");
+  if (kvq::is_b64(layout) && capacity % 64) return fail(KVQ_ESHAPE, "capacity %d not a multiple of 64 (block layouts)", capacity);
   const size_t rows = (size_t)batch * n_kv_heads * capacity;
   const size_t nb = (size_t)head_dim / kvq::kBlock;
   out_sizes[0] = rows * rb;
-  out_sizes[1] = kvq::is_hadamard(layout) ? rows * sizeof(float) : rows * nb * 2;
+  out_sizes[1] = scale_bytes_of(layout, rows, head_dim);
   out_sizes[2] = layout == KVQ_ASYM4_G32 ? rows * nb * 2 : 0;
   out_sizes[3] = kvq::is_hadamard(layout) ? (size_t)batch * n_kv_heads * n_recent * head_dim * sizeof(float) : 0;
   return KVQ_OK;
@@ -426,7 +441,8 @@ kvq_status prepare_attend(const kvq_cache *cache, const void *q, int32_t q_dtype
 // Phase 1 (tensor-core or CUDA-core kernel) and phase 2 on `s`, with the optional phase-1 events.
 cudaError_t launch_attend_sequence(kvq::AttendArgs &a, cudaStream_t s, bool events) {
   cudaError_t e = cudaSuccess;
-  const bool mma = kvq::mma_supported(a);
+  const bool b64 = kvq::is_b64(a.cache.layout);
+  const bool mma = b64 || kvq::mma_supported(a);
   // the decode tensor-core kernels (and the row-side kernel's decode form) cover the body chunks only
   a.win_in_reduce = mma && a.n_win > 0 &&
                     (!kvq::prefill_supported(a) ||
@@ -444,7 +460,7 @@ cudaError_t launch_attend_sequence(kvq::AttendArgs &a, cudaStream_t s, bool even
   if (e == cudaSuccess && prof) e = cudaStreamIsCapturing(s, &cap);
   const unsigned rec_flags = cap == cudaStreamCaptureStatusActive ? cudaEventRecordExternal : cudaEventRecordDefault;
   if (e == cudaSuccess && prof) e = cudaEventRecordWithFlags(g_ev_begin, s, rec_flags);
-  if (e == cudaSuccess) e = mma ? kvq::launch_attend_mma(a, s) : kvq::launch_attend_generic(a, s);
+  if (e == cudaSuccess) e = b64 ? kvq::launch_attend_b64(a, s) : mma ? kvq::launch_attend_mma(a, s) : kvq::launch_attend_generic(a, s);
   if (e == cudaSuccess && prof) e = cudaEventRecordWithFlags(g_ev_end, s, rec_flags);
   if (e == cudaSuccess) e = kvq::launch_attend_reduce(a, s, true);
   return e;
@@ -456,7 +472,8 @@ cudaError_t launch_append_attend(const kvq::CacheView &v, kvq::AttendArgs &a, co
   cudaError_t e = cudaSuccess;
   if (n_new > 0) {
     e = kvq::launch_store(v, k_new, v_new, kv_dtype, n_new, pos0, s);
-    a.fresh_lo = pos0;                                   // the rows (and window slots) it writes
+    // the rows (and window slots) it writes; a block layout's append may touch the rows in front of them too
+    a.fresh_lo = kvq::is_b64(v.layout) ? pos0 / 64 * 64 : pos0;
     a.fresh_hi = pos0 + n_new;
   }
   if (e == cudaSuccess) e = launch_attend_sequence(a, s, true);
@@ -613,10 +630,11 @@ kvq_status kvq_paged_cache_bytes(int32_t layout, int32_t n_pages, int32_t n_kv_h
   const size_t rb = row_bytes_of(layout, head_dim);
   if (!rb) return fail(KVQ_ESHAPE, "head_dim %d not 128/256", head_dim);
   if (n_pages < 1 || n_kv_heads < 1 || page_size < 1 || batch < 1 || n_recent < 0) return fail(KVQ_EINVAL, "bad sizes");
+  if (kvq::is_b64(layout) && page_size % 64) return fail(KVQ_ESHAPE, "page_size %d not a multiple of 64 (block layouts)", page_size);
   const size_t rows = (size_t)n_pages * n_kv_heads * page_size;
   const size_t nb = (size_t)head_dim / kvq::kBlock;
   out_sizes[0] = rows * rb;
-  out_sizes[1] = kvq::is_hadamard(layout) ? rows * sizeof(float) : rows * nb * 2;
+  out_sizes[1] = scale_bytes_of(layout, rows, head_dim);
   out_sizes[2] = layout == KVQ_ASYM4_G32 ? rows * nb * 2 : 0;
   out_sizes[3] = kvq::is_hadamard(layout) ? (size_t)batch * n_kv_heads * n_recent * head_dim * sizeof(float) : 0;
   return KVQ_OK;
@@ -664,7 +682,7 @@ cudaError_t launch_paged_append_attend(const kvq::CacheView &v, kvq::AttendArgs 
   if (n_new > 0) {
     // the new tokens end each sequence: positions seq_lens[b] - n_new + j
     e = kvq::launch_store(v, k_new, v_new, kv_dtype, n_new, 0, s, seq_lens, -n_new);
-    a.fresh_tail = n_new;                                 // the rows (and window slots) it writes
+    a.fresh_tail = kvq::is_b64(v.layout) ? n_new + 63 : n_new;   // the rows (and window slots) it writes, and their blocks
   }
   if (e == cudaSuccess) e = launch_attend_sequence(a, s, true);
   return e;
@@ -692,7 +710,10 @@ void phase1_capacity(const kvq::CacheView &c, int rows, int q_dtype, int &ctas_p
                      bool &window_ctas) {
   ctas_per_unit = 1;
   window_ctas = false;                                   // the decode kernels leave the window to phase 2
-  if (c.layout == KVQ_Q6_0 && c.v_layout == KVQ_Q6_0 && kvq::mma_q6_shape(c.D, rows) &&
+  if (kvq::is_b64(c.layout)) {
+    ctas_per_sm = kvq::kB64CtasPerSm(c.D);
+    ctas_per_unit = (rows + 7) / 8;
+  } else if (c.layout == KVQ_Q6_0 && c.v_layout == KVQ_Q6_0 && kvq::mma_q6_shape(c.D, rows) &&
       !(kvq::prefill_shape(c.layout, c.v_layout, c.D, rows) && q_dtype != KVQ_F32)) {
     ctas_per_sm = kvq::kMmaQ6CtasPerSm(c.D);
     ctas_per_unit = (rows + 3) / 4;
@@ -836,6 +857,7 @@ kvq_status check_rows(const char *name, const kvq_rows *r, int dtype, kvq::RowsI
 kvq_status check_rope_store(const kvq::CacheView &v, const kvq_rope *rope, const kvq_rows *k_new, const kvq_rows *v_new,
                             const kvq_rows *q, int dtype, int n_q_heads, int n_new, void *q_out, kvq::RopeStore &g) {
   if (!rope || !rope->table) return fail(KVQ_EINVAL, "rope or its table is NULL");
+  if (kvq::is_b64(v.layout)) return fail(KVQ_EUNSUPPORTED, "the rotary append has no block layouts (rotate, then kvq_store)");
   if (dtype < KVQ_F32 || dtype > KVQ_F16) return fail(KVQ_EINVAL, "unknown dtype %d", dtype);
   if (n_new < 0) return fail(KVQ_EINVAL, "n_new must be >= 0");
   if (n_q_heads < 0) return fail(KVQ_EINVAL, "n_q_heads must be >= 0");
@@ -1118,6 +1140,7 @@ kvq_status check_evict(const int32_t *keep, int n_keep, int kv_len, const int32_
 kvq_status run_compact(const kvq::CacheView &src, const kvq::CacheView &dst, bool in_place, const int32_t *keep, int n_keep,
                        int kv_len, const int32_t *seq_lens, float *scores, int64_t scores_stride, float *scores_out,
                        int64_t out_stride, cudaStream_t s) {
+  if (kvq::is_b64(src.layout)) return fail(KVQ_EUNSUPPORTED, "rows of a block layout share their block's scale: they do not move one by one");
   if (n_keep < src.n_recent) return fail(KVQ_EINVAL, "n_keep %d < n_recent %d: the window's tokens stay", n_keep, src.n_recent);
   const int most = n_keep < kv_len ? n_keep : kv_len;
   if (scores) {
@@ -1184,6 +1207,7 @@ kvq_status kvq_decode_attend_weights(const kvq_cache *cache, const void *q, int3
   chunk = contiguous_chunk(cache, n_q_heads, n_q, kv_len, chunk, q_dtype == KVQ_F32);
   kvq_status st = prepare_attend(cache, q, q_dtype, n_q_heads, n_q, kv_len, causal, q_pos0, attn_scale, chunk, out,
                                  workspace, workspace_bytes, a);
+  if (st == KVQ_OK && kvq::is_b64(a.cache.layout)) st = fail(KVQ_EUNSUPPORTED, "token weights are not provided for the block layouts");
   if (st == KVQ_OK) st = check_scores(scores_in, scores_out, scores_stride, kv_len, decay, (int64_t)a.cache.B * a.cache.H);
   if (st != KVQ_OK) return st;
   const size_t need = kvq_attend_workspace_bytes(cache, n_q_heads, n_q, kv_len, chunk);   // of the same chunk
@@ -1201,6 +1225,7 @@ kvq_status kvq_paged_decode_attend_weights(const kvq_paged_cache *cache, const v
   chunk = paged_chunk(cache, n_q_heads, n_q, max_kv_len, chunk, q_dtype == KVQ_F32);
   kvq_status st = prepare_paged(cache, q, q_dtype, n_q_heads, n_q, seq_lens, max_kv_len, causal, attn_scale, chunk, out,
                                 workspace, workspace_bytes, a);
+  if (st == KVQ_OK && kvq::is_b64(a.cache.layout)) st = fail(KVQ_EUNSUPPORTED, "token weights are not provided for the block layouts");
   if (st == KVQ_OK) st = check_scores(scores_in, scores_out, scores_stride, max_kv_len, decay, (int64_t)a.cache.B * a.cache.H);
   if (st != KVQ_OK) return st;
   const size_t need = kvq_paged_attend_workspace_bytes(cache, n_q_heads, n_q, max_kv_len, chunk);

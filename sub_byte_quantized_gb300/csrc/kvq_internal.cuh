@@ -14,13 +14,17 @@
 namespace kvq {
 
 constexpr int kBlock = 32;          // values per Q4_0 / Q6_0 / Q8_0 / asymmetric block
-constexpr int kLastLayout = KVQ_HAD_INT2;
+constexpr int kLastLayout = KVQ_E4M3_B64;
 // Tokens per chunk of the exact-f32 window (a wide window is split over several chunks).
 constexpr int kWinChunk = 64;
 // Layouts in the fixed Hadamard basis: one f32 scale per token, rotated query, optional f32 window.
 __host__ __device__ constexpr bool is_hadamard(int layout) {
   return layout == KVQ_HAD_INT4 || layout == KVQ_HAD_INT2;
 }
+// 8-bit layouts with one f32 scale per block of 64 tokens, head and plane.
+__host__ __device__ constexpr bool is_b64(int layout) { return layout == KVQ_INT8_B64 || layout == KVQ_E4M3_B64; }
+// Their phase 1: resident CTAs (of four warps) per SM.
+__host__ __device__ constexpr int kB64CtasPerSm(int D) { return D == 128 ? 3 : 2; }
 constexpr int kMaxDevices = 64;     // per-device one-time kernel attribute set-up
 
 // Tensor-core phase 1: resident CTAs (of four warps) per SM the kernel is built for; the
@@ -212,6 +216,9 @@ __device__ __forceinline__ void capture_score(const AttendArgs &a, int bb, int k
 cudaError_t launch_store(const CacheView &c, const void *k_new, const void *v_new, int dtype,
                          int n_new, int pos0, cudaStream_t st, const int32_t *seq_pos = nullptr,
                          int pos_offset = 0);
+// The same for the 8-bit block layouts, whose appends go by blocks.
+cudaError_t launch_store_b64(const CacheView &c, const void *k_new, const void *v_new, int dtype, int n_new, int pos0,
+                             cudaStream_t st, const int32_t *seq_pos, int pos_offset);
 // Rotary table rows of positions [pos0, pos0 + n_pos); the frequencies as 2^-64 fractions of a turn.
 constexpr int kMaxRotHalf = 128;
 struct RopeTurns {
@@ -252,6 +259,7 @@ struct SlotRows {
   const long long *slots;
 };
 cudaError_t launch_store_slots(const CacheView &c, const SlotRows &g, cudaStream_t st);
+cudaError_t launch_store_b64_slots(const CacheView &c, const SlotRows &g, cudaStream_t st);
 // A step's pages and slots. Everything on the device; in place (lens_out = seq_lens, granted = new_lens, n_free_out =
 // n_free) every value is read before it is written.
 struct PlanArgs {
@@ -310,6 +318,7 @@ bool mma_supported(const AttendArgs &a);
 // Whether the call's body is scored by a tensor-core kernel that is also built with score capture.
 bool capture_supported(const AttendArgs &a);
 cudaError_t launch_attend_mma(const AttendArgs &a, cudaStream_t st);
+cudaError_t launch_attend_b64(const AttendArgs &a, cudaStream_t st);
 cudaError_t launch_attend_mma4(const AttendArgs &a, cudaStream_t st);
 bool mma_q6_supported(const AttendArgs &a);
 cudaError_t launch_attend_mma_q6(const AttendArgs &a, cudaStream_t st);

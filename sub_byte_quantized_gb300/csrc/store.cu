@@ -191,6 +191,7 @@ cudaError_t launch_store_planes(const CacheView &c, const void *k_new, const voi
 
 cudaError_t launch_store(const CacheView &c, const void *k_new, const void *v_new, int dtype, int n_new,
                          int pos0, cudaStream_t st, const int32_t *seq_pos, int pos_offset) {
+  if (is_b64(c.layout)) return launch_store_b64(c, k_new, v_new, dtype, n_new, pos0, st, seq_pos, pos_offset);
   StoreGeom g = {};
   g.n_new = n_new; g.pos0 = pos0;
   g.seq_pos = seq_pos; g.pos_offset = pos_offset;
@@ -199,6 +200,7 @@ cudaError_t launch_store(const CacheView &c, const void *k_new, const void *v_ne
 }
 
 cudaError_t launch_store_slots(const CacheView &c, const SlotRows &r, cudaStream_t st) {
+  if (is_b64(c.layout)) return launch_store_b64_slots(c, r, st);
   StoreGeom g = {};
   g.head[0] = r.k.head; g.head[1] = r.v.head;
   g.token[0] = r.k.token; g.token[1] = r.v.token;

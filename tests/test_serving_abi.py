@@ -82,3 +82,35 @@ def test_store_slots_refusals(L):
     assert _store(L, k=(P + 8, 0, 128, 256)) == EALIGN and _store(L, v=(P, 0, 128, 252)) == EALIGN and _store(L, k=(P, 0, -128, 256)) == EINVAL
     assert _store(L, cache=_paged(2, n_recent=32)) == EUNSUPPORTED and _store(L, cache=_paged(page=96)) == ESHAPE
     assert _store(L, cache=_paged(heads=1 << 10), n=2 ** 31 - 1) == ESHAPE
+
+
+@pytest.mark.parametrize("layout", [6, 7])
+def test_block_layout_sizes_and_refusals(L, layout):
+    from sub_byte_quantized_gb300._lib import KvqCache, KvqRope, KvqRows, mixed
+    assert L.kvq_row_bytes(layout, 128) == 128 and L.kvq_row_bytes(layout, 256) == 256 and L.kvq_row_bytes(8, 128) == 0
+    out = (C.c_size_t * 4)()
+    assert L.kvq_cache_bytes(layout, 2, 3, 128, 192, 0, out) == 0 and list(out) == [2 * 3 * 192 * 128, 2 * 3 * 3 * 4, 0, 0]
+    assert L.kvq_cache_bytes(layout, 2, 3, 128, 100, 0, out) == ESHAPE
+    assert L.kvq_paged_cache_bytes(layout, 5, 3, 256, 128, 2, 0, out) == 0 and list(out) == [5 * 3 * 128 * 256, 5 * 3 * 2 * 4, 0, 0]
+    assert L.kvq_paged_cache_bytes(layout, 5, 3, 256, 32, 2, 0, out) == ESHAPE
+    p = C.byref
+    store = lambda c: L.kvq_store(p(c), 16, 16, 1, 1, 0, None)                     # noqa: E731
+    assert store(_cache(layout, cap=100)) == ESHAPE and store(_cache(layout, D=64)) == ESHAPE
+    for bad in (mixed(layout, 4), mixed(0, layout), mixed(6, 7), mixed(7, 6), mixed(2, layout)):
+        assert store(_cache(bad)) == EINVAL
+    assert store(_cache(layout, n_recent=32)) == EUNSUPPORTED
+    c, pg = _cache(layout), _paged(layout)
+    r, k = KvqRope(P, 64, 128, 0, None), KvqRows(P, 512, 256, 128)
+    assert L.kvq_rope_store(p(c), p(r), p(k), p(k), None, 1, 0, 1, 0, None, None) == EUNSUPPORTED
+    assert L.kvq_paged_rope_store(p(pg), p(r), p(k), p(k), None, 1, 0, 1, P, None, None) == EUNSUPPORTED
+    assert L.kvq_decode_attend_weights(p(c), P, 1, 2, 1, 10, 0, 0, 0.1, 0, P, P, P, 64, 1.0, P, 1 << 40, None) == EUNSUPPORTED
+    assert L.kvq_paged_decode_attend_weights(p(pg), P, 1, 2, 1, P, 10, 0, 0.1, 0, P, P, P, 64, 1.0, P, 1 << 40, None) == EUNSUPPORTED
+    assert L.kvq_evict_compact(p(c), None, P, 20, 60, None, 0, None, 0, None) == EUNSUPPORTED
+    assert L.kvq_paged_evict_compact(p(pg), P, 20, P, 60, None, 0, None) == EUNSUPPORTED
+    assert L.kvq_debug_scores_i32(p(c), P, 1, 2, 1, 10, P, P, None) == EUNSUPPORTED
+    ws = L.kvq_attend_workspace_bytes(p(c), 2, 1, 60, 64)
+    assert ws > 0 and L.kvq_decode_attend(p(c), 16, 1, 2, 1, 60, 0, 0, 1.0, 64, 16, 256, ws - 1, None) == EWORKSPACE
+    assert L.kvq_attend_chunk(p(c), 2, 1, 60, 0) % 64 == 0
+    for name in ("kvq_store_q8_0", "kvq_store_q4_0"):
+        assert getattr(L, name)(p(c), 16, 16, 1, 1, 0, None) == EUNSUPPORTED
+    assert KvqCache is not None
