@@ -545,6 +545,79 @@ kvq_status kvq_paged_store_slots(const kvq_paged_cache *cache, const kvq_rows *k
                                  int32_t dtype, int32_t n_tokens, const int64_t *slots, kvq_stream_t stream);
 
 /* ------------------------------------------------------------------------------------------
+ * Attention over the blocks of 64 tokens that a cheap score selects for each query (no counterpart on the
+ * pages), for any layout of keys and values without a recent window; contiguous caches: capacity a multiple of
+ * 64; batch * n_kv_heads * n_q <= 65535.
+ *
+ * Bounds of the keys, per block of 64 tokens and kv head, beside the cache's rows (a block's place is that of
+ * its rows / 64, so bounds follow pages that sequences share):
+ *   codes  i8  [batch][n_kv_heads][capacity/64][2][head_dim]   (paged: [n_pages][n_kv_heads][page_size/64][2][head_dim])
+ *          the smallest value of each channel over the block's tokens, then the largest, by the block's scale:
+ *          floor(min / scale) and ceil(max / scale), each division rounded once, within [-127, 127]
+ *   scale  f32 [batch][n_kv_heads][capacity/64]                (paged: [n_pages][n_kv_heads][page_size/64])
+ *          the largest magnitude of these / 127 (0: all codes 0)
+ * of the values that the packed rows stand for (Hadamard layouts: in the rotated basis).
+ */
+typedef struct kvq_block_bounds {
+  int8_t *codes;
+  float *scale;
+} kvq_block_bounds;
+
+/* Bounds of every block that holds a token of [first, kv_len), over the block's tokens below kv_len: after an append
+ * at pos0, first = pos0 (a block layout's append changes its block's values; they are in it). first == kv_len is a
+ * no-op. Paged: the blocks of each sequence's newest n_fresh tokens (seq_lens device i32 [batch], clamped into [0,
+ * max_pages_per_seq * page_size]); n_fresh == 0 is a no-op. One launch. */
+kvq_status kvq_block_bounds_update(const kvq_cache *cache, const kvq_block_bounds *bounds, int32_t first, int32_t kv_len,
+                                   kvq_stream_t stream);
+kvq_status kvq_paged_block_bounds_update(const kvq_paged_cache *cache, const kvq_block_bounds *bounds,
+                                         const int32_t *seq_lens, int32_t n_fresh, kvq_stream_t stream);
+
+/*
+ * The blocks selected for each query and kv head. A query row (Hadamard layouts: rotated) in int8, q8 = clamp(rint(q /
+ * s_q), -127, 127) with s_q = amax / 127, gives a block the score
+ *   (sum over q8_d > 0 of q8_d hi_d, over q8_d < 0 of q8_d lo_d) * s_q * scale     an exact integer, then two rounded
+ *                                                       products; no q8 . k s_q of the block is larger
+ * and the largest score over the query heads of a kv head counts. Of the blocks that row i sees (its limit as in
+ * kvq_decode_attend / kvq_paged_decode_attend, causal or not) the list holds the first n_sink, the last n_recent, and
+ * among the others those with the highest scores, ties going to the lowest index, n_sel in all.
+ *   q    device [batch][n_q_heads][n_q][head_dim] in q_dtype
+ *   sel  device i32 [batch][n_kv_heads][n_q][n_sel]: ascending; a row that sees at most n_sel blocks has all of them,
+ *        and -1 fills the rest
+ *   workspace  at least kvq_block_select_workspace_bytes (shared with no call in flight)
+ * Scores are meant for a positive attn_scale. Deterministic.
+ */
+size_t kvq_block_select_workspace_bytes(const kvq_cache *cache, int32_t n_q, int32_t kv_len);
+size_t kvq_paged_block_select_workspace_bytes(const kvq_paged_cache *cache, int32_t n_q, int32_t max_kv_len);
+kvq_status kvq_block_select(const kvq_cache *cache, const kvq_block_bounds *bounds, const void *q, int32_t q_dtype,
+                            int32_t n_q_heads, int32_t n_q, int32_t kv_len, int32_t causal, int32_t q_pos0,
+                            int32_t n_sel, int32_t n_sink, int32_t n_recent, int32_t *sel, void *workspace,
+                            size_t workspace_bytes, kvq_stream_t stream);
+kvq_status kvq_paged_block_select(const kvq_paged_cache *cache, const kvq_block_bounds *bounds, const void *q,
+                                  int32_t q_dtype, int32_t n_q_heads, int32_t n_q, const int32_t *seq_lens,
+                                  int32_t max_kv_len, int32_t causal, int32_t n_sel, int32_t n_sink, int32_t n_recent,
+                                  int32_t *sel, void *workspace, size_t workspace_bytes, kvq_stream_t stream);
+
+/*
+ * kvq_decode_attend (kvq_paged_decode_attend) in which row i of the query heads of a kv head sees only the tokens
+ * of the blocks in its list sel[b][kv head][i] (device i32 [batch][n_kv_heads][n_q][n_sel], ascending; a list ends at the
+ * first entry that is not above the one before it, is negative, or lies behind what the row sees). A row whose list
+ * is empty gets zeros. chunk: as there, in tokens of the lists. The lists may come from kvq_block_select or from anywhere.
+ *   workspace  at least kvq_sparse_attend_workspace_bytes (shared with no call in flight)
+ */
+size_t kvq_sparse_attend_workspace_bytes(const kvq_cache *cache, int32_t n_q_heads, int32_t n_q, int32_t n_sel,
+                                         int32_t chunk);
+size_t kvq_paged_sparse_attend_workspace_bytes(const kvq_paged_cache *cache, int32_t n_q_heads, int32_t n_q,
+                                               int32_t n_sel, int32_t chunk);
+kvq_status kvq_sparse_attend(const kvq_cache *cache, const void *q, int32_t q_dtype, int32_t n_q_heads, int32_t n_q,
+                             int32_t kv_len, int32_t causal, int32_t q_pos0, float attn_scale, const int32_t *sel,
+                             int32_t n_sel, int32_t chunk, float *out, void *workspace, size_t workspace_bytes,
+                             kvq_stream_t stream);
+kvq_status kvq_paged_sparse_attend(const kvq_paged_cache *cache, const void *q, int32_t q_dtype, int32_t n_q_heads,
+                                   int32_t n_q, const int32_t *seq_lens, int32_t max_kv_len, int32_t causal,
+                                   float attn_scale, const int32_t *sel, int32_t n_sel, int32_t chunk, float *out,
+                                   void *workspace, size_t workspace_bytes, kvq_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
  * Host-buffer forms of the two append + attend calls, for callers whose new rows and queries are
  * in host memory and who want the result there (no counterpart on the pages: the steps are
  * those of the device-buffer calls above, with the copies around them).

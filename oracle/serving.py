@@ -173,3 +173,48 @@ def attend(values, H, q, alpha, lens, causal=False, blocks=None):
                 ds = (mass * ((D / 16 + 4) * 2.0 ** -23 + 2.0 ** -21) + 6 * 2.0 ** -24 * np.abs(s)).max()
                 tol[b, hq, i] = (p @ np.abs(vv)) * (2 * ds + 2.0 ** -20 + (len(s) / 32 + 24) * 2.0 ** -23) + 2.0 ** -37 * np.abs(vv).sum(0)
     return out, tol
+
+
+# ------------------------------------------------------------------ bounds and selection of blocks
+def key_rows(cache, b, h, n):
+    """float32 key rows [n][D] that a contiguous cache's packed rows stand for (Hadamard layouts: rotated)."""
+    if isinstance(cache, BlockCache):
+        return cache.values("k", b, h, n).astype(np.float32)
+    return cache.dequantized("k", n)[b, h].astype(np.float32)
+
+
+def bounds(rows):
+    """(codes int8 [blocks][2][D], scale f32 [blocks]) of the blocks of key rows [n][D]."""
+    codes, scales = [], []
+    for t in range(0, len(rows), BLOCK_TOKENS):
+        lo, hi = rows[t:t + BLOCK_TOKENS].min(0), rows[t:t + BLOCK_TOKENS].max(0)
+        s = np.float32(max(np.abs(lo).max(), np.abs(hi).max())) / np.float32(127)
+        if s > 0:
+            lo, hi = np.floor(lo / s), np.ceil(hi / s)
+        else:
+            lo, hi = lo * 0, hi * 0
+        codes.append(np.clip(np.stack((lo, hi)), -127, 127).astype(np.int8))
+        scales.append(s)
+    return np.array(codes), np.array(scales, np.float32)
+
+
+def select(codes, scale, q, limits, n_sel, n_sink, n_recent):
+    """Lists [n_q][n_sel] of one kv head: codes [blocks][2][D], scale [blocks], q float32 [heads][n_q][D] (rotated where the
+    layout is), limits [n_q]: the last token that each row sees."""
+    out = np.full((q.shape[1], n_sel), -1, np.int32)
+    for i, last in enumerate(limits):
+        n = 0 if last < 0 else last // BLOCK_TOKENS + 1
+        if n <= n_sel:
+            out[i, :n] = np.arange(n)
+            continue
+        best = np.full(n, -np.inf, np.float32)
+        for x in q[:, i].astype(np.float32):
+            s = np.float32(np.abs(x).max()) / np.float32(127)
+            q8 = np.clip(np.rint(x / s), -127, 127).astype(np.int64) if s > 0 else np.zeros(len(x), np.int64)
+            dots = np.where(q8 > 0, q8 * codes[:n, 1].astype(np.int64), q8 * codes[:n, 0].astype(np.int64)).sum(1)
+            best = np.maximum(best, dots.astype(np.float32) * s)
+        best = best * scale[:n]
+        keep = set(range(n_sink)) | set(range(n - n_recent, n))
+        others = sorted((b for b in range(n) if b not in keep), key=lambda b: (-float(best[b]), b))
+        out[i] = sorted(keep | set(others[:n_sel - len(keep)]))
+    return out

@@ -46,7 +46,11 @@ EXPORTS = ("kvq_row_bytes", "kvq_cache_bytes", "kvq_store_q4_0", "kvq_store_q6_0
            "kvq_attend_weights_workspace_bytes", "kvq_decode_attend_weights",
            "kvq_paged_attend_weights_workspace_bytes", "kvq_paged_decode_attend_weights",
            "kvq_evict_select", "kvq_evict_compact", "kvq_paged_evict_compact",
-           "kvq_page_plan", "kvq_paged_store_slots")
+           "kvq_page_plan", "kvq_paged_store_slots",
+           "kvq_block_bounds_update", "kvq_paged_block_bounds_update", "kvq_block_select_workspace_bytes",
+           "kvq_paged_block_select_workspace_bytes", "kvq_block_select", "kvq_paged_block_select",
+           "kvq_sparse_attend_workspace_bytes", "kvq_paged_sparse_attend_workspace_bytes", "kvq_sparse_attend",
+           "kvq_paged_sparse_attend")
 ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "banded": 3, "yarn": 4}   # kvq_rope_scaling
 STATIC_SCRATCH_BYTES = 16 * 1024 * 1024   # KVQ_STATIC_SCRATCH_BYTES in include/kvq.h
 
@@ -84,6 +88,10 @@ class KvqRope(C.Structure):
 class KvqRows(C.Structure):
     _fields_ = [("data", C.c_void_p), ("batch_stride", C.c_int64), ("head_stride", C.c_int64),
                 ("token_stride", C.c_int64)]
+
+
+class KvqBlockBounds(C.Structure):
+    _fields_ = [("codes", C.c_void_p), ("scale", C.c_void_p)]
 
 
 class KvqError(RuntimeError):
@@ -149,6 +157,7 @@ def lib() -> C.CDLL:
     L.kvq_paged_append_decode_attend_host_workspace_bytes.restype = SZ
     L.kvq_paged_append_decode_attend_host.argtypes = L.kvq_paged_append_decode_attend.argtypes
     L.kvq_paged_append_decode_attend_host.restype = I32
+    bounds_p = C.POINTER(KvqBlockBounds)
     rope_p, rows_p, I64, F = C.POINTER(KvqRope), C.POINTER(KvqRows), C.c_int64, C.c_float
     for name, args in (
             ("kvq_rope_frequencies", [C.POINTER(KvqRopeConfig), P, C.POINTER(F)]),
@@ -162,9 +171,21 @@ def lib() -> C.CDLL:
             ("kvq_evict_compact", [cache_p, cache_p, P, I32, I32, P, I64, P, I64, P]),
             ("kvq_paged_evict_compact", [paged_p, P, I32, P, I32, P, I64, P]),
             ("kvq_page_plan", [I32, I32, I32, P, P, P, P, I32, P, I32, P, P, P, P, P, P, P]),
-            ("kvq_paged_store_slots", [paged_p, rows_p, rows_p, I32, I32, P, P])):
+            ("kvq_paged_store_slots", [paged_p, rows_p, rows_p, I32, I32, P, P]),
+            ("kvq_block_bounds_update", [cache_p, bounds_p, I32, I32, P]),
+            ("kvq_paged_block_bounds_update", [paged_p, bounds_p, P, I32, P]),
+            ("kvq_block_select", [cache_p, bounds_p, P, I32, I32, I32, I32, I32, I32, I32, I32, I32, P, P, SZ, P]),
+            ("kvq_paged_block_select", [paged_p, bounds_p, P, I32, I32, I32, P, I32, I32, I32, I32, I32, P, P, SZ, P]),
+            ("kvq_sparse_attend", [cache_p, P, I32, I32, I32, I32, I32, I32, F, P, I32, I32, P, P, SZ, P]),
+            ("kvq_paged_sparse_attend", [paged_p, P, I32, I32, I32, P, I32, I32, F, P, I32, I32, P, P, SZ, P])):
         f = getattr(L, name)
         f.argtypes, f.restype = args, I32
+    for name, args in (("kvq_block_select_workspace_bytes", [cache_p, I32, I32]),
+                       ("kvq_paged_block_select_workspace_bytes", [paged_p, I32, I32]),
+                       ("kvq_sparse_attend_workspace_bytes", [cache_p, I32, I32, I32, I32]),
+                       ("kvq_paged_sparse_attend_workspace_bytes", [paged_p, I32, I32, I32, I32])):
+        f = getattr(L, name)
+        f.argtypes, f.restype = args, SZ
     L.kvq_attend_weights_workspace_bytes.argtypes = [cache_p, I32, I32, I32, I32]
     L.kvq_attend_weights_workspace_bytes.restype = SZ
     L.kvq_paged_attend_weights_workspace_bytes.argtypes = [paged_p, I32, I32, I32, I32]

@@ -875,3 +875,139 @@ def paged_store_slots(cache: PagedKVCache, k_new: torch.Tensor, v_new: torch.Ten
     k, v = (_rows(name, t.transpose(0, 1).unsqueeze(0)) for name, t in (("k_new", k_new), ("v_new", v_new)))
     L.check(L.lib().kvq_paged_store_slots(C.byref(cache.struct), C.byref(k), C.byref(v), _DTYPES[dtype], shape[0],
                                           slots.data_ptr(), _stream_of(stream, dev)), "kvq_paged_store_slots")
+
+
+# ------------------------------------------------------------------ attention over selected blocks
+class BlockBounds:
+    """Bounds of a cache's keys per block of 64 tokens and kv head: codes int8 [B][H_kv][cap/64][2][D] (smallest, then
+    largest value of each channel) and scale f32 [B][H_kv][cap/64]; of a paged pool [n_pages][H_kv][page_size/64]..."""
+
+    def __init__(self, cache):
+        payload = cache.planes["k"]["payload"]
+        lead = payload.shape[:2] + ((payload.shape[2] + 63) // 64,)
+        self.codes = torch.zeros(lead + (2, cache.head_dim), dtype=torch.int8, device=payload.device)
+        self.scale = torch.zeros(lead, dtype=torch.float32, device=payload.device)
+        self.struct = L.KvqBlockBounds(self.codes.data_ptr(), self.scale.data_ptr())
+
+    def fits(self, cache) -> None:
+        shape = cache.planes["k"]["payload"].shape
+        if self.scale.shape != shape[:2] + ((shape[2] + 63) // 64,) or self.codes.shape[-1] != cache.head_dim:
+            raise ValueError("the bounds belong to a cache of another shape")
+
+
+def block_bounds(cache: KVCache, bounds: BlockBounds, first: int, kv_len: int, stream=None) -> None:
+    """Renew the bounds of every block that holds a token of [first, kv_len) (after an append at `first`)."""
+    bounds.fits(cache)
+    dev = _here(("cache", cache.planes["k"]["payload"]), ("bounds", bounds.codes))
+    L.check(L.lib().kvq_block_bounds_update(C.byref(cache.struct), C.byref(bounds.struct), first, kv_len, _stream_of(stream, dev)),
+            "kvq_block_bounds_update")
+
+
+def paged_block_bounds(cache: PagedKVCache, bounds: BlockBounds, seq_lens: torch.Tensor, n_fresh: int, stream=None) -> None:
+    """Renew the bounds of the blocks that hold each sequence's newest n_fresh tokens (seq_lens: the lengths with them)."""
+    bounds.fits(cache)
+    _ints("seq_lens", seq_lens, cache.batch)
+    dev = _here(("cache", cache.planes["k"]["payload"]), ("bounds", bounds.codes), ("seq_lens", seq_lens))
+    L.check(L.lib().kvq_paged_block_bounds_update(C.byref(cache.struct), C.byref(bounds.struct), seq_lens.data_ptr(), n_fresh,
+                                                  _stream_of(stream, dev)), "kvq_paged_block_bounds_update")
+
+
+def block_select_workspace_bytes(cache: KVCache, n_q: int, kv_len: int) -> int:
+    return L.lib().kvq_block_select_workspace_bytes(C.byref(cache.struct), n_q, kv_len)
+
+
+def paged_block_select_workspace_bytes(cache: PagedKVCache, n_q: int, max_kv_len: int) -> int:
+    return L.lib().kvq_paged_block_select_workspace_bytes(C.byref(cache.struct), n_q, max_kv_len)
+
+
+def sparse_attend_workspace_bytes(cache: KVCache, n_q_heads: int, n_q: int, n_sel: int, chunk: int = 0) -> int:
+    return L.lib().kvq_sparse_attend_workspace_bytes(C.byref(cache.struct), n_q_heads, n_q, n_sel, chunk)
+
+
+def paged_sparse_attend_workspace_bytes(cache: PagedKVCache, n_q_heads: int, n_q: int, n_sel: int, chunk: int = 0) -> int:
+    return L.lib().kvq_paged_sparse_attend_workspace_bytes(C.byref(cache.struct), n_q_heads, n_q, n_sel, chunk)
+
+
+def _blocks_call(cache, q, seq_lens, need, workspace, stream):
+    """The checks and the workspace that the calls below share."""
+    shape = q.shape
+    if len(shape) != 4 or shape[0] != cache.batch or shape[3] != cache.head_dim:
+        raise ValueError("q shape does not match the cache")
+    if q.dtype not in _DTYPES or not q.is_contiguous():
+        raise ValueError("q must be contiguous f32, bf16 or f16")
+    if seq_lens is not None:
+        _ints("seq_lens", seq_lens, cache.batch)
+    if workspace is None:
+        with _made_on(stream):
+            workspace = torch.empty(max(need(), 256), dtype=torch.uint8, device=q.device)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _select_call(fn, need, cache, bounds, q, seq_lens, lengths, n_sel, n_sink, n_recent, sel, workspace, stream):
+    bounds.fits(cache)
+    workspace, nbytes = _blocks_call(cache, q, seq_lens, need, workspace, stream)
+    shape = (cache.batch, cache.n_kv_heads, q.shape[2], max(n_sel, 1))
+    if sel is None:
+        sel = _output(stream, shape, torch.int32, q.device)
+    else:
+        _dense("sel", sel, torch.int32, shape)
+    dev = _here(("cache", cache.planes["k"]["payload"]), ("bounds", bounds.codes), ("q", q), ("seq_lens", seq_lens), ("sel", sel),
+                ("workspace", workspace))
+    L.check(getattr(L.lib(), fn)(C.byref(cache.struct), C.byref(bounds.struct), q.data_ptr(), _DTYPES[q.dtype], q.shape[1], q.shape[2],
+                                 *lengths, n_sel, n_sink, n_recent, sel.data_ptr(), workspace.data_ptr(), nbytes,
+                                 _stream_of(stream, dev)), fn)
+    return sel
+
+
+def block_select(cache: KVCache, bounds: BlockBounds, q: torch.Tensor, kv_len: int, n_sel: int, n_sink: int = 1, n_recent: int = 1,
+                 causal: bool = False, q_pos0: int = 0, sel: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                 stream=None) -> torch.Tensor:
+    """The n_sel blocks of 64 tokens for each query row and kv head, ascending (int32 [B][H_kv][n_q][n_sel]): the first n_sink, the
+    last n_recent that the row sees, and those whose bounds allow the largest scores, ties to the lowest index; -1 behind the
+    blocks of a row that sees fewer."""
+    return _select_call("kvq_block_select", lambda: block_select_workspace_bytes(cache, q.shape[2], kv_len), cache, bounds, q, None,
+                        (kv_len, 1 if causal else 0, q_pos0), n_sel, n_sink, n_recent, sel, workspace, stream)
+
+
+def paged_block_select(cache: PagedKVCache, bounds: BlockBounds, q: torch.Tensor, seq_lens: torch.Tensor, max_kv_len: int, n_sel: int,
+                       n_sink: int = 1, n_recent: int = 1, causal: bool = False, sel: torch.Tensor | None = None,
+                       workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """block_select over a paged pool, each sequence by its own length (causal rows are its newest n_q tokens)."""
+    return _select_call("kvq_paged_block_select", lambda: paged_block_select_workspace_bytes(cache, q.shape[2], max_kv_len), cache, bounds,
+                        q, seq_lens, (seq_lens.data_ptr(), max_kv_len, 1 if causal else 0), n_sel, n_sink, n_recent, sel, workspace, stream)
+
+
+def _sparse_call(fn, need, cache, q, sel, seq_lens, lengths, attn_scale, chunk, out, workspace, stream):
+    shape = q.shape
+    if sel.dtype is not torch.int32 or sel.dim() != 4 or len(shape) != 4 or sel.shape[:3] != (cache.batch, cache.n_kv_heads, shape[2]) or \
+            not sel.is_contiguous():
+        raise ValueError("sel must be contiguous int32 [batch][n_kv_heads][n_q][n_sel]")
+    workspace, nbytes = _blocks_call(cache, q, seq_lens, lambda: need(cache, shape[1], shape[2], sel.shape[3], chunk), workspace, stream)
+    if out is None:
+        out = _output(stream, shape, torch.float32, q.device)
+    else:
+        _dense("out", out, torch.float32, shape)
+    dev = _here(("cache", cache.planes["k"]["payload"]), ("q", q), ("sel", sel), ("seq_lens", seq_lens), ("out", out), ("workspace", workspace))
+    L.check(getattr(L.lib(), fn)(C.byref(cache.struct), q.data_ptr(), _DTYPES[q.dtype], shape[1], shape[2], *lengths,
+                                 1.0 / math.sqrt(shape[3]) if attn_scale is None else attn_scale, sel.data_ptr(), sel.shape[3], chunk,
+                                 out.data_ptr(), workspace.data_ptr(), nbytes, _stream_of(stream, dev)), fn)
+    return out
+
+
+def sparse_attend(cache: KVCache, q: torch.Tensor, sel: torch.Tensor, kv_len: int, causal: bool = False, q_pos0: int = 0,
+                  attn_scale: float | None = None, chunk: int = 0, out: torch.Tensor | None = None,
+                  workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """decode_attend in which each query row sees only the blocks of 64 tokens in its list sel [B][H_kv][n_q][n_sel] (block_select's,
+    or any ascending one) -> f32 out [B][H_q][n_q][D]."""
+    return _sparse_call("kvq_sparse_attend", sparse_attend_workspace_bytes, cache, q, sel, None, (kv_len, 1 if causal else 0, q_pos0),
+                        attn_scale, chunk, out, workspace, stream)
+
+
+def paged_sparse_attend(cache: PagedKVCache, q: torch.Tensor, sel: torch.Tensor, seq_lens: torch.Tensor, max_kv_len: int,
+                        causal: bool = False, attn_scale: float | None = None, chunk: int = 0, out: torch.Tensor | None = None,
+                        workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """sparse_attend over a paged pool, each sequence by its own length."""
+    return _sparse_call("kvq_paged_sparse_attend", paged_sparse_attend_workspace_bytes, cache, q, sel, seq_lens,
+                        (seq_lens.data_ptr(), max_kv_len, 1 if causal else 0), attn_scale, chunk, out, workspace, stream)

@@ -294,6 +294,7 @@ kvq_status resolve_core(int n_q_heads, int n_q, int kv_len, int causal, int q_po
   a.lse = nullptr;
   a.part_s = nullptr;
   a.s_rows = a.s_tokens = 0;
+  a.out_nq = 1;
   const size_t rows = (size_t)c.B * n_q_heads * n_q;
   size_t off = 0;
   const size_t o_m = off; off = round_up(off + rows * a.C * sizeof(float), 256);
@@ -1369,6 +1370,252 @@ kvq_status kvq_paged_store_slots(const kvq_paged_cache *cache, const kvq_rows *k
   const cudaError_t e = kvq::launch_store_slots(v, g, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(KVQ_ECUDA, "store launch: %s", cudaGetErrorString(e));
   return KVQ_OK;
+}
+
+// ------------------------------------------------------------------ attention over selected blocks
+namespace {
+
+// What the calls over blocks ask of a checked cache view: whole blocks, one basis, grids that hold every list.
+kvq_status check_blocks(const kvq::CacheView &v, int n_q_heads, int n_q) {
+  if (v.n_recent > 0) return fail(KVQ_EUNSUPPORTED, "blocks of a cache with a recent window are not provided");
+  if (v.page_shift < 0 && v.cap % 64) return fail(KVQ_ESHAPE, "capacity %d not a multiple of 64", v.cap);
+  if (n_q_heads < 1 || n_q < 1) return fail(KVQ_EINVAL, "n_q_heads and n_q must be >= 1");
+  if (n_q_heads % v.H) return fail(KVQ_ESHAPE, "n_q_heads %d not a multiple of n_kv_heads %d", n_q_heads, v.H);
+  if ((long long)v.B * v.H * n_q > 65535) return fail(KVQ_ESHAPE, "batch * n_kv_heads * n_q > 65535");
+  const long long rows = v.page_shift < 0 ? (long long)v.B * v.H * v.cap : ((long long)v.n_pages * v.H) << v.page_shift;
+  if (rows / 64 > INT_MAX) return fail(KVQ_ESHAPE, "more than INT_MAX blocks");
+  return KVQ_OK;
+}
+
+kvq_status check_lengths(const kvq::CacheView &v, int n_q, const int32_t *seq_lens, int kv_len, int causal, int q_pos0) {
+  const bool paged = v.page_shift >= 0;
+  if (paged && !seq_lens) return fail(KVQ_EINVAL, "seq_lens is NULL");
+  if (!aligned(seq_lens, 16)) return fail(KVQ_EALIGN, "seq_lens not 16-byte aligned");
+  if (kv_len < 1) return fail(KVQ_EINVAL, "kv_len must be >= 1");
+  if (kv_len > v.cap) return fail(KVQ_ECAPACITY, "kv_len %d > capacity %d", kv_len, v.cap);
+  if (!paged && causal && (q_pos0 < 0 || (long long)q_pos0 + n_q > kv_len))
+    return fail(KVQ_EINVAL, "causal call needs 0 <= q_pos0 and q_pos0 + n_q <= kv_len");
+  return KVQ_OK;
+}
+
+kvq_status check_bounds(const kvq_block_bounds *bounds) {
+  if (!bounds || !bounds->codes || !bounds->scale) return fail(KVQ_EINVAL, "bounds or one of its planes is NULL");
+  if (!aligned(bounds->codes, 16) || !aligned(bounds->scale, 16)) return fail(KVQ_EALIGN, "bounds not 16-byte aligned");
+  return KVQ_OK;
+}
+
+kvq_status run_bounds(const kvq::CacheView &v, const kvq_block_bounds *bounds, int first, int kv_len, int n_fresh,
+                      const int32_t *seq_lens, kvq_stream_t stream) {
+  kvq_status st = check_blocks(v, v.H, 1);
+  if (st == KVQ_OK) st = check_bounds(bounds);
+  if (st != KVQ_OK) return st;
+  const kvq::BoundsArgs a = {v, bounds->codes, bounds->scale, first, kv_len, n_fresh, seq_lens};
+  const cudaError_t e = kvq::launch_block_bounds(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(KVQ_ECUDA, "block bounds launch: %s", cudaGetErrorString(e));
+  return KVQ_OK;
+}
+
+// Workspace of a selection: the blocks' scores, then the number of blocks that each list sees.
+struct SelectSpace {
+  long long stride;
+  size_t counts, total;
+};
+SelectSpace select_space(const kvq::CacheView &v, int n_q, int kv_len) {
+  SelectSpace w;
+  const size_t lists = (size_t)v.B * v.H * n_q;
+  w.stride = (((long long)kv_len + 63) / 64 + 3) / 4 * 4;
+  w.counts = round_up(lists * w.stride * sizeof(float), 256);
+  w.total = w.counts + round_up(lists * sizeof(int32_t), 256);
+  return w;
+}
+
+kvq_status run_block_select(const kvq::CacheView &v, const kvq_block_bounds *bounds, const void *q, int q_dtype, int n_q_heads,
+                            int n_q, const int32_t *seq_lens, int kv_len, int causal, int q_pos0, int n_sel, int n_sink,
+                            int n_recent, int32_t *sel, void *workspace, size_t workspace_bytes, kvq_stream_t stream) {
+  kvq_status st = check_blocks(v, n_q_heads, n_q);
+  if (st == KVQ_OK) st = check_lengths(v, n_q, seq_lens, kv_len, causal, q_pos0);
+  if (st == KVQ_OK) st = check_bounds(bounds);
+  if (st != KVQ_OK) return st;
+  if (q_dtype < KVQ_F32 || q_dtype > KVQ_F16) return fail(KVQ_EINVAL, "unknown q dtype %d", q_dtype);
+  if (!q || !sel || !workspace) return fail(KVQ_EINVAL, "q/sel/workspace is NULL");
+  if (!aligned(q, 16) || !aligned(sel, 16)) return fail(KVQ_EALIGN, "q/sel not 16-byte aligned");
+  if (!aligned(workspace, 256)) return fail(KVQ_EALIGN, "workspace not 256-byte aligned");
+  if (n_sel < 1) return fail(KVQ_EINVAL, "n_sel must be >= 1");
+  if (n_sink < 0 || n_recent < 0 || (long long)n_sink + n_recent > n_sel)
+    return fail(KVQ_EINVAL, "n_sink and n_recent must be >= 0 and together at most n_sel");
+  const SelectSpace w = select_space(v, n_q, kv_len);
+  if (workspace_bytes < w.total) return fail(KVQ_EWORKSPACE, "workspace %zu < required %zu", workspace_bytes, w.total);
+  char *ws = static_cast<char *>(workspace);
+  const kvq::BlockSelectArgs a = {v, bounds->codes, bounds->scale, q, q_dtype, n_q_heads / v.H, n_q, kv_len, causal ? 1 : 0,
+                                  q_pos0, kvq::is_hadamard(v.layout) ? 1 : 0, seq_lens, n_sel, n_sink, n_recent, w.stride,
+                                  reinterpret_cast<float *>(ws), reinterpret_cast<int32_t *>(ws + w.counts), sel};
+  const cudaError_t e = kvq::launch_block_select(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(KVQ_ECUDA, "block select launch: %s", cudaGetErrorString(e));
+  return KVQ_OK;
+}
+
+// The cache as a pool of pages of 64 tokens of one head, read by one sequence per list.
+kvq::CacheView list_view(const kvq::CacheView &v, int n_q, int n_sel) {
+  kvq::CacheView c = v;
+  const long long rows = v.page_shift < 0 ? (long long)v.B * v.H * v.cap : ((long long)v.n_pages * v.H) << v.page_shift;
+  c.B = v.B * v.H * n_q;
+  c.H = 1;
+  c.cap = n_sel * 64;
+  c.page_shift = 6;
+  c.table_stride = n_sel;
+  c.n_pages = (int)(rows / 64);
+  return c;
+}
+
+// The attention's arguments and workspace (its own, then the tables, the lengths and the queries by list).
+struct SparseSpace {
+  size_t table, lens, queries, total;
+};
+kvq_status resolve_sparse(const kvq::CacheView &v, int n_q_heads, int n_q, int n_sel, int chunk, kvq::AttendArgs &a, SparseSpace &w,
+                          void *ws) {
+  if (n_sel < 1 || n_sel > INT_MAX / 64) return fail(KVQ_EINVAL, "n_sel %d not in [1, 2^25)", n_sel);
+  a.cache = list_view(v, n_q, n_sel);
+  size_t need = 0;
+  const kvq_status st = resolve_core(n_q_heads / v.H, 1, n_sel * 64, 0, 0, true, chunk, a, need, ws);
+  if (st != KVQ_OK) return st;
+  const size_t lists = (size_t)a.cache.B;
+  w.table = round_up(need, 256);
+  w.lens = w.table + round_up(lists * n_sel * sizeof(int32_t), 256);
+  w.queries = w.lens + round_up(lists * sizeof(int32_t), 256);
+  w.total = w.queries + (n_q > 1 ? lists * (n_q_heads / v.H) * v.D * sizeof(float) : 0);
+  return KVQ_OK;
+}
+
+kvq_status run_sparse(const kvq::CacheView &v, const void *q, int q_dtype, int n_q_heads, int n_q, const int32_t *seq_lens,
+                      int kv_len, int causal, int q_pos0, float attn_scale, const int32_t *sel, int n_sel, int chunk, float *out,
+                      void *workspace, size_t workspace_bytes, kvq_stream_t stream) {
+  kvq::AttendArgs a;
+  SparseSpace w;
+  kvq_status st = check_blocks(v, n_q_heads, n_q);
+  if (st == KVQ_OK) st = check_lengths(v, n_q, seq_lens, kv_len, causal, q_pos0);
+  if (st == KVQ_OK) st = resolve_sparse(v, n_q_heads, n_q, n_sel, chunk, a, w, nullptr);
+  if (st == KVQ_OK) st = check_call(w.total, q, q_dtype, attn_scale, out, workspace, workspace_bytes);
+  if (st != KVQ_OK) return st;
+  if (!sel) return fail(KVQ_EINVAL, "sel is NULL");
+  if (!aligned(sel, 16)) return fail(KVQ_EALIGN, "sel not 16-byte aligned");
+  resolve_sparse(v, n_q_heads, n_q, n_sel, chunk, a, w, workspace);
+  char *ws = static_cast<char *>(workspace);
+  const kvq::SparseArgs p = {v, q, reinterpret_cast<uint4 *>(ws + w.queries), q_dtype, n_q_heads / v.H, n_q, kv_len,
+                             causal ? 1 : 0, q_pos0, seq_lens, sel, n_sel, reinterpret_cast<int32_t *>(ws + w.table),
+                             reinterpret_cast<int32_t *>(ws + w.lens)};
+  a.cache.table = p.table;
+  a.seq_lens = p.lens;
+  a.q = n_q > 1 ? static_cast<const void *>(ws + w.queries) : q;
+  a.q_dtype = q_dtype;
+  a.scale = attn_scale;
+  a.out = out;
+  a.out_nq = n_q;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = kvq::launch_sparse_prepare(p, s);
+  if (e == cudaSuccess) e = launch_attend_sequence(a, s, false);
+  if (e != cudaSuccess) return fail(KVQ_ECUDA, "sparse attend launch: %s", cudaGetErrorString(e));
+  return KVQ_OK;
+}
+
+}  // namespace
+
+kvq_status kvq_block_bounds_update(const kvq_cache *cache, const kvq_block_bounds *bounds, int32_t first, int32_t kv_len,
+                                   kvq_stream_t stream) {
+  g_last_error[0] = 0;
+  kvq::CacheView v;
+  const kvq_status st = check_cache(cache, v);
+  if (st != KVQ_OK) return st;
+  if (first < 0 || kv_len < first) return fail(KVQ_EINVAL, "0 <= first <= kv_len is needed");
+  if (kv_len > v.cap) return fail(KVQ_ECAPACITY, "kv_len %d > capacity %d", kv_len, v.cap);
+  if (kv_len == first) return KVQ_OK;
+  return run_bounds(v, bounds, first, kv_len, 0, nullptr, stream);
+}
+
+kvq_status kvq_paged_block_bounds_update(const kvq_paged_cache *cache, const kvq_block_bounds *bounds, const int32_t *seq_lens,
+                                         int32_t n_fresh, kvq_stream_t stream) {
+  g_last_error[0] = 0;
+  kvq::CacheView v;
+  const kvq_status st = check_paged_cache(cache, v);
+  if (st != KVQ_OK) return st;
+  if (n_fresh < 0) return fail(KVQ_EINVAL, "n_fresh must be >= 0");
+  if (n_fresh == 0) return KVQ_OK;
+  if (!seq_lens) return fail(KVQ_EINVAL, "seq_lens is NULL");
+  if (!aligned(seq_lens, 16)) return fail(KVQ_EALIGN, "seq_lens not 16-byte aligned");
+  return run_bounds(v, bounds, 0, v.cap, n_fresh, seq_lens, stream);
+}
+
+size_t kvq_block_select_workspace_bytes(const kvq_cache *cache, int32_t n_q, int32_t kv_len) {
+  kvq::CacheView v;
+  if (check_cache(cache, v) != KVQ_OK || check_blocks(v, v.H, n_q) != KVQ_OK || kv_len < 1 || kv_len > v.cap) return 0;
+  return select_space(v, n_q, kv_len).total;
+}
+size_t kvq_paged_block_select_workspace_bytes(const kvq_paged_cache *cache, int32_t n_q, int32_t max_kv_len) {
+  kvq::CacheView v;
+  if (check_paged_cache(cache, v) != KVQ_OK || check_blocks(v, v.H, n_q) != KVQ_OK || max_kv_len < 1 || max_kv_len > v.cap) return 0;
+  return select_space(v, n_q, max_kv_len).total;
+}
+
+kvq_status kvq_block_select(const kvq_cache *cache, const kvq_block_bounds *bounds, const void *q, int32_t q_dtype,
+                            int32_t n_q_heads, int32_t n_q, int32_t kv_len, int32_t causal, int32_t q_pos0, int32_t n_sel,
+                            int32_t n_sink, int32_t n_recent, int32_t *sel, void *workspace, size_t workspace_bytes,
+                            kvq_stream_t stream) {
+  g_last_error[0] = 0;
+  kvq::CacheView v;
+  const kvq_status st = check_cache(cache, v);
+  if (st != KVQ_OK) return st;
+  return run_block_select(v, bounds, q, q_dtype, n_q_heads, n_q, nullptr, kv_len, causal, q_pos0, n_sel, n_sink, n_recent, sel,
+                          workspace, workspace_bytes, stream);
+}
+kvq_status kvq_paged_block_select(const kvq_paged_cache *cache, const kvq_block_bounds *bounds, const void *q, int32_t q_dtype,
+                                  int32_t n_q_heads, int32_t n_q, const int32_t *seq_lens, int32_t max_kv_len, int32_t causal,
+                                  int32_t n_sel, int32_t n_sink, int32_t n_recent, int32_t *sel, void *workspace,
+                                  size_t workspace_bytes, kvq_stream_t stream) {
+  g_last_error[0] = 0;
+  kvq::CacheView v;
+  const kvq_status st = check_paged_cache(cache, v);
+  if (st != KVQ_OK) return st;
+  return run_block_select(v, bounds, q, q_dtype, n_q_heads, n_q, seq_lens, max_kv_len, causal, 0, n_sel, n_sink, n_recent, sel,
+                          workspace, workspace_bytes, stream);
+}
+
+size_t kvq_sparse_attend_workspace_bytes(const kvq_cache *cache, int32_t n_q_heads, int32_t n_q, int32_t n_sel, int32_t chunk) {
+  kvq::CacheView v;
+  kvq::AttendArgs a;
+  SparseSpace w;
+  if (check_cache(cache, v) != KVQ_OK || check_blocks(v, n_q_heads, n_q) != KVQ_OK ||
+      resolve_sparse(v, n_q_heads, n_q, n_sel, chunk, a, w, nullptr) != KVQ_OK) return 0;
+  return w.total;
+}
+size_t kvq_paged_sparse_attend_workspace_bytes(const kvq_paged_cache *cache, int32_t n_q_heads, int32_t n_q, int32_t n_sel,
+                                               int32_t chunk) {
+  kvq::CacheView v;
+  kvq::AttendArgs a;
+  SparseSpace w;
+  if (check_paged_cache(cache, v) != KVQ_OK || check_blocks(v, n_q_heads, n_q) != KVQ_OK ||
+      resolve_sparse(v, n_q_heads, n_q, n_sel, chunk, a, w, nullptr) != KVQ_OK) return 0;
+  return w.total;
+}
+
+kvq_status kvq_sparse_attend(const kvq_cache *cache, const void *q, int32_t q_dtype, int32_t n_q_heads, int32_t n_q, int32_t kv_len,
+                             int32_t causal, int32_t q_pos0, float attn_scale, const int32_t *sel, int32_t n_sel, int32_t chunk,
+                             float *out, void *workspace, size_t workspace_bytes, kvq_stream_t stream) {
+  g_last_error[0] = 0;
+  kvq::CacheView v;
+  const kvq_status st = check_cache(cache, v);
+  if (st != KVQ_OK) return st;
+  return run_sparse(v, q, q_dtype, n_q_heads, n_q, nullptr, kv_len, causal, q_pos0, attn_scale, sel, n_sel, chunk, out, workspace,
+                    workspace_bytes, stream);
+}
+kvq_status kvq_paged_sparse_attend(const kvq_paged_cache *cache, const void *q, int32_t q_dtype, int32_t n_q_heads, int32_t n_q,
+                                   const int32_t *seq_lens, int32_t max_kv_len, int32_t causal, float attn_scale,
+                                   const int32_t *sel, int32_t n_sel, int32_t chunk, float *out, void *workspace,
+                                   size_t workspace_bytes, kvq_stream_t stream) {
+  g_last_error[0] = 0;
+  kvq::CacheView v;
+  const kvq_status st = check_paged_cache(cache, v);
+  if (st != KVQ_OK) return st;
+  return run_sparse(v, q, q_dtype, n_q_heads, n_q, seq_lens, max_kv_len, causal, 0, attn_scale, sel, n_sel, chunk, out, workspace,
+                    workspace_bytes, stream);
 }
 
 // ------------------------------------------------------------------ host-buffer calls

@@ -180,7 +180,16 @@ struct AttendArgs {
   // written by the decode kernels when not nullptr; tokens no row sees are left out
   float *part_s;
   int s_rows, s_tokens;
+  // > 1: the call's sequences are (sequence, kv head, query) triples of out_nq queries each, whose outputs go to
+  // [B][Hq][out_nq][D]
+  int out_nq;
 };
+// Output row of query row `row` of the call.
+__device__ __forceinline__ size_t out_row(const AttendArgs &a, size_t row) {
+  if (a.out_nq <= 1) return row;
+  const size_t vb = row / a.gqa, bh = vb / a.out_nq;
+  return (bh * a.gqa + (row - vb * a.gqa)) * a.out_nq + (vb - bh * a.out_nq);
+}
 // Rows per token of the scores a call's phase 1 can leave behind (0: the kernel it runs on has none).
 // Up to eight query rows on the tensor-core decode kernels.
 __host__ __device__ constexpr int score_rows(int kl, int vl, int D, int rows) {
@@ -280,6 +289,42 @@ struct SelectArgs {
   int32_t *keep, *new_lens;
 };
 cudaError_t launch_evict_select(const SelectArgs &a, cudaStream_t st);
+// Bounds of each channel over the tokens of a block of 64, of the keys: codes [blocks of the plane][2][D], scale [blocks]. Blocks
+// that hold tokens [first, kv_len), or (seq_lens [B] on the device, clamped into [0, kv_len]) each sequence's newest n_fresh.
+struct BoundsArgs {
+  CacheView cache;
+  int8_t *codes;
+  float *scale;
+  int first, kv_len, n_fresh;
+  const int32_t *seq_lens;
+};
+cudaError_t launch_block_bounds(const BoundsArgs &a, cudaStream_t st);
+// The blocks selected for each (sequence, kv head, query): sel [B][H][n_q][n_sel]; scores [lists][stride] and counts [lists] are
+// workspace.
+struct BlockSelectArgs {
+  CacheView cache;
+  const int8_t *codes;
+  const float *scale;
+  const void *q;
+  int q_dtype, gqa, n_q, kv_len, causal, q_pos0, rotated;
+  const int32_t *seq_lens;
+  int n_sel, n_sink, n_recent;
+  long long stride;
+  float *scores;
+  int32_t *counts, *sel;
+};
+cudaError_t launch_block_select(const BlockSelectArgs &a, cudaStream_t st);
+// Lists -> the tables [lists][n_sel] and lengths [lists] of sequences of one kv head, and (n_q > 1) the queries by list.
+struct SparseArgs {
+  CacheView cache;
+  const void *q;
+  uint4 *q_out;
+  int q_dtype, gqa, n_q, kv_len, causal, q_pos0;
+  const int32_t *seq_lens, *sel;
+  int n_sel;
+  int32_t *table, *lens;
+};
+cudaError_t launch_sparse_prepare(const SparseArgs &a, cudaStream_t st);
 // Compaction of src into dst (in place: the same view twice); the scores [B][H][stride] may be nullptr.
 struct CompactArgs {
   CacheView src, dst;

@@ -211,9 +211,9 @@ __global__ void __launch_bounds__(kWarps * 32) attend_reduce_kernel(AttendArgs a
     warp_fwht<VPL>(x, lane);
     const float cD = inv_sqrt_dim(D);
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) a.out[row * D + lane * VPL + i] = x[i] * cD;
+    for (int i = 0; i < VPL; ++i) a.out[out_row(a, row) * D + lane * VPL + i] = x[i] * cD;
   } else {
-    a.out[row * D + d0 + lane] = x[0];
+    a.out[out_row(a, row) * D + d0 + lane] = x[0];
   }
 }
 
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(kWarps * 32, KB >= 8 ? 1 : (D == 128 ? 8 - KB 
 #pragma unroll
     for (int i = 0; i < VPL; ++i) O[i] *= cD;
   }
-  float *out = a.out + row * D + lane * VPL;
+  float *out = a.out + out_row(a, row) * D + lane * VPL;
   if constexpr (VPL == 4) {
     *reinterpret_cast<float4 *>(out) = make_float4(O[0], O[1], O[2], O[3]);
   } else {

@@ -84,3 +84,27 @@ def test_attend_sees_blocks_and_rows():
     assert np.allclose(one[0, 0, 0], p @ v[64:128] / p.sum(), rtol=1e-12)
     none, _ = OV.attend(values, 1, q, 0.3, [0], False)
     assert not none.any()
+
+
+def test_bounds_and_selection_pins():
+    rows = np.array([[1.0, -2.0], [3.0, 0.5], [-0.1, 0.0]], np.float32)
+    codes, scale = OV.bounds(rows)
+    s = np.float32(3) / np.float32(127)
+    assert scale.tolist() == [s] and codes.tolist() == [[[-5, -85], [127, 22]]]     # -0.1 / s = -4.2, -2 / s = -84.7, 0.5 / s = 21.2
+    assert OV.bounds(np.zeros((65, 2), np.float32))[1].tolist() == [0.0, 0.0]
+    rng = np.random.default_rng(0)
+    k, q = rng.standard_normal((64 * 9, 16)).astype(np.float32), rng.standard_normal((3, 1, 16)).astype(np.float32)
+    codes, scale = OV.bounds(k)
+    for blk in range(9):                                   # no product of a block passes its score
+        for x in q[:, 0]:
+            sq = np.abs(x).max() / 127
+            q8 = np.rint(x / sq)
+            top = np.maximum(q8 * codes[blk, 0].astype(float), q8 * codes[blk, 1].astype(float)).sum() * sq * scale[blk]
+            assert (k[blk * 64:blk * 64 + 64] @ (q8 * sq)).max() <= top + 1e-5
+    one = np.zeros((9, 2, 16), np.int8)
+    one[3, 1], one[5, 1], one[7, 0] = 100, 100, -100
+    x = np.ones((1, 2, 16), np.float32)
+    x[:, 1] = -1
+    got = OV.select(one, np.ones(9, np.float32), x, [64 * 9 - 1, 64 * 8 - 1], 3, 1, 1)
+    assert got.tolist() == [[0, 3, 8], [0, 1, 7]]          # ties to the lowest; the recent block counts by itself
+    assert OV.select(one, np.ones(9, np.float32), x, [-1, 100], 4, 0, 0).tolist() == [[-1] * 4, [0, 1, -1, -1]]

@@ -114,3 +114,70 @@ def test_block_layout_sizes_and_refusals(L, layout):
     for name in ("kvq_store_q8_0", "kvq_store_q4_0"):
         assert getattr(L, name)(p(c), 16, 16, 1, 1, 0, None) == EUNSUPPORTED
     assert KvqCache is not None
+
+
+def _bounds(codes=P, scale=P):
+    from sub_byte_quantized_gb300._lib import KvqBlockBounds
+    return KvqBlockBounds(codes, scale)
+
+
+BIG = 1 << 40
+
+
+def _sel(L, paged=False, cache=None, bounds=None, q=P, qdt=1, hq=2, nq=1, lens=P, kv=60, causal=0, q0=0, n=4, sink=1, recent=1, sel=P, ws=P, wsb=BIG):
+    c = cache if cache is not None else (_paged() if paged else _cache())
+    b = C.byref(bounds if bounds is not None else _bounds())
+    if paged:
+        return L.kvq_paged_block_select(C.byref(c), b, q, qdt, hq, nq, lens, kv, causal, n, sink, recent, sel, ws, wsb, None)
+    return L.kvq_block_select(C.byref(c), b, q, qdt, hq, nq, kv, causal, q0, n, sink, recent, sel, ws, wsb, None)
+
+
+def _sparse(L, paged=False, cache=None, q=P, qdt=1, hq=2, nq=1, lens=P, kv=60, causal=0, q0=0, scale=0.1, sel=P, n=4, chunk=0, out=P, ws=P, wsb=BIG):
+    c = cache if cache is not None else (_paged() if paged else _cache())
+    if paged:
+        return L.kvq_paged_sparse_attend(C.byref(c), q, qdt, hq, nq, lens, kv, causal, scale, sel, n, chunk, out, ws, wsb, None)
+    return L.kvq_sparse_attend(C.byref(c), q, qdt, hq, nq, kv, causal, q0, scale, sel, n, chunk, out, ws, wsb, None)
+
+
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("f", [_sel, _sparse])
+def test_block_calls_refusals(L, f, paged):
+    call = lambda **kw: f(L, paged, **kw)                                          # noqa: E731
+    assert call(q=None) == EINVAL and call(sel=None) == EINVAL and call(ws=None) == EINVAL
+    assert call(q=P + 4) == EALIGN and call(sel=P + 4) == EALIGN and call(ws=P + 16) == EALIGN
+    assert call(qdt=3) == EINVAL and call(hq=0) == EINVAL and call(nq=0) == EINVAL and call(hq=3) == ESHAPE
+    assert call(n=0) == EINVAL and call(kv=0) == EINVAL and call(kv=65 if not paged else 257) == ECAPACITY
+    assert call(nq=40000) == ESHAPE                                                # batch * heads * n_q
+    assert call(wsb=0) == EWORKSPACE
+    cache = _paged if paged else _cache
+    assert call(cache=cache(2, n_recent=32)) == EUNSUPPORTED
+    if paged:
+        assert call(lens=None) == EINVAL and call(lens=P + 4) == EALIGN
+    else:
+        assert call(causal=1, q0=60) == EINVAL and call(causal=1, q0=-1) == EINVAL and call(cache=_cache(cap=100)) == ESHAPE
+    if f is _sel:
+        assert call(sink=-1) == EINVAL and call(recent=-1) == EINVAL and call(sink=3, recent=2) == EINVAL and call(sink=2 ** 31 - 1, recent=2 ** 31 - 1) == EINVAL
+        assert call(bounds=_bounds(None)) == EINVAL and call(bounds=_bounds(P, None)) == EINVAL and call(bounds=_bounds(P + 8)) == EALIGN
+    else:
+        assert call(scale=float("nan")) == EINVAL and call(chunk=100) == ESHAPE and call(out=None) == EINVAL and call(n=1 << 25) == EINVAL
+
+
+def test_block_workspaces(L):
+    c, pg = _cache(cap=640), _paged(pages=10)
+    assert L.kvq_block_select_workspace_bytes(C.byref(c), 2, 640) > 0 and L.kvq_paged_block_select_workspace_bytes(C.byref(pg), 2, 640) > 0
+    assert L.kvq_block_select_workspace_bytes(C.byref(c), 2, 641) == 0 and L.kvq_block_select_workspace_bytes(None, 2, 64) == 0
+    need = L.kvq_sparse_attend_workspace_bytes(C.byref(c), 4, 3, 5, 64)
+    assert need > 0 and L.kvq_sparse_attend_workspace_bytes(C.byref(c), 3, 3, 5, 64) == 0
+    assert _sparse(L, cache=c, hq=4, nq=3, n=5, chunk=64, kv=640, wsb=need - 1) == EWORKSPACE
+    assert L.kvq_paged_sparse_attend_workspace_bytes(C.byref(pg), 4, 3, 5, 64) == need
+    assert L.kvq_sparse_attend_workspace_bytes(C.byref(_cache(cap=100)), 4, 3, 5, 64) == 0
+
+
+def test_bounds_refusals(L):
+    c, pg, b = _cache(), _paged(), _bounds()
+    f = lambda first=0, kv=60, cache=c, bounds=b: L.kvq_block_bounds_update(C.byref(cache), C.byref(bounds), first, kv, None)     # noqa: E731
+    assert f(60, 60) == 0 and f(-1) == EINVAL and f(61) == EINVAL and f(kv=65) == ECAPACITY
+    assert f(bounds=_bounds(None)) == EINVAL and f(bounds=_bounds(P, P + 4)) == EALIGN and f(cache=_cache(cap=100)) == ESHAPE
+    assert f(cache=_cache(5, n_recent=16)) == EUNSUPPORTED
+    g = lambda lens=P, n=3, bounds=b: L.kvq_paged_block_bounds_update(C.byref(pg), C.byref(bounds), lens, n, None)                # noqa: E731
+    assert g(n=0) == 0 and g(n=-1) == EINVAL and g(lens=None) == EINVAL and g(lens=P + 4) == EALIGN and g(bounds=_bounds(P, None)) == EINVAL
