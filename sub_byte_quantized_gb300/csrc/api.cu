@@ -196,7 +196,7 @@ int auto_chunk(const kvq::CacheView &c, int rows, int n_body, int n_heads, long 
   if (!total_given) work = (long long)(n_body > 0 ? n_body : 1) * n_heads;
   long long chunk;
   if (kvq::is_b64(c.layout)) {
-    // one chunk per resident CTA; each group of eight query rows has its own CTAs
+    // every resident CTA takes as many tokens; each group of eight query rows counts
     const long long ctas = (long long)sms * kvq::kB64CtasPerSm(c.D), groups = (rows + 7) / 8;
     chunk = ((work * groups + ctas - 1) / ctas + 63) / 64 * 64;
   } else if (c.layout == KVQ_Q6_0 && kvq::mma_q6_shape(c.D, rows) && !kvq::prefill_shape(c.layout, c.v_layout, c.D, rows)) {
@@ -253,6 +253,37 @@ int auto_chunk(const kvq::CacheView &c, int rows, int n_body, int n_heads, long 
   return (int)chunk;
 }
 
+// The block layouts' part of resolve_core: phase 1's CTAs (`chunk` 0: one wave, among which the call's units are dealt out on
+// the device; else one for each piece of at most chunk tokens of every head) and the workspace of their partials.
+kvq_status resolve_b64(kvq::AttendArgs &a, int chunk, size_t &need, void *ws) {
+  const kvq::CacheView &c = a.cache;
+  int dev = 0, sms = 148;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const long long heads = (long long)c.B * c.H * ((a.gqa * (long long)a.n_q + 7) / 8);
+  const long long units = heads * (((long long)a.kv_len + 63) / 64);
+  a.per = chunk / 64;
+  const long long grid = chunk ? heads * ((((long long)a.kv_len + 63) / 64 + a.per - 1) / a.per) : std::min((long long)sms * kvq::kB64CtasPerSm(c.D), units);
+  if (grid + heads > INT_MAX / 8) return fail(KVQ_ESHAPE, "too many rows and chunks for one call");
+  a.grid = (int)grid;
+  const size_t parts = (size_t)(grid + heads);
+  size_t off = 0;
+  const size_t o_m = off; off = round_up(off + parts * 8 * sizeof(float), 256);
+  const size_t o_l = off; off = round_up(off + parts * 8 * sizeof(float), 256);
+  const size_t o_s = off; off = round_up(off + (size_t)heads * sizeof(int2), 256);
+  const size_t o_o = off; off = round_up(off + parts * 8 * c.D * sizeof(float), 256);
+  need = off;
+  if (ws) {
+    char *w = static_cast<char *>(ws);
+    a.part_m = reinterpret_cast<float *>(w + o_m);
+    a.part_l = reinterpret_cast<float *>(w + o_l);
+    a.spans = reinterpret_cast<int2 *>(w + o_s);
+    a.part_o = reinterpret_cast<float *>(w + o_o);
+    a.q8 = nullptr;
+    a.s_q = a.q_rot = nullptr;
+  }
+  return KVQ_OK;
+}
+
 // Resolve the attention arguments and the workspace layout for a checked cache view `a.cache`
 // (kv_len: the call's length, or the largest per-sequence length of a paged call). When `ws` is
 // NULL only sizes are computed (returned through `need`).
@@ -265,6 +296,7 @@ kvq_status resolve_core(int n_q_heads, int n_q, int kv_len, int causal, int q_po
   if (kv_len > c.cap) return fail(KVQ_ECAPACITY, "kv_len %d > capacity %d", kv_len, c.cap);
   if (!paged && causal && (q_pos0 < 0 || (long long)q_pos0 + n_q > kv_len))
     return fail(KVQ_EINVAL, "causal call needs 0 <= q_pos0 and q_pos0 + n_q <= kv_len");
+  const int given = chunk;
   if (chunk == 0)
   {
     const int n_win = kvq::is_hadamard(c.layout) ? (c.n_recent < kv_len ? c.n_recent : kv_len) : 0;
@@ -295,6 +327,9 @@ kvq_status resolve_core(int n_q_heads, int n_q, int kv_len, int causal, int q_po
   a.part_s = nullptr;
   a.s_rows = a.s_tokens = 0;
   a.out_nq = 1;
+  a.grid = a.per = 0;
+  a.spans = nullptr;
+  if (kvq::is_b64(c.layout)) return resolve_b64(a, given, need, ws);
   const size_t rows = (size_t)c.B * n_q_heads * n_q;
   size_t off = 0;
   const size_t o_m = off; off = round_up(off + rows * a.C * sizeof(float), 256);
@@ -463,7 +498,7 @@ cudaError_t launch_attend_sequence(kvq::AttendArgs &a, cudaStream_t s, bool even
   if (e == cudaSuccess && prof) e = cudaEventRecordWithFlags(g_ev_begin, s, rec_flags);
   if (e == cudaSuccess) e = b64 ? kvq::launch_attend_b64(a, s) : mma ? kvq::launch_attend_mma(a, s) : kvq::launch_attend_generic(a, s);
   if (e == cudaSuccess && prof) e = cudaEventRecordWithFlags(g_ev_end, s, rec_flags);
-  if (e == cudaSuccess) e = kvq::launch_attend_reduce(a, s, true);
+  if (e == cudaSuccess) e = b64 ? kvq::launch_join_b64(a, s) : kvq::launch_attend_reduce(a, s, true);
   return e;
 }
 

@@ -11,13 +11,22 @@
 // which also keeps the tensor cores' truncated additions short. The probabilities are taken 2^12 times larger, so that
 // both f16 parts of p (p = hi + lo, 22 bits) stay above f16's subnormals for tokens of little weight.
 //
-// Data movement: each of a CTA's four warps streams a contiguous quarter of the chunk's stages (32 tokens at head_dim
-// 128, 16 at 256: 8 KB for both planes) through its own ring with 16-byte cp.async; rows are placed with an XOR swizzle
-// of their 16-byte columns, so that ldmatrix (plain for K: 4 codes of a token per lane; transposed for V: 2 dims of 2
-// tokens) is free of bank conflicts. The warps' states are combined in shared memory, one partial per row and chunk.
+// Work: a unit is one block of 64 tokens of one (sequence, kv head, group of eight rows); the call's units stand in one row,
+// heads one after the other. From the lengths, each CTA finds the units of its own. Where every head can be cut into
+// equal pieces of few more units than an even share, so that all pieces fit the CTAs, a CTA has one piece of one head;
+// else every CTA takes the same number of neighbouring units, and one whose units pass from a head to the next finishes the
+// one (a partial each: running maximum, sum, output) and goes on with the other. So ragged batches, short lists and few
+// heads leave as much to do to every CTA, without a plan from the host. Head `i` in CTA `c` has partial c + i: a head's
+// partials are neighbours, and the last kernel joins them.
+//
+// Data movement: a CTA's four warps take the stages of its units in turn (32 tokens at head_dim 128, 16 at 256: 8 KB for
+// both planes), each through its own ring with 16-byte cp.async; rows are placed with an XOR swizzle of their 16-byte
+// columns, so that ldmatrix (plain for K: 4 codes of a token per lane; transposed for V: 2 dims of 2 tokens) is free of
+// bank conflicts. At a head's end the warps' states are combined in shared memory.
 //
 // Bound: the packed cache's bytes from HBM.
 #include <cfloat>
+#include <type_traits>
 
 #include "kvq_internal.cuh"
 #include "mma_util.cuh"
@@ -28,18 +37,20 @@ using namespace mma;
 
 constexpr int kWarps = 4;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 
 template <int D>
 struct Cfg {
   static constexpr int STAGE = D == 128 ? 32 : 16;       // tokens
-  static constexpr int RING = 2;
+  static constexpr int RING = D == 128 ? 2 : 3;
   static constexpr int PLANE = STAGE * D;                // bytes of one plane's rows
   static constexpr int BYTES = 2 * PLANE + 16;           // both planes, and the block's two scales
-  static constexpr int CTAS = kB64CtasPerSm(D);
   static constexpr int SMEM = kWarps * RING * BYTES;
-  static_assert(kWarps * 8 * (D + 2) * 4 <= SMEM, "the warps' states reuse the stages");
+  static constexpr int PITCH = D + 4;                     // floats of a row of a warp's state: free of bank conflicts
+  static_assert(kWarps * 8 * (PITCH + 2) * 4 <= SMEM, "the warps' states reuse the stages");
 };
+constexpr float kRise = 3.9f;            // 2^(12 + 3.9) < 65504
+// What a CTA pays for a second head, in units: a piece may be so much longer than an even share.
+constexpr int kSlack = 5;
 
 // 16-byte column j of row `row`.
 template <int D>
@@ -59,8 +70,70 @@ __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t &a, uint32_t &b) 
   }
 }
 
+// Where a run of units stands: sequence b, head `hd` of it (kv head * groups + group), its blocks [blk, blk + n).
+struct Span {
+  int b, hd, blk, n, len;      // len: tokens of the sequence that some row sees
+};
+// Tokens of sequence b that the call looks at.
+template <bool PAGED>
+__device__ __forceinline__ int seen_len(const AttendArgs &a, int b) {
+  if constexpr (PAGED) return min(max(__ldg(a.seq_lens + b), 0), a.kv_len);
+  else return a.causal ? min(a.kv_len, a.q_pos0 + a.n_q) : a.kv_len;
+}
+__device__ __forceinline__ int blocks_of(int len) { return (int)(((long long)len + 63) >> 6); }
+__device__ __forceinline__ int pieces_of(int blocks, int per) { return (blocks + per - 1) / per; }
+__device__ __forceinline__ long long warp_sum(long long x) {
+#pragma unroll
+  for (int m = 16; m; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
+  return x;
+}
+
+// How a call's units are dealt out (by one warp).
+struct Deal {
+  long long per;               // units a CTA
+  bool pieces;                 // a CTA has one piece of one head
+};
+template <bool PAGED>
+__device__ __forceinline__ Deal deal_of(const AttendArgs &a, int heads, int lane) {
+  if (a.per > 0) return {a.per, true};                   // the caller's chunk: its grid holds every piece
+  const int B = a.cache.B;
+  long long total = 0;
+  if constexpr (PAGED) {
+    for (int b = lane; b < B; b += 32) total += (long long)heads * blocks_of(seen_len<PAGED>(a, b));
+    total = warp_sum(total);
+  } else {
+    total = (long long)B * heads * blocks_of(seen_len<PAGED>(a, 0));
+  }
+  const long long per = max(1LL, (total + gridDim.x - 1) / gridDim.x);
+  if (per > INT_MAX - kSlack) return {per, false};
+  long long n[kSlack] = {};                              // pieces of at most per + j units
+  if constexpr (PAGED) {
+    for (int b = lane; b < B; b += 32) {
+      const int nb = blocks_of(seen_len<PAGED>(a, b));
+#pragma unroll
+      for (int j = 0; j < kSlack; ++j) n[j] += pieces_of(nb, (int)per + j);
+    }
+#pragma unroll
+    for (int j = 0; j < kSlack; ++j) n[j] = warp_sum(n[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < kSlack; ++j) n[j] = (long long)B * pieces_of(blocks_of(seen_len<PAGED>(a, 0)), (int)per + j);
+  }
+#pragma unroll
+  for (int j = 0; j < kSlack; ++j)
+    if (n[j] * heads <= gridDim.x) return {per + j, true};
+  return {per, false};
+}
+// Weight of sequence b in the row of what is dealt out: its heads' pieces, or their units.
+template <bool PAGED>
+__device__ __forceinline__ long long share_of(const AttendArgs &a, const Deal &d, int heads, int b) {
+  if (b >= a.cache.B) return 0;
+  const int nb = blocks_of(seen_len<PAGED>(a, b));
+  return (long long)heads * (d.pieces ? pieces_of(nb, (int)d.per) : nb);
+}
+
 template <int D, bool E4M3, bool QSPLIT, bool PAGED>
-__global__ void __launch_bounds__(kWarps * 32, Cfg<D>::CTAS) attend_b64_kernel(AttendArgs a) {
+__global__ void __maxnreg__(D == 128 ? 152 : 224) attend_b64_kernel(AttendArgs a) {
   using C = Cfg<D>;
   constexpr int KS = D / 16, TILES = C::STAGE / 16, CPR = D / 16;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -69,55 +142,163 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D>::CTAS) attend_b64_kernel(A
 #endif
   const CacheView &cv = a.cache;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, mi = lane >> 3;
-  const int bh = blockIdx.y, bb = bh / cv.H, kvh = bh - bb * cv.H;
-  const SeqLen sl = seq_of_t<PAGED>(a, bb);
-  const int row0 = blockIdx.z * 8, R = min(8, a.gqa * a.n_q - row0);
-  const int t0 = blockIdx.x * sl.chunk, t1 = min(sl.n_body, t0 + sl.chunk);
-  const int w_lim = max_row_limit(a, sl, row0, row0 + R);
-  pdl_wait_if(t0 <= w_lim && t0 < sl.fresh_hi && sl.fresh_lo < min(t1, w_lim + 1));
-  if (t0 > w_lim || t0 >= t1) return;                    // no row sees this chunk (phase 2 skips it)
-  const int t_end = min(t1, w_lim + 1);
-  const int n_stages = (t_end - t0 + C::STAGE - 1) / C::STAGE, spw = (n_stages + kWarps - 1) / kWarps;
-  const int s_first = min(n_stages, warp * spw), n_mine = min(n_stages, s_first + spw) - s_first;
-  const int tw0 = t0 + s_first * C::STAGE;
+  const int R = a.gqa * a.n_q, groups = (R + 7) / 8, heads = cv.H * groups;
+#if defined(__CUDA_ARCH__) && __CUDA_ARCH__ >= 900
+  // lengths that the kernel before may have written (this call's own append does not)
+  if (PAGED && a.fresh_tail == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+#endif
+  // This CTA's first span, and (units dealt out) how many units it has.
+  const Deal deal = deal_of<PAGED>(a, heads, lane);
+  Span sp = {0, 0, 0, 0, 0};
+  const long long u0 = deal.pieces ? (long long)blockIdx.x : deal.per * blockIdx.x;
+  long long left;
+  {
+    long long before = 0;                                // what the sequences in front of sp.b weigh
+    bool none = false;
+    if constexpr (PAGED) {
+      for (;; sp.b += 32) {
+        const long long own = share_of<PAGED>(a, deal, heads, sp.b + lane);
+        long long upto = own;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+          const long long o = __shfl_up_sync(0xffffffffu, upto, m);
+          if (lane >= m) upto += o;
+        }
+        const unsigned over = __ballot_sync(0xffffffffu, before + upto > u0);
+        if (over) {
+          const int at = __ffs((int)over) - 1;
+          before += __shfl_sync(0xffffffffu, upto - own, at);
+          sp.b += at;
+          break;
+        }
+        before += __shfl_sync(0xffffffffu, upto, 31);
+        none = sp.b + 32 >= cv.B;
+        if (none) break;
+      }
+    } else {
+      const long long each = share_of<PAGED>(a, deal, heads, 0);
+      none = u0 >= each * cv.B;
+      sp.b = none ? 0 : (int)(u0 / each);
+      before = each * sp.b;
+    }
+    if (none) {                                          // more CTAs than work
+      pdl_wait_if(false);
+      return;
+    }
+    sp.len = seen_len<PAGED>(a, sp.b);
+    const int nb = blocks_of(sp.len);
+    if (deal.pieces) {                                   // a head in equal pieces
+      const int n = pieces_of(nb, (int)deal.per), at = (int)(u0 - before), size = (nb + n - 1) / n;
+      sp.hd = at / n;
+      sp.blk = (at - sp.hd * n) * size;
+      sp.n = max(0, min(size, nb - sp.blk));
+      left = sp.n;
+    } else {
+      sp.hd = (int)((u0 - before) / nb);
+      sp.blk = (int)((u0 - before) - (long long)sp.hd * nb);
+      sp.n = (int)min(deal.per, (long long)nb - sp.blk);
+      left = deal.per;                                   // (the last CTA's may end earlier: there is no head behind it)
+    }
+  }
+  // the next head with tokens
+  auto advance = [&](Span &s) {
+    left -= s.n;
+    s.n = 0;
+    if (left <= 0) return;
+    if (++s.hd == heads) {
+      s.hd = 0;
+      do {
+        if (++s.b == cv.B) return;
+        s.len = seen_len<PAGED>(a, s.b);
+      } while (s.len <= 0);
+    }
+    s.blk = 0;
+    s.n = (int)min(left, (long long)blocks_of(s.len));
+  };
+
+  // Rows that the kernel before appends: CTAs that read them wait for it. (A CTA looks at its first head only where it
+  // has one alone.)
+  {
+    int lo = a.fresh_lo, hi = a.fresh_hi;
+    if (PAGED && a.fresh_tail > 0) lo = sp.len - a.fresh_tail, hi = sp.len;
+    pdl_wait_if(left > sp.n || (64 * sp.blk < hi && lo < 64 * (sp.blk + sp.n)));
+  }
 
   uint8_t *ring = smem + warp * C::RING * C::BYTES;
-  const size_t head_row0 = (size_t)bh * cv.cap;
+  float *sm = reinterpret_cast<float *>(smem), *so = sm + kWarps * 16;
+  for (; sp.n > 0; advance(sp)) {
+  const int kvh = sp.hd / groups, row0 = 8 * (sp.hd - kvh * groups), rows = min(8, R - row0);
+  const int t_first = 64 * sp.blk, t_end = min(sp.len, t_first + 64 * sp.n);
+  SeqLen sl;
+  sl.kv_len = sp.len;
+  sl.q_pos0 = PAGED ? sp.len - a.n_q : a.q_pos0;
+  // the warp's stages: tokens t_first + (4 i + warp) STAGE
+  const int n_stages = (t_end - t_first + C::STAGE - 1) / C::STAGE, n_mine = (n_stages - warp + kWarps - 1) / kWarps;
+  const size_t head_row0 = ((size_t)sp.b * cv.H + kvh) * cv.cap;
   auto issue = [&](int i) {
     if (i < n_mine) {
-      const int ts = tw0 + i * C::STAGE;
-      const size_t r = cache_row_t<PAGED>(cv, bb, kvh, head_row0, ts);   // a stage lies in one block
-      const uint8_t *kp = cv.payload[0] + r * D, *vp = cv.payload[1] + r * D;
-      uint8_t *sb = ring + (i % C::RING) * C::BYTES;
-      const uint32_t sK = smem_addr(sb), sV = sK + C::PLANE;
-      const int live = (t_end - ts) * CPR;               // 16-byte pieces of rows in the chunk; the rest is zero-filled
+      const int ts = t_first + (kWarps * i + warp) * C::STAGE;
+      const size_t r = cache_row_t<PAGED>(cv, sp.b, kvh, head_row0, ts);   // a stage lies in one block
+      const uint8_t *kp = cv.payload[0] + r * D + 16 * lane, *vp = cv.payload[1] + r * D + 16 * lane;
+      const uint32_t sK = smem_addr(ring + (i % C::RING) * C::BYTES), sV = sK + C::PLANE;
+      const int live = (t_end - ts) * CPR;               // 16-byte pieces of rows in the piece; the rest is zero-filled
+      if (live >= C::STAGE * CPR) {
 #pragma unroll
-      for (int k = 0; k < C::STAGE * CPR / 32; ++k) {
-        const int q = lane + 32 * k, row = q / CPR, j = q % CPR;
-        const bool ok = q < live;
-        cp_async16(sK + swz<D>(row, j), kp + (ok ? 16 * q : 0), ok ? 16 : 0);
-        cp_async16(sV + swz<D>(row, j), vp + (ok ? 16 * q : 0), ok ? 16 : 0);
+        for (int k = 0; k < C::STAGE * CPR / 32; ++k) {
+          const uint32_t at = swz<D>((lane + 32 * k) / CPR, (lane + 32 * k) % CPR);
+          cp_async16(sK + at, kp + 512 * k, 16);
+          cp_async16(sV + at, vp + 512 * k, 16);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < C::STAGE * CPR / 32; ++k) {
+          const uint32_t at = swz<D>((lane + 32 * k) / CPR, (lane + 32 * k) % CPR);
+          const bool ok = lane + 32 * k < live;
+          cp_async16(sK + at, ok ? kp + 512 * k : cv.payload[0], ok ? 16 : 0);
+          cp_async16(sV + at, ok ? vp + 512 * k : cv.payload[1], ok ? 16 : 0);
+        }
       }
-      if (lane < 2) cp_async4(sK + 2 * C::PLANE + 4 * lane, static_cast<const float *>(cv.scale[lane]) + (r >> 6), 4);
+      if (lane < 2) cp_async4(sK + 2 * C::PLANE + 4 * lane, static_cast<const float *>(lane ? cv.scale[1] : cv.scale[0]) + (r >> 6), 4);
     }
     cp_async_commit();
   };
-#pragma unroll
-  for (int i = 0; i < C::RING; ++i) issue(i);
-
-  // query fragments: row g, dims 16 j + 4 c + 0..3 (the k order in which ldmatrix hands out K's codes)
+  // Query fragments: row g, dims 16 j + 4 c + 0..3 (the k order in which ldmatrix hands out K's codes). They are asked for in
+  // front of the first stages: behind those of all CTAs they would arrive microseconds later.
   uint32_t bq[KS][2], bl[QSPLIT ? KS : 1][2];
   float row_alpha = 0.0f;
   {
-    float x[KS][4], mx = 0.0f;
-    const size_t qr = g < R ? query_row_index(a, bb, kvh, row0 + g) * D : 0;
+    uint2 raw[KS][QSPLIT ? 2 : 1];                       // four values each
+    const size_t qr = query_row_index(a, sp.b, kvh, row0 + min(g, rows - 1)) * D + 4 * c;
 #pragma unroll
     for (int j = 0; j < KS; ++j) {
+      if constexpr (QSPLIT) {
+        const uint4 w = __ldg(reinterpret_cast<const uint4 *>(static_cast<const float *>(a.q) + qr + 16 * j));
+        raw[j][0] = make_uint2(w.x, w.y);
+        raw[j][1] = make_uint2(w.z, w.w);
+      } else {
+        raw[j][0] = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.q) + qr + 16 * j));
+      }
+    }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[j][i] = 0.0f;
-      if (g < R) load4_f32(a.q, a.q_dtype, qr + 16 * j + 4 * c, x[j]);
+    for (int i = 0; i < C::RING; ++i) issue(i);
+    float x[KS][4], mx = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fabsf(x[j][i]));
+    for (int j = 0; j < KS; ++j) {
+      if constexpr (QSPLIT) {
+        x[j][0] = __uint_as_float(raw[j][0].x); x[j][1] = __uint_as_float(raw[j][0].y);
+        x[j][2] = __uint_as_float(raw[j][1].x); x[j][3] = __uint_as_float(raw[j][1].y);
+      } else if (a.q_dtype == KVQ_BF16) {
+        x[j][0] = bf16_bits_to_f32(raw[j][0].x & 0xFFFFu); x[j][1] = bf16_bits_to_f32(raw[j][0].x >> 16);
+        x[j][2] = bf16_bits_to_f32(raw[j][0].y & 0xFFFFu); x[j][3] = bf16_bits_to_f32(raw[j][0].y >> 16);
+      } else {
+        const float2 lo = __half22float2(u32_as_h2(raw[j][0].x)), hi = __half22float2(u32_as_h2(raw[j][0].y));
+        x[j][0] = lo.x; x[j][1] = lo.y; x[j][2] = hi.x; x[j][3] = hi.y;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (g >= rows) x[j][i] = 0.0f;
+        mx = fmaxf(mx, fabsf(x[j][i]));
+      }
     }
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
@@ -145,7 +326,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D>::CTAS) attend_b64_kernel(A
   const float alpha[2] = {__shfl_sync(0xffffffffu, row_alpha, 8 * c), __shfl_sync(0xffffffffu, row_alpha, 8 * c + 4)};
   int lim[2];
 #pragma unroll
-  for (int k = 0; k < 2; ++k) lim[k] = 2 * c + k < R ? min(t_end - 1, row_limit(a, sl, (row0 + 2 * c + k) % a.n_q)) : -1;
+  for (int k = 0; k < 2; ++k) lim[k] = 2 * c + k < rows ? row_limit(a, sl, (row0 + 2 * c + k) % a.n_q) : -1;
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
   float O[KS][4];
 #pragma unroll
@@ -159,13 +340,15 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D>::CTAS) attend_b64_kernel(A
     const uint8_t *sb = ring + (i % C::RING) * C::BYTES;
     const uint32_t sK = smem_addr(sb), sV = sK + C::PLANE;
     const float2 sc = *reinterpret_cast<const float2 *>(sb + 2 * C::PLANE);
-    const int ts = tw0 + i * C::STAGE;
+    const int ts = t_first + (kWarps * i + warp) * C::STAGE;
+    const float f[2] = {alpha[0] * sc.x, alpha[1] * sc.x};
 
-    float s[TILES][4];
+    // scores in base 2: x[t][k] is token ts + 16 t + g + 8 (k >> 1), row 2c + (k & 1)
+    float x[TILES][4];
+    bool rise = false;
 #pragma unroll
     for (int t = 0; t < TILES; ++t) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) s[t][k] = 0.0f;
+      float s2[2][4] = {};                               // two chains of dependent products
 #pragma unroll
       for (int j = 0; j < KS; j += 2) {
         uint32_t w[4];
@@ -175,39 +358,45 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D>::CTAS) attend_b64_kernel(A
           uint32_t A[4];
           codes_f16<E4M3, false>(w[2 * u], A[0], A[2]);
           codes_f16<E4M3, false>(w[2 * u + 1], A[1], A[3]);
-          mma16816(s[t], A, bq[j + u][0], bq[j + u][1]);
-          if constexpr (QSPLIT) mma16816(s[t], A, bl[j + u][0], bl[j + u][1]);
+          mma16816(s2[u], A, bq[j + u][0], bq[j + u][1]);
+          if constexpr (QSPLIT) mma16816(s2[u], A, bl[j + u][0], bl[j + u][1]);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        x[t][k] = ts + 16 * t + g + 8 * (k >> 1) <= lim[k & 1] ? (s2[0][k] + s2[1][k]) * f[k & 1] : -INFINITY;
+        rise = rise || x[t][k] > m[k & 1] + kRise;
+      }
+    }
+    // The reference m follows the maximum only where a score passes it by kRise: then 2^12 p still fits f16, and most
+    // stages have no reduction over lanes and nothing to rescale.
+    if (__any_sync(0xffffffffu, rise)) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float mx = m[k];
+#pragma unroll
+        for (int t = 0; t < TILES; ++t) mx = fmaxf(mx, fmaxf(x[t][k], x[t][k + 2]));
+#pragma unroll
+        for (int y = 4; y < 32; y <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, y));
+        const float corr = m[k] == -INFINITY ? 0.0f : ex2(m[k] - mx);
+        m[k] = mx;
+        l[k] *= corr;
+#pragma unroll
+        for (int j = 0; j < KS; ++j) {
+          O[j][k] *= corr;
+          O[j][k + 2] *= corr;
         }
       }
     }
-    // token of s[t][k]: ts + 16 t + g + 8 (k >> 1), row 2c + (k & 1)
-    const float f[2] = {alpha[0] * sc.x, alpha[1] * sc.x};
-    float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-    for (int t = 0; t < TILES; ++t)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        s[t][k] = ts + 16 * t + g + 8 * (k >> 1) <= lim[k & 1] ? s[t][k] * f[k & 1] : -INFINITY;
-        mx[k & 1] = fmaxf(mx[k & 1], s[t][k]);
-      }
-    float corr[2], base[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-#pragma unroll
-      for (int x = 4; x < 32; x <<= 1) mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], x));
-      const float mn = fmaxf(m[k], mx[k]);
-      base[k] = mn == -INFINITY ? 0.0f : mn;             // a row that has seen nothing yet: p = 2^-inf = 0
-      corr[k] = ex2(m[k] - base[k]);
-      m[k] = mn;
-      l[k] *= corr[k];
-    }
+    const float sv = sc.y * 0x1p-12f;
+    const float base[2] = {m[0] == -INFINITY ? 0.0f : m[0], m[1] == -INFINITY ? 0.0f : m[1]};    // nothing seen yet: p = 2^-inf
     uint32_t ph[TILES][2], pl[TILES][2];
 #pragma unroll
     for (int t = 0; t < TILES; ++t) {
       float p[4], h[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        p[k] = ex2(s[t][k] - base[k & 1]);
+        p[k] = ex2(x[t][k] - base[k & 1]);
         l[k & 1] += p[k];
         p[k] *= 4096.0f;
         h[k] = __half2float(__float2half_rn(p[k]));
@@ -218,14 +407,9 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D>::CTAS) attend_b64_kernel(A
         pl[t][k] = movm_t(pack_f16x2(p[2 * k] - h[2 * k], p[2 * k + 1] - h[2 * k + 1]));
       }
     }
-    const float sv = sc.y * 0x1p-12f;
 #pragma unroll
     for (int j = 0; j < KS; j += 2) {
-      float acc[2][4];
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) acc[u][k] = 0.0f;
+      float acc[2][4] = {};
 #pragma unroll
       for (int t = 0; t < TILES; ++t) {
         uint32_t w[4];
@@ -242,7 +426,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D>::CTAS) attend_b64_kernel(A
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) O[j + u][k] = fmaf(acc[u][k], sv, O[j + u][k] * corr[k & 1]);
+        for (int k = 0; k < 4; ++k) O[j + u][k] = fmaf(acc[u][k], sv, O[j + u][k]);
     }
     __syncwarp();                                        // the stage is read: its place is free
     issue(i + C::RING);
@@ -254,7 +438,6 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D>::CTAS) attend_b64_kernel(A
     for (int x = 4; x < 32; x <<= 1) l[k] += __shfl_xor_sync(0xffffffffu, l[k], x);
   __syncthreads();
   // the warps' states: [warp][row]: m, l; then [warp][row][D]
-  float *sm = reinterpret_cast<float *>(smem), *so = sm + kWarps * 16;
   if (lane < 4) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -266,38 +449,152 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D>::CTAS) attend_b64_kernel(A
   for (int j = 0; j < KS; ++j)
 #pragma unroll
     for (int k = 0; k < 2; ++k)
-      *reinterpret_cast<float2 *>(so + (size_t)(warp * 8 + 2 * c + k) * D + 16 * j + 2 * g) = make_float2(O[j][k], O[j][2 + k]);
+      *reinterpret_cast<float2 *>(so + (warp * 8 + 2 * c + k) * C::PITCH + 16 * j + 2 * g) = make_float2(O[j][k], O[j][2 + k]);
   __syncthreads();
-  for (int r = warp; r < R; r += kWarps) {
-    if (t0 > row_limit(a, sl, (row0 + r) % a.n_q)) continue;             // this row does not see the chunk
+  const int head = sp.b * heads + sp.hd;
+  const size_t part = (size_t)blockIdx.x + head;
+  for (int r = warp; r < rows; r += kWarps) {
     float M = -INFINITY, w[kWarps], L = 0.0f;
 #pragma unroll
     for (int k = 0; k < kWarps; ++k) M = fmaxf(M, sm[(k * 8 + r) * 2]);
-    const float ref = M == -INFINITY ? 0.0f : M;         // (NaN states)
+    const float ref = M == -INFINITY ? 0.0f : M;
 #pragma unroll
     for (int k = 0; k < kWarps; ++k) {
       w[k] = ex2(sm[(k * 8 + r) * 2] - ref);
       L = fmaf(sm[(k * 8 + r) * 2 + 1], w[k], L);
     }
-    const size_t pi = query_row_index(a, bb, kvh, row0 + r) * a.C + blockIdx.x;
 #pragma unroll
     for (int d = 0; d < D; d += 128) {
       float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
       for (int k = 0; k < kWarps; ++k) {
-        const float4 x = *reinterpret_cast<const float4 *>(so + (size_t)(k * 8 + r) * D + d + 4 * lane);
+        const float4 x = *reinterpret_cast<const float4 *>(so + (k * 8 + r) * C::PITCH + d + 4 * lane);
         o.x = fmaf(x.x, w[k], o.x);
         o.y = fmaf(x.y, w[k], o.y);
         o.z = fmaf(x.z, w[k], o.z);
         o.w = fmaf(x.w, w[k], o.w);
       }
-      *reinterpret_cast<float4 *>(a.part_o + pi * D + d + 4 * lane) = o;
+      *reinterpret_cast<float4 *>(a.part_o + (part * 8 + r) * D + d + 4 * lane) = o;
     }
     if (lane == 0) {
-      a.part_m[pi] = M * kLn2;
-      a.part_l[pi] = L;
+      a.part_m[part * 8 + r] = M;                        // (base 2)
+      a.part_l[part * 8 + r] = L;
     }
   }
+  if (sp.blk == 0 && threadIdx.x == 0) {                 // the head's first and last CTA
+    const int nb = blocks_of(sp.len);
+    int last = (int)blockIdx.x;
+    if (deal.pieces) {
+      const int n = pieces_of(nb, (int)deal.per), size = (nb + n - 1) / n;
+      last += pieces_of(nb, size) - 1;                   // (equal sizes may need fewer pieces than there is room for)
+    } else {
+      last = (int)((u0 + (deal.per - left) + nb - 1) / deal.per);
+    }
+    a.spans[head] = make_int2((int)blockIdx.x, last);
+  }
+  __syncthreads();                                       // the ring is free again
+  }
+}
+
+// Joins the partials of every row: M = max m, out = sum o 2^(m - M) / sum l 2^(m - M). SPLIT: a CTA per row, whose warps
+// split the partials; else a warp per row.
+constexpr int kJoinWarps = 4, kBatch = 4;
+template <int D, bool SPLIT>
+__global__ void __launch_bounds__(kJoinWarps * 32) join_b64_kernel(AttendArgs a, unsigned n_rows) {
+  constexpr int V = D / 128;                             // float4 per lane
+  __shared__ float sm_m[kJoinWarps], sm_l[kJoinWarps];
+  __shared__ __align__(16) float sm_o[SPLIT ? kJoinWarps : 1][SPLIT ? D : 4];
+#if defined(__CUDA_ARCH__) && __CUDA_ARCH__ >= 900
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+#endif
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const size_t row = SPLIT ? (size_t)blockIdx.x : (size_t)blockIdx.x * kJoinWarps + warp;
+  if (row >= n_rows) return;
+  const int R = a.gqa * a.n_q, groups = (R + 7) / 8;
+  const size_t bh = row / R;
+  const int r = (int)(row - bh * R), b = (int)(bh / a.cache.H);
+  const int len = a.seq_lens ? min(max(__ldg(a.seq_lens + b), 0), a.kv_len) : a.kv_len;
+  float M = -INFINITY, L = 0.0f;
+  float4 O[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) O[v] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (len > 0) {
+    const size_t head = bh * groups + r / 8;
+    const int2 span = a.spans[head];
+    const size_t p0 = (head + span.x) * 8 + r % 8;
+    const int n = span.y - span.x + 1;
+    for (int i0 = SPLIT ? warp : 0; i0 < n; i0 += kBatch * (SPLIT ? kJoinWarps : 1)) {
+      float mc[kBatch], lc[kBatch], bm = M;
+      float4 oc[kBatch][V];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int i = i0 + u * (SPLIT ? kJoinWarps : 1);
+        const bool ok = i < n;
+        const size_t p = p0 + 8 * (size_t)(ok ? i : 0);
+        mc[u] = ok ? a.part_m[p] : -INFINITY;
+        lc[u] = ok ? a.part_l[p] : 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          oc[u][v] = ok ? *reinterpret_cast<const float4 *>(a.part_o + p * D + 128 * v + 4 * lane) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        bm = fmaxf(bm, mc[u]);
+      }
+      if (bm == -INFINITY) continue;                     // pieces that the row does not see
+      const float corr = exp2f(M - bm);
+      L *= corr;
+#pragma unroll
+      for (int v = 0; v < V; ++v) O[v].x *= corr, O[v].y *= corr, O[v].z *= corr, O[v].w *= corr;
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const float w = exp2f(mc[u] - bm);
+        L = fmaf(lc[u], w, L);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          O[v].x = fmaf(oc[u][v].x, w, O[v].x);
+          O[v].y = fmaf(oc[u][v].y, w, O[v].y);
+          O[v].z = fmaf(oc[u][v].z, w, O[v].z);
+          O[v].w = fmaf(oc[u][v].w, w, O[v].w);
+        }
+      }
+      M = bm;
+    }
+  }
+  if constexpr (SPLIT) {
+    if (lane == 0) sm_m[warp] = M, sm_l[warp] = L;
+#pragma unroll
+    for (int v = 0; v < V; ++v) *reinterpret_cast<float4 *>(&sm_o[warp][128 * v + 4 * lane]) = O[v];
+    __syncthreads();
+    float Mt = sm_m[0];
+#pragma unroll
+    for (int w = 1; w < kJoinWarps; ++w) Mt = fmaxf(Mt, sm_m[w]);
+    for (int d = threadIdx.x; d < D; d += kJoinWarps * 32) {
+      float Lt = 0.0f, x = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kJoinWarps; ++w) {
+        const float f = sm_m[w] == -INFINITY ? 0.0f : exp2f(sm_m[w] - Mt);
+        Lt = fmaf(sm_l[w], f, Lt);
+        x = fmaf(sm_o[w][d], f, x);
+      }
+      a.out[out_row(a, row) * D + d] = Lt > 0.0f ? x / Lt : 0.0f;
+    }
+  } else {
+    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      *reinterpret_cast<float4 *>(a.out + out_row(a, row) * D + 128 * v + 4 * lane) = make_float4(O[v].x * inv, O[v].y * inv, O[v].z * inv, O[v].w * inv);
+  }
+}
+
+// A launch that may begin while the kernel before it still runs.
+void chained(cudaLaunchConfig_t &cfg, cudaLaunchAttribute &attr, unsigned ctas, int threads, int smem, cudaStream_t st) {
+  cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
 }
 
 template <int D, bool E4M3, bool QSPLIT, bool PAGED>
@@ -306,16 +603,9 @@ cudaError_t launch_t(const AttendArgs &a, cudaStream_t st) {
   auto kernel = attend_b64_kernel<D, E4M3, QSPLIT, PAGED>;
   const cudaError_t e = set_smem_once(configured, kernel, Cfg<D>::SMEM);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.n_chunks, a.cache.B * a.cache.H, (a.gqa * a.n_q + 7) / 8);
-  cfg.blockDim = dim3(kWarps * 32);
-  cfg.dynamicSmemBytes = Cfg<D>::SMEM;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr;
+  chained(cfg, attr, a.grid, kWarps * 32, Cfg<D>::SMEM, st);
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
@@ -327,6 +617,20 @@ cudaError_t launch_de(const AttendArgs &a, cudaStream_t st) {
 }
 
 }  // namespace
+
+cudaError_t launch_join_b64(const AttendArgs &a, cudaStream_t st) {
+  const unsigned rows = (unsigned)((size_t)a.cache.B * a.Hq * a.n_q);
+  int dev = 0, sms = 148;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  // few rows have many partials each
+  const bool split = rows <= 8u * (unsigned)sms;
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr;
+  chained(cfg, attr, split ? rows : (rows + kJoinWarps - 1) / kJoinWarps, kJoinWarps * 32, 0, st);
+  if (a.cache.D == 128)
+    return split ? cudaLaunchKernelEx(&cfg, join_b64_kernel<128, true>, a, rows) : cudaLaunchKernelEx(&cfg, join_b64_kernel<128, false>, a, rows);
+  return split ? cudaLaunchKernelEx(&cfg, join_b64_kernel<256, true>, a, rows) : cudaLaunchKernelEx(&cfg, join_b64_kernel<256, false>, a, rows);
+}
 
 cudaError_t launch_attend_b64(const AttendArgs &a, cudaStream_t st) {
   if (a.cache.layout == KVQ_E4M3_B64) return a.cache.D == 128 ? launch_de<128, true>(a, st) : launch_de<256, true>(a, st);

@@ -183,6 +183,11 @@ struct AttendArgs {
   // > 1: the call's sequences are (sequence, kv head, query) triples of out_nq queries each, whose outputs go to
   // [B][Hq][out_nq][D]
   int out_nq;
+  // 8-bit block layouts: the CTAs of phase 1, the longest piece of a head in blocks of 64 tokens (0: the call's blocks are
+  // dealt out evenly), and each head's first and last CTA [B][H_kv][groups of eight rows]; the partials are then
+  // [grid + B * H_kv * groups][8], maxima in base 2
+  int grid, per;
+  int2 *spans;
 };
 // Output row of query row `row` of the call.
 __device__ __forceinline__ size_t out_row(const AttendArgs &a, size_t row) {
@@ -364,6 +369,7 @@ bool mma_supported(const AttendArgs &a);
 bool capture_supported(const AttendArgs &a);
 cudaError_t launch_attend_mma(const AttendArgs &a, cudaStream_t st);
 cudaError_t launch_attend_b64(const AttendArgs &a, cudaStream_t st);
+cudaError_t launch_join_b64(const AttendArgs &a, cudaStream_t st);
 cudaError_t launch_attend_mma4(const AttendArgs &a, cudaStream_t st);
 bool mma_q6_supported(const AttendArgs &a);
 cudaError_t launch_attend_mma_q6(const AttendArgs &a, cudaStream_t st);
