@@ -583,19 +583,15 @@ kvq_status kvq_paged_block_bounds_update(const kvq_paged_cache *cache, const kvq
  *   q    device [batch][n_q_heads][n_q][head_dim] in q_dtype
  *   sel  device i32 [batch][n_kv_heads][n_q][n_sel]: ascending; a row that sees at most n_sel blocks has all of them,
  *        and -1 fills the rest
- *   workspace  at least kvq_block_select_workspace_bytes (shared with no call in flight)
- * Scores are meant for a positive attn_scale. Deterministic.
+ * Scores are meant for a positive attn_scale. kv_len (max_kv_len) at most 2^24. One launch; deterministic.
  */
-size_t kvq_block_select_workspace_bytes(const kvq_cache *cache, int32_t n_q, int32_t kv_len);
-size_t kvq_paged_block_select_workspace_bytes(const kvq_paged_cache *cache, int32_t n_q, int32_t max_kv_len);
 kvq_status kvq_block_select(const kvq_cache *cache, const kvq_block_bounds *bounds, const void *q, int32_t q_dtype,
                             int32_t n_q_heads, int32_t n_q, int32_t kv_len, int32_t causal, int32_t q_pos0,
-                            int32_t n_sel, int32_t n_sink, int32_t n_recent, int32_t *sel, void *workspace,
-                            size_t workspace_bytes, kvq_stream_t stream);
+                            int32_t n_sel, int32_t n_sink, int32_t n_recent, int32_t *sel, kvq_stream_t stream);
 kvq_status kvq_paged_block_select(const kvq_paged_cache *cache, const kvq_block_bounds *bounds, const void *q,
                                   int32_t q_dtype, int32_t n_q_heads, int32_t n_q, const int32_t *seq_lens,
                                   int32_t max_kv_len, int32_t causal, int32_t n_sel, int32_t n_sink, int32_t n_recent,
-                                  int32_t *sel, void *workspace, size_t workspace_bytes, kvq_stream_t stream);
+                                  int32_t *sel, kvq_stream_t stream);
 
 /*
  * kvq_decode_attend (kvq_paged_decode_attend) in which row i of the query heads of a kv head sees only the tokens

@@ -14,7 +14,6 @@ from .api import (  # noqa: F401
     paged_attend_weights_workspace_bytes, evict_select, evict_compact, paged_evict_compact,
     PagePlan, page_plan, paged_store_slots,
     BlockBounds, block_bounds, paged_block_bounds, block_select, paged_block_select, sparse_attend, paged_sparse_attend,
-    block_select_workspace_bytes, paged_block_select_workspace_bytes, sparse_attend_workspace_bytes,
-    paged_sparse_attend_workspace_bytes,
+    sparse_attend_workspace_bytes, paged_sparse_attend_workspace_bytes,
 )
 from ._lib import KvqError, LAYOUT_IDS, EXPORTS  # noqa: F401

@@ -47,8 +47,7 @@ EXPORTS = ("kvq_row_bytes", "kvq_cache_bytes", "kvq_store_q4_0", "kvq_store_q6_0
            "kvq_paged_attend_weights_workspace_bytes", "kvq_paged_decode_attend_weights",
            "kvq_evict_select", "kvq_evict_compact", "kvq_paged_evict_compact",
            "kvq_page_plan", "kvq_paged_store_slots",
-           "kvq_block_bounds_update", "kvq_paged_block_bounds_update", "kvq_block_select_workspace_bytes",
-           "kvq_paged_block_select_workspace_bytes", "kvq_block_select", "kvq_paged_block_select",
+           "kvq_block_bounds_update", "kvq_paged_block_bounds_update", "kvq_block_select", "kvq_paged_block_select",
            "kvq_sparse_attend_workspace_bytes", "kvq_paged_sparse_attend_workspace_bytes", "kvq_sparse_attend",
            "kvq_paged_sparse_attend")
 ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "banded": 3, "yarn": 4}   # kvq_rope_scaling
@@ -174,15 +173,13 @@ def lib() -> C.CDLL:
             ("kvq_paged_store_slots", [paged_p, rows_p, rows_p, I32, I32, P, P]),
             ("kvq_block_bounds_update", [cache_p, bounds_p, I32, I32, P]),
             ("kvq_paged_block_bounds_update", [paged_p, bounds_p, P, I32, P]),
-            ("kvq_block_select", [cache_p, bounds_p, P, I32, I32, I32, I32, I32, I32, I32, I32, I32, P, P, SZ, P]),
-            ("kvq_paged_block_select", [paged_p, bounds_p, P, I32, I32, I32, P, I32, I32, I32, I32, I32, P, P, SZ, P]),
+            ("kvq_block_select", [cache_p, bounds_p, P, I32, I32, I32, I32, I32, I32, I32, I32, I32, P, P]),
+            ("kvq_paged_block_select", [paged_p, bounds_p, P, I32, I32, I32, P, I32, I32, I32, I32, I32, P, P]),
             ("kvq_sparse_attend", [cache_p, P, I32, I32, I32, I32, I32, I32, F, P, I32, I32, P, P, SZ, P]),
             ("kvq_paged_sparse_attend", [paged_p, P, I32, I32, I32, P, I32, I32, F, P, I32, I32, P, P, SZ, P])):
         f = getattr(L, name)
         f.argtypes, f.restype = args, I32
-    for name, args in (("kvq_block_select_workspace_bytes", [cache_p, I32, I32]),
-                       ("kvq_paged_block_select_workspace_bytes", [paged_p, I32, I32]),
-                       ("kvq_sparse_attend_workspace_bytes", [cache_p, I32, I32, I32, I32]),
+    for name, args in (("kvq_sparse_attend_workspace_bytes", [cache_p, I32, I32, I32, I32]),
                        ("kvq_paged_sparse_attend_workspace_bytes", [paged_p, I32, I32, I32, I32])):
         f = getattr(L, name)
         f.argtypes, f.restype = args, SZ

@@ -63,9 +63,13 @@ def _ptr(t: torch.Tensor | None) -> int | None:
     return None if t is None else t.data_ptr()
 
 
+_DEVICE, _RAW_STREAM = (getattr(torch._C, n, None) for n in ("_cuda_getDevice", "_cuda_getCurrentRawStream"))
+
+
 def _stream(stream) -> int | None:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream if isinstance(s, torch.cuda.Stream) else int(s)
+    if stream is None:
+        return _RAW_STREAM(_DEVICE())
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
 _CURRENT = contextlib.nullcontext()
@@ -89,6 +93,26 @@ def _output(stream, shape, dtype, device) -> torch.Tensor:
         t = torch.empty(shape, dtype=dtype, device=device)
     t.record_stream(torch.cuda.current_stream(t.device))
     return t
+
+
+def _workspace(stream, nbytes: int, device) -> torch.Tensor:
+    """A call's workspace, made on its stream."""
+    if stream is None:
+        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+    with _made_on(stream):
+        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+
+
+def _sized(cache, fn, *args) -> int:
+    """fn(cache, *args), a workspace's bytes, remembered with the cache: a decode loop asks for the same again and again."""
+    known = cache.__dict__.setdefault("_sizes", {})
+    key = (fn, _DEVICE(), *args)
+    n = known.get(key)
+    if n is None:
+        if len(known) >= 256:
+            known.clear()
+        n = known[key] = fn(cache, *args)
+    return n
 
 
 def _need_cuda(name: str, t: torch.Tensor) -> None:
@@ -185,10 +209,8 @@ def decode_attend(cache: KVCache, q: torch.Tensor, kv_len: int, causal: bool = F
     if out is None:
         out = _output(stream, (B, Hq, n_q, D), torch.float32, q.device)
     _need_cuda("out", out)
-    need = attend_workspace_bytes(cache, Hq, n_q, kv_len, chunk)
     if workspace is None:
-        with _made_on(stream):
-            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        workspace = _workspace(stream, _sized(cache, attend_workspace_bytes, Hq, n_q, kv_len, chunk), q.device)
     _need_cuda("workspace", workspace)
     L.check(L.lib().kvq_decode_attend(C.byref(cache.struct), q.data_ptr(), _DTYPES[q.dtype], Hq, n_q, kv_len,
                                       int(bool(causal)), q_pos0, float(attn_scale), chunk, out.data_ptr(),
@@ -218,10 +240,8 @@ def append_decode_attend(cache: KVCache, k_new: torch.Tensor, v_new: torch.Tenso
     if out is None:
         out = _output(stream, (B, Hq, n_q, D), torch.float32, q.device)
     _need_cuda("out", out)
-    need = attend_workspace_bytes(cache, Hq, n_q, kv_len, chunk)
     if workspace is None:
-        with _made_on(stream):
-            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        workspace = _workspace(stream, _sized(cache, attend_workspace_bytes, Hq, n_q, kv_len, chunk), q.device)
     _need_cuda("workspace", workspace)
     L.check(L.lib().kvq_append_decode_attend(
         C.byref(cache.struct), k_new.data_ptr(), v_new.data_ptr(), _DTYPES[k_new.dtype], n_new, pos0, q.data_ptr(),
@@ -398,10 +418,8 @@ def _paged_out_ws(cache, q, max_kv_len, chunk, out, workspace, stream):
     if out is None:
         out = _output(stream, (B, Hq, n_q, D), torch.float32, q.device)
     _need_cuda("out", out)
-    need = paged_attend_workspace_bytes(cache, Hq, n_q, max_kv_len, chunk)
     if workspace is None:
-        with _made_on(stream):
-            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        workspace = _workspace(stream, _sized(cache, paged_attend_workspace_bytes, Hq, n_q, max_kv_len, chunk), q.device)
     _need_cuda("workspace", workspace)
     return out, workspace
 
@@ -545,9 +563,6 @@ def paged_append_decode_attend_host(cache: PagedKVCache, k_new: torch.Tensor, v_
 # ------------------------------------------------------------------ rotary positions
 # The calls below check with few torch calls: a decode step makes them once per layer, and their kernels
 # take a few microseconds.
-_DEVICE, _RAW_STREAM = (getattr(torch._C, n, None) for n in ("_cuda_getDevice", "_cuda_getCurrentRawStream"))
-
-
 def _here(*named) -> int:
     """The current device, which every one of the (name, tensor) pairs has to live on (None passes)."""
     dev = _DEVICE()
@@ -709,8 +724,7 @@ def _weights_call(cache, need_fn, q, n, seq_lens, scores, scores_out, attn_scale
     else:
         _dense("out", out, torch.float32, shape)
     if workspace is None:
-        with _made_on(stream):
-            workspace = torch.empty(max(need_fn(cache, shape[1], shape[2], n, chunk), 256), dtype=torch.uint8, device=q.device)
+        workspace = _workspace(stream, _sized(cache, need_fn, shape[1], shape[2], n, chunk), q.device)
     elif not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     dev = _here(("cache", cache.planes["k"]["payload"]), ("q", q), ("scores", scores), ("scores_out", scores_out),
@@ -837,15 +851,16 @@ def page_plan(seq_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch
     if block_table.dim() != 2:
         raise ValueError("block_table must be int32 [batch][max_pages_per_seq]")
     B, per = block_table.shape
-    dev = seq_lens.device
-    made = {"lens_out": (lens_out, B, torch.int32), "granted": (granted, B, torch.int32), "n_free_out": (n_free_out, 1, torch.int32),
-            "cu_new": (cu_new, B + 1, torch.int32), "slots": (slots, max(max_tokens, 0), torch.int64),
-            "positions": (positions, max(max_tokens, 0), torch.int32)}
-    out = {name: _output(stream, n, dtype, dev) if t is None else t for name, (t, n, dtype) in made.items()}
-    for name, (t, n, dtype) in made.items():
-        _dense(name, out[name], dtype)
-        if out[name].numel() != n:
-            raise ValueError(f"{name} must have {n} entries")
+    n_tok = max(max_tokens, 0)
+    out = {"lens_out": lens_out, "granted": granted, "n_free_out": n_free_out, "cu_new": cu_new, "slots": slots, "positions": positions}
+    for (name, t), n in zip(out.items(), (B, B, 1, B + 1, n_tok, n_tok)):
+        dtype = torch.int64 if name == "slots" else torch.int32
+        if t is None:
+            out[name] = _output(stream, n, dtype, seq_lens.device)
+        else:
+            _dense(name, t, dtype)
+            if t.numel() != n:
+                raise ValueError(f"{name} must have {n} entries")
     _ints("seq_lens", seq_lens, B)
     _ints("new_lens", new_lens, B)
     _ints("n_free", n_free, 1)
@@ -855,7 +870,7 @@ def page_plan(seq_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch
                  ("n_free", n_free), *out.items())
     L.check(L.lib().kvq_page_plan(B, page_size, per, seq_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(),
                                   free_pages.data_ptr(), free_pages.numel(), n_free.data_ptr(), max_tokens,
-                                  *(out[name].data_ptr() for name in made), _stream_of(stream, here)), "kvq_page_plan")
+                                  *(t.data_ptr() for t in out.values()), _stream_of(stream, here)), "kvq_page_plan")
     return PagePlan(*out.values())
 
 
@@ -912,14 +927,6 @@ def paged_block_bounds(cache: PagedKVCache, bounds: BlockBounds, seq_lens: torch
                                                   _stream_of(stream, dev)), "kvq_paged_block_bounds_update")
 
 
-def block_select_workspace_bytes(cache: KVCache, n_q: int, kv_len: int) -> int:
-    return L.lib().kvq_block_select_workspace_bytes(C.byref(cache.struct), n_q, kv_len)
-
-
-def paged_block_select_workspace_bytes(cache: PagedKVCache, n_q: int, max_kv_len: int) -> int:
-    return L.lib().kvq_paged_block_select_workspace_bytes(C.byref(cache.struct), n_q, max_kv_len)
-
-
 def sparse_attend_workspace_bytes(cache: KVCache, n_q_heads: int, n_q: int, n_sel: int, chunk: int = 0) -> int:
     return L.lib().kvq_sparse_attend_workspace_bytes(C.byref(cache.struct), n_q_heads, n_q, n_sel, chunk)
 
@@ -928,8 +935,8 @@ def paged_sparse_attend_workspace_bytes(cache: PagedKVCache, n_q_heads: int, n_q
     return L.lib().kvq_paged_sparse_attend_workspace_bytes(C.byref(cache.struct), n_q_heads, n_q, n_sel, chunk)
 
 
-def _blocks_call(cache, q, seq_lens, need, workspace, stream):
-    """The checks and the workspace that the calls below share."""
+def _blocks_call(cache, q, seq_lens) -> None:
+    """The checks that the calls below share."""
     shape = q.shape
     if len(shape) != 4 or shape[0] != cache.batch or shape[3] != cache.head_dim:
         raise ValueError("q shape does not match the cache")
@@ -937,46 +944,37 @@ def _blocks_call(cache, q, seq_lens, need, workspace, stream):
         raise ValueError("q must be contiguous f32, bf16 or f16")
     if seq_lens is not None:
         _ints("seq_lens", seq_lens, cache.batch)
-    if workspace is None:
-        with _made_on(stream):
-            workspace = torch.empty(max(need(), 256), dtype=torch.uint8, device=q.device)
-    elif not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    return workspace, workspace.numel() * workspace.element_size()
 
 
-def _select_call(fn, need, cache, bounds, q, seq_lens, lengths, n_sel, n_sink, n_recent, sel, workspace, stream):
+def _select_call(fn, cache, bounds, q, seq_lens, lengths, n_sel, n_sink, n_recent, sel, stream):
     bounds.fits(cache)
-    workspace, nbytes = _blocks_call(cache, q, seq_lens, need, workspace, stream)
+    _blocks_call(cache, q, seq_lens)
     shape = (cache.batch, cache.n_kv_heads, q.shape[2], max(n_sel, 1))
     if sel is None:
         sel = _output(stream, shape, torch.int32, q.device)
     else:
         _dense("sel", sel, torch.int32, shape)
-    dev = _here(("cache", cache.planes["k"]["payload"]), ("bounds", bounds.codes), ("q", q), ("seq_lens", seq_lens), ("sel", sel),
-                ("workspace", workspace))
+    dev = _here(("cache", cache.planes["k"]["payload"]), ("bounds", bounds.codes), ("q", q), ("seq_lens", seq_lens), ("sel", sel))
     L.check(getattr(L.lib(), fn)(C.byref(cache.struct), C.byref(bounds.struct), q.data_ptr(), _DTYPES[q.dtype], q.shape[1], q.shape[2],
-                                 *lengths, n_sel, n_sink, n_recent, sel.data_ptr(), workspace.data_ptr(), nbytes,
-                                 _stream_of(stream, dev)), fn)
+                                 *lengths, n_sel, n_sink, n_recent, sel.data_ptr(), _stream_of(stream, dev)), fn)
     return sel
 
 
 def block_select(cache: KVCache, bounds: BlockBounds, q: torch.Tensor, kv_len: int, n_sel: int, n_sink: int = 1, n_recent: int = 1,
-                 causal: bool = False, q_pos0: int = 0, sel: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
-                 stream=None) -> torch.Tensor:
+                 causal: bool = False, q_pos0: int = 0, sel: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The n_sel blocks of 64 tokens for each query row and kv head, ascending (int32 [B][H_kv][n_q][n_sel]): the first n_sink, the
     last n_recent that the row sees, and those whose bounds allow the largest scores, ties to the lowest index; -1 behind the
     blocks of a row that sees fewer."""
-    return _select_call("kvq_block_select", lambda: block_select_workspace_bytes(cache, q.shape[2], kv_len), cache, bounds, q, None,
-                        (kv_len, 1 if causal else 0, q_pos0), n_sel, n_sink, n_recent, sel, workspace, stream)
+    return _select_call("kvq_block_select", cache, bounds, q, None, (kv_len, 1 if causal else 0, q_pos0), n_sel, n_sink, n_recent, sel,
+                        stream)
 
 
 def paged_block_select(cache: PagedKVCache, bounds: BlockBounds, q: torch.Tensor, seq_lens: torch.Tensor, max_kv_len: int, n_sel: int,
                        n_sink: int = 1, n_recent: int = 1, causal: bool = False, sel: torch.Tensor | None = None,
-                       workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+                       stream=None) -> torch.Tensor:
     """block_select over a paged pool, each sequence by its own length (causal rows are its newest n_q tokens)."""
-    return _select_call("kvq_paged_block_select", lambda: paged_block_select_workspace_bytes(cache, q.shape[2], max_kv_len), cache, bounds,
-                        q, seq_lens, (seq_lens.data_ptr(), max_kv_len, 1 if causal else 0), n_sel, n_sink, n_recent, sel, workspace, stream)
+    return _select_call("kvq_paged_block_select", cache, bounds, q, seq_lens, (seq_lens.data_ptr(), max_kv_len, 1 if causal else 0),
+                        n_sel, n_sink, n_recent, sel, stream)
 
 
 def _sparse_call(fn, need, cache, q, sel, seq_lens, lengths, attn_scale, chunk, out, workspace, stream):
@@ -984,7 +982,12 @@ def _sparse_call(fn, need, cache, q, sel, seq_lens, lengths, attn_scale, chunk, 
     if sel.dtype is not torch.int32 or sel.dim() != 4 or len(shape) != 4 or sel.shape[:3] != (cache.batch, cache.n_kv_heads, shape[2]) or \
             not sel.is_contiguous():
         raise ValueError("sel must be contiguous int32 [batch][n_kv_heads][n_q][n_sel]")
-    workspace, nbytes = _blocks_call(cache, q, seq_lens, lambda: need(cache, shape[1], shape[2], sel.shape[3], chunk), workspace, stream)
+    _blocks_call(cache, q, seq_lens)
+    if workspace is None:
+        workspace = _workspace(stream, _sized(cache, need, shape[1], shape[2], sel.shape[3], chunk), q.device)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    nbytes = workspace.numel() * workspace.element_size()
     if out is None:
         out = _output(stream, shape, torch.float32, q.device)
     else:

@@ -190,8 +190,7 @@ kvq_status store_common(int want_layout, const kvq_cache *cache, const void *k_n
 // batch passes its true total so the chunk fits the work that exists.
 // n_wchunks: window chunks per (batch, kv head) that the row-side kernel scores in the same grid.
 int auto_chunk(const kvq::CacheView &c, int rows, int n_body, int n_heads, long long work = 0, int n_wchunks = 0) {
-  int dev = 0, sms = 148;
-  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int sms = kvq::sm_count();
   const bool total_given = work > 0;
   if (!total_given) work = (long long)(n_body > 0 ? n_body : 1) * n_heads;
   long long chunk;
@@ -257,8 +256,7 @@ int auto_chunk(const kvq::CacheView &c, int rows, int n_body, int n_heads, long 
 // the device; else one for each piece of at most chunk tokens of every head) and the workspace of their partials.
 kvq_status resolve_b64(kvq::AttendArgs &a, int chunk, size_t &need, void *ws) {
   const kvq::CacheView &c = a.cache;
-  int dev = 0, sms = 148;
-  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int sms = kvq::sm_count();
   const long long heads = (long long)c.B * c.H * ((a.gqa * (long long)a.n_q + 7) / 8);
   const long long units = heads * (((long long)a.kv_len + 63) / 64);
   a.per = chunk / 64;
@@ -1450,40 +1448,22 @@ kvq_status run_bounds(const kvq::CacheView &v, const kvq_block_bounds *bounds, i
   return KVQ_OK;
 }
 
-// Workspace of a selection: the blocks' scores, then the number of blocks that each list sees.
-struct SelectSpace {
-  long long stride;
-  size_t counts, total;
-};
-SelectSpace select_space(const kvq::CacheView &v, int n_q, int kv_len) {
-  SelectSpace w;
-  const size_t lists = (size_t)v.B * v.H * n_q;
-  w.stride = (((long long)kv_len + 63) / 64 + 3) / 4 * 4;
-  w.counts = round_up(lists * w.stride * sizeof(float), 256);
-  w.total = w.counts + round_up(lists * sizeof(int32_t), 256);
-  return w;
-}
-
 kvq_status run_block_select(const kvq::CacheView &v, const kvq_block_bounds *bounds, const void *q, int q_dtype, int n_q_heads,
                             int n_q, const int32_t *seq_lens, int kv_len, int causal, int q_pos0, int n_sel, int n_sink,
-                            int n_recent, int32_t *sel, void *workspace, size_t workspace_bytes, kvq_stream_t stream) {
+                            int n_recent, int32_t *sel, kvq_stream_t stream) {
   kvq_status st = check_blocks(v, n_q_heads, n_q);
   if (st == KVQ_OK) st = check_lengths(v, n_q, seq_lens, kv_len, causal, q_pos0);
   if (st == KVQ_OK) st = check_bounds(bounds);
   if (st != KVQ_OK) return st;
   if (q_dtype < KVQ_F32 || q_dtype > KVQ_F16) return fail(KVQ_EINVAL, "unknown q dtype %d", q_dtype);
-  if (!q || !sel || !workspace) return fail(KVQ_EINVAL, "q/sel/workspace is NULL");
+  if (!q || !sel) return fail(KVQ_EINVAL, "q/sel is NULL");
   if (!aligned(q, 16) || !aligned(sel, 16)) return fail(KVQ_EALIGN, "q/sel not 16-byte aligned");
-  if (!aligned(workspace, 256)) return fail(KVQ_EALIGN, "workspace not 256-byte aligned");
+  if (((long long)kv_len + 63) / 64 > kvq::kMaxSelectBlocks) return fail(KVQ_ECAPACITY, "kv_len %d > 2^24", kv_len);
   if (n_sel < 1) return fail(KVQ_EINVAL, "n_sel must be >= 1");
   if (n_sink < 0 || n_recent < 0 || (long long)n_sink + n_recent > n_sel)
     return fail(KVQ_EINVAL, "n_sink and n_recent must be >= 0 and together at most n_sel");
-  const SelectSpace w = select_space(v, n_q, kv_len);
-  if (workspace_bytes < w.total) return fail(KVQ_EWORKSPACE, "workspace %zu < required %zu", workspace_bytes, w.total);
-  char *ws = static_cast<char *>(workspace);
   const kvq::BlockSelectArgs a = {v, bounds->codes, bounds->scale, q, q_dtype, n_q_heads / v.H, n_q, kv_len, causal ? 1 : 0,
-                                  q_pos0, kvq::is_hadamard(v.layout) ? 1 : 0, seq_lens, n_sel, n_sink, n_recent, w.stride,
-                                  reinterpret_cast<float *>(ws), reinterpret_cast<int32_t *>(ws + w.counts), sel};
+                                  q_pos0, kvq::is_hadamard(v.layout) ? 1 : 0, seq_lens, n_sel, n_sink, n_recent, sel};
   const cudaError_t e = kvq::launch_block_select(a, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(KVQ_ECUDA, "block select launch: %s", cudaGetErrorString(e));
   return KVQ_OK;
@@ -1504,7 +1484,7 @@ kvq::CacheView list_view(const kvq::CacheView &v, int n_q, int n_sel) {
 
 // The attention's arguments and workspace (its own, then the tables, the lengths and the queries by list).
 struct SparseSpace {
-  size_t table, lens, queries, total;
+  size_t table, lens, queries, scores, total;
 };
 kvq_status resolve_sparse(const kvq::CacheView &v, int n_q_heads, int n_q, int n_sel, int chunk, kvq::AttendArgs &a, SparseSpace &w,
                           void *ws) {
@@ -1517,7 +1497,13 @@ kvq_status resolve_sparse(const kvq::CacheView &v, int n_q_heads, int n_q, int n
   w.table = round_up(need, 256);
   w.lens = w.table + round_up(lists * n_sel * sizeof(int32_t), 256);
   w.queries = w.lens + round_up(lists * sizeof(int32_t), 256);
-  w.total = w.queries + (n_q > 1 ? lists * (n_q_heads / v.H) * v.D * sizeof(float) : 0);
+  w.scores = w.queries + (n_q > 1 ? round_up(lists * (n_q_heads / v.H) * v.D * sizeof(float), 256) : 0);
+  // The decode kernels of the other layouts are held to float32 where they leave scores behind (their probabilities are taken
+  // 2^12 larger then): Q8_0, 64 rows of 32 blocks 1.0e-5 -> 7e-7 of the output's norm, 79 -> 89 us
+  a.s_rows = kvq::is_b64(v.layout) ? 0 : kvq::score_rows(v.layout, v.v_layout, v.D, a.gqa);
+  a.s_tokens = n_sel * 64;
+  if (ws && a.s_rows > 0) a.part_s = reinterpret_cast<float *>(static_cast<char *>(ws) + w.scores);
+  w.total = w.scores + lists * a.s_tokens * a.s_rows * sizeof(float);
   return KVQ_OK;
 }
 
@@ -1579,38 +1565,25 @@ kvq_status kvq_paged_block_bounds_update(const kvq_paged_cache *cache, const kvq
   return run_bounds(v, bounds, 0, v.cap, n_fresh, seq_lens, stream);
 }
 
-size_t kvq_block_select_workspace_bytes(const kvq_cache *cache, int32_t n_q, int32_t kv_len) {
-  kvq::CacheView v;
-  if (check_cache(cache, v) != KVQ_OK || check_blocks(v, v.H, n_q) != KVQ_OK || kv_len < 1 || kv_len > v.cap) return 0;
-  return select_space(v, n_q, kv_len).total;
-}
-size_t kvq_paged_block_select_workspace_bytes(const kvq_paged_cache *cache, int32_t n_q, int32_t max_kv_len) {
-  kvq::CacheView v;
-  if (check_paged_cache(cache, v) != KVQ_OK || check_blocks(v, v.H, n_q) != KVQ_OK || max_kv_len < 1 || max_kv_len > v.cap) return 0;
-  return select_space(v, n_q, max_kv_len).total;
-}
-
 kvq_status kvq_block_select(const kvq_cache *cache, const kvq_block_bounds *bounds, const void *q, int32_t q_dtype,
                             int32_t n_q_heads, int32_t n_q, int32_t kv_len, int32_t causal, int32_t q_pos0, int32_t n_sel,
-                            int32_t n_sink, int32_t n_recent, int32_t *sel, void *workspace, size_t workspace_bytes,
-                            kvq_stream_t stream) {
+                            int32_t n_sink, int32_t n_recent, int32_t *sel, kvq_stream_t stream) {
   g_last_error[0] = 0;
   kvq::CacheView v;
   const kvq_status st = check_cache(cache, v);
   if (st != KVQ_OK) return st;
   return run_block_select(v, bounds, q, q_dtype, n_q_heads, n_q, nullptr, kv_len, causal, q_pos0, n_sel, n_sink, n_recent, sel,
-                          workspace, workspace_bytes, stream);
+                          stream);
 }
 kvq_status kvq_paged_block_select(const kvq_paged_cache *cache, const kvq_block_bounds *bounds, const void *q, int32_t q_dtype,
                                   int32_t n_q_heads, int32_t n_q, const int32_t *seq_lens, int32_t max_kv_len, int32_t causal,
-                                  int32_t n_sel, int32_t n_sink, int32_t n_recent, int32_t *sel, void *workspace,
-                                  size_t workspace_bytes, kvq_stream_t stream) {
+                                  int32_t n_sel, int32_t n_sink, int32_t n_recent, int32_t *sel, kvq_stream_t stream) {
   g_last_error[0] = 0;
   kvq::CacheView v;
   const kvq_status st = check_paged_cache(cache, v);
   if (st != KVQ_OK) return st;
   return run_block_select(v, bounds, q, q_dtype, n_q_heads, n_q, seq_lens, max_kv_len, causal, 0, n_sel, n_sink, n_recent, sel,
-                          workspace, workspace_bytes, stream);
+                          stream);
 }
 
 size_t kvq_sparse_attend_workspace_bytes(const kvq_cache *cache, int32_t n_q_heads, int32_t n_q, int32_t n_sel, int32_t chunk) {

@@ -620,8 +620,7 @@ cudaError_t launch_de(const AttendArgs &a, cudaStream_t st) {
 
 cudaError_t launch_join_b64(const AttendArgs &a, cudaStream_t st) {
   const unsigned rows = (unsigned)((size_t)a.cache.B * a.Hq * a.n_q);
-  int dev = 0, sms = 148;
-  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int sms = sm_count();
   // few rows have many partials each
   const bool split = rows <= 8u * (unsigned)sms;
   cudaLaunchConfig_t cfg;

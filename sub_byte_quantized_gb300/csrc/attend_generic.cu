@@ -19,7 +19,6 @@
 #include <cfloat>
 
 #include "kvq_internal.cuh"
-#include "unpack.cuh"
 
 namespace kvq {
 namespace {
@@ -36,6 +35,53 @@ __device__ __forceinline__ void chunk_range(const AttendArgs &a, const SeqLen &s
   } else {
     t0 = sl.n_body + (c - a.n_chunks) * kWinChunk;
     t1 = min(sl.kv_len, t0 + kWinChunk);
+  }
+}
+
+// Unpack 8 values (group gi of a token row) of a packed row into f32 (value = code * scale [+ zero]).
+// For the Hadamard layouts the raw signed codes are produced (the per-token scale is applied by
+// the caller).
+__device__ __forceinline__ void unpack8(const CacheView &c, int kv, size_t row, int gi, float out[8]) {
+  const int layout = kv ? c.v_layout : c.layout;          // each plane's own layout (mixed K/V)
+  const uint8_t *p = (kv ? c.payload[1] : c.payload[0]) + row * (size_t)(kv ? c.v_row_bytes : c.row_bytes);
+  const int blk = gi >> 2, sub = gi & 3;
+  if (layout == KVQ_HAD_INT4) {
+    const uint32_t w = *reinterpret_cast<const uint32_t *>(p + gi * 4);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) out[i] = (float)((int)((w >> (4 * i)) & 0xFu ^ 0x8u) - 8);
+    return;
+  }
+  if (layout == KVQ_HAD_INT2) {                       // four 2-bit fields per byte, (v ^ 2) - 2
+    const uint32_t w = *reinterpret_cast<const uint16_t *>(p + gi * 2);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) out[i] = (float)((int)((w >> (2 * i)) & 0x3u ^ 0x2u) - 2);
+    return;
+  }
+  const float s = __half2float(static_cast<const __half *>((kv ? c.scale[1] : c.scale[0]))[row * (c.D / kBlock) + blk]);
+  if (layout == KVQ_Q4_0) {
+    const uint32_t w = *reinterpret_cast<const uint32_t *>(p + blk * 16 + sub * 4);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) out[i] = (float)((int)((w >> (4 * i)) & 0xFu ^ 0x8u) - 8) * s;
+  } else if (layout == KVQ_Q6_0) {
+    const uint32_t lo = *reinterpret_cast<const uint32_t *>(p + blk * 24 + sub * 4);
+    const uint32_t hi = *reinterpret_cast<const uint16_t *>(p + blk * 24 + 16 + sub * 2);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t v = ((lo >> (4 * i)) & 0xFu) | (((hi >> (2 * i)) & 0x3u) << 4);
+      out[i] = (float)((int)(v ^ 0x20u) - 0x20) * s;
+    }
+  } else if (layout == KVQ_Q8_0) {                    // byte i = value i, (v ^ 0x80) - 0x80
+    const uint2 w = *reinterpret_cast<const uint2 *>(p + blk * 32 + sub * 8);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t b = ((i < 4 ? w.x : w.y) >> (8 * (i & 3))) & 0xFFu;
+      out[i] = (float)((int)(b ^ 0x80u) - 0x80) * s;
+    }
+  } else {  // ASYM4_G32
+    const float z = __half2float((kv ? c.zero[1] : c.zero[0])[row * (c.D / kBlock) + blk]);
+    const uint32_t w = *reinterpret_cast<const uint32_t *>(p + blk * 16 + sub * 4);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) out[i] = fmaf((float)((w >> (4 * i)) & 0xFu), s, z);
   }
 }
 
@@ -123,7 +169,7 @@ __global__ void __launch_bounds__(kThreads) attend_generic_kernel(AttendArgs a) 
           v[0] = x0.x; v[1] = x0.y; v[2] = x0.z; v[3] = x0.w; v[4] = x1.x; v[5] = x1.y; v[6] = x1.z; v[7] = x1.w;
         } else {
           const size_t crow = cache_row(c, b, kvh, tok);
-          unpack8(kv ? c.v_layout : c.layout, c, kv, crow, gi, v);
+          unpack8(c, kv, crow, gi, v);
           if (had && gi == 0) {
             const float s = static_cast<const float *>((kv ? c.scale[1] : c.scale[0]))[crow];
             (kv ? vs : ks)[t] = s;

@@ -36,6 +36,8 @@ __host__ __device__ constexpr int digit_at(int d) { return d == 0 ? 0 : 4096 + 1
 constexpr int kBins = digit_at(3), kGroups = kBins / 32;   // counters; their sums in groups of 32
 template <int THREADS>                   // histograms, their groups' sums, per-warp counts, results
 __host__ __device__ constexpr int select_fixed() { return (kBins + kGroups + 2 * (THREADS / 32) + 4) * 4; }
+constexpr int kBlockSelectSmem = (kMaxSelectBlocks / 8 + 256) * 4 + select_fixed<512>();   // of the longest lists
+static_assert(kBlockSelectSmem <= 200 * 1024, "the longest lists' scores fit");
 constexpr int kSelMaxKeys = (227 * 1024 - select_fixed<1024>()) / 4 / 128 * 128;   // keys one CTA can hold
 
 // Keys compare like the scores: NaN counts as -infinity, -0 as +0. No score has a key below 2^22: key 0 stands for
@@ -84,11 +86,111 @@ __device__ __forceinline__ int find_bin(const uint32_t (&c)[OWN], const uint32_t
   return bin;
 }
 
-// RESIDENT: the slice's keys fit shared memory (else every pass reads the scores again).
-template <int THREADS, bool RESIDENT>
-__global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_select_kernel(SelectArgs a) {
+// Where the scores come from: memory, or (the blocks that a query selects) the bounds of the keys.
+struct ScoresInMemory {
+  static constexpr int D = 0;
+};
+template <int DIM>
+struct ScoresOfBlocks {
+  static constexpr int D = DIM;
+  BlockSelectArgs s;
+};
+// The blocks that list `vb` = (sequence, kv head, query) sees.
+__device__ __forceinline__ int blocks_seen(const BlockSelectArgs &s, int vb) {
+  const int bh = vb / s.n_q, i = vb - bh * s.n_q, b = bh / s.cache.H;
+  const int len = s.seq_lens ? min(max(__ldg(s.seq_lens + b), 0), s.kv_len) : s.kv_len;
+  const int limit = s.causal ? min(len - 1, (s.seq_lens ? len - s.n_q : s.q_pos0) + i) : len - 1;
+  return limit < 0 ? 0 : (limit >> 6) + 1;
+}
+// Scores of the blocks [s0, s0 + n) of list vb into `score`: the query heads' rows in int8 (their negative and positive parts
+// apart, eight heads at a time), four threads per block.
+constexpr int kRowsAtOnce = 8;
+template <int THREADS, int D>
+__device__ __forceinline__ void score_blocks(const BlockSelectArgs &a, int vb, int s0, int n, float *score) {
+  constexpr int V = D / 32;
+  __shared__ __align__(16) int8_t q_neg[kRowsAtOnce][D], q_pos[kRowsAtOnce][D];
+  __shared__ float q_step[kRowsAtOnce];
+  const CacheView &c = a.cache;
+  const int bh = vb / a.n_q, i = vb - bh * a.n_q, b = bh / c.H, h = bh - b * c.H;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, part = tid & 3;
+  for (int r0 = 0; r0 < a.gqa; r0 += kRowsAtOnce) {
+    if (r0 > 0) __syncthreads();
+    if (warp < kRowsAtOnce && r0 + warp < a.gqa) {
+      const size_t row = ((size_t)bh * a.gqa + r0 + warp) * a.n_q + i;
+      float x[V], s;
+      int q8[V];
+      if (V == 4) load4_f32(a.q, a.q_dtype, row * D + lane * 4, x);
+      else load8_f32(a.q, a.q_dtype, row * D + lane * 8, x);
+      if (a.rotated) {
+        s = had_query_row<V>(x, q8, lane);
+      } else {
+        float top = 0.0f;
+#pragma unroll
+        for (int k = 0; k < V; ++k) top = fmaxf(top, fabsf(x[k]));
+#pragma unroll
+        for (int m = 16; m; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+        s = __fdiv_rn(top, 127.0f);
+#pragma unroll
+        for (int k = 0; k < V; ++k) q8[k] = s > 0.0f ? (int)fminf(fmaxf(rintf(__fdiv_rn(x[k], s)), -127.0f), 127.0f) : 0;
+      }
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        q_neg[warp][lane * V + k] = (int8_t)min(q8[k], 0);
+        q_pos[warp][lane * V + k] = (int8_t)max(q8[k], 0);
+      }
+      if (lane == 0) q_step[warp] = s;
+    }
+    __syncthreads();
+    const int rows = min(kRowsAtOnce, a.gqa - r0);
+    for (int i0 = 0; i0 < n; i0 += THREADS / 4) {        // whole warps: the sums below need all lanes
+      const int j = i0 + (tid >> 2);
+      const bool live = j < n;
+      uint4 lo[D / 64], hi[D / 64];                      // the thread's quarter of the block's bounds
+      float scale = 0.0f;
+      if (live) {
+        const size_t at = cache_row(c, b, h, (s0 + j) << 6) >> 6;
+        const uint4 *p = reinterpret_cast<const uint4 *>(a.codes + at * 2 * D) + part * (D / 64);
+#pragma unroll
+        for (int k = 0; k < D / 64; ++k) {
+          lo[k] = __ldg(p + k);
+          hi[k] = __ldg(p + D / 16 + k);
+        }
+        scale = __ldg(a.scale + at);
+      } else {
+#pragma unroll
+        for (int k = 0; k < D / 64; ++k) lo[k] = hi[k] = make_uint4(0u, 0u, 0u, 0u);
+      }
+      float best = -INFINITY;
+      for (int r = 0; r < rows; ++r) {
+        int dot = 0;
+#pragma unroll
+        for (int k = 0; k < D / 64; ++k) {
+          const uint4 x = *reinterpret_cast<const uint4 *>(&q_neg[r][(part * (D / 64) + k) * 16]);
+          const uint4 y = *reinterpret_cast<const uint4 *>(&q_pos[r][(part * (D / 64) + k) * 16]);
+          dot = __dp4a((int)x.x, (int)lo[k].x, dot);
+          dot = __dp4a((int)x.y, (int)lo[k].y, dot);
+          dot = __dp4a((int)x.z, (int)lo[k].z, dot);
+          dot = __dp4a((int)x.w, (int)lo[k].w, dot);
+          dot = __dp4a((int)y.x, (int)hi[k].x, dot);
+          dot = __dp4a((int)y.y, (int)hi[k].y, dot);
+          dot = __dp4a((int)y.z, (int)hi[k].z, dot);
+          dot = __dp4a((int)y.w, (int)hi[k].w, dot);
+        }
+        dot += __shfl_xor_sync(0xffffffffu, dot, 1);
+        dot += __shfl_xor_sync(0xffffffffu, dot, 2);
+        best = fmaxf(best, __fmul_rn((float)dot, q_step[r]));
+      }
+      best = __fmul_rn(best, scale);                     // (its rounding keeps the order: as if the largest were taken after it)
+      if (live && part == 0) score[j] = r0 > 0 ? fmaxf(score[j], best) : best;
+    }
+  }
+  __syncthreads();
+}
+
+// RESIDENT: the slice's keys fit shared memory (else every pass reads the scores again). RANKS: CTAs of a cluster, at most.
+template <int THREADS, int RANKS, bool RESIDENT, class Source>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_select_kernel(SelectArgs a, Source src) {
   constexpr int WARPS = THREADS / 32;
-  constexpr int RANKS = THREADS == 512 ? 1 : 8;          // CTAs of a cluster, at most
   extern __shared__ __align__(16) uint32_t sm[];
   uint32_t *hist = sm, *group = hist + kBins;
   uint32_t *wcount = group + kGroups;                    // [2][WARPS]
@@ -98,7 +200,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_select_kernel(S
   const int rank = (int)cl.block_rank(), ranks = (int)cl.num_blocks();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int bh = blockIdx.x / ranks, b = bh / a.H;
-  const int L = a.seq_lens ? min(max(__ldg(a.seq_lens + b), 0), a.kv_len) : a.kv_len;
+  int L;
+  if constexpr (Source::D > 0) L = blocks_seen(src.s, bh);
+  else L = a.seq_lens ? min(max(__ldg(a.seq_lens + b), 0), a.kv_len) : a.kv_len;
   int32_t *keep = a.keep + (size_t)bh * a.n_keep;
   if (a.new_lens && bh % a.H == 0 && rank == 0 && tid == 0) a.new_lens[b] = min(L, a.n_keep);
   if (L <= a.n_keep) {                                   // everything stays (the whole cluster takes this branch)
@@ -116,7 +220,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_select_kernel(S
   const int lo4 = lo & ~3, per = ((hi - lo4 + ranks - 1) / ranks + 31) / 32 * 32;
   const int s0 = (int)min((long long)hi, lo4 + (long long)rank * per);
   const int n = min(per, hi - s0), np = (n + 127) / 128 * 128;
-  const float *score = a.scores + (size_t)bh * a.stride + s0;
+  const float *score = nullptr;
+  if constexpr (Source::D == 0) score = a.scores + (size_t)bh * a.stride + s0;
   auto key_of = [&](int i, float x) { return i < n && s0 + i >= lo ? score_key(x) : 0u; };
   auto four = [&](int i, uint32_t (&key)[4]) {
     if constexpr (RESIDENT) {
@@ -127,7 +232,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_select_kernel(S
       for (int j = 0; j < 4; ++j) key[j] = key_of(i + j, i + j < n ? __ldg(score + i + j) : 0.0f);
     }
   };
-  if constexpr (RESIDENT) {
+  if constexpr (Source::D > 0) {
+    float *fresh = reinterpret_cast<float *>(keys);
+    score_blocks<THREADS, Source::D>(src.s, bh, s0, max(n, 0), fresh);
+    for (int i = tid; i < np; i += THREADS) keys[i] = key_of(i, i < n ? fresh[i] : 0.0f);
+  } else if constexpr (RESIDENT) {
     if (a.stride % 4 == 0) {                             // rows and slices begin at 16-byte boundaries
 #pragma unroll 1
       for (int i0 = 4 * tid; i0 < np; i0 += 16 * THREADS) {   // four loads in flight
@@ -507,10 +616,11 @@ int device_sms() {
   return sms;
 }
 
-template <int THREADS, bool RESIDENT>
-cudaError_t launch_select(const SelectArgs &a, int ranks, int keys, cudaStream_t st) {
+template <int THREADS, int RANKS, bool RESIDENT, class Source>
+cudaError_t launch_select(const SelectArgs &a, const Source &src, int ranks, int keys, cudaStream_t st) {
   static std::atomic<bool> done[kMaxDevices];
-  cudaError_t e = set_smem_once(done, evict_select_kernel<THREADS, RESIDENT>, 227 * 1024);
+  auto kernel = evict_select_kernel<THREADS, RANKS, RESIDENT, Source>;
+  cudaError_t e = set_smem_once(done, kernel, Source::D > 0 ? kBlockSelectSmem : 227 * 1024);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ranks * a.B * a.H);
@@ -523,7 +633,7 @@ cudaError_t launch_select(const SelectArgs &a, int ranks, int keys, cudaStream_t
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, evict_select_kernel<THREADS, RESIDENT>, a);
+  return cudaLaunchKernelEx(&cfg, kernel, a, src);
 }
 
 }  // namespace
@@ -533,9 +643,22 @@ cudaError_t launch_evict_select(const SelectArgs &a, cudaStream_t st) {
   int ranks = 1;
   while (ranks < 8 && (long long)ranks * 8192 < a.kv_len) ranks *= 2;
   const int keys = ((a.kv_len + ranks - 1) / ranks + 31 + 127) / 128 * 128;
-  if (keys > kSelMaxKeys) return launch_select<1024, false>(a, ranks, 0, st);
+  if (keys > kSelMaxKeys) return launch_select<1024, 8, false>(a, ScoresInMemory{}, ranks, 0, st);
   // rows of one CTA: half the threads, two CTAs per SM
-  return ranks == 1 ? launch_select<512, true>(a, ranks, keys, st) : launch_select<1024, true>(a, ranks, keys, st);
+  return ranks == 1 ? launch_select<512, 1, true>(a, ScoresInMemory{}, ranks, keys, st)
+                    : launch_select<1024, 8, true>(a, ScoresInMemory{}, ranks, keys, st);
+}
+
+cudaError_t launch_block_select(const BlockSelectArgs &b, cudaStream_t st) {
+  const int lists = b.cache.B * b.cache.H * b.n_q, blocks = (int)(((long long)b.kv_len + 63) / 64);
+  // CTAs per list: one per 128 blocks (the scores of as many are one pass of its threads) where all are resident at once (two
+  // per SM), and at most 8192 blocks each
+  int ranks = 1;
+  while (ranks < 8 && (ranks * 8192LL < blocks || (ranks * 128 < blocks && ranks * lists <= sm_count()))) ranks *= 2;
+  const int keys = ((blocks + ranks - 1) / ranks + 31 + 127) / 128 * 128;
+  const SelectArgs a = {lists, 1, blocks, b.n_sel, b.n_sink, b.n_recent, 0, nullptr, nullptr, b.sel, nullptr};
+  return b.cache.D == 128 ? launch_select<512, 8, true>(a, ScoresOfBlocks<128>{b}, ranks, keys, st)
+                          : launch_select<512, 8, true>(a, ScoresOfBlocks<256>{b}, ranks, keys, st);
 }
 
 namespace {

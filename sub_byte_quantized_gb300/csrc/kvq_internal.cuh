@@ -101,6 +101,18 @@ inline cudaError_t set_smem_once(std::atomic<bool> (&done)[kMaxDevices], K *kern
   return cudaSuccess;
 }
 
+// SMs of the current device, asked for once per device.
+inline int sm_count() {
+  static std::atomic<int> known[kMaxDevices];
+  int dev = 0, sms = 148;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return sms;
+  const int n = known[dev].load(std::memory_order_relaxed);
+  if (n > 0) return n;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 148;
+  known[dev].store(sms, std::memory_order_relaxed);
+  return sms;
+}
+
 // Device-side view of a cache; index 0 = K, 1 = V. Rows of the payload / scale / zero planes:
 // contiguous [B][H][cap] (page_shift < 0), or a paged pool [n_pages][H][page] addressed through
 // the block table [B][table_stride] (page = 1 << page_shift tokens, at least 64; cap is then the
@@ -304,8 +316,8 @@ struct BoundsArgs {
   const int32_t *seq_lens;
 };
 cudaError_t launch_block_bounds(const BoundsArgs &a, cudaStream_t st);
-// The blocks selected for each (sequence, kv head, query): sel [B][H][n_q][n_sel]; scores [lists][stride] and counts [lists] are
-// workspace.
+// The blocks selected for each (sequence, kv head, query): sel [B][H][n_q][n_sel].
+constexpr int kMaxSelectBlocks = 1 << 18;
 struct BlockSelectArgs {
   CacheView cache;
   const int8_t *codes;
@@ -314,9 +326,7 @@ struct BlockSelectArgs {
   int q_dtype, gqa, n_q, kv_len, causal, q_pos0, rotated;
   const int32_t *seq_lens;
   int n_sel, n_sink, n_recent;
-  long long stride;
-  float *scores;
-  int32_t *counts, *sel;
+  int32_t *sel;
 };
 cudaError_t launch_block_select(const BlockSelectArgs &a, cudaStream_t st);
 // Lists -> the tables [lists][n_sel] and lengths [lists] of sequences of one kv head, and (n_q > 1) the queries by list.

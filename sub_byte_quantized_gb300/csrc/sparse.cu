@@ -7,7 +7,7 @@
 // no q8 . k of the block exceeds. q8 >= 0 takes hi and q8 < 0 takes lo, so with q+ = max(q8, 0) and q- = min(q8, 0) it is
 // q+ . hi + q- . lo: dp4a, exact integers (below 2^24), then two rounded products: the same bits whatever the order. The
 // query heads of a kv head read one cache, so they share a list: the largest of their scores counts.
-// Lists: the blocks with the highest scores, by the radix selection that the budget's calls use.
+// Lists: the blocks with the highest scores, by the radix selection that the budget's calls use, whose kernel scores them too.
 // Attention: each (query, kv head) is a sequence of its own of one kv head, whose table names the selected blocks in the
 // same pool: a page of one head is a contiguous run of rows, so a pool [n_pages][H][page] is a pool of n_pages * H * page / 64
 // pages of one head and 64 tokens, and a contiguous cache [B][H][cap] one of B * H * cap / 64. The attention kernels read it
@@ -15,8 +15,9 @@
 //
 // Bound: the bounds pass by the packed keys' bytes (a decode step renews one block per head: latency); scores and selection
 // by latency; the attention by the selected rows' bytes, a few of them by latency too.
+#include <cuda_fp8.h>
+
 #include "kvq_internal.cuh"
-#include "unpack.cuh"
 
 namespace kvq {
 namespace {
@@ -31,166 +32,137 @@ __device__ __forceinline__ int clamped_len(const int32_t *seq_lens, int b, int k
   return seq_lens ? min(max(__ldg(seq_lens + b), 0), kv_len) : kv_len;
 }
 
-// One CTA per (block, head): threads hold 8 channels each and split the tokens.
-template <int LAYOUT, int D>
-__global__ void __launch_bounds__(kThreads) block_bounds_kernel(BoundsArgs a) {
-  constexpr int GROUPS = D / 8, LANES = kThreads / GROUPS, LEN = 64 / LANES;   // LANES threads share a channel group
-  __shared__ float lo_s[kWarps][D], hi_s[kWarps][D], top_s[kWarps];
-  const CacheView &c = a.cache;
-  const int b = blockIdx.y / c.H, h = blockIdx.y - b * c.H, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int end = clamped_len(a.seq_lens, b, a.kv_len), first = a.seq_lens ? max(end - a.n_fresh, 0) : a.first;
-  const int blk = (first >> 6) + blockIdx.x;
-  if (first >= end || (blk << 6) >= end) return;
-  const int gi = tid % GROUPS, t0 = (blk << 6) + tid / GROUPS;
-  const size_t row0 = cache_row(c, b, h, blk << 6);
-  float lo[8], hi[8];
+// Codes of 32 consecutive channels of a row, as they were read and as floats (value = code * scale [+ zero]). Integer fields
+// become floats under the exponent of 2^23 (and an addition that takes the offset away): the conversion instructions run at a
+// quarter of the rate.
+template <int LAYOUT>
+struct Raw32 {
+  static constexpr int WORDS = LAYOUT == KVQ_HAD_INT2 ? 2 : LAYOUT == KVQ_Q6_0 ? 6 : LAYOUT == KVQ_Q8_0 || is_b64(LAYOUT) ? 8 : 4;
+  uint32_t w[WORDS];
+  float scale, zero;
+  __device__ __forceinline__ void load(const CacheView &c, size_t row, int blk) {
+    const uint8_t *p = c.payload[0] + row * (size_t)c.row_bytes + blk * 4 * WORDS;
+    if constexpr (WORDS % 4 == 0) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) lo[i] = INFINITY, hi[i] = -INFINITY;
+      for (int i = 0; i < WORDS; i += 4) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p) + i / 4);
+        w[i] = v.x; w[i + 1] = v.y; w[i + 2] = v.z; w[i + 3] = v.w;
+      }
+    } else {
 #pragma unroll
-  for (int j = 0; j < LEN; ++j) {
-    const int t = t0 + j * LANES;
-    if (t < end) {
-      const size_t row = row0 + (t & 63);
-      float x[8];
-      unpack8(LAYOUT, c, 0, row, gi, x);
-      const float s = is_b64(LAYOUT) ? static_cast<const float *>(c.scale[0])[row >> 6]
-                      : is_hadamard(LAYOUT) ? static_cast<const float *>(c.scale[0])[row] : 1.0f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (is_b64(LAYOUT) || is_hadamard(LAYOUT)) x[i] = __fmul_rn(x[i], s);
-        lo[i] = fminf(lo[i], x[i]);
-        hi[i] = fmaxf(hi[i], x[i]);
+      for (int i = 0; i < WORDS; i += 2) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p) + i / 2);
+        w[i] = v.x; w[i + 1] = v.y;
       }
     }
+    if constexpr (is_b64(LAYOUT)) scale = 1.0f;          // one scale per block: it joins the bounds
+    else if constexpr (is_hadamard(LAYOUT)) scale = __ldg(static_cast<const float *>(c.scale[0]) + row);
+    else scale = __half2float(static_cast<const __half *>(c.scale[0])[row * (c.D / kBlock) + blk]);
+    zero = LAYOUT == KVQ_ASYM4_G32 ? __half2float(c.zero[0][row * (c.D / kBlock) + blk]) : 0.0f;
   }
-  if constexpr (GROUPS == 16) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      lo[i] = fminf(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], 16));
-      hi[i] = fmaxf(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], 16));
+  static __device__ __forceinline__ float offset_code(uint32_t u, float offset) {   // u < 2^23
+    return __uint_as_float(0x4B000000u | u) - (8388608.0f + offset);
+  }
+  __device__ __forceinline__ float value(int i) const {
+    float x;
+    if constexpr (LAYOUT == KVQ_Q4_0 || LAYOUT == KVQ_ASYM4_G32) {
+      // The field stays where it is: code 2^p under 2^23, and the scale is divided by 2^p (f16 scales: exact).
+      const int p = 4 * (i & 3);
+      const uint32_t word = (i & 4) ? w[i >> 3] >> 16 : w[i >> 3], flip = LAYOUT == KVQ_Q4_0 ? 8u << p : 0u;
+      x = __uint_as_float((word & (0xFu << p)) ^ (0x4B000000u | flip)) - (8388608.0f + (float)flip);
+      const float s = scale * (1.0f / (float)(1 << p));
+      return LAYOUT == KVQ_Q4_0 ? __fmul_rn(x, s) : fmaf(x, s, zero);
+    } else if constexpr (LAYOUT == KVQ_HAD_INT4) {
+      x = offset_code(((w[i >> 3] >> (4 * (i & 7))) & 0xFu) ^ 8u, 8.0f);
+    } else if constexpr (LAYOUT == KVQ_HAD_INT2) {
+      x = offset_code(((w[i >> 4] >> (2 * (i & 15))) & 3u) ^ 2u, 2.0f);
+    } else if constexpr (LAYOUT == KVQ_Q6_0) {
+      x = offset_code((((w[i >> 3] >> (4 * (i & 7))) & 0xFu) | (((w[4 + (i >> 4)] >> (2 * (i & 15))) & 3u) << 4)) ^ 32u, 32.0f);
+    } else if constexpr (LAYOUT == KVQ_E4M3_B64) {
+      const uint32_t two = (w[i >> 2] >> (16 * ((i >> 1) & 1))) & 0xFFFFu;
+      const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3)));
+      return (i & 1) ? f.y : f.x;
+    } else {
+      x = offset_code(((w[i >> 2] >> (8 * (i & 3))) & 0xFFu) ^ 0x80u, 128.0f);
     }
+    return is_b64(LAYOUT) ? x : __fmul_rn(x, scale);
   }
-  if (lane < GROUPS) {
+};
+
+// One warp per (block, head): lane = (token lane, 32 channels); each passes over its tokens, then the token lanes halve their
+// channels with each other until every lane has the bounds of a few.
+template <int LAYOUT, int D>
+__global__ void __launch_bounds__(kThreads) block_bounds_kernel(BoundsArgs a) {
+  constexpr int PARTS = D / 32, TL = 32 / PARTS, EACH = 64 / TL, OWN = 32 / TL;   // token lanes, tokens each, channels in the end
+  const CacheView &c = a.cache;
+  const int b = blockIdx.y / c.H, h = blockIdx.y - b * c.H, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int end = clamped_len(a.seq_lens, b, a.kv_len), first = a.seq_lens ? max(end - a.n_fresh, 0) : a.first;
+  const long long blk64 = (long long)(first >> 6) + (long long)blockIdx.x * kWarps + warp;
+  if (first >= end || blk64 * 64 >= end) return;         // whole warps
+  const int blk = (int)blk64, part = lane % PARTS, tl = lane / PARTS, n = min(64, end - 64 * blk);
+  const size_t row0 = cache_row(c, b, h, 64 * blk);
+  float lo[32], hi[32];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      lo_s[warp][8 * gi + i] = lo[i];
-      hi_s[warp][8 * gi + i] = hi[i];
+  for (int i = 0; i < 32; ++i) lo[i] = INFINITY, hi[i] = -INFINITY;
+  constexpr int AT_ONCE = Raw32<LAYOUT>::WORDS > 4 ? 2 : 4;
+#pragma unroll 1
+  for (int j0 = 0; j0 < EACH; j0 += AT_ONCE) {
+    Raw32<LAYOUT> raw[AT_ONCE];
+    // tokens behind the end read the block's first row again: what they bring is there already
+#pragma unroll
+    for (int j = 0; j < AT_ONCE; ++j) {
+      const int t = tl + (j0 + j) * TL;
+      raw[j].load(c, row0 + (t < n ? t : 0), part);
     }
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+#pragma unroll
+      for (int j = 0; j < AT_ONCE; j += 2) {
+        const float x = raw[j].value(i), y = raw[j + 1].value(i);
+        lo[i] = fminf(fminf(lo[i], x), y);
+        hi[i] = fmaxf(fmaxf(hi[i], x), y);
+      }
   }
-  __syncthreads();
-  // thread: D * 2 / 256 bounds, those of dims d = tid % D
-  constexpr int OWN = 2 * D / kThreads;
-  float v[OWN], top = 0.0f;
+  int mine = 32 * part;                                  // the first channel of the lane's
 #pragma unroll
-  for (int k = 0; k < OWN; ++k) {
-    const int e = tid + k * kThreads, d = e % D;
-    const bool up = e >= D;
-    v[k] = up ? hi_s[0][d] : lo_s[0][d];
+  for (int half = 16, m = 16; half >= OWN; half >>= 1, m >>= 1) {
+    const bool up = lane & m;
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) v[k] = up ? fmaxf(v[k], hi_s[w][d]) : fminf(v[k], lo_s[w][d]);
-    top = fmaxf(top, fabsf(v[k]));
+    for (int i = 0; i < half; ++i) {
+      const float l = __shfl_xor_sync(0xffffffffu, up ? lo[i] : lo[i + half], m);
+      const float g = __shfl_xor_sync(0xffffffffu, up ? hi[i] : hi[i + half], m);
+      lo[i] = fminf(up ? lo[i + half] : lo[i], l);
+      hi[i] = fmaxf(up ? hi[i + half] : hi[i], g);
+    }
+    if (up) mine += half;
+  }
+  const float each = is_b64(LAYOUT) ? __ldg(static_cast<const float *>(c.scale[0]) + (row0 >> 6)) : 1.0f;
+  float top = 0.0f;
+#pragma unroll
+  for (int i = 0; i < OWN; ++i) {
+    if (is_b64(LAYOUT)) {                                // (a rounded product keeps the order)
+      lo[i] = __fmul_rn(lo[i], each);
+      hi[i] = __fmul_rn(hi[i], each);
+    }
+    top = fmaxf(top, fmaxf(fabsf(lo[i]), fabsf(hi[i])));
   }
 #pragma unroll
   for (int m = 16; m; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-  if (lane == 0) top_s[warp] = top;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, top_s[w]);
   const float s = __fdiv_rn(top, 127.0f);
   const size_t at = row0 >> 6;
-  if (tid == 0) a.scale[at] = s;
+  if (lane == 0) a.scale[at] = s;
+  uint32_t code[2][OWN / 4];
 #pragma unroll
-  for (int k = 0; k < OWN; ++k) {
-    const int e = tid + k * kThreads;
-    const float x = s > 0.0f ? __fdiv_rn(v[k], s) : 0.0f;
-    a.codes[at * 2 * D + e] = (int8_t)fminf(fmaxf(e >= D ? ceilf(x) : floorf(x), -127.0f), 127.0f);
+  for (int i = 0; i < OWN; ++i) {
+    const float l = s > 0.0f ? floorf(__fdiv_rn(lo[i], s)) : 0.0f, g = s > 0.0f ? ceilf(__fdiv_rn(hi[i], s)) : 0.0f;
+    const uint32_t cl = (uint32_t)(int)fminf(fmaxf(l, -127.0f), 127.0f) & 0xFFu, cg = (uint32_t)(int)fminf(fmaxf(g, -127.0f), 127.0f) & 0xFFu;
+    code[0][i >> 2] = (i & 3) ? code[0][i >> 2] | cl << (8 * (i & 3)) : cl;
+    code[1][i >> 2] = (i & 3) ? code[1][i >> 2] | cg << (8 * (i & 3)) : cg;
   }
-}
-
-// Scores of kTile blocks for one (query, kv head): the heads' rows in int8 in shared memory, four threads per block.
-constexpr int kTile = 64;
-constexpr int kRows = 8;                                 // query heads at a time
-template <int D>
-__global__ void __launch_bounds__(kThreads) block_scores_kernel(BlockSelectArgs a) {
-  constexpr int V = D / 32;
-  __shared__ __align__(16) int8_t q_neg[kRows][D], q_pos[kRows][D];
-  __shared__ float q_step[kRows];
-  const CacheView &c = a.cache;
-  const int vb = blockIdx.y, bh = vb / a.n_q, i = vb - bh * a.n_q, b = bh / c.H, h = bh - b * c.H;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int len = clamped_len(a.seq_lens, b, a.kv_len);
-  const int limit = a.causal ? min(len - 1, (a.seq_lens ? len - a.n_q : a.q_pos0) + i) : len - 1;
-  const int n = limit < 0 ? 0 : (limit >> 6) + 1;        // blocks that the row sees
-  if (blockIdx.x == 0 && tid == 0) a.counts[vb] = n;
-  const int blk = blockIdx.x * kTile + (tid >> 2);
-  if (blockIdx.x * kTile >= n || n <= a.n_sel) return;   // (few blocks: all are kept, and no score is read)
-  uint4 lo[D / 64], hi[D / 64];                          // the thread's quarter of the block's bounds
-  float scale = 0.0f;
-  const bool live = blk < n;
-  if (live) {
-    const size_t at = block_index(c, b, h, blk);
-    const uint4 *p = reinterpret_cast<const uint4 *>(a.codes + at * 2 * D) + (tid & 3) * (D / 64);
 #pragma unroll
-    for (int k = 0; k < D / 64; ++k) {
-      lo[k] = __ldg(p + k);
-      hi[k] = __ldg(p + D / 16 + k);
-    }
-    scale = __ldg(a.scale + at);
-  }
-  float best = -INFINITY;
-  for (int r0 = 0; r0 < a.gqa; r0 += kRows) {
-    __syncthreads();
-    if (r0 + warp < a.gqa) {
-      const size_t row = ((size_t)bh * a.gqa + r0 + warp) * a.n_q + i;
-      float x[V];
-      int q8[V];
-      if (V == 4) load4_f32(a.q, a.q_dtype, row * D + lane * 4, x);
-      else load8_f32(a.q, a.q_dtype, row * D + lane * 8, x);
-      float s;
-      if (a.rotated) {
-        s = had_query_row<V>(x, q8, lane);
-      } else {
-        float top = 0.0f;
+  for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int k = 0; k < V; ++k) top = fmaxf(top, fabsf(x[k]));
-#pragma unroll
-        for (int m = 16; m; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-        s = __fdiv_rn(top, 127.0f);
-#pragma unroll
-        for (int k = 0; k < V; ++k) q8[k] = s > 0.0f ? (int)fminf(fmaxf(rintf(__fdiv_rn(x[k], s)), -127.0f), 127.0f) : 0;
-      }
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        q_neg[warp][lane * V + k] = (int8_t)min(q8[k], 0);
-        q_pos[warp][lane * V + k] = (int8_t)max(q8[k], 0);
-      }
-      if (lane == 0) q_step[warp] = s;
-    }
-    __syncthreads();
-    const int rows = min(kRows, a.gqa - r0);
-    for (int r = 0; r < rows; ++r) {
-      int dot = 0;
-#pragma unroll
-      for (int k = 0; k < D / 64; ++k) {
-        const uint4 n4 = *reinterpret_cast<const uint4 *>(&q_neg[r][((tid & 3) * (D / 64) + k) * 16]);
-        const uint4 p4 = *reinterpret_cast<const uint4 *>(&q_pos[r][((tid & 3) * (D / 64) + k) * 16]);
-        if (live) {
-          dot = __dp4a((int)n4.x, (int)lo[k].x, dot);
-          dot = __dp4a((int)n4.y, (int)lo[k].y, dot);
-          dot = __dp4a((int)n4.z, (int)lo[k].z, dot);
-          dot = __dp4a((int)n4.w, (int)lo[k].w, dot);
-          dot = __dp4a((int)p4.x, (int)hi[k].x, dot);
-          dot = __dp4a((int)p4.y, (int)hi[k].y, dot);
-          dot = __dp4a((int)p4.z, (int)hi[k].z, dot);
-          dot = __dp4a((int)p4.w, (int)hi[k].w, dot);
-        }
-      }
-      dot += __shfl_xor_sync(0xffffffffu, dot, 1);
-      dot += __shfl_xor_sync(0xffffffffu, dot, 2);
-      best = fmaxf(best, __fmul_rn((float)dot, q_step[r]));
-    }
-  }
-  if (live && (tid & 3) == 0) a.scores[(size_t)vb * a.stride + blk] = __fmul_rn(best, scale);
+    for (int i = 0; i < OWN / 4; ++i) *reinterpret_cast<uint32_t *>(a.codes + (at * 2 + k) * D + mine + 4 * i) = code[k][i];
 }
 
 // One warp per list: the selected blocks as pages of one head, and the sequence's length. A list ends at the first
@@ -240,7 +212,7 @@ cudaError_t launch_bounds_t(const BoundsArgs &a, dim3 grid, cudaStream_t st) {
 
 cudaError_t launch_block_bounds(const BoundsArgs &a, cudaStream_t st) {
   const long long blocks = a.seq_lens ? ((long long)min(a.n_fresh, a.kv_len) + 62) / 64 + 1 : ((long long)a.kv_len + 63) / 64 - a.first / 64;
-  const dim3 grid((unsigned)blocks, (unsigned)(a.cache.B * a.cache.H));
+  const dim3 grid((unsigned)((blocks + kWarps - 1) / kWarps), (unsigned)(a.cache.B * a.cache.H));
   switch (a.cache.layout) {
     case KVQ_Q4_0: return launch_bounds_t<KVQ_Q4_0>(a, grid, st);
     case KVQ_Q6_0: return launch_bounds_t<KVQ_Q6_0>(a, grid, st);
@@ -251,17 +223,6 @@ cudaError_t launch_block_bounds(const BoundsArgs &a, cudaStream_t st) {
     case KVQ_INT8_B64: return launch_bounds_t<KVQ_INT8_B64>(a, grid, st);
     default: return launch_bounds_t<KVQ_E4M3_B64>(a, grid, st);
   }
-}
-
-cudaError_t launch_block_select(const BlockSelectArgs &a, cudaStream_t st) {
-  const int lists = a.cache.B * a.cache.H * a.n_q, blocks = (int)(((long long)a.kv_len + 63) / 64);
-  const dim3 grid((unsigned)((blocks + kTile - 1) / kTile), (unsigned)lists);
-  if (a.cache.D == 128) block_scores_kernel<128><<<grid, kThreads, 0, st>>>(a);
-  else block_scores_kernel<256><<<grid, kThreads, 0, st>>>(a);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  SelectArgs s = {lists, 1, blocks, a.n_sel, a.n_sink, a.n_recent, a.stride, a.scores, a.counts, a.sel, nullptr};
-  return launch_evict_select(s, st);
 }
 
 cudaError_t launch_sparse_prepare(const SparseArgs &a, cudaStream_t st) {

@@ -124,12 +124,12 @@ def _bounds(codes=P, scale=P):
 BIG = 1 << 40
 
 
-def _sel(L, paged=False, cache=None, bounds=None, q=P, qdt=1, hq=2, nq=1, lens=P, kv=60, causal=0, q0=0, n=4, sink=1, recent=1, sel=P, ws=P, wsb=BIG):
+def _sel(L, paged=False, cache=None, bounds=None, q=P, qdt=1, hq=2, nq=1, lens=P, kv=60, causal=0, q0=0, n=4, sink=1, recent=1, sel=P):
     c = cache if cache is not None else (_paged() if paged else _cache())
     b = C.byref(bounds if bounds is not None else _bounds())
     if paged:
-        return L.kvq_paged_block_select(C.byref(c), b, q, qdt, hq, nq, lens, kv, causal, n, sink, recent, sel, ws, wsb, None)
-    return L.kvq_block_select(C.byref(c), b, q, qdt, hq, nq, kv, causal, q0, n, sink, recent, sel, ws, wsb, None)
+        return L.kvq_paged_block_select(C.byref(c), b, q, qdt, hq, nq, lens, kv, causal, n, sink, recent, sel, None)
+    return L.kvq_block_select(C.byref(c), b, q, qdt, hq, nq, kv, causal, q0, n, sink, recent, sel, None)
 
 
 def _sparse(L, paged=False, cache=None, q=P, qdt=1, hq=2, nq=1, lens=P, kv=60, causal=0, q0=0, scale=0.1, sel=P, n=4, chunk=0, out=P, ws=P, wsb=BIG):
@@ -143,12 +143,10 @@ def _sparse(L, paged=False, cache=None, q=P, qdt=1, hq=2, nq=1, lens=P, kv=60, c
 @pytest.mark.parametrize("f", [_sel, _sparse])
 def test_block_calls_refusals(L, f, paged):
     call = lambda **kw: f(L, paged, **kw)                                          # noqa: E731
-    assert call(q=None) == EINVAL and call(sel=None) == EINVAL and call(ws=None) == EINVAL
-    assert call(q=P + 4) == EALIGN and call(sel=P + 4) == EALIGN and call(ws=P + 16) == EALIGN
+    assert call(q=None) == EINVAL and call(sel=None) == EINVAL and call(q=P + 4) == EALIGN and call(sel=P + 4) == EALIGN
     assert call(qdt=3) == EINVAL and call(hq=0) == EINVAL and call(nq=0) == EINVAL and call(hq=3) == ESHAPE
     assert call(n=0) == EINVAL and call(kv=0) == EINVAL and call(kv=65 if not paged else 257) == ECAPACITY
     assert call(nq=40000) == ESHAPE                                                # batch * heads * n_q
-    assert call(wsb=0) == EWORKSPACE
     cache = _paged if paged else _cache
     assert call(cache=cache(2, n_recent=32)) == EUNSUPPORTED
     if paged:
@@ -158,14 +156,15 @@ def test_block_calls_refusals(L, f, paged):
     if f is _sel:
         assert call(sink=-1) == EINVAL and call(recent=-1) == EINVAL and call(sink=3, recent=2) == EINVAL and call(sink=2 ** 31 - 1, recent=2 ** 31 - 1) == EINVAL
         assert call(bounds=_bounds(None)) == EINVAL and call(bounds=_bounds(P, None)) == EINVAL and call(bounds=_bounds(P + 8)) == EALIGN
+        big = _paged(page=1 << 20, pages=17) if paged else _cache(cap=(1 << 24) + 64)
+        assert call(cache=big, kv=(1 << 24) + 1) == ECAPACITY
     else:
+        assert call(ws=None) == EINVAL and call(ws=P + 16) == EALIGN and call(wsb=0) == EWORKSPACE
         assert call(scale=float("nan")) == EINVAL and call(chunk=100) == ESHAPE and call(out=None) == EINVAL and call(n=1 << 25) == EINVAL
 
 
 def test_block_workspaces(L):
     c, pg = _cache(cap=640), _paged(pages=10)
-    assert L.kvq_block_select_workspace_bytes(C.byref(c), 2, 640) > 0 and L.kvq_paged_block_select_workspace_bytes(C.byref(pg), 2, 640) > 0
-    assert L.kvq_block_select_workspace_bytes(C.byref(c), 2, 641) == 0 and L.kvq_block_select_workspace_bytes(None, 2, 64) == 0
     need = L.kvq_sparse_attend_workspace_bytes(C.byref(c), 4, 3, 5, 64)
     assert need > 0 and L.kvq_sparse_attend_workspace_bytes(C.byref(c), 3, 3, 5, 64) == 0
     assert _sparse(L, cache=c, hq=4, nq=3, n=5, chunk=64, kv=640, wsb=need - 1) == EWORKSPACE
