@@ -195,8 +195,8 @@ int auto_chunk(const kvq::CacheView &c, int rows, int n_body, int n_heads, long 
   if (!total_given) work = (long long)(n_body > 0 ? n_body : 1) * n_heads;
   long long chunk;
   if (kvq::is_b64(c.layout)) {
-    // every resident CTA takes as many tokens; each group of eight query rows counts
-    const long long ctas = (long long)sms * kvq::kB64CtasPerSm(c.D), groups = (rows + 7) / 8;
+    // every resident CTA takes as many tokens; each group of query rows counts
+    const long long ctas = (long long)sms * kvq::b64_ctas(c.D, rows), per = kvq::b64_group(c.D, rows), groups = (rows + per - 1) / per;
     chunk = ((work * groups + ctas - 1) / ctas + 63) / 64 * 64;
   } else if (c.layout == KVQ_Q6_0 && kvq::mma_q6_shape(c.D, rows) && !kvq::prefill_shape(c.layout, c.v_layout, c.D, rows)) {
     // one chunk per resident CTA; each group of four query rows has its own CTAs
@@ -257,18 +257,20 @@ int auto_chunk(const kvq::CacheView &c, int rows, int n_body, int n_heads, long 
 kvq_status resolve_b64(kvq::AttendArgs &a, int chunk, size_t &need, void *ws) {
   const kvq::CacheView &c = a.cache;
   const int sms = kvq::sm_count();
-  const long long heads = (long long)c.B * c.H * ((a.gqa * (long long)a.n_q + 7) / 8);
+  const long long rows = a.gqa * (long long)a.n_q;
+  a.group = kvq::b64_group(c.D, rows);
+  const long long heads = (long long)c.B * c.H * ((rows + a.group - 1) / a.group);
   const long long units = heads * (((long long)a.kv_len + 63) / 64);
   a.per = chunk / 64;
-  const long long grid = chunk ? heads * ((((long long)a.kv_len + 63) / 64 + a.per - 1) / a.per) : std::min((long long)sms * kvq::kB64CtasPerSm(c.D), units);
-  if (grid + heads > INT_MAX / 8) return fail(KVQ_ESHAPE, "too many rows and chunks for one call");
+  const long long grid = chunk ? heads * ((((long long)a.kv_len + 63) / 64 + a.per - 1) / a.per) : std::min((long long)sms * kvq::b64_ctas(c.D, rows), units);
+  if (grid + heads > INT_MAX / a.group) return fail(KVQ_ESHAPE, "too many rows and chunks for one call");
   a.grid = (int)grid;
   const size_t parts = (size_t)(grid + heads);
   size_t off = 0;
-  const size_t o_m = off; off = round_up(off + parts * 8 * sizeof(float), 256);
-  const size_t o_l = off; off = round_up(off + parts * 8 * sizeof(float), 256);
+  const size_t o_m = off; off = round_up(off + parts * a.group * sizeof(float), 256);
+  const size_t o_l = off; off = round_up(off + parts * a.group * sizeof(float), 256);
   const size_t o_s = off; off = round_up(off + (size_t)heads * sizeof(int2), 256);
-  const size_t o_o = off; off = round_up(off + parts * 8 * c.D * sizeof(float), 256);
+  const size_t o_o = off; off = round_up(off + parts * a.group * c.D * sizeof(float), 256);
   need = off;
   if (ws) {
     char *w = static_cast<char *>(ws);
@@ -326,6 +328,7 @@ kvq_status resolve_core(int n_q_heads, int n_q, int kv_len, int causal, int q_po
   a.s_rows = a.s_tokens = 0;
   a.out_nq = 1;
   a.grid = a.per = 0;
+  a.group = 8;
   a.spans = nullptr;
   if (kvq::is_b64(c.layout)) return resolve_b64(a, given, need, ws);
   const size_t rows = (size_t)c.B * n_q_heads * n_q;
@@ -745,8 +748,8 @@ void phase1_capacity(const kvq::CacheView &c, int rows, int q_dtype, int &ctas_p
   ctas_per_unit = 1;
   window_ctas = false;                                   // the decode kernels leave the window to phase 2
   if (kvq::is_b64(c.layout)) {
-    ctas_per_sm = kvq::kB64CtasPerSm(c.D);
-    ctas_per_unit = (rows + 7) / 8;
+    ctas_per_sm = kvq::b64_ctas(c.D, rows);
+    ctas_per_unit = (rows + kvq::b64_group(c.D, rows) - 1) / kvq::b64_group(c.D, rows);
   } else if (c.layout == KVQ_Q6_0 && c.v_layout == KVQ_Q6_0 && kvq::mma_q6_shape(c.D, rows) &&
       !(kvq::prefill_shape(c.layout, c.v_layout, c.D, rows) && q_dtype != KVQ_F32)) {
     ctas_per_sm = kvq::kMmaQ6CtasPerSm(c.D);

@@ -25,18 +25,14 @@
 // bank conflicts. At a head's end the warps' states are combined in shared memory.
 //
 // Bound: the packed cache's bytes from HBM.
-#include <cfloat>
-#include <type_traits>
-
-#include "kvq_internal.cuh"
-#include "mma_util.cuh"
+#include "attend_b64.cuh"
 
 namespace kvq {
 namespace {
 using namespace mma;
+using namespace b64;
 
 constexpr int kWarps = 4;
-constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D>
 struct Cfg {
@@ -48,90 +44,12 @@ struct Cfg {
   static constexpr int PITCH = D + 4;                     // floats of a row of a warp's state: free of bank conflicts
   static_assert(kWarps * 8 * (PITCH + 2) * 4 <= SMEM, "the warps' states reuse the stages");
 };
-constexpr float kRise = 3.9f;            // 2^(12 + 3.9) < 65504
-// What a CTA pays for a second head, in units: a piece may be so much longer than an even share.
-constexpr int kSlack = 5;
 
 // 16-byte column j of row `row`.
 template <int D>
 __device__ __forceinline__ uint32_t swz(int row, int j) {
   return (uint32_t)(row * D + ((j ^ (row & 7)) << 4));
 }
-// Two codes each -> exact f16 pairs. K: bytes (0, 1) and (2, 3) of a word; V: bytes (0, 2) and (1, 3).
-template <bool E4M3, bool V>
-__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t &a, uint32_t &b) {
-  if constexpr (E4M3) {
-    if (V) w = prmt(w, 0u, 0x3120u);
-    asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %2;\ncvt.rn.f16x2.e4m3x2 %0, l;\ncvt.rn.f16x2.e4m3x2 %1, h;\n}\n" : "=r"(a), "=r"(b) : "r"(w));
-  } else {                                               // the code plus 128 under the exponent of 1024, less 1152
-    const uint32_t x = w ^ 0x80808080u;
-    a = hadd2(prmt(x, 0x64646464u, V ? 0x4240u : 0x4140u), 0xE480E480u);
-    b = hadd2(prmt(x, 0x64646464u, V ? 0x4341u : 0x4342u), 0xE480E480u);
-  }
-}
-
-// Where a run of units stands: sequence b, head `hd` of it (kv head * groups + group), its blocks [blk, blk + n).
-struct Span {
-  int b, hd, blk, n, len;      // len: tokens of the sequence that some row sees
-};
-// Tokens of sequence b that the call looks at.
-template <bool PAGED>
-__device__ __forceinline__ int seen_len(const AttendArgs &a, int b) {
-  if constexpr (PAGED) return min(max(__ldg(a.seq_lens + b), 0), a.kv_len);
-  else return a.causal ? min(a.kv_len, a.q_pos0 + a.n_q) : a.kv_len;
-}
-__device__ __forceinline__ int blocks_of(int len) { return (int)(((long long)len + 63) >> 6); }
-__device__ __forceinline__ int pieces_of(int blocks, int per) { return (blocks + per - 1) / per; }
-__device__ __forceinline__ long long warp_sum(long long x) {
-#pragma unroll
-  for (int m = 16; m; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
-  return x;
-}
-
-// How a call's units are dealt out (by one warp).
-struct Deal {
-  long long per;               // units a CTA
-  bool pieces;                 // a CTA has one piece of one head
-};
-template <bool PAGED>
-__device__ __forceinline__ Deal deal_of(const AttendArgs &a, int heads, int lane) {
-  if (a.per > 0) return {a.per, true};                   // the caller's chunk: its grid holds every piece
-  const int B = a.cache.B;
-  long long total = 0;
-  if constexpr (PAGED) {
-    for (int b = lane; b < B; b += 32) total += (long long)heads * blocks_of(seen_len<PAGED>(a, b));
-    total = warp_sum(total);
-  } else {
-    total = (long long)B * heads * blocks_of(seen_len<PAGED>(a, 0));
-  }
-  const long long per = max(1LL, (total + gridDim.x - 1) / gridDim.x);
-  if (per > INT_MAX - kSlack) return {per, false};
-  long long n[kSlack] = {};                              // pieces of at most per + j units
-  if constexpr (PAGED) {
-    for (int b = lane; b < B; b += 32) {
-      const int nb = blocks_of(seen_len<PAGED>(a, b));
-#pragma unroll
-      for (int j = 0; j < kSlack; ++j) n[j] += pieces_of(nb, (int)per + j);
-    }
-#pragma unroll
-    for (int j = 0; j < kSlack; ++j) n[j] = warp_sum(n[j]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < kSlack; ++j) n[j] = (long long)B * pieces_of(blocks_of(seen_len<PAGED>(a, 0)), (int)per + j);
-  }
-#pragma unroll
-  for (int j = 0; j < kSlack; ++j)
-    if (n[j] * heads <= gridDim.x) return {per + j, true};
-  return {per, false};
-}
-// Weight of sequence b in the row of what is dealt out: its heads' pieces, or their units.
-template <bool PAGED>
-__device__ __forceinline__ long long share_of(const AttendArgs &a, const Deal &d, int heads, int b) {
-  if (b >= a.cache.B) return 0;
-  const int nb = blocks_of(seen_len<PAGED>(a, b));
-  return (long long)heads * (d.pieces ? pieces_of(nb, (int)d.per) : nb);
-}
-
 template <int D, bool E4M3, bool QSPLIT, bool PAGED>
 __global__ void __maxnreg__(D == 128 ? 152 : 224) attend_b64_kernel(AttendArgs a) {
   using C = Cfg<D>;
@@ -147,86 +65,18 @@ __global__ void __maxnreg__(D == 128 ? 152 : 224) attend_b64_kernel(AttendArgs a
   // lengths that the kernel before may have written (this call's own append does not)
   if (PAGED && a.fresh_tail == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
 #endif
-  // This CTA's first span, and (units dealt out) how many units it has.
   const Deal deal = deal_of<PAGED>(a, heads, lane);
-  Span sp = {0, 0, 0, 0, 0};
-  const long long u0 = deal.pieces ? (long long)blockIdx.x : deal.per * blockIdx.x;
-  long long left;
-  {
-    long long before = 0;                                // what the sequences in front of sp.b weigh
-    bool none = false;
-    if constexpr (PAGED) {
-      for (;; sp.b += 32) {
-        const long long own = share_of<PAGED>(a, deal, heads, sp.b + lane);
-        long long upto = own;
-#pragma unroll
-        for (int m = 1; m < 32; m <<= 1) {
-          const long long o = __shfl_up_sync(0xffffffffu, upto, m);
-          if (lane >= m) upto += o;
-        }
-        const unsigned over = __ballot_sync(0xffffffffu, before + upto > u0);
-        if (over) {
-          const int at = __ffs((int)over) - 1;
-          before += __shfl_sync(0xffffffffu, upto - own, at);
-          sp.b += at;
-          break;
-        }
-        before += __shfl_sync(0xffffffffu, upto, 31);
-        none = sp.b + 32 >= cv.B;
-        if (none) break;
-      }
-    } else {
-      const long long each = share_of<PAGED>(a, deal, heads, 0);
-      none = u0 >= each * cv.B;
-      sp.b = none ? 0 : (int)(u0 / each);
-      before = each * sp.b;
-    }
-    if (none) {                                          // more CTAs than work
-      pdl_wait_if(false);
-      return;
-    }
-    sp.len = seen_len<PAGED>(a, sp.b);
-    const int nb = blocks_of(sp.len);
-    if (deal.pieces) {                                   // a head in equal pieces
-      const int n = pieces_of(nb, (int)deal.per), at = (int)(u0 - before), size = (nb + n - 1) / n;
-      sp.hd = at / n;
-      sp.blk = (at - sp.hd * n) * size;
-      sp.n = max(0, min(size, nb - sp.blk));
-      left = sp.n;
-    } else {
-      sp.hd = (int)((u0 - before) / nb);
-      sp.blk = (int)((u0 - before) - (long long)sp.hd * nb);
-      sp.n = (int)min(deal.per, (long long)nb - sp.blk);
-      left = deal.per;                                   // (the last CTA's may end earlier: there is no head behind it)
-    }
+  Walk<PAGED> walk(a, deal, heads, lane);
+  Span &sp = walk.sp;
+  if (sp.n == 0) {                                       // more CTAs than work
+    pdl_wait_if(false);
+    return;
   }
-  // the next head with tokens
-  auto advance = [&](Span &s) {
-    left -= s.n;
-    s.n = 0;
-    if (left <= 0) return;
-    if (++s.hd == heads) {
-      s.hd = 0;
-      do {
-        if (++s.b == cv.B) return;
-        s.len = seen_len<PAGED>(a, s.b);
-      } while (s.len <= 0);
-    }
-    s.blk = 0;
-    s.n = (int)min(left, (long long)blocks_of(s.len));
-  };
-
-  // Rows that the kernel before appends: CTAs that read them wait for it. (A CTA looks at its first head only where it
-  // has one alone.)
-  {
-    int lo = a.fresh_lo, hi = a.fresh_hi;
-    if (PAGED && a.fresh_tail > 0) lo = sp.len - a.fresh_tail, hi = sp.len;
-    pdl_wait_if(left > sp.n || (64 * sp.blk < hi && lo < 64 * (sp.blk + sp.n)));
-  }
+  walk.wait_for_append(a);
 
   uint8_t *ring = smem + warp * C::RING * C::BYTES;
   float *sm = reinterpret_cast<float *>(smem), *so = sm + kWarps * 16;
-  for (; sp.n > 0; advance(sp)) {
+  for (; sp.n > 0; walk.advance(a, heads)) {
   const int kvh = sp.hd / groups, row0 = 8 * (sp.hd - kvh * groups), rows = min(8, R - row0);
   const int t_first = 64 * sp.blk, t_end = min(sp.len, t_first + 64 * sp.n);
   SeqLen sl;
@@ -481,17 +331,7 @@ __global__ void __maxnreg__(D == 128 ? 152 : 224) attend_b64_kernel(AttendArgs a
       a.part_l[part * 8 + r] = L;
     }
   }
-  if (sp.blk == 0 && threadIdx.x == 0) {                 // the head's first and last CTA
-    const int nb = blocks_of(sp.len);
-    int last = (int)blockIdx.x;
-    if (deal.pieces) {
-      const int n = pieces_of(nb, (int)deal.per), size = (nb + n - 1) / n;
-      last += pieces_of(nb, size) - 1;                   // (equal sizes may need fewer pieces than there is room for)
-    } else {
-      last = (int)((u0 + (deal.per - left) + nb - 1) / deal.per);
-    }
-    a.spans[head] = make_int2((int)blockIdx.x, last);
-  }
+  if (sp.blk == 0 && threadIdx.x == 0) a.spans[head] = walk.ctas_of_head(deal);
   __syncthreads();                                       // the ring is free again
   }
 }
@@ -510,7 +350,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_b64_kernel(AttendArgs a,
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const size_t row = SPLIT ? (size_t)blockIdx.x : (size_t)blockIdx.x * kJoinWarps + warp;
   if (row >= n_rows) return;
-  const int R = a.gqa * a.n_q, groups = (R + 7) / 8;
+  const int R = a.gqa * a.n_q, groups = (R + a.group - 1) / a.group;
   const size_t bh = row / R;
   const int r = (int)(row - bh * R), b = (int)(bh / a.cache.H);
   const int len = a.seq_lens ? min(max(__ldg(a.seq_lens + b), 0), a.kv_len) : a.kv_len;
@@ -519,9 +359,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_b64_kernel(AttendArgs a,
 #pragma unroll
   for (int v = 0; v < V; ++v) O[v] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (len > 0) {
-    const size_t head = bh * groups + r / 8;
+    const size_t head = bh * groups + r / a.group;
     const int2 span = a.spans[head];
-    const size_t p0 = (head + span.x) * 8 + r % 8;
+    const size_t p0 = (head + span.x) * a.group + r % a.group;
     const int n = span.y - span.x + 1;
     for (int i0 = SPLIT ? warp : 0; i0 < n; i0 += kBatch * (SPLIT ? kJoinWarps : 1)) {
       float mc[kBatch], lc[kBatch], bm = M;
@@ -530,7 +370,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_b64_kernel(AttendArgs a,
       for (int u = 0; u < kBatch; ++u) {
         const int i = i0 + u * (SPLIT ? kJoinWarps : 1);
         const bool ok = i < n;
-        const size_t p = p0 + 8 * (size_t)(ok ? i : 0);
+        const size_t p = p0 + (size_t)a.group * (ok ? i : 0);
         mc[u] = ok ? a.part_m[p] : -INFINITY;
         lc[u] = ok ? a.part_l[p] : 0.0f;
 #pragma unroll
@@ -584,19 +424,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_b64_kernel(AttendArgs a,
   }
 }
 
-// A launch that may begin while the kernel before it still runs.
-void chained(cudaLaunchConfig_t &cfg, cudaLaunchAttribute &attr, unsigned ctas, int threads, int smem, cudaStream_t st) {
-  cfg = {};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-}
-
 template <int D, bool E4M3, bool QSPLIT, bool PAGED>
 cudaError_t launch_t(const AttendArgs &a, cudaStream_t st) {
   static std::atomic<bool> configured[kMaxDevices];
@@ -632,6 +459,7 @@ cudaError_t launch_join_b64(const AttendArgs &a, cudaStream_t st) {
 }
 
 cudaError_t launch_attend_b64(const AttendArgs &a, cudaStream_t st) {
+  if (a.group != 8) return launch_attend_b64_rows(a, st);
   if (a.cache.layout == KVQ_E4M3_B64) return a.cache.D == 128 ? launch_de<128, true>(a, st) : launch_de<256, true>(a, st);
   return a.cache.D == 128 ? launch_de<128, false>(a, st) : launch_de<256, false>(a, st);
 }

@@ -23,8 +23,14 @@ __host__ __device__ constexpr bool is_hadamard(int layout) {
 }
 // 8-bit layouts with one f32 scale per block of 64 tokens, head and plane.
 __host__ __device__ constexpr bool is_b64(int layout) { return layout == KVQ_INT8_B64 || layout == KVQ_E4M3_B64; }
-// Their phase 1: resident CTAs (of four warps) per SM.
+// Their phase 1: query rows of a kv head that a CTA takes at once (`rows`: of a kv head), and resident CTAs per SM.
+constexpr int kB64ManyRows = 128;
+#ifndef KVQ_B64_MANY
+#define KVQ_B64_MANY 32
+#endif
+__host__ __device__ constexpr int b64_group(int D, long long rows) { return D == 128 && rows > KVQ_B64_MANY ? kB64ManyRows : 8; }
 __host__ __device__ constexpr int kB64CtasPerSm(int D) { return D == 128 ? 3 : 2; }
+__host__ __device__ constexpr int b64_ctas(int D, long long rows) { return b64_group(D, rows) == 8 ? kB64CtasPerSm(D) : 1; }
 constexpr int kMaxDevices = 64;     // per-device one-time kernel attribute set-up
 
 // Tensor-core phase 1: resident CTAs (of four warps) per SM the kernel is built for; the
@@ -196,9 +202,9 @@ struct AttendArgs {
   // [B][Hq][out_nq][D]
   int out_nq;
   // 8-bit block layouts: the CTAs of phase 1, the longest piece of a head in blocks of 64 tokens (0: the call's blocks are
-  // dealt out evenly), and each head's first and last CTA [B][H_kv][groups of eight rows]; the partials are then
-  // [grid + B * H_kv * groups][8], maxima in base 2
-  int grid, per;
+  // dealt out evenly), the query rows of a kv head that a CTA takes at once, and each head's first and last CTA
+  // [B][H_kv][groups of such rows]; the partials are then [grid + B * H_kv * groups][group], maxima in base 2
+  int grid, per, group;
   int2 *spans;
 };
 // Output row of query row `row` of the call.
@@ -379,6 +385,7 @@ bool mma_supported(const AttendArgs &a);
 bool capture_supported(const AttendArgs &a);
 cudaError_t launch_attend_mma(const AttendArgs &a, cudaStream_t st);
 cudaError_t launch_attend_b64(const AttendArgs &a, cudaStream_t st);
+cudaError_t launch_attend_b64_rows(const AttendArgs &a, cudaStream_t st);
 cudaError_t launch_join_b64(const AttendArgs &a, cudaStream_t st);
 cudaError_t launch_attend_mma4(const AttendArgs &a, cudaStream_t st);
 bool mma_q6_supported(const AttendArgs &a);

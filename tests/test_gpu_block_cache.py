@@ -293,3 +293,59 @@ def test_ragged_runs_of_one_block(layout):
         for t in ("k", "v"):
             assert np.array_equal(c.planes[t]["scale"].transpose(0, 1).flatten(1, 2).cpu().numpy(), o.planes[t]["scale"][0])
             assert np.array_equal(c.planes[t]["payload"].transpose(0, 1).flatten(1, 2).cpu().numpy(), o.planes[t]["payload"][0])
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("D,dtype", [(128, "bf16"), (128, "f32"), (128, "f16"), (256, "bf16")])
+@pytest.mark.parametrize("gqa,n_q,S,causal", [(2, 130, 300, True), (8, 40, 130, True), (1, 33, 64, False), (16, 3, 500, False), (3, 129, 129, True), (1, 128, 1, False)])
+def test_attend_many_rows(layout, D, dtype, gqa, n_q, S, causal):
+    """Groups of rows of every kind: full, ended by the last row, rows that see one token, blocks that no row of a group sees."""
+    rng = np.random.default_rng(13)
+    B, H = 1, 2
+    c, o = _filled(layout, B, H, D, S, rng)
+    q, qn = _rows(rng, (B, H * gqa, n_q, D), dtype)
+    want = o.attend(qn, 1 / np.sqrt(D), [S] * B, causal)
+    for chunk in (0, 64, 192):
+        _near(kvq.decode_attend(c, q, S, causal=causal, q_pos0=S - n_q if causal else 0, chunk=chunk), want, chunk)
+    if causal and S > n_q:                                 # rows that are not the newest
+        kv = S - 1
+        got = kvq.decode_attend(c, q, S, causal=True, q_pos0=kv - n_q)
+        _near(got, o.attend(qn, 1 / np.sqrt(D), [kv] * B, True))
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_paged_attend_many_rows(layout, dtype):
+    rng = np.random.default_rng(14)
+    B, H, S, D, n_q = 4, 2, 330, 128, 70
+    c, o = _filled(layout, B, H, D, S, rng, 64)
+    q, qn = _rows(rng, (B, 2 * H, n_q, D), dtype)
+    lens = [0, 20, 191, 330]
+    d = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    for causal in (False, True):
+        want = [o.attend(qn, 1 / np.sqrt(D), [n if i == b else 0 for i in range(B)], causal) for b, n in enumerate(lens)]
+        for chunk in (0, 128):
+            got = kvq.paged_decode_attend(c, q, d, S, causal=causal, chunk=chunk)
+            _near(got, (sum(w[0] for w in want), sum(w[1] for w in want)), (causal, chunk))
+
+
+@pytest.mark.parametrize("n_q", [1, 64])
+@pytest.mark.parametrize("paged", [False, True])
+def test_units_dealt_over_many_heads(n_q, paged):
+    """More heads than CTAs, so that CTAs pass from one head to the next, and sequences of every length in between."""
+    rng = np.random.default_rng(15)
+    B, H, D, S = 70, 8, 128, 200
+    c, o = _filled("int8_b64", B, H, D, S, rng, 64 if paged else 0)
+    q, qn = _rows(rng, (B, 2 * H, n_q, D))
+    lens = rng.integers(0, S + 1, B) if paged else np.full(B, S)
+    lens[:3] = [S, 0, 1] if paged else S
+    if paged:
+        got = kvq.paged_decode_attend(c, q, torch.from_numpy(lens.astype(np.int32)).cuda(), S, causal=n_q > 1)
+    else:
+        got = kvq.decode_attend(c, q, S, causal=n_q > 1, q_pos0=S - n_q if n_q > 1 else 0)
+    some = [0, 1, 2, 3, 34, 69]
+    keep = np.zeros(B, int)
+    keep[some] = lens[some]
+    want, tol = o.attend(qn, 1 / np.sqrt(D), keep, n_q > 1)
+    err = np.abs(got.cpu().numpy() - want)
+    assert (err[some] <= tol[some]).all() and torch.isfinite(got).all()
