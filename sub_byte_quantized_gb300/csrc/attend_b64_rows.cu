@@ -4,8 +4,8 @@
 //   x = alpha log2(e) s_k (q . c),  p = 2^(x - m),  o += s_v (p . v)     as in attend_b64.cu, with the same exactness
 // Here the rows are on the M side of mma.sync.m16n8k16 and a warp holds its rows' queries, scores and outputs in registers: a
 // score's accumulator is the A operand of the product with V as it stands. A block's codes become f16 once for all 128 rows,
-// in shared memory (two buffers: while one is computed from, each thread turns the codes that it read a block ahead into the other),
-// rows of 256 bytes with an XOR swizzle of their 16-byte columns, so that ldmatrix (plain for K, transposed for V) is free of
+// in shared memory: each thread turns the codes that it read a block ahead into the next of three buffers, whose barriers let
+// warps run up to a block apart, so that one's softmax meets another's products. Rows of 256 bytes with an XOR swizzle of their 16-byte columns, so that ldmatrix (plain for K, transposed for V) is free of
 // bank conflicts. No warp needs another's state: partials are written from registers.
 //
 // Work is dealt out as in attend_b64.cu, with groups of 128 rows.
@@ -22,7 +22,8 @@ using namespace b64;
 constexpr int kThreads = 256, kRows = kB64ManyRows;
 constexpr int kD = 128, kKS = kD / 16;
 constexpr int kTile = 64 * kD * 2;                       // bytes of one plane of a block in f16
-constexpr int kSmem = 4 * kTile;
+constexpr int kBuffers = 3;
+constexpr int kSmem = 2 * kBuffers * kTile + 64;       // and a barrier pair per buffer
 
 // 16-byte column j of token row `row` of a tile.
 __device__ __forceinline__ uint32_t swz(int row, int j) { return (uint32_t)(row * 256 + ((j ^ (row & 7)) << 4)); }
@@ -46,7 +47,25 @@ __global__ void __launch_bounds__(kThreads, 1) attend_b64_rows_kernel(AttendArgs
     pdl_wait_if(false);
     return;
   }
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + 2 * kBuffers * kTile), *empty = full + kBuffers;
+  if (tid == 0) {
+#pragma unroll
+    for (int k = 0; k < 2 * kBuffers; ++k) bar_init(full + k, kThreads / 32);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
   walk.wait_for_append(a);
+  // Block number `it` of the CTA lies in buffer it % kBuffers, for the (it / kBuffers)-th time. Waits are bounded: a warp whose wait
+  // gives up goes on without waiting and leaves NaN behind.
+  int it = 0;
+  bool failed = false;
+  auto wait = [&](uint64_t *bar, int times) {
+    if (!failed && !bar_wait(bar, (uint32_t)(times & 1))) failed = true;
+  };
+  auto arrive = [&](uint64_t *bar) {
+    __syncwarp();
+    if (lane == 0) bar_arrive(bar);
+  };
 
   for (; sp.n > 0; walk.advance(a, heads)) {
     const int kvh = sp.hd / groups, row0 = kRows * (sp.hd - kvh * groups), wrow = row0 + 16 * warp;   // the warp's first row
@@ -60,7 +79,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_b64_rows_kernel(AttendArgs
 
     // A thread's codes: 16-byte pieces tid and tid + 256 of each plane (token p / 8, column p % 8), and the block's scales.
     uint4 raw[4];
-    float2 sc = make_float2(0.0f, 0.0f), sc_next = sc;
+    float2 sc = make_float2(0.0f, 0.0f), sc_next = sc;   // scales of the block computed from, and of the codes at hand
     auto fetch = [&](int i) {
       if (i >= n) return;
       const int t0 = 64 * (sp.blk + i);
@@ -140,24 +159,32 @@ __global__ void __launch_bounds__(kThreads, 1) attend_b64_rows_kernel(AttendArgs
 #pragma unroll
       for (int k = 0; k < 4; ++k) O[j][k] = 0.0f;
 
-    if (n > 0) convert(0);
-    sc = sc_next;
-    fetch(1);
-    __syncthreads();
+    float2 sc_then = sc;
+    auto prepare = [&](int i) {                          // block i of the span, whose codes have been read, and the read of the next
+      const int at = it + i, buffer = at % kBuffers;
+      if (at >= kBuffers) wait(empty + buffer, at / kBuffers - 1);
+      convert(buffer);
+      arrive(full + buffer);
+      sc_then = sc_next;
+      fetch(i + 1);
+    };
+    if (n > 0) prepare(0);
     for (int i = 0; i < n; ++i) {
+      sc = sc_then;
+      if (i + 1 < n) prepare(i + 1);
+      const int buffer = (it + i) % kBuffers;
+      wait(full + buffer, (it + i) / kBuffers);
       if (work) {
-        const uint32_t sK = smem_addr(smem + 2 * (i & 1) * kTile), sV = sK + kTile;
+        const uint32_t sK = smem_addr(smem + 2 * buffer * kTile), sV = sK + kTile;
         const int t0 = 64 * (sp.blk + i);
         const float f[2] = {alpha[0] * sc.x, alpha[1] * sc.x};
         // scores: s[t][k] is token t0 + 8 t + 2c + (k & 1), row g + 8 (k >> 1)
-        float s[8][4];
+        float s[8][4] = {};
         bool rise = false;
 #pragma unroll
-        for (int t = 0; t < 8; t += 2) {
+        for (int j = 0; j < kKS; ++j)                    // eight chains of products
 #pragma unroll
-          for (int k = 0; k < 4; ++k) s[t][k] = s[t + 1][k] = 0.0f;
-#pragma unroll
-          for (int j = 0; j < kKS; ++j) {                // matrices: tokens 8t .. (dims 16j, + 8), tokens 8(t + 1) .. (the same)
+          for (int t = 0; t < 8; t += 2) {               // matrices: tokens 8t .. (dims 16j, + 8), tokens 8(t + 1) .. (the same)
             uint32_t b[4];
             ldsm_x4(sK + swz(8 * t + 8 * (mi >> 1) + (lane & 7), 2 * j + (mi & 1)), b);
             mma16816(s[t], qh[j], b[0], b[1]);
@@ -168,14 +195,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_b64_rows_kernel(AttendArgs
             }
           }
 #pragma unroll
-          for (int u = 0; u < 2; ++u)
+        for (int t = 0; t < 8; ++t)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int tok = t0 + 8 * (t + u) + 2 * c + (k & 1);
-              s[t + u][k] = tok <= lim[k >> 1] ? s[t + u][k] * f[k >> 1] : -INFINITY;
-              rise = rise || s[t + u][k] > m[k >> 1] + kRise;
-            }
-        }
+          for (int k = 0; k < 4; ++k) {
+            const int tok = t0 + 8 * t + 2 * c + (k & 1);
+            s[t][k] = tok <= lim[k >> 1] ? s[t][k] * f[k >> 1] : -INFINITY;
+            rise = rise || s[t][k] > m[k >> 1] + kRise;
+          }
         // the reference follows the maximum only where a score passes it by kRise (attend_b64.cu)
         if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
@@ -209,28 +235,27 @@ __global__ void __launch_bounds__(kThreads, 1) attend_b64_rows_kernel(AttendArgs
           }
         const float sv = sc.y * 0x1p-12f;
 #pragma unroll
-        for (int j = 0; j < 2 * kKS; j += 2) {           // dims 8 j .. and 8 (j + 1) ..
-          float acc[2][4] = {};
+        for (int j = 0; j < 2 * kKS; j += 4) {           // dims 8 j .. 8 (j + 4)
+          float acc[4][4] = {};
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
-            uint32_t b[4];
-            ldsm_x4_t(sV + swz(16 * t + 8 * (mi & 1) + (lane & 7), j + (mi >> 1)), b);
-            mma16816(acc[0], ph[t], b[0], b[1]);
-            mma16816(acc[1], ph[t], b[2], b[3]);
-            mma16816(acc[0], pl[t], b[0], b[1]);
-            mma16816(acc[1], pl[t], b[2], b[3]);
+            uint32_t b[2][4];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) ldsm_x4_t(sV + swz(16 * t + 8 * (mi & 1) + (lane & 7), j + 2 * u + (mi >> 1)), b[u]);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) mma16816(acc[u], ph[t], b[u >> 1][2 * (u & 1)], b[u >> 1][2 * (u & 1) + 1]);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) mma16816(acc[u], pl[t], b[u >> 1][2 * (u & 1)], b[u >> 1][2 * (u & 1) + 1]);
           }
 #pragma unroll
-          for (int u = 0; u < 2; ++u)
+          for (int u = 0; u < 4; ++u)
 #pragma unroll
             for (int k = 0; k < 4; ++k) O[j + u][k] = fmaf(acc[u][k], sv, O[j + u][k]);
         }
       }
-      if (i + 1 < n) convert((i + 1) & 1);
-      sc = sc_next;
-      fetch(i + 2);
-      __syncthreads();                                   // the next block stands; this one's place is free
+      arrive(empty + buffer);
     }
+    it += max(n, 0);
     const size_t head = (size_t)sp.b * heads + sp.hd, part = (size_t)blockIdx.x + head;
     if (work) {
 #pragma unroll
@@ -245,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_b64_rows_kernel(AttendArgs
             *reinterpret_cast<float2 *>(a.part_o + p * kD + 8 * j + 2 * c) = make_float2(O[j][2 * k], O[j][2 * k + 1]);
           if (c == 0) {
             a.part_m[p] = m[k];
-            a.part_l[p] = l[k];
+            a.part_l[p] = failed ? __int_as_float(0x7FC00000) : l[k];
           }
         }
       }

@@ -26,7 +26,7 @@ __host__ __device__ constexpr bool is_b64(int layout) { return layout == KVQ_INT
 // Their phase 1: query rows of a kv head that a CTA takes at once (`rows`: of a kv head), and resident CTAs per SM.
 constexpr int kB64ManyRows = 128;
 #ifndef KVQ_B64_MANY
-#define KVQ_B64_MANY 32
+#define KVQ_B64_MANY 40
 #endif
 __host__ __device__ constexpr int b64_group(int D, long long rows) { return D == 128 && rows > KVQ_B64_MANY ? kB64ManyRows : 8; }
 __host__ __device__ constexpr int kB64CtasPerSm(int D) { return D == 128 ? 3 : 2; }
