@@ -1487,7 +1487,7 @@ kvq::CacheView list_view(const kvq::CacheView &v, int n_q, int n_sel) {
 
 // The attention's arguments and workspace (its own, then the tables, the lengths and the queries by list).
 struct SparseSpace {
-  size_t table, lens, queries, scores, total;
+  size_t table, lens, queries, total;
 };
 kvq_status resolve_sparse(const kvq::CacheView &v, int n_q_heads, int n_q, int n_sel, int chunk, kvq::AttendArgs &a, SparseSpace &w,
                           void *ws) {
@@ -1500,13 +1500,10 @@ kvq_status resolve_sparse(const kvq::CacheView &v, int n_q_heads, int n_q, int n
   w.table = round_up(need, 256);
   w.lens = w.table + round_up(lists * n_sel * sizeof(int32_t), 256);
   w.queries = w.lens + round_up(lists * sizeof(int32_t), 256);
-  w.scores = w.queries + (n_q > 1 ? round_up(lists * (n_q_heads / v.H) * v.D * sizeof(float), 256) : 0);
-  // The decode kernels of the other layouts are held to float32 where they leave scores behind (their probabilities are taken
-  // 2^12 larger then): Q8_0, 64 rows of 32 blocks 1.0e-5 -> 7e-7 of the output's norm, 79 -> 89 us
-  a.s_rows = kvq::is_b64(v.layout) ? 0 : kvq::score_rows(v.layout, v.v_layout, v.D, a.gqa);
-  a.s_tokens = n_sel * 64;
-  if (ws && a.s_rows > 0) a.part_s = reinterpret_cast<float *>(static_cast<char *>(ws) + w.scores);
-  w.total = w.scores + lists * a.s_tokens * a.s_rows * sizeof(float);
+  w.total = w.queries + (n_q > 1 ? lists * (n_q_heads / v.H) * v.D * sizeof(float) : 0);
+  // The decode kernels of the other layouts are held to float32 where they keep scores (their probabilities are taken 2^12
+  // larger then): here they keep none of their rows. Q8_0, 64 rows of 32 blocks 1.0e-5 -> 7e-7 of the output's norm
+  if (ws && kvq::score_rows(v.layout, v.v_layout, v.D, a.gqa) > 0) a.part_s = static_cast<float *>(ws);
   return KVQ_OK;
 }
 

@@ -215,13 +215,21 @@ __device__ __forceinline__ void store_run(const Run &u, int dtype, int tid, floa
   if (tid == 0) *u.scale = s;
   if (k > 0) {
     const float f = ldexpf(1.0f, -min(k, 64));
-    for (int r = r0; r < u.o; r += RP) {
-      uint2 *p = reinterpret_cast<uint2 *>(u.rows + r * D + col);
-      float y[8];
-      decode8<E4M3>(*p, y);
+    constexpr int AT_ONCE = 8;                           // rows read together: a decode step's warp has up to 63 of them
+    for (int r = r0; r < u.o; r += AT_ONCE * RP) {
+      uint2 was[AT_ONCE];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] *= f;
-      *p = encode8<E4M3>(y);
+      for (int j = 0; j < AT_ONCE; ++j)
+        was[j] = r + j * RP < u.o ? *reinterpret_cast<const uint2 *>(u.rows + (r + j * RP) * D + col) : make_uint2(0u, 0u);
+#pragma unroll
+      for (int j = 0; j < AT_ONCE; ++j) {
+        if (r + j * RP >= u.o) break;
+        float y[8];
+        decode8<E4M3>(was[j], y);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] *= f;
+        *reinterpret_cast<uint2 *>(u.rows + (r + j * RP) * D + col) = encode8<E4M3>(y);
+      }
     }
   }
   const float inv = s > 0x1p-100f && s < 0x1p100f && amax <= FLT_MAX ? __frcp_rn(s) : 0.0f;
