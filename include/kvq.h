@@ -200,7 +200,8 @@ int32_t kvq_attend_chunk(const kvq_cache *cache, int32_t n_q_heads, int32_t n_q,
  * (a multiple of 64 in [64, 8192], e.g. 512 as in [OTQ]; 0 = automatic, sized for the phase-1
  * kernel that runs and the current device's SM count -- one wave of resident warps or CTAs for
  * decode shapes, about four waves of 64-row CTAs for many query rows; kvq_attend_chunk returns
- * it) and writes per (row, chunk) the
+ * it; block layouts with chunk 0: the blocks are dealt out to one wave of CTAs from the lengths, on the
+ * device) and writes per (row, chunk) the
  * running max, the sum of exponentials and the unnormalised output to the workspace; phase 2
  * combines them with the online-softmax correction ([OTQ] Section 3.2). HAD_INT4 / HAD_INT2: the query
  * is rotated and quantised to int8 (one f32 scale per row, amax / 127), body tokens are

@@ -1502,7 +1502,7 @@ kvq_status resolve_sparse(const kvq::CacheView &v, int n_q_heads, int n_q, int n
   w.queries = w.lens + round_up(lists * sizeof(int32_t), 256);
   w.total = w.queries + (n_q > 1 ? lists * (n_q_heads / v.H) * v.D * sizeof(float) : 0);
   // The decode kernels of the other layouts are held to float32 where they keep scores (their probabilities are taken 2^12
-  // larger then): here they keep none of their rows. Q8_0, 64 rows of 32 blocks 1.0e-5 -> 7e-7 of the output's norm
+  // larger then): here they keep none of their rows. Q8_0, 64 rows of 32 blocks 1.0e-5 -> 7e-7 of the output's norm, 79 -> 87 us
   if (ws && kvq::score_rows(v.layout, v.v_layout, v.D, a.gqa) > 0) a.part_s = static_cast<float *>(ws);
   return KVQ_OK;
 }
