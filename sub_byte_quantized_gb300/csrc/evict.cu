@@ -652,7 +652,7 @@ cudaError_t launch_evict_select(const SelectArgs &a, cudaStream_t st) {
 cudaError_t launch_block_select(const BlockSelectArgs &b, cudaStream_t st) {
   const int lists = b.cache.B * b.cache.H * b.n_q, blocks = (int)(((long long)b.kv_len + 63) / 64);
   // CTAs per list: one per 128 blocks (the scores of as many are one pass of its threads) where all are resident at once (two
-  // per SM), and at most 8192 blocks each
+  // per SM), and at most 8192 blocks each (2048 blocks, 8 lists, with the bounds in front: 57.5 us with eight CTAs, 78.2 with one)
   int ranks = 1;
   while (ranks < 8 && (ranks * 8192LL < blocks || (ranks * 128 < blocks && ranks * lists <= sm_count()))) ranks *= 2;
   const int keys = ((blocks + ranks - 1) / ranks + 31 + 127) / 128 * 128;

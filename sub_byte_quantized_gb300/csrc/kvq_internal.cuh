@@ -24,6 +24,8 @@ __host__ __device__ constexpr bool is_hadamard(int layout) {
 // 8-bit layouts with one f32 scale per block of 64 tokens, head and plane.
 __host__ __device__ constexpr bool is_b64(int layout) { return layout == KVQ_INT8_B64 || layout == KVQ_E4M3_B64; }
 // Their phase 1: query rows of a kv head that a CTA takes at once (`rows`: of a kv head), and resident CTAs per SM.
+// Groups of 8 rows read the cache once each, groups of 128 compute for 128 (64 heads of 4096 tokens, 8 / 128: 32 rows 44 / 57 us,
+// 48 rows 58 in either).
 constexpr int kB64ManyRows = 128;
 #ifndef KVQ_B64_MANY
 #define KVQ_B64_MANY 40

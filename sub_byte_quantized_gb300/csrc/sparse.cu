@@ -15,6 +15,7 @@
 //
 // Bound: the bounds pass by the packed keys' bytes (a decode step renews one block per head: latency); scores and selection
 // by latency; the attention by the selected rows' bytes, a few of them by latency too.
+// Bounds of 128K tokens of 8 kv heads in Q4_0: 46 us, bound by their instructions (issue 65 %, DRAM 21 %); with the selection 57.5.
 #include <cuda_fp8.h>
 
 #include "kvq_internal.cuh"

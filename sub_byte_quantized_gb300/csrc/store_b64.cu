@@ -13,7 +13,9 @@
 // decode step: one row), a CTA of 8 warps else (a whole block: 16 KB of bf16 at head_dim 128); either way the rows stay in
 // registers between the pass over their maximum and the codes. This file is compiled with -fmad=false.
 //
-// Bound: the rows read and the codes written, once each; small appends by latency (load, reduce, divide, store).
+// Bound: the rows read and the codes written, once each; small appends by latency (load, reduce, divide, store). One token of 64
+// sequences, 8 kv heads, e4m3: 4.2 us, 5.3 where scales grow (the kept rows of a block are read eight at a time); 12200 tokens of 16 prompts by
+// slots 35.1 us, where instructions bind it (issue slots 54 % busy).
 #include <cfloat>
 #include <cuda_fp8.h>
 #include <type_traits>
@@ -390,6 +392,7 @@ __global__ void __launch_bounds__(kThreads) store_b64_slots_kernel(CacheView c, 
 
 template <int D, bool E4M3, bool F32>
 cudaError_t launch_dt(const CacheView &c, const void *k_new, const void *v_new, int dtype, const BlockGeom &g, cudaStream_t st) {
+  // a warp or a CTA for each run (64 sequences, 8 kv heads: one row 2.9 / 5.1 us, 8 rows 4.6 / 6.7)
   if (g.n_new <= kFewRows)
     store_b64_kernel<D, E4M3, 32, F32><<<(unsigned)((g.units + 7) / 8), kThreads, 0, st>>>(c, k_new, v_new, dtype, g);
   else

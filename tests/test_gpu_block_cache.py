@@ -349,3 +349,30 @@ def test_units_dealt_over_many_heads(n_q, paged):
     want, tol = o.attend(qn, 1 / np.sqrt(D), keep, n_q > 1)
     err = np.abs(got.cpu().numpy() - want)
     assert (err[some] <= tol[some]).all() and torch.isfinite(got).all()
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("D,n_q", [(128, 1), (128, 70), (256, 1)])
+def test_nothing_to_attend_to(layout, D, n_q):
+    """All sequences empty: zeros, whatever the output held, for dealt out and for planned chunks."""
+    rng = np.random.default_rng(21)
+    c, _ = _filled(layout, 3, 2, D, 100, rng, 64)
+    q, _ = _rows(rng, (3, 4, n_q, D))
+    lens = torch.zeros(3, dtype=torch.int32, device="cuda")
+    for chunk in (0, kvq.paged_attend_plan_chunk(c, 4, n_q, [0, 0, 0])):
+        out = torch.full((3, 4, n_q, D), float("nan"), device="cuda")
+        kvq.paged_decode_attend(c, q, lens, 100, chunk=chunk, out=out)
+        assert (out == 0).all()
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("n_q", [1, 70])
+def test_planned_chunk(layout, n_q):
+    rng = np.random.default_rng(22)
+    c, o = _filled(layout, 3, 2, 128, 700, rng, 64)
+    q, qn = _rows(rng, (3, 4, n_q, 128))
+    lens = [700, 3, 129]
+    chunk = kvq.paged_attend_plan_chunk(c, 4, n_q, lens)
+    got = kvq.paged_decode_attend(c, q, torch.tensor(lens, dtype=torch.int32, device="cuda"), 700, chunk=chunk)
+    want = [o.attend(qn, 1 / np.sqrt(128), [n if i == b else 0 for i in range(3)]) for b, n in enumerate(lens)]
+    _near(got, (sum(w[0] for w in want), sum(w[1] for w in want)), chunk)

@@ -180,3 +180,15 @@ def test_bounds_refusals(L):
     assert f(cache=_cache(5, n_recent=16)) == EUNSUPPORTED
     g = lambda lens=P, n=3, bounds=b: L.kvq_paged_block_bounds_update(C.byref(pg), C.byref(bounds), lens, n, None)                # noqa: E731
     assert g(n=0) == 0 and g(n=-1) == EINVAL and g(lens=None) == EINVAL and g(lens=P + 4) == EALIGN and g(bounds=_bounds(P, None)) == EINVAL
+
+
+@pytest.mark.parametrize("layout", [6, 7])
+@pytest.mark.parametrize("n_q", [1, 40, 64])
+def test_block_layouts_have_a_balanced_chunk(L, layout, n_q):
+    import numpy as np
+    c = _paged(layout, pages=16, batch=3)
+    lens = np.array([0, 5, 1000], np.int32)
+    ch = L.kvq_paged_attend_plan_chunk(C.byref(c), 2, n_q, 1, lens.ctypes.data_as(C.c_void_p))
+    assert ch >= 64 and ch % 64 == 0
+    zero = np.zeros(3, np.int32)
+    assert L.kvq_paged_attend_plan_chunk(C.byref(c), 2, n_q, 1, zero.ctypes.data_as(C.c_void_p)) >= 64
