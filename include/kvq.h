@@ -540,7 +540,9 @@ kvq_status kvq_page_plan(int32_t batch, int32_t page_size, int32_t max_pages_per
  *                 (block layouts: as below).
  * Quantisation as kvq_paged_store. Block layouts: consecutive slots of a block (64 pool rows) are one append to
  * it, and several such runs that follow each other in the call (up to 64 tokens without a slot between them) are
- * appended in their order; the values of a block that is met again behind other blocks are unspecified. The block table is not read. Hadamard caches with a window are refused (its ring goes by sequence). One launch (mixed K/V layouts: one per plane). n_tokens == 0 is a no-op.
+ * appended in their order; the values of a block that is met again behind other blocks, or behind more than 64
+ * tokens without a slot, are unspecified. The block table is not read. Hadamard caches with a window are refused
+ * (its ring goes by sequence). One launch (mixed K/V layouts: one per plane). n_tokens == 0 is a no-op.
  */
 kvq_status kvq_paged_store_slots(const kvq_paged_cache *cache, const kvq_rows *k_new, const kvq_rows *v_new,
                                  int32_t dtype, int32_t n_tokens, const int64_t *slots, kvq_stream_t stream);
