@@ -339,7 +339,8 @@ __global__ void __maxnreg__(D == 128 ? 152 : 224) attend_b64_kernel(AttendArgs a
 }
 
 // Joins the partials of every row: M = max m, out = sum o 2^(m - M) / sum l 2^(m - M). SPLIT: a CTA per row, whose warps
-// split the partials; else a warp per row.
+// split the partials; else a warp per row. Zeros only where the sum is 0 (a row that sees nothing): a sum that is not a number,
+// as scores that are none or a wait that gave up leave it, stays one.
 constexpr int kJoinWarps = 4, kBatch = 4;
 template <int D, bool SPLIT>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_b64_kernel(AttendArgs a, unsigned n_rows) {
@@ -380,14 +381,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_b64_kernel(AttendArgs a,
           oc[u][v] = ok ? *reinterpret_cast<const float4 *>(a.part_o + p * D + 128 * v + 4 * lane) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         bm = fmaxf(bm, mc[u]);
       }
-      if (bm == -INFINITY) continue;                     // pieces that the row does not see
-      const float corr = exp2f(M - bm);
+      const float ref = bm == -INFINITY ? 0.0f : bm;     // pieces that the row does not see weigh 2^-inf
+      const float corr = exp2f(M - ref);
       L *= corr;
 #pragma unroll
       for (int v = 0; v < V; ++v) O[v].x *= corr, O[v].y *= corr, O[v].z *= corr, O[v].w *= corr;
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
-        const float w = exp2f(mc[u] - bm);
+        const float w = exp2f(mc[u] - ref);
         L = fmaf(lc[u], w, L);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -416,10 +417,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_b64_kernel(AttendArgs a,
         Lt = fmaf(sm_l[w], f, Lt);
         x = fmaf(sm_o[w][d], f, x);
       }
-      a.out[out_row(a, row) * D + d] = Lt > 0.0f ? x / Lt : 0.0f;
+      a.out[out_row(a, row) * D + d] = Lt == 0.0f ? 0.0f : x / Lt;
     }
   } else {
-    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
 #pragma unroll
     for (int v = 0; v < V; ++v)
       *reinterpret_cast<float4 *>(a.out + out_row(a, row) * D + 128 * v + 4 * lane) = make_float4(O[v].x * inv, O[v].y * inv, O[v].z * inv, O[v].w * inv);

@@ -12,7 +12,8 @@
 //
 // Bound: the tensor cores' rate for mma.sync and its operands from shared memory (per 64 tokens and warp 64 products for the
 // scores, 128 for both parts of p, 64 ldmatrix of 512 bytes).
-// 256 rows x 8 sequences over 4096 tokens, 8 kv heads: 299 us with the join, the tensor pipe 61 % busy.
+// 256 rows x 8 sequences over 4096 tokens, 8 kv heads: 301 us with the join (298 where a wait that gave up marked its own warp alone),
+// the tensor pipe 61 % busy.
 #include "attend_b64.cuh"
 
 namespace kvq {
@@ -49,7 +50,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_b64_rows_kernel(AttendArgs
     return;
   }
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + 2 * kBuffers * kTile), *empty = full + kBuffers;
+  volatile int *gave_up = reinterpret_cast<int *>(empty + kBuffers);
   if (tid == 0) {
+    *gave_up = 0;
 #pragma unroll
     for (int k = 0; k < 2 * kBuffers; ++k) bar_init(full + k, kThreads / 32);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -57,7 +60,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_b64_rows_kernel(AttendArgs
   __syncthreads();
   walk.wait_for_append(a);
   // Block number `it` of the CTA lies in buffer it % kBuffers, for the (it / kBuffers)-th time. Waits are bounded: a warp whose wait
-  // gives up goes on without waiting and leaves NaN behind.
+  // gives up goes on without waiting, and may then write over a block that another warp still reads. It says so before it writes
+  // anything more, so a warp that has read such bytes finds `gave_up` set when it leaves its rows behind: they are NaN, as
+  // are all that the CTA leaves from then on. Rows left before were read from whole blocks.
   int it = 0;
   bool failed = false;
   auto wait = [&](uint64_t *bar, int times) {
@@ -164,6 +169,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_b64_rows_kernel(AttendArgs
     auto prepare = [&](int i) {                          // block i of the span, whose codes have been read, and the read of the next
       const int at = it + i, buffer = at % kBuffers;
       if (at >= kBuffers) wait(empty + buffer, at / kBuffers - 1);
+      if (failed) {
+        *gave_up = 1;
+        __threadfence_block();
+      }
       convert(buffer);
       arrive(full + buffer);
       sc_then = sc_next;
@@ -259,6 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_b64_rows_kernel(AttendArgs
     it += max(n, 0);
     const size_t head = (size_t)sp.b * heads + sp.hd, part = (size_t)blockIdx.x + head;
     if (work) {
+      const bool lost = failed || *gave_up;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         l[k] += __shfl_xor_sync(0xffffffffu, l[k], 1);
@@ -271,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_b64_rows_kernel(AttendArgs
             *reinterpret_cast<float2 *>(a.part_o + p * kD + 8 * j + 2 * c) = make_float2(O[j][2 * k], O[j][2 * k + 1]);
           if (c == 0) {
             a.part_m[p] = m[k];
-            a.part_l[p] = failed ? __int_as_float(0x7FC00000) : l[k];
+            a.part_l[p] = lost ? __int_as_float(0x7FC00000) : l[k];
           }
         }
       }
