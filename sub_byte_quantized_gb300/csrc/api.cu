@@ -781,12 +781,16 @@ int32_t kvq_paged_attend_plan_chunk(const kvq_paged_cache *cache, int32_t n_q_he
     fail(KVQ_EINVAL, "host_seq_lens is NULL or bad head counts");
     return 0;
   }
+  if ((long long)(n_q_heads / v.H) * n_q > INT_MAX) {
+    fail(KVQ_ESHAPE, "more than INT_MAX query rows of a kv head");
+    return 0;
+  }
   int dev = 0, sms = 148;
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   int per_sm = 1, per_unit = 1;
   bool window_ctas = false;
   phase1_capacity(v, (n_q_heads / v.H) * n_q, q_dtype, per_sm, per_unit, window_ctas);
-  const long long capacity = (long long)sms * per_sm / per_unit;       // (head, chunk) units in one wave
+  const long long ctas = (long long)sms * per_sm, capacity = ctas / per_unit;   // (head, chunk) units in one wave
   const int cap_len = v.cap;
   auto units = [&](int ch) {
     long long u = 0;
@@ -806,7 +810,9 @@ int32_t kvq_paged_attend_plan_chunk(const kvq_paged_cache *cache, int32_t n_q_he
   long long best = -1;
   int best_ch = 8192;
   for (int ch = 64; ch <= 8192; ch += 64) {
-    const long long cost = (units(ch) + capacity - 1) / capacity * ch;
+    // (a unit of more CTAs than a wave holds: counted by CTAs)
+    const long long waves = capacity > 0 ? (units(ch) + capacity - 1) / capacity : (units(ch) * per_unit + ctas - 1) / ctas;
+    const long long cost = waves * ch;
     if (best < 0 || cost < best) {
       best = cost;
       best_ch = ch;
