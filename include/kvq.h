@@ -93,7 +93,7 @@ typedef enum {
    *   - else s 2^k with the smallest k >= 1 that s 2^k >= need, and the codes of the block's rows in front of the new
    *     ones are rounded again: round(code 2^-k), half to even.
    * New codes are round(x / scale) by that scale (int8 half to even, e4m3 to nearest even, saturating; an infinity
-   * counts as the largest finite value); all 0 where it is 0. Rows
+   * counts as the largest finite value, a NaN not at all, and its own code is unspecified); all 0 where it is 0. Rows
    * behind the new ones are not touched, but what they stand for may change with the scale: an append ends its block.
    * A row kept through several growths is off by at most one step of the last scale more. Contiguous caches: capacity
    * a multiple of 64. One block layout in both planes; not provided by the rotary appends, the calls with token

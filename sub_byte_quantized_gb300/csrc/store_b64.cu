@@ -141,6 +141,13 @@ struct Raw8 {
     m = max(m & 0xFFFFu, m >> 16);
     return bf16 ? __uint_as_float(m << 16) : __half2float(__ushort_as_half((unsigned short)m));
   }
+  // max with the magnitudes of the values that are numbers (the bits of the others lie above infinity's)
+  __device__ void amax_of_numbers(bool bf16, float &m) const {
+    float v[8];
+    get(bf16, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
+  }
   __device__ __forceinline__ void get(bool bf16, float (&v)[8]) const {
     if constexpr (F32) {
       const uint32_t u[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
@@ -190,6 +197,18 @@ __device__ __forceinline__ void store_run(const Run &u, int dtype, int tid, floa
     }
   }
   float amax = Raw8<F32>::amax_value(bf16, bits);
+  if (amax != amax) {                                    // values that are no numbers do not count
+    amax = 0.0f;
+#pragma unroll
+    for (int p = 0; p < P; ++p) raw[p].amax_of_numbers(bf16, amax);
+    if constexpr (NT == 32) {
+      for (int r = P * RP + r0; r < u.m; r += RP) {
+        Raw8<F32> more;
+        more.load(u.src, u.elem + (size_t)r * u.stride + col);
+        more.amax_of_numbers(bf16, amax);
+      }
+    }
+  }
 #pragma unroll
   for (int k = 16; k; k >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, k));
   if constexpr (NT > 32) {                               // (two buffers in turn: the next run's maxima do not meet this one's)
