@@ -122,7 +122,8 @@ __device__ __forceinline__ void unpack4_s8_t(uint32_t w, uint32_t &d0, uint32_t 
 
 // CAP: score capture (Hadamard layout, contiguous cache): the exact integer score of every
 // (row, body token) this CTA computes and each row's int8 query scale go to a.cap_scores / a.cap_sq.
-// SCORES: the masked scores go to a.part_s, for the kernel that sums the tokens' weights. SIGNED: 4-bit K codes enter
+// SCORES (a.held): the output is held to float32, and the masked scores go to a.part_s, for the kernel that sums the tokens'
+// weights (sparse calls keep none: a.s_rows is 0). SIGNED: 4-bit K codes enter
 // as exact signed values, so that a score's terms are as small as the keys (f32 and f16 queries of such calls: the
 // weights' error over 7900 tokens falls from 2e-6 to 4e-7, 128K tokens take 51.6 instead of 50.4 us; bf16 products
 // are short and lose little either way).
@@ -427,7 +428,7 @@ __global__ void __launch_bounds__(kWarps * 32, kMinBlocks) attend_mma_kernel(Att
   const int lim0 = r0 < R ? row_limit_of(a, sl, r0) : -1;
   const int lim1 = r1 < R ? row_limit_of(a, sl, r1) : -1;
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
-  // Calls that also score the tokens are held to float32: their probabilities are taken 2^12 times larger (up to
+  // Calls that also score the tokens and sparse ones are held to float32: their probabilities are taken 2^12 times larger (up to
   // 2^12 instead of 1), so that P' and its lo part stay above f16's subnormals for tokens of little weight and
   // small scales (16 sequences of up to 16379 tokens in Q8_0, scales near 0.02: 6.7e-6 of the output's norm without,
   // 5.8e-7 with it; 79.7 and 81.0 us). A scale of 2 or more could take P' out of f16's range: from the first one on
@@ -884,10 +885,10 @@ template <int LAYOUT, int VLAYOUT, bool QSPLIT>
 cudaError_t launch_kind_t(const AttendArgs &a, cudaStream_t st) {
   const bool paged = a.cache.page_shift >= 0;
   if constexpr (LAYOUT == KVQ_Q4_0) {
-    if (a.part_s && a.q_dtype != KVQ_BF16)
+    if (a.held && a.q_dtype != KVQ_BF16)
       return paged ? launch_t<LAYOUT, VLAYOUT, QSPLIT, true, false, true, true>(a, st) : launch_t<LAYOUT, VLAYOUT, QSPLIT, false, false, true, true>(a, st);
   }
-  if (a.part_s) return paged ? launch_t<LAYOUT, VLAYOUT, QSPLIT, true, false, true>(a, st) : launch_t<LAYOUT, VLAYOUT, QSPLIT, false, false, true>(a, st);
+  if (a.held) return paged ? launch_t<LAYOUT, VLAYOUT, QSPLIT, true, false, true>(a, st) : launch_t<LAYOUT, VLAYOUT, QSPLIT, false, false, true>(a, st);
   return paged ? launch_t<LAYOUT, VLAYOUT, QSPLIT, true>(a, st) : launch_t<LAYOUT, VLAYOUT, QSPLIT, false>(a, st);
 }
 template <int LAYOUT, int VLAYOUT>

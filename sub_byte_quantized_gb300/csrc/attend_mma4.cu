@@ -70,7 +70,8 @@ __device__ __forceinline__ uint32_t swz(int row, int j) {
   return (uint32_t)(row * kRowBytes + ((j ^ ((row >> 1) & 3)) << 4));
 }
 
-// SCORES: the masked scores go to a.part_s, for the kernel that sums the tokens' weights. CENTRED: K codes enter as
+// SCORES (a.held): the masked scores go to a.part_s, for the kernel that sums the tokens' weights (sparse calls keep none:
+// a.s_rows is 0). CENTRED: K codes enter as
 // exact u - 8 and zero-points as z + 8 s, so that a score's terms are as small as the keys (f32 and f16 queries of
 // such calls: the weights' error over 7900 tokens falls from 1.2e-6 to 4e-7; bf16 products are short and lose
 // little either way). 128K tokens, f16: 80.5 -> 82.9 us with the contiguous caches' chunk of that time.
@@ -707,7 +708,7 @@ cudaError_t launch_kind(const AttendArgs &a, cudaStream_t st) {
 
 cudaError_t launch_attend_mma4(const AttendArgs &a, cudaStream_t st) {
   if (a.cache.layout != KVQ_ASYM4_G32) return cudaErrorNotSupported;   // built for the layout that uses it
-  if (!a.part_s) return launch_kind<false, false>(a, st);
+  if (!a.held) return launch_kind<false, false>(a, st);
   return a.q_dtype == KVQ_BF16 ? launch_kind<true, false>(a, st) : launch_kind<true, true>(a, st);
 }
 

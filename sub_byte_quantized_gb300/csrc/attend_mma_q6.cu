@@ -95,7 +95,7 @@ __device__ __forceinline__ int row_limit_of(const AttendArgs &a, const SeqLen &s
 __device__ __forceinline__ uint32_t lds32(const uint8_t *p) { return *reinterpret_cast<const uint32_t *>(p); }
 
 // SIGNED: V codes enter as exact signed values, no offset mass goes through the long P'V accumulation
-// (calls that also score the tokens, whose output is held to float32: over 32K tokens of random keys its
+// (calls that also score the tokens and sparse ones (a.held), whose output is held to float32: over 32K tokens of random keys its
 // error falls from 4e-5 of the output's norm to 1e-6). Their probabilities are taken 2^12 larger, so that P' and
 // its lo part stay above f16's subnormals for small scales and tokens of little weight (4096 tokens with values of
 // 0.01: 4e-5 of the output's norm without); see kLift.
@@ -589,7 +589,7 @@ cudaError_t launch_pages(const AttendArgs &a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_attend_mma_q6(const AttendArgs &a, cudaStream_t st) {
-  return a.lse ? launch_pages<true>(a, st) : launch_pages<false>(a, st);
+  return a.held ? launch_pages<true>(a, st) : launch_pages<false>(a, st);
 }
 
 }  // namespace kvq

@@ -232,7 +232,7 @@ __device__ __forceinline__ int row_limit_of(const AttendArgs &a, const SeqLen &s
 // one warp scoring every token while the other three only unpack.
 // CAP: score capture (Hadamard layouts, contiguous cache): every exact integer body score the CTA
 // computes and each row's int8 query scale also go to a.cap_scores / a.cap_sq.
-// SCORES: calls that also score the tokens, whose output is held to float32. Probabilities are taken 2^kLift larger
+// SCORES: calls that also score the tokens and sparse ones (a.held), whose output is held to float32. Probabilities are taken 2^kLift larger
 // (4096 tokens in Hadamard int4 with values of 0.001: 6e-5 of the output's norm without; beside a token of 2^14
 // times the others' weight 6e-5 to 2e-4 in every layout), and a pass's products with V are summed by themselves, the
 // small ones first, and reach the output by a rounded addition (the tensor core truncates its sums: 1.4e-5 of the
@@ -916,7 +916,7 @@ cudaError_t launch_pair(const AttendArgs &a, cudaStream_t st) {
       return cudaErrorNotSupported;
     }
   }
-  return a.lse ? launch_kind<KL, VL, true>(a, st) : launch_kind<KL, VL, false>(a, st);
+  return a.held ? launch_kind<KL, VL, true>(a, st) : launch_kind<KL, VL, false>(a, st);
 }
 
 }  // namespace

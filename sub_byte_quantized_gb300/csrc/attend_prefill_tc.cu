@@ -710,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_tc_kernel(AttendAr
     const float fabs_row = fabsf(arow);
     if (CAP && live && chunk_id == 0) a.cap_sq[qrow] = a.s_q[qrow];
     const uint32_t lane_base = (uint32_t)(32 * q4) << 16;
-    const int most = a.lse ? 20 : 8;                    // log2 of the largest p
+    const int most = a.held ? 20 : 8;                    // log2 of the largest p
     float m = -INFINITY, l = 0.0f;
     for (int j = ALT ? b : 0; j < n_st && ok; j += ALT ? 2 : 1) {
       const int tb = j % TB, ts = t0 + j * kStage, jb = ALT ? j >> 1 : j;   // jb: the block's own count
@@ -910,7 +910,7 @@ template <int L>
 cudaError_t launch_layout(const AttendArgs &a, cudaStream_t st) {
   const bool paged = a.cache.page_shift >= 0;
   if (a.cap_scores) return paged ? cudaErrorNotSupported : launch_tc<L, false, true, false>(a, st);
-  if (a.lse && a.gqa * a.n_q <= kRows) return paged ? launch_tc<L, true, false, true>(a, st) : launch_tc<L, false, false, true>(a, st);
+  if (a.held && a.gqa * a.n_q <= kRows) return paged ? launch_tc<L, true, false, true>(a, st) : launch_tc<L, false, false, true>(a, st);
   return paged ? launch_tc<L, true, false, false>(a, st) : launch_tc<L, false, false, false>(a, st);
 }
 

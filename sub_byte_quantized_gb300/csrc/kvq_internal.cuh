@@ -197,9 +197,11 @@ struct AttendArgs {
   // written by phase 2 when not nullptr
   float *lse;
   // masked scores in base 2, [B][H_kv][s_tokens][s_rows] (query rows of the kv head, tokens of the body),
-  // written by the decode kernels when not nullptr (s_rows 0: none are); tokens no row sees are left out
+  // written by the decode kernels when not nullptr; tokens no row sees are left out
   float *part_s;
   int s_rows, s_tokens;
+  // the output is held to float32: phase 1 in the form that the calls with token weights run, whether or not it keeps scores
+  bool held;
   // > 1: the call's sequences are (sequence, kv head, query) triples of out_nq queries each, whose outputs go to
   // [B][Hq][out_nq][D]
   int out_nq;
