@@ -83,6 +83,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_b64_rows_kernel(AttendArgs
     const int n = seen < 0 ? 0 : min(sp.n, (seen >> 6) - sp.blk + 1);
     const size_t head_row0 = ((size_t)sp.b * cv.H + kvh) * cv.cap;
 
+    // (Plain loads: the append in front of this grid may write while it is already running, a scale next to one that another
+    // CTA has read. The read-only path is for what nobody writes.)
     // A thread's codes: 16-byte pieces tid and tid + 256 of each plane (token p / 8, column p % 8), and the block's scales.
     uint4 raw[4];
     float2 sc = make_float2(0.0f, 0.0f), sc_next = sc;   // scales of the block computed from, and of the codes at hand
@@ -94,10 +96,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_b64_rows_kernel(AttendArgs
       for (int k = 0; k < 2; ++k) {
         const int p = tid + kThreads * k;
         const bool ok = t0 + p / 8 < sp.len;             // rows behind the sequence: codes 0
-        raw[k] = ok ? __ldg(reinterpret_cast<const uint4 *>(cv.payload[0] + r * kD) + p) : make_uint4(0u, 0u, 0u, 0u);
-        raw[2 + k] = ok ? __ldg(reinterpret_cast<const uint4 *>(cv.payload[1] + r * kD) + p) : make_uint4(0u, 0u, 0u, 0u);
+        raw[k] = ok ? reinterpret_cast<const uint4 *>(cv.payload[0] + r * kD)[p] : make_uint4(0u, 0u, 0u, 0u);
+        raw[2 + k] = ok ? reinterpret_cast<const uint4 *>(cv.payload[1] + r * kD)[p] : make_uint4(0u, 0u, 0u, 0u);
       }
-      sc_next = make_float2(__ldg(static_cast<const float *>(cv.scale[0]) + (r >> 6)), __ldg(static_cast<const float *>(cv.scale[1]) + (r >> 6)));
+      sc_next = make_float2(static_cast<const float *>(cv.scale[0])[r >> 6], static_cast<const float *>(cv.scale[1])[r >> 6]);
     };
     auto convert = [&](int buffer) {
 #pragma unroll
