@@ -381,14 +381,18 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_b64_kernel(AttendArgs a,
           oc[u][v] = ok ? *reinterpret_cast<const float4 *>(a.part_o + p * D + 128 * v + 4 * lane) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         bm = fmaxf(bm, mc[u]);
       }
-      const float ref = bm == -INFINITY ? 0.0f : bm;     // pieces that the row does not see weigh 2^-inf
-      const float corr = exp2f(M - ref);
+      if (bm == -INFINITY) {                             // pieces that the row does not see: sums of 0, or no numbers
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) L += lc[u];
+        continue;
+      }
+      const float corr = exp2f(M - bm);
       L *= corr;
 #pragma unroll
       for (int v = 0; v < V; ++v) O[v].x *= corr, O[v].y *= corr, O[v].z *= corr, O[v].w *= corr;
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
-        const float w = exp2f(mc[u] - ref);
+        const float w = exp2f(mc[u] - bm);
         L = fmaf(lc[u], w, L);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
