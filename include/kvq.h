@@ -536,8 +536,8 @@ kvq_status kvq_page_plan(int32_t batch, int32_t page_size, int32_t max_pages_per
  *   k_new, v_new  [n_tokens][n_kv_heads][head_dim] in `dtype` by token_stride and head_stride (kvq_rows;
  *                 batch_stride is not used)
  *   slots         device i64 [n_tokens], as kvq_page_plan writes them; a token whose slot lies outside
- *                 [0, n_pages * page_size) is not written. A slot that occurs twice gets either row
- *                 (block layouts: as below).
+ *                 [0, n_pages * page_size) is not written. What a slot that occurs twice holds is unspecified:
+ *                 codes and scales may come from different tokens (block layouts: as below).
  * Quantisation as kvq_paged_store. Block layouts: consecutive slots of a block (64 pool rows) are one append to
  * it, and several such runs that follow each other in the call (up to 64 tokens without a slot between them) are
  * appended in their order; the values of a block that is met again behind other blocks, or behind more than 64
@@ -569,7 +569,8 @@ typedef struct kvq_block_bounds {
 /* Bounds of every block that holds a token of [first, kv_len), over the block's tokens below kv_len: after an append
  * at pos0, first = pos0 (a block layout's append changes its block's values; they are in it). first == kv_len is a
  * no-op. Paged: the blocks of each sequence's newest n_fresh tokens (seq_lens device i32 [batch], clamped into [0,
- * max_pages_per_seq * page_size]); n_fresh == 0 is a no-op. One launch. */
+ * max_pages_per_seq * page_size]); n_fresh == 0 is a no-op; where sequences differ, the largest append of the step: blocks
+ * renewed without need come out the same. One launch. */
 kvq_status kvq_block_bounds_update(const kvq_cache *cache, const kvq_block_bounds *bounds, int32_t first, int32_t kv_len,
                                    kvq_stream_t stream);
 kvq_status kvq_paged_block_bounds_update(const kvq_paged_cache *cache, const kvq_block_bounds *bounds,
@@ -579,7 +580,8 @@ kvq_status kvq_paged_block_bounds_update(const kvq_paged_cache *cache, const kvq
  * The blocks selected for each query and kv head. A query row (Hadamard layouts: rotated) in int8, q8 = clamp(rint(q /
  * s_q), -127, 127) with s_q = amax / 127, gives a block the score
  *   (sum over q8_d > 0 of q8_d hi_d, over q8_d < 0 of q8_d lo_d) * s_q * scale     an exact integer, then two rounded
- *                                                       products; no q8 . k s_q of the block is larger
+ *                                                       products; no q8 . k s_q of the block is larger but by
+ *                                                       the roundings of the bounds' divisions and these (2^-24 each)
  * and the largest score over the query heads of a kv head counts. Of the blocks that row i sees (its limit as in
  * kvq_decode_attend / kvq_paged_decode_attend, causal or not) the list holds the first n_sink, the last n_recent, and
  * among the others those with the highest scores, ties going to the lowest index, n_sel in all.

@@ -26,7 +26,8 @@
 //
 // Bound: the packed cache's bytes from HBM. 128K tokens of 8 kv heads (268 MB) 55 to 57 us by the GPU with the join, where the
 // bytes alone take 41 in a kernel that only reads; 16 ragged paged sequences (285 MB) 58 to 59. 16-token stages, three in flight and four
-// CTAs per SM 58.8 (57.3 in the same run), four in flight and three CTAs 57.8.
+// CTAs per SM 58.8 (57.3 in the same run), four in flight and three CTAs 57.8 (dealt out as here; an
+// earlier kernel, with such stages interleaved over a head's CTAs, took 51.9, and 97.9 for ragged: not tried on this one).
 #include "attend_b64.cuh"
 
 namespace kvq {
@@ -456,7 +457,8 @@ cudaError_t launch_join_b64(const AttendArgs &a, cudaStream_t st) {
   const unsigned rows = (unsigned)((size_t)a.cache.B * a.Hq * a.n_q);
   const int sms = sm_count();
   // Few rows have many partials each: a CTA for a row, else a warp (64 rows, 128K tokens: 57.3 / 63.3 us with phase 1; 512 rows
-  // 59.3 / 60.3; 1024 rows of 32 blocks 38.4 / 36.9; 32768 rows 330 / 299)
+  // 59.3 / 60.3; 640 rows 98.3 / 98.3; 1024 rows 97.3 / 97.4, of 32 blocks 36.1 / 35.7; 2048 rows 100.1 / 98.9, of 32 blocks
+  // 39.4 / 37.5; 32768 rows 330 / 299)
   const bool split = rows <= 8u * (unsigned)sms;
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr;

@@ -24,13 +24,12 @@ __host__ __device__ constexpr bool is_hadamard(int layout) {
 // 8-bit layouts with one f32 scale per block of 64 tokens, head and plane.
 __host__ __device__ constexpr bool is_b64(int layout) { return layout == KVQ_INT8_B64 || layout == KVQ_E4M3_B64; }
 // Their phase 1: query rows of a kv head that a CTA takes at once (`rows`: of a kv head), and resident CTAs per SM.
-// Groups of 8 rows read the cache once each, groups of 128 compute for 128 (64 heads of 4096 tokens, 8 / 128: 32 rows 44 / 57 us,
-// 48 rows 58 in either).
-constexpr int kB64ManyRows = 128;
-#ifndef KVQ_B64_MANY
-#define KVQ_B64_MANY 40
-#endif
-__host__ __device__ constexpr int b64_group(int D, long long rows) { return D == 128 && rows > KVQ_B64_MANY ? kB64ManyRows : 8; }
+// Groups of 8 rows read the cache once each, groups of 128 compute for 128. In us, 8 / 128, for 32, 40 and 48 rows: 128 heads of
+// 16384 tokens (537 MB) int8 340 / 420, 421 / 424, 503 / 427, e4m3 335 / 415, 420 / 419, 493 / 420; 64 heads of 4096 (67 MB, in
+// L2) 44 / 62, 52 / 63, 60 / 64, with f32 queries 47 / 70, 57 / 70, 65 / 71 (64 rows 83 / 72);
+// 8 heads of 131072 139 / 214, 213 / 217, 200 / 217 (64 rows 323 / 220).
+constexpr int kB64ManyRows = 128, kB64FewRows = 40;
+__host__ __device__ constexpr int b64_group(int D, long long rows) { return D == 128 && rows > kB64FewRows ? kB64ManyRows : 8; }
 __host__ __device__ constexpr int kB64CtasPerSm(int D) { return D == 128 ? 3 : 2; }
 __host__ __device__ constexpr int b64_ctas(int D, long long rows) { return b64_group(D, rows) == 8 ? kB64CtasPerSm(D) : 1; }
 constexpr int kMaxDevices = 64;     // per-device one-time kernel attribute set-up

@@ -4,7 +4,7 @@
 // packed rows stand for; Hadamard layouts: in the rotated basis), in int8 by one scale per block, s = max(|lo|, |hi|) / 127:
 // floor(lo / s) and ceil(hi / s), so that the bounds stay bounds.
 // Score of a block for one query row: sum_d max(q8_d lo_d, q8_d hi_d) s_q s, with the row in int8 (s_q = amax / 127), which
-// no q8 . k of the block exceeds. q8 >= 0 takes hi and q8 < 0 takes lo, so with q+ = max(q8, 0) and q- = min(q8, 0) it is
+// no q8 . k of the block exceeds but by rounding (each division before its floor or ceil, and at 127 the scale's own). q8 >= 0 takes hi and q8 < 0 takes lo, so with q+ = max(q8, 0) and q- = min(q8, 0) it is
 // q+ . hi + q- . lo: dp4a, exact integers (below 2^24), then two rounded products: the same bits whatever the order. The
 // query heads of a kv head read one cache, so they share a list: the largest of their scores counts.
 // Lists: the blocks with the highest scores, by the radix selection that the budget's calls use, whose kernel scores them too.
